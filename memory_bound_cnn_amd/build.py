@@ -28,7 +28,9 @@ SOURCES = ["wtconv_fused.hip", "wtconv_fused_k1.hip", "wtconv_fused_k3.hip", "wt
            "wtconv_fused_k7.hip", "wtconv_fused_s_p64.hip", "wtconv_fused_s_p32.hip",
            "wtconv_fused_s_p128a.hip", "wtconv_fused_s_p128b.hip", "wtconv_fused_s_small.hip", "wtconv_fused_s_p112.hip",
            "wtconv_fused_s_dw.hip",
-           "wtconv_tiny.hip", "wtconv_lane.hip", "wtconv_unfused.hip", "wtconv_top.hip", "wtconv_layout.hip", "wtconv_noalloc.hip", "wtconv_corr.hip", "wtconv_api.cpp", "wtconv_plan.cpp"]
+           "wtconv_tiny.hip", "wtconv_lane.hip", "wtconv_unfused.hip", "wtconv_top.hip", "wtconv_layout.hip", "wtconv_noalloc.hip", "wtconv_corr.hip", "wtconv_api.cpp", "wtconv_plan.cpp",
+           "wtconv_tok_rms.hip", "wtconv_tok_rotary.hip", "wtconv_tok_dropout.hip", "wtconv_tok_attn.hip",
+           "wtconv_tok_attn_bf16.hip", "wtconv_tok_attn_fp32.hip", "wtconv_tok_api.cpp"]
 
 
 def _compile(src):

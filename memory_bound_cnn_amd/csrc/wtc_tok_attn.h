@@ -1,0 +1,280 @@
+// Building blocks of the attention kernels (wtconv_tok_attn_*.hip).
+//
+// Products run on the matrix cores as 32 x 32 tiles over 16 terms.  A lane
+// holds, of an A tile, row (lane % 32), and of a B tile, column (lane % 32),
+// at the eight terms of its half of the wave (h = lane / 32); of a result, 16
+// values of column (lane % 32), register r being row 8 (r / 4) + 4 h + r % 4.
+// Any assignment of terms to (h, i) serves as long as A and B agree, and that
+// is what lets a result feed the next product without moving between lanes:
+// registers 8 s .. 8 s + 7 of a result are, as a B tile, the terms
+//   16 s + 4 h + {0, 1, 2, 3} and 16 s + 8 + 4 h + {0, 1, 2, 3}     ("turned" order)
+// and the A tile of that product is read from shared memory in this order.
+// bfloat16 takes one v_mfma_f32_32x32x16_bf16 a tile, float32 eight
+// v_mfma_f32_32x32x2_f32, whose two terms are the same i of both halves.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "wtc_tok_device.h"
+#include "wtc_tok_internal.h"
+
+namespace wtc {
+namespace attn {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) char lds_char;
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// Eight terms of a lane.
+template <typename T>
+struct Frag;
+template <>
+struct Frag<uint16_t> {
+    u32x4 v;
+};
+template <>
+struct Frag<float> {
+    f32x8 v;
+};
+
+__device__ __forceinline__ void mma(const Frag<uint16_t>& a, const Frag<uint16_t>& b, f32x16& c) {
+    c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a.v), __builtin_bit_cast(bf16x8, b.v), c,
+                                                0, 0, 0);
+}
+__device__ __forceinline__ void mma(const Frag<float>& a, const Frag<float>& b, f32x16& c) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a.v[i], b.v[i], c, 0, 0, 0);
+}
+
+// Registers 8 s .. 8 s + 7 of a result as the terms of a B tile.  bfloat16:
+// rounded to nearest even; the sums stay in 32 bits, and the tile's values
+// reach them with the same 8 bits as the tensors they are multiplied with.
+__device__ __forceinline__ void as_terms(const f32x16& c, int s, Frag<uint16_t>& f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f.v[i] = bf16x2_rne(c[8 * s + 2 * i], c[8 * s + 2 * i + 1]);
+}
+__device__ __forceinline__ void as_terms(const f32x16& c, int s, Frag<float>& f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f.v[i] = c[8 * s + i];
+}
+
+// A tile of rows in shared memory: 16-byte chunks, chunk c of row r at place
+// c ^ turn(r) of its row.  turn() gives any 16 rows (8 for 128-byte rows, ...)
+// the banks of different places when lanes read the same chunk of consecutive
+// rows, and any 4 consecutive rows different 64-byte segments when they are
+// read transposed.
+template <typename T, int DP>
+struct Tile {
+    static constexpr int kRowBytes = (DP == 96 ? 128 : DP) * (int)sizeof(T);
+    static constexpr int kChunks = kRowBytes / 16;   // a power of two, >= 4
+
+    static __device__ __forceinline__ int turn(int r) {
+        if constexpr (kChunks >= 16) return ((r & 3) << 2) | ((r >> 2) & 3);
+        if constexpr (kChunks == 8) return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+        return (r >> 2) & 3;
+    }
+
+    // Copies rows j0 .. j0 + ROWS - 1 of a [., D] matrix into the tile at byte
+    // address `dst` of shared memory: rows past `last` repeat row `last`,
+    // chunks past D the last chunk, so that nothing outside the sequence is
+    // read (those places meet zeros or are not stored).  `base` points at row
+    // j0.  Asynchronous: the caller waits with dma_wait() and a barrier.
+    template <int ROWS, int WAVES>
+    static __device__ __forceinline__ void copy(uint32_t dst, const char* base, uint32_t row_bytes, int last_row,
+                                                int chunks, int wave, int lane) {
+        constexpr int PER = 64 / kChunks > 0 ? 64 / kChunks : 1;   // rows of one instruction
+        constexpr int CALLS = ROWS * kChunks / 64 / WAVES;
+        static_assert(kChunks <= 64 && ROWS * kChunks % (64 * WAVES) == 0, "whole instructions");
+#pragma unroll
+        for (int i = 0; i < CALLS; ++i) {
+            const int r0 = (wave * CALLS + i) * PER;
+            const int r = r0 + lane / kChunks, c = (lane % kChunks) ^ turn(r);
+            const uint32_t off = (uint32_t)min(r, last_row) * row_bytes + (uint32_t)min(c, chunks - 1) * 16u;
+            const uint32_t at = dst + (uint32_t)r0 * kRowBytes;
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                         :
+                         : "s"(__builtin_amdgcn_readfirstlane(at)), "v"(off), "s"(base)
+                         : "memory");
+        }
+    }
+
+    // Terms 16 ks + 8 h .. + 7 of row (lane % 32) + r0: an A tile whose rows are rows of the matrix.
+    static __device__ __forceinline__ Frag<T> rows(const char* tile, int r0, int ks, int lane) {
+        const int r = r0 + (lane & 31), h = lane >> 5;
+        const char* p = tile + r * kRowBytes;
+        Frag<T> f;
+        if constexpr (sizeof(T) == 2) {
+            f.v = *reinterpret_cast<const u32x4*>(p + (((2 * ks + h) ^ turn(r)) << 4));
+        } else {
+            const u32x4 lo = *reinterpret_cast<const u32x4*>(p + (((4 * ks + 2 * h) ^ turn(r)) << 4));
+            const u32x4 hi = *reinterpret_cast<const u32x4*>(p + (((4 * ks + 2 * h + 1) ^ turn(r)) << 4));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t l = lo[i], u = hi[i];
+                f.v[i] = __builtin_bit_cast(float, l);
+                f.v[4 + i] = __builtin_bit_cast(float, u);
+            }
+        }
+        return f;
+    }
+
+    // Rows r0 + 16 s + the turned order, of column 32 db + lane % 32: an A tile
+    // whose rows are columns of the matrix.  bfloat16: 16 lanes read 4 rows of
+    // 16 columns and get them transposed, 4 rows of a column each.
+    static __device__ __forceinline__ Frag<T> cols(const char* tile, int r0, int s, int db, int lane) {
+        const int h = lane >> 5;
+        Frag<T> f;
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int r = r0 + 16 * s + 8 * k + 4 * h + ((lane & 15) >> 2);
+                const int c = 4 * db + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
+                const char* p = tile + r * kRowBytes + ((c ^ turn(r)) << 4) + (lane & 1) * 8;
+                const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (__attribute__((address_space(3))) s16x4*)(lds_char*)p);
+                const u32x2 u = __builtin_bit_cast(u32x2, t);
+                f.v[2 * k] = u[0];
+                f.v[2 * k + 1] = u[1];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = r0 + 16 * s + 8 * (i >> 2) + 4 * h + (i & 3);
+                const int col = 32 * db + (lane & 31), c = col >> 2;
+                f.v[i] = *reinterpret_cast<const float*>(tile + r * kRowBytes + ((c ^ turn(r)) << 4) + (col & 3) * 4);
+            }
+        }
+        return f;
+    }
+};
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) { return (uint32_t)(uintptr_t)(lds_char*)p; }
+
+// Waits for this wave's copies; a barrier then makes all waves' visible.
+__device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// Terms 16 ks + 8 h .. + 7 of one row in device memory (D channels, the others
+// zero), times `sign` (+1 or -1): a B tile whose columns are rows of the matrix.
+template <typename T>
+__device__ __forceinline__ Frag<T> row_terms(const T* row, int ks, int D, int lane, float sign) {
+    const int c = 16 * ks + 8 * (lane >> 5);
+    Frag<T> f;
+    if constexpr (sizeof(T) == 2) {
+        u32x4 u = {0u, 0u, 0u, 0u};
+        if (c < D) u = *reinterpret_cast<const u32x4*>(row + c);
+        if (sign < 0.f) u ^= 0x80008000u;
+        f.v = u;
+    } else {
+        f.v = f32x8{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (c < D) f.v = *reinterpret_cast<const f32x8*>(row + c) * sign;
+    }
+    return f;
+}
+
+__device__ __forceinline__ float dot(const Frag<uint16_t>& a, const Frag<uint16_t>& b) {
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v = fmaf(__builtin_bit_cast(float, a.v[i] << 16), __builtin_bit_cast(float, b.v[i] << 16), v);
+        v = fmaf(__builtin_bit_cast(float, a.v[i] & 0xFFFF0000u), __builtin_bit_cast(float, b.v[i] & 0xFFFF0000u), v);
+    }
+    return v;
+}
+__device__ __forceinline__ float dot(const Frag<float>& a, const Frag<float>& b) {
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v = fmaf(a.v[i], b.v[i], v);
+    return v;
+}
+
+// The value of the lane with the same column in the other half, joined with
+// this one's: both halves get the maximum or the sum.
+__device__ __forceinline__ float both_max(float v) {
+    const u32x2 r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v),
+                                                     false, false);
+    const uint32_t x = r[0], y = r[1];
+    return fmaxf(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y));
+}
+__device__ __forceinline__ float both_sum(float v) {
+    const u32x2 r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v),
+                                                     false, false);
+    const uint32_t x = r[0], y = r[1];
+    return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+}
+
+// Registers 4 g .. 4 g + 3 of the result tile `db` of a transposed output:
+// channels 32 db + 8 g + 4 h .. + 3 of the lane's row.
+template <typename T>
+__device__ __forceinline__ void store4(T* row, int db, int g, int D, int lane, float a, float b, float c, float d) {
+    const int at = 32 * db + 8 * g + 4 * (lane >> 5);
+    if (at >= D) return;
+    if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<u32x2*>(row + at) = u32x2{bf16x2_rne(a, b), bf16x2_rne(c, d)};
+    } else {
+        typedef float f32x4 __attribute__((ext_vector_type(4)));
+        *reinterpret_cast<f32x4*>(row + at) = f32x4{a, b, c, d};
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store_tile(T* row, int db, int D, int lane, const f32x16& c, float factor) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+        store4(row, db, g, D, lane, c[4 * g] * factor, c[4 * g + 1] * factor, c[4 * g + 2] * factor,
+               c[4 * g + 3] * factor);
+}
+
+struct Args {
+    const void *q, *k, *v, *o, *g;
+    const int* cu;
+    void *out, *dq, *dk, *dv;
+    float *lse, *delta;
+    int T, n_seq, Hq, Hk, group, D, causal;
+    float scale;
+    wtc_attn_strides sq, sk, sv, so, sg, sdq, sdk, sdv;
+};
+
+// The segment and the tile of `size` rows that a workgroup works on.  Segments
+// are the tokens before the first sequence, the sequences, and the tokens
+// after the last one; segment s may use the slots from floor(start / size) + s
+// on: that leaves ceil(length / size) slots at least to each, so a slot's
+// segment is found by searching cu_seqlens itself, with no plan on the host
+// and no prefix sums.  64 entries are probed at a time.
+struct Work {
+    int start, len, tile;
+    bool pad;    // tokens of no sequence
+    bool none;   // a slot that no tile has
+};
+__device__ __forceinline__ int bound_of(const Args& a, int s) {
+    if (s <= 0) return 0;
+    if (s >= a.n_seq + 2) return a.T;
+    return min(max(a.cu[s - 1], 0), a.T);
+}
+template <int SIZE>
+__device__ __forceinline__ Work find_work(const Args& a, int slot, int lane) {
+    int lo = 0, hi = a.n_seq + 2;   // the segment is in lo .. hi - 1
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 63) / 64, s = lo + lane * step;
+        const bool yes = s < hi && bound_of(a, s) / SIZE + s <= slot;
+        const int n = __builtin_popcountll(__builtin_amdgcn_ballot_w64(yes));
+        lo += max(n - 1, 0) * step;
+        hi = min(hi, lo + step);
+    }
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    Work w;
+    w.start = __builtin_amdgcn_readfirstlane(bound_of(a, lo));
+    w.len = max(__builtin_amdgcn_readfirstlane(bound_of(a, lo + 1)) - w.start, 0);
+    w.tile = slot - (w.start / SIZE + lo);
+    w.pad = lo == 0 || lo == a.n_seq + 1;
+    w.none = w.tile < 0 || (long long)w.tile * SIZE >= w.len;
+    return w;
+}
+inline long long slots(long long T, int n_seq, int size) { return T / size + n_seq + 2; }
+
+}  // namespace attn
+}  // namespace wtc

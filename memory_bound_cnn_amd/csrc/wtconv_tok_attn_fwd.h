@@ -1,0 +1,153 @@
+// Attention, forward: O = softmax(scale Q K^T) V inside each sequence, one pass
+// over the keys with the running maximum and sum of the softmax.
+//
+// A workgroup of four waves takes one head and 128 queries, 32 a wave; tiles of
+// 64 keys and values pass through shared memory, two tiles deep, copied there
+// directly from device memory while the tile before is worked on.  Per tile a
+// wave computes S^T = K Q^T (rows are keys, columns its queries), so that a lane
+// has 32 of the 64 products of one query: the maximum and the sum take one
+// exchange between the two halves of the wave, the scale of the running sums is
+// the lane's own, and P^T feeds O^T = V^T P^T from the registers it is in.
+#pragma once
+
+#include "wtc_tok_attn.h"
+
+namespace wtc {
+namespace attn {
+
+constexpr int kFwdRows = 128;   // queries of a workgroup
+constexpr int kFwdKeys = 64;    // keys of a tile
+
+// The running maximum is raised, and the sums rescaled, only when a tile
+// exceeds it by more than this many powers of two: P then reaches 2^8 instead
+// of 1, far from overflow in 32-bit sums, with the same relative rounding.
+constexpr float kRaise = 8.f;
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(256) k_attn_fwd(Args a) {
+    using L = Tile<T, DP>;
+    constexpr int KS = DP / 16, DB = DP / 32, TILE = kFwdKeys * L::kRowBytes;
+    __shared__ __align__(16) char lds[4 * TILE];   // 2 x (K tile, V tile)
+    static_assert(4 * TILE <= 160 * 1024, "shared memory");
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n_slots = gridDim.x / a.Hq, head = blockIdx.x % a.Hq;
+    const int slot = n_slots - 1 - blockIdx.x / a.Hq;   // late tiles have the most keys when causal: they go first
+    const Work w = find_work<kFwdRows>(a, slot, lane);
+    if (w.none) return;
+    const int row0 = w.tile * kFwdRows + wave * 32, row = row0 + (lane & 31);   // inside the segment
+    const int rows_left = w.len - row0;                                         // <= 0: this wave has none
+    const bool live = row < w.len;
+    T* out = static_cast<T*>(a.out) + (long long)(w.start + row) * a.so.token + head * a.so.head;
+    float* lse = a.lse ? a.lse + (long long)head * a.T + w.start + row : nullptr;
+    if (w.pad) {
+        if (live) {
+            f32x16 zero = {};
+#pragma unroll
+            for (int db = 0; db < DB; ++db) store_tile(out, db, a.D, lane, zero, 0.f);
+            if (lse && lane < 32) *lse = __builtin_inff();
+        }
+        return;
+    }
+    const int kvh = head / a.group, chunks = a.D * (int)sizeof(T) / 16;
+    const char* kbase = reinterpret_cast<const char*>(static_cast<const T*>(a.k) + (long long)w.start * a.sk.token + kvh * a.sk.head);
+    const char* vbase = reinterpret_cast<const char*>(static_cast<const T*>(a.v) + (long long)w.start * a.sv.token + kvh * a.sv.head);
+    const uint32_t krow = (uint32_t)a.sk.token * sizeof(T), vrow = (uint32_t)a.sv.token * sizeof(T);
+    const int keys = a.causal ? min(w.len, (w.tile + 1) * kFwdRows) : w.len;
+    const int tiles = (keys + kFwdKeys - 1) / kFwdKeys;
+    const uint32_t lds0 = lds_address(lds);
+    auto copy = [&](int j) {
+        const int j0 = j * kFwdKeys, last = min(w.len - 1 - j0, kFwdKeys - 1);
+        const uint32_t at = lds0 + (uint32_t)(j & 1) * (2 * TILE);
+        L::template copy<kFwdKeys, 4>(at, kbase + (long long)j0 * krow, krow, last, chunks, wave, lane);
+        L::template copy<kFwdKeys, 4>(at + TILE, vbase + (long long)j0 * vrow, vrow, last, chunks, wave, lane);
+    };
+    copy(0);
+
+    // a negative scale is taken into Q, so that the largest product is the largest logit
+    const float c = fabsf(a.scale) * kLog2e;
+    Frag<T> q[KS];
+    {
+        const T* qrow = static_cast<const T*>(a.q) + (long long)(w.start + min(row, w.len - 1)) * a.sq.token + head * a.sq.head;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) q[ks] = row_terms(qrow, ks, a.D, lane, a.scale < 0.f ? -1.f : 1.f);
+    }
+    f32x16 o[DB] = {};
+    float m = -__builtin_inff(), mc = 0.f, l = 0.f;   // mc = m c, finite
+    for (int j = 0; j < tiles; ++j) {
+        dma_wait();
+        __syncthreads();   // tile j is there; everyone is done with the other one
+        if (j + 1 < tiles) copy(j + 1);
+        const int j0 = j * kFwdKeys;
+        if (rows_left <= 0 || (a.causal && j0 > row0 + 31)) continue;   // nothing of this tile for this wave
+        const char* kt = lds + (j & 1) * (2 * TILE);
+        const char* vt = kt + TILE;
+        f32x16 s[2] = {};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) mma(L::rows(kt, 32 * kb, ks, lane), q[ks], s[kb]);
+        const int limit = a.causal ? min(w.len - 1, row) : w.len - 1;   // last key this query sees
+        const bool edge = j0 + kFwdKeys - 1 > (a.causal ? min(w.len - 1, row0) : w.len - 1);
+        if (edge) {
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (j0 + 32 * kb + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3) > limit) s[kb][r] = -__builtin_inff();
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, s[kb][r]);
+        top = both_max(top);
+        // raised where a lane's tile is above its maximum by more than kRaise powers of two
+        if (__builtin_amdgcn_ballot_w64((top - m) * c > kRaise || m == -__builtin_inff())) {
+            const bool first = m == -__builtin_inff();
+            m = fmaxf(m, top);
+            const float next = m == -__builtin_inff() ? 0.f : m * c;
+            const float alpha = first ? 0.f : __builtin_amdgcn_exp2f(mc - next);
+            mc = next;
+            l *= alpha;
+#pragma unroll
+            for (int db = 0; db < DB; ++db) o[db] *= alpha;
+        }
+        float sum = 0.f;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const bool seen = !edge || s[kb][r] != -__builtin_inff();
+                const float p = __builtin_amdgcn_exp2f(fmaf(s[kb][r], c, -mc));
+                s[kb][r] = seen ? p : 0.f;   // a zero scale leaves no infinity to vanish
+                sum += s[kb][r];
+            }
+        l += sum;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                Frag<T> p;
+                as_terms(s[kb], t, p);
+#pragma unroll
+                for (int db = 0; db < DB; ++db) mma(L::cols(vt, 32 * kb, t, db, lane), p, o[db]);
+            }
+    }
+    if (!live) return;
+    l = both_sum(l);
+    const float inv = 1.f / l;
+#pragma unroll
+    for (int db = 0; db < DB; ++db) store_tile(out, db, a.D, lane, o[db], inv);
+    if (lse && lane < 32) *lse = (mc + log2f(l)) * kLn2;
+}
+
+template <typename T, int DP>
+int run_fwd(const Args& a, hipStream_t st) {
+    const long long grid = slots(a.T, a.n_seq, kFwdRows) * a.Hq;
+    if (grid >= 1LL << 23) return WTC_ESHAPE;
+    hipLaunchKernelGGL((k_attn_fwd<T, DP>), dim3((unsigned)grid), dim3(256), 0, st, a);
+    return hipGetLastError() == hipSuccess ? WTC_OK : WTC_EHIP;
+}
+
+}  // namespace attn
+}  // namespace wtc
