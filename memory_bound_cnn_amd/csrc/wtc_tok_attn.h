@@ -64,56 +64,79 @@ __device__ __forceinline__ void as_terms(const f32x16& c, int s, Frag<float>& f)
     for (int i = 0; i < 8; ++i) f.v[i] = c[8 * s + i];
 }
 
-// A tile of rows in shared memory: 16-byte chunks, chunk c of row r at place
-// c ^ turn(r) of its row.  turn() gives any 16 rows (8 for 128-byte rows, ...)
-// the banks of different places when lanes read the same chunk of consecutive
-// rows, and any 4 consecutive rows different 64-byte segments when they are
-// read transposed.
+// A tile of rows in shared memory, as it is copied there: groups of 1024 bytes
+// (kGroup whole rows, what one instruction copies), 32 bytes between groups.
+// Lane l of an A tile stands for row place(l) of 32, not for row l: its low
+// bits choose the group, so that lanes next to each other read addresses 32
+// bytes (then 128, ..) apart modulo the banks, with no chunks to permute, and
+// every read of a tile is one register plus a constant.  place() moves bits, so
+// place(a + b) = place(a) + place(b) where a and b share no bit, and row_at()
+// likewise.  Results whose rows are rows of the tile have them in that order.
 template <typename T, int DP>
 struct Tile {
     static constexpr int kRowBytes = (DP == 96 ? 128 : DP) * (int)sizeof(T);
-    static constexpr int kChunks = kRowBytes / 16;   // a power of two, >= 4
+    static constexpr int kChunks = kRowBytes / 16;     // of 16 bytes; a power of two
+    static constexpr int kGroup = 1024 / kRowBytes;    // rows of a group: 2 .. 16
+    static constexpr int kGroups = 32 / kGroup;        // groups of 32 rows
+    static constexpr int kStride = 1024 + 32;
+    static constexpr int bytes(int rows) { return rows / kGroup * kStride; }
+    static_assert(kGroup >= 2 && kGroup <= 16, "place() splits 32 rows into groups");
 
-    static __device__ __forceinline__ int turn(int r) {
-        if constexpr (kChunks >= 16) return ((r & 3) << 2) | ((r >> 2) & 3);
-        if constexpr (kChunks == 8) return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
-        return (r >> 2) & 3;
-    }
+    static constexpr __host__ __device__ int place(int l) { return (l % kGroups) * kGroup + l / kGroups; }
+    static constexpr __host__ __device__ int row_at(int r) { return r / kGroup * kStride + r % kGroup * kRowBytes; }
 
-    // Copies rows j0 .. j0 + ROWS - 1 of a [., D] matrix into the tile at byte
-    // address `dst` of shared memory: rows past `last` repeat row `last`,
-    // chunks past D the last chunk, so that nothing outside the sequence is
-    // read (those places meet zeros or are not stored).  `base` points at row
+    // Copies rows j0 .. j0 + ROWS - 1 of a matrix into the tile at byte address
+    // `dst` of shared memory: rows past `last` repeat row `last`, chunks past
+    // the head's channels its last chunk, so that nothing outside the sequence
+    // is read (those places meet zeros or are not used).  `base` points at row
     // j0.  Asynchronous: the caller waits with dma_wait() and a barrier.
     template <int ROWS, int WAVES>
-    static __device__ __forceinline__ void copy(uint32_t dst, const char* base, uint32_t row_bytes, int last_row,
+    static __device__ __forceinline__ void copy(uint32_t dst, const char* base, uint32_t row_bytes, int last,
                                                 int chunks, int wave, int lane) {
-        constexpr int PER = 64 / kChunks > 0 ? 64 / kChunks : 1;   // rows of one instruction
-        constexpr int CALLS = ROWS * kChunks / 64 / WAVES;
-        static_assert(kChunks <= 64 && ROWS * kChunks % (64 * WAVES) == 0, "whole instructions");
+        constexpr int CALLS = ROWS / kGroup / WAVES;
+        static_assert(ROWS % (kGroup * WAVES) == 0, "whole groups");
+        const int r = lane / kChunks;
+        const uint32_t c = (uint32_t)min(lane % kChunks, chunks - 1) * 16u;
+        if (last >= ROWS - 1) {
+            const uint32_t off = (uint32_t)r * row_bytes + c;
 #pragma unroll
-        for (int i = 0; i < CALLS; ++i) {
-            const int r0 = (wave * CALLS + i) * PER;
-            const int r = r0 + lane / kChunks, c = (lane % kChunks) ^ turn(r);
-            const uint32_t off = (uint32_t)min(r, last_row) * row_bytes + (uint32_t)min(c, chunks - 1) * 16u;
-            const uint32_t at = dst + (uint32_t)r0 * kRowBytes;
-            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                         :
-                         : "s"(__builtin_amdgcn_readfirstlane(at)), "v"(off), "s"(base)
-                         : "memory");
+            for (int i = 0; i < CALLS; ++i) {
+                const int g = wave * CALLS + i;
+                dma(dst + (uint32_t)(g * kStride), base + (size_t)(uint32_t)(g * kGroup) * row_bytes, off);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < CALLS; ++i) {
+                const int g = wave * CALLS + i;
+                dma(dst + (uint32_t)(g * kStride), base, (uint32_t)min(g * kGroup + r, last) * row_bytes + c);
+            }
         }
     }
+    // 16 bytes a lane from base + off to 1024 consecutive bytes at dst.
+    static __device__ __forceinline__ void dma(uint32_t dst, const char* base, uint32_t off) {
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                     :
+                     : "s"(__builtin_amdgcn_readfirstlane(dst)), "v"(off), "s"(base)
+                     : "memory");
+    }
 
-    // Terms 16 ks + 8 h .. + 7 of row (lane % 32) + r0: an A tile whose rows are rows of the matrix.
-    static __device__ __forceinline__ Frag<T> rows(const char* tile, int r0, int ks, int lane) {
-        const int r = r0 + (lane & 31), h = lane >> 5;
-        const char* p = tile + r * kRowBytes;
+    // The lane's part of the addresses that rows() and cols() read.
+    static __device__ __forceinline__ int rows_lane(int lane) { return row_at(place(lane & 31)) + (lane >> 5) * 8 * (int)sizeof(T); }
+    static __device__ __forceinline__ int cols_lane(int lane) {
+        if constexpr (sizeof(T) == 2)
+            return row_at(place(4 * (lane >> 5) + ((lane & 15) >> 2))) + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+        return row_at(place(4 * (lane >> 5))) + (lane & 31) * 4;
+    }
+
+    // Terms 16 ks + 8 h .. + 7 of row r0 + place(lane % 32), r0 a multiple of
+    // 32: an A tile whose rows are rows of the matrix.  p = tile + rows_lane().
+    static __device__ __forceinline__ Frag<T> rows(const char* p, int r0, int ks) {
+        p += row_at(r0) + 16 * ks * (int)sizeof(T);
         Frag<T> f;
         if constexpr (sizeof(T) == 2) {
-            f.v = *reinterpret_cast<const u32x4*>(p + (((2 * ks + h) ^ turn(r)) << 4));
+            f.v = *reinterpret_cast<const u32x4*>(p);
         } else {
-            const u32x4 lo = *reinterpret_cast<const u32x4*>(p + (((4 * ks + 2 * h) ^ turn(r)) << 4));
-            const u32x4 hi = *reinterpret_cast<const u32x4*>(p + (((4 * ks + 2 * h + 1) ^ turn(r)) << 4));
+            const u32x4 lo = *reinterpret_cast<const u32x4*>(p), hi = *reinterpret_cast<const u32x4*>(p + 16);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t l = lo[i], u = hi[i];
@@ -124,34 +147,33 @@ struct Tile {
         return f;
     }
 
-    // Rows r0 + 16 s + the turned order, of column 32 db + lane % 32: an A tile
-    // whose rows are columns of the matrix.  bfloat16: 16 lanes read 4 rows of
-    // 16 columns and get them transposed, 4 rows of a column each.
-    static __device__ __forceinline__ Frag<T> cols(const char* tile, int r0, int s, int db, int lane) {
-        const int h = lane >> 5;
+    // Rows r0 + place(16 s + the turned order), of column 32 db + lane % 32: an
+    // A tile whose rows are columns of the matrix.  p = tile + cols_lane().
+    // bfloat16: 16 lanes read 4 rows of 16 columns and get them transposed, 4
+    // rows of a column each.
+    static __device__ __forceinline__ Frag<T> cols(const char* p, int r0, int s, int db) {
+        p += row_at(r0) + 32 * db * (int)sizeof(T);
         Frag<T> f;
         if constexpr (sizeof(T) == 2) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const int r = r0 + 16 * s + 8 * k + 4 * h + ((lane & 15) >> 2);
-                const int c = 4 * db + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
-                const char* p = tile + r * kRowBytes + ((c ^ turn(r)) << 4) + (lane & 1) * 8;
                 const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (__attribute__((address_space(3))) s16x4*)(lds_char*)p);
+                    (__attribute__((address_space(3))) s16x4*)(lds_char*)(p + row_at(place(16 * s + 8 * k))));
                 const u32x2 u = __builtin_bit_cast(u32x2, t);
                 f.v[2 * k] = u[0];
                 f.v[2 * k + 1] = u[1];
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = r0 + 16 * s + 8 * (i >> 2) + 4 * h + (i & 3);
-                const int col = 32 * db + (lane & 31), c = col >> 2;
-                f.v[i] = *reinterpret_cast<const float*>(tile + r * kRowBytes + ((c ^ turn(r)) << 4) + (col & 3) * 4);
-            }
+            for (int i = 0; i < 8; ++i)
+                f.v[i] = *reinterpret_cast<const float*>(p + row_at(place(16 * s + 8 * (i >> 2) + (i & 3))));
         }
         return f;
     }
+
+    // Row of register r of a result whose rows are rows of the tile (32 of them): + 4 h's part.
+    static constexpr __host__ __device__ int row_of(int r) { return place(8 * (r >> 2) + (r & 3)); }
+    static __device__ __forceinline__ int row_of_half(int lane) { return place(4) * (lane >> 5); }
 };
 
 __device__ __forceinline__ uint32_t lds_address(const void* p) { return (uint32_t)(uintptr_t)(lds_char*)p; }
@@ -227,6 +249,14 @@ __device__ __forceinline__ void store_tile(T* row, int db, int D, int lane, cons
     for (int g = 0; g < 4; ++g)
         store4(row, db, g, D, lane, c[4 * g] * factor, c[4 * g + 1] * factor, c[4 * g + 2] * factor,
                c[4 * g + 3] * factor);
+}
+
+// Workgroups (of four waves, one on each vector unit) that the registers of a
+// compute unit hold at least.
+enum Kernel { kFwd, kDq, kDkv };
+constexpr int occupancy(Kernel k, int elem, int dp) {
+    if (elem == 4) return dp <= 64 ? 2 : 1;
+    return 2;
 }
 
 struct Args {

@@ -21,9 +21,9 @@ template <typename T>
 constexpr int kDkvRows = sizeof(T) == 2 ? 64 : 32;   // queries of a tile
 
 template <typename T, int DP>
-__global__ void __launch_bounds__(256) k_attn_dq(Args a) {
+__global__ void __launch_bounds__(256, occupancy(kDq, sizeof(T), DP)) k_attn_dq(Args a) {
     using L = Tile<T, DP>;
-    constexpr int KS = DP / 16, DB = DP / 32, TILE = kDqKeys * L::kRowBytes;
+    constexpr int KS = DP / 16, DB = DP / 32, TILE = L::bytes(kDqKeys);
     __shared__ __align__(16) char lds[4 * TILE];   // 2 x (K tile, V tile)
     static_assert(4 * TILE <= 160 * 1024, "shared memory");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(256) k_attn_dq(Args a) {
         if (live && lane < 32) a.delta[stat] = delta;   // for the other kernel
     }
     const float lse2 = a.lse[stat] * kLog2e;
+    const int rlane = L::rows_lane(lane), clane = L::cols_lane(lane), half = L::row_of_half(lane);
     f32x16 acc[DB] = {};
     for (int j = 0; j < tiles; ++j) {
         dma_wait();
@@ -84,8 +85,8 @@ __global__ void __launch_bounds__(256) k_attn_dq(Args a) {
         if (j + 1 < tiles) copy(j + 1);
         const int j0 = j * kDqKeys;
         if (rows_left <= 0 || (a.causal && j0 > row0 + 31)) continue;
-        const char* kt = lds + (j & 1) * (2 * TILE);
-        const char* vt = kt + TILE;
+        const char* kt = lds + (j & 1) * (2 * TILE) + rlane;
+        const char* kc = lds + (j & 1) * (2 * TILE) + clane;
         const int limit = a.causal ? min(w.len - 1, row) : w.len - 1;
         const bool edge = j0 + kDqKeys - 1 > (a.causal ? min(w.len - 1, row0) : w.len - 1);
 #pragma unroll
@@ -93,8 +94,8 @@ __global__ void __launch_bounds__(256) k_attn_dq(Args a) {
             f32x16 s = {}, dp = {};
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                mma(L::rows(kt, 32 * kb, ks, lane), q[ks], s);
-                mma(L::rows(vt, 32 * kb, ks, lane), g[ks], dp);
+                mma(L::rows(kt, 32 * kb, ks), q[ks], s);
+                mma(L::rows(kt + TILE, 32 * kb, ks), g[ks], dp);
             }
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
@@ -104,14 +105,14 @@ __global__ void __launch_bounds__(256) k_attn_dq(Args a) {
             if (edge) {
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    if (j0 + 32 * kb + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3) > limit) s[r] = 0.f;
+                    if (j0 + 32 * kb + L::row_of(r) + half > limit) s[r] = 0.f;
             }
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 Frag<T> ds;
                 as_terms(s, t, ds);
 #pragma unroll
-                for (int db = 0; db < DB; ++db) mma(L::cols(kt, 32 * kb, t, db, lane), ds, acc[db]);
+                for (int db = 0; db < DB; ++db) mma(L::cols(kc, 32 * kb, t, db), ds, acc[db]);
             }
         }
     }
@@ -121,9 +122,9 @@ __global__ void __launch_bounds__(256) k_attn_dq(Args a) {
 }
 
 template <typename T, int DP>
-__global__ void __launch_bounds__(256) k_attn_dkv(Args a) {
+__global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dkv(Args a) {
     using L = Tile<T, DP>;
-    constexpr int KS = DP / 16, DB = DP / 32, ROWS = kDkvRows<T>, TILE = ROWS * L::kRowBytes;
+    constexpr int KS = DP / 16, DB = DP / 32, ROWS = kDkvRows<T>, TILE = L::bytes(ROWS);
     __shared__ __align__(16) char lds[4 * TILE];   // 2 x (Q tile, dO tile)
     __shared__ __align__(16) float stats[2][2][ROWS];   // 2 x (lse log2(e), delta) of the tile's queries
     static_assert(4 * TILE + 4 * ROWS * 4 <= 160 * 1024, "shared memory");
@@ -162,7 +163,8 @@ __global__ void __launch_bounds__(256) k_attn_dkv(Args a) {
         L::template copy<ROWS, 4>(at, reinterpret_cast<const char*>(qp), qrow, last, chunks, wave, lane);
         L::template copy<ROWS, 4>(at + TILE, reinterpret_cast<const char*>(gp), grow, last, chunks, wave, lane);
         if (threadIdx.x < 2 * ROWS) {
-            const int r = threadIdx.x % ROWS;
+            // kept in the order that a result's registers have the rows in
+            const int r = threadIdx.x % ROWS / 32 * 32 + L::place(threadIdx.x % 32);
             const long long t = (long long)head * a.T + w.start + j0 + min(r, last);
             // queries past the end: exp2(. - infinity) leaves nothing of them
             stat = threadIdx.x < ROWS ? (r <= last ? a.lse[t] * kLog2e : __builtin_inff()) : a.delta[t];
@@ -182,6 +184,7 @@ __global__ void __launch_bounds__(256) k_attn_dkv(Args a) {
             vf[ks] = row_terms(vrow, ks, a.D, lane, 1.f);
         }
     }
+    const int rlane = L::rows_lane(lane), clane = L::cols_lane(lane), half = L::row_of_half(lane);
     f32x16 ak[DB] = {}, av[DB] = {};
     for (int i = 0; i < steps; ++i) {
         if (threadIdx.x < 2 * ROWS) stats[i & 1][threadIdx.x / ROWS][threadIdx.x % ROWS] = stat;
@@ -190,15 +193,15 @@ __global__ void __launch_bounds__(256) k_attn_dkv(Args a) {
         if (i + 1 < steps) copy(i + 1);
         const int j0 = (first + i % per_head) * ROWS;
         if (keys_left <= 0 || (a.causal && j0 + ROWS - 1 < key0)) continue;
-        const char* qt = lds + (i & 1) * (2 * TILE);
-        const char* gt = qt + TILE;
+        const char* qt = lds + (i & 1) * (2 * TILE) + rlane;
+        const char* qc = lds + (i & 1) * (2 * TILE) + clane;
 #pragma unroll
         for (int qb = 0; qb < ROWS / 32; ++qb) {
             f32x16 s = {}, dp = {};
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                mma(L::rows(qt, 32 * qb, ks, lane), kf[ks], s);
-                mma(L::rows(gt, 32 * qb, ks, lane), vf[ks], dp);
+                mma(L::rows(qt, 32 * qb, ks), kf[ks], s);
+                mma(L::rows(qt + TILE, 32 * qb, ks), vf[ks], dp);
             }
             const float* lse = &stats[i & 1][0][32 * qb + 4 * (lane >> 5)];
             const float* del = &stats[i & 1][1][32 * qb + 4 * (lane >> 5)];
@@ -207,7 +210,7 @@ __global__ void __launch_bounds__(256) k_attn_dkv(Args a) {
                 const int at = 8 * (r >> 2) + (r & 3);
                 float p = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse[at]));
                 float ds = p * (dp[r] - del[at]);
-                if (a.causal && j0 + 32 * qb + 4 * (lane >> 5) + at < key) p = ds = 0.f;
+                if (a.causal && j0 + 32 * qb + L::row_of(r) + half < key) p = ds = 0.f;
                 s[r] = p;
                 dp[r] = ds;
             }
@@ -218,8 +221,8 @@ __global__ void __launch_bounds__(256) k_attn_dkv(Args a) {
                 as_terms(dp, t, ds);
 #pragma unroll
                 for (int db = 0; db < DB; ++db) {
-                    mma(L::cols(gt, 32 * qb, t, db, lane), p, av[db]);
-                    mma(L::cols(qt, 32 * qb, t, db, lane), ds, ak[db]);
+                    mma(L::cols(qc + TILE, 32 * qb, t, db), p, av[db]);
+                    mma(L::cols(qc, 32 * qb, t, db), ds, ak[db]);
                 }
             }
         }

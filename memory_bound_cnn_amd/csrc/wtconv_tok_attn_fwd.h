@@ -24,9 +24,9 @@ constexpr int kFwdKeys = 64;    // keys of a tile
 constexpr float kRaise = 8.f;
 
 template <typename T, int DP>
-__global__ void __launch_bounds__(256) k_attn_fwd(Args a) {
+__global__ void __launch_bounds__(256, occupancy(kFwd, sizeof(T), DP)) k_attn_fwd(Args a) {
     using L = Tile<T, DP>;
-    constexpr int KS = DP / 16, DB = DP / 32, TILE = kFwdKeys * L::kRowBytes;
+    constexpr int KS = DP / 16, DB = DP / 32, TILE = L::bytes(kFwdKeys);
     __shared__ __align__(16) char lds[4 * TILE];   // 2 x (K tile, V tile)
     static_assert(4 * TILE <= 160 * 1024, "shared memory");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(256) k_attn_fwd(Args a) {
         for (int ks = 0; ks < KS; ++ks) q[ks] = row_terms(qrow, ks, a.D, lane, a.scale < 0.f ? -1.f : 1.f);
     }
     f32x16 o[DB] = {};
+    const int rlane = L::rows_lane(lane), clane = L::cols_lane(lane), half = L::row_of_half(lane);
     float m = -__builtin_inff(), mc = 0.f, l = 0.f;   // mc = m c, finite
     for (int j = 0; j < tiles; ++j) {
         dma_wait();
@@ -79,13 +80,13 @@ __global__ void __launch_bounds__(256) k_attn_fwd(Args a) {
         if (j + 1 < tiles) copy(j + 1);
         const int j0 = j * kFwdKeys;
         if (rows_left <= 0 || (a.causal && j0 > row0 + 31)) continue;   // nothing of this tile for this wave
-        const char* kt = lds + (j & 1) * (2 * TILE);
-        const char* vt = kt + TILE;
+        const char* kt = lds + (j & 1) * (2 * TILE) + rlane;
+        const char* vt = lds + (j & 1) * (2 * TILE) + TILE + clane;
         f32x16 s[2] = {};
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb) mma(L::rows(kt, 32 * kb, ks, lane), q[ks], s[kb]);
+            for (int kb = 0; kb < 2; ++kb) mma(L::rows(kt, 32 * kb, ks), q[ks], s[kb]);
         const int limit = a.causal ? min(w.len - 1, row) : w.len - 1;   // last key this query sees
         const bool edge = j0 + kFwdKeys - 1 > (a.causal ? min(w.len - 1, row0) : w.len - 1);
         if (edge) {
@@ -93,7 +94,7 @@ __global__ void __launch_bounds__(256) k_attn_fwd(Args a) {
             for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    if (j0 + 32 * kb + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3) > limit) s[kb][r] = -__builtin_inff();
+                    if (j0 + 32 * kb + L::row_of(r) + half > limit) s[kb][r] = -__builtin_inff();
         }
         float top = s[0][0];
 #pragma unroll
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(256) k_attn_fwd(Args a) {
                 Frag<T> p;
                 as_terms(s[kb], t, p);
 #pragma unroll
-                for (int db = 0; db < DB; ++db) mma(L::cols(vt, 32 * kb, t, db, lane), p, o[db]);
+                for (int db = 0; db < DB; ++db) mma(L::cols(vt, 32 * kb, t, db), p, o[db]);
             }
     }
     if (!live) return;
