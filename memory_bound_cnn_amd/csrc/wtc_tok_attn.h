@@ -259,11 +259,14 @@ constexpr int occupancy(Kernel k, int elem, int dp) {
     return 2;
 }
 
+constexpr long long kMaxGroups = 1LL << 23;   // workgroups of a launch: 2^31 threads
+
 struct Args {
     const void *q, *k, *v, *o, *g;
     const int* cu;
     void *out, *dq, *dk, *dv;
-    float *lse, *delta;
+    float *lse, *delta, *parts;
+    int splits;   // of a key tile's queries in the backward pass; their sums in parts when there are several
     int T, n_seq, Hq, Hk, group, D, causal;
     float scale;
     wtc_attn_strides sq, sk, sv, so, sg, sdq, sdk, sdv;

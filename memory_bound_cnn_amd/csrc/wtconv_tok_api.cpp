@@ -133,7 +133,7 @@ int wtconv_attention_forward(const wtc_attn_desc* d, const void* q, const void* 
 
 size_t wtconv_attention_backward_workspace(const wtc_attn_desc* d) {
     if (check_attn(d) != WTC_OK) return 0;
-    return (size_t)d->Hq * (size_t)d->T * sizeof(float);
+    return attn_backward_bytes(d);
 }
 
 int wtconv_attention_backward(const wtc_attn_desc* d, const void* q, const void* k, const void* v, const void* out,
@@ -148,8 +148,7 @@ int wtconv_attention_backward(const wtc_attn_desc* d, const void* q, const void*
                                  check_strides(d, d->dk, dk), check_strides(d, d->dv, dv)});
     if (bad != WTC_OK) return bad;
     if (!workspace || workspace_bytes < wtconv_attention_backward_workspace(d)) return WTC_EWORKSPACE;
-    return launch_attn_backward(d, q, k, v, out, lse, dout, cu_seqlens, dq, dk, dv, static_cast<float*>(workspace),
-                                stream);
+    return launch_attn_backward(d, q, k, v, out, lse, dout, cu_seqlens, dq, dk, dv, workspace, stream);
 }
 
 }  // extern "C"

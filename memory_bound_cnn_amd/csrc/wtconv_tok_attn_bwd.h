@@ -126,36 +126,57 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
     using L = Tile<T, DP>;
     constexpr int KS = DP / 16, DB = DP / 32, ROWS = kDkvRows<T>, TILE = L::bytes(ROWS);
     __shared__ __align__(16) char lds[4 * TILE];   // 2 x (Q tile, dO tile)
-    __shared__ __align__(16) float stats[2][2][ROWS];   // 2 x (lse log2(e), delta) of the tile's queries
+    __shared__ __align__(16) float stats[2][2][ROWS];   // 2 x what S and dP of the tile's queries start from
     static_assert(4 * TILE + 4 * ROWS * 4 <= 160 * 1024, "shared memory");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int kvh = blockIdx.x % a.Hk, slot = blockIdx.x / a.Hk;   // early tiles have the most queries when causal
+    const int kvh = blockIdx.x % a.Hk, split = blockIdx.x / a.Hk % a.splits;
+    const int slot = blockIdx.x / a.Hk / a.splits;   // early tiles have the most queries when causal: they go first
     const Work w = find_work<kDkvKeys>(a, slot, lane);
     if (w.none) return;
     const int key0 = w.tile * kDkvKeys + wave * 32, key = key0 + (lane & 31);
     const int keys_left = w.len - key0;
     const bool live = key < w.len;
-    T* dk = static_cast<T*>(a.dk) + (long long)(w.start + key) * a.sdk.token + kvh * a.sdk.head;
-    T* dv = static_cast<T*>(a.dv) + (long long)(w.start + key) * a.sdv.token + kvh * a.sdv.head;
-    if (w.pad) {
-        if (live) {
-            f32x16 zero = {};
+    f32x16 ak[DB] = {}, av[DB] = {};
+    auto store = [&] {
+        if (!live) return;
+        const long long t = w.start + key;
+        if (a.splits == 1) {
+            T* dk = static_cast<T*>(a.dk) + t * a.sdk.token + kvh * a.sdk.head;
+            T* dv = static_cast<T*>(a.dv) + t * a.sdv.token + kvh * a.sdv.head;
 #pragma unroll
             for (int db = 0; db < DB; ++db) {
-                store_tile(dk, db, a.D, lane, zero, 0.f);
-                store_tile(dv, db, a.D, lane, zero, 0.f);
+                store_tile(dk, db, a.D, lane, ak[db], a.scale);
+                store_tile(dv, db, a.D, lane, av[db], 1.f);
+            }
+        } else {
+            const long long n = (long long)a.T * a.Hk * a.D;
+            float* dk = a.parts + 2 * split * n + (t * a.Hk + kvh) * a.D;
+#pragma unroll
+            for (int db = 0; db < DB; ++db) {
+                store_tile(dk, db, a.D, lane, ak[db], a.scale);
+                store_tile(dk + n, db, a.D, lane, av[db], 1.f);
             }
         }
+    };
+    if (w.pad) {
+        store();
         return;
     }
     const int chunks = a.D * (int)sizeof(T) / 16;
     const uint32_t qrow = (uint32_t)a.sq.token * sizeof(T), grow = (uint32_t)a.sg.token * sizeof(T);
     const int first = a.causal ? w.tile * kDkvKeys / ROWS : 0;   // the first query tile that sees these keys
-    const int per_head = (w.len + ROWS - 1) / ROWS - first, steps = per_head * a.group;
+    const int per_head = (w.len + ROWS - 1) / ROWS - first, all = per_head * a.group;
+    const int begin = (int)((long long)all * split / a.splits), end = (int)((long long)all * (split + 1) / a.splits);
+    if (begin == end) {
+        store();
+        return;
+    }
     const uint32_t lds0 = lds_address(lds);
+    // no scale below 2^-100 (a zero one): what it multiplies is then lost beside lse, as it should be
+    const float c = copysignf(fmaxf(fabsf(a.scale) * kLog2e, 0x1p-100f), a.scale), inv_c = 1.f / c;
     float stat = 0.f;   // of the tile copied last, on its way to shared memory
+    int head = kvh * a.group + begin / per_head, j0 = (first + begin % per_head) * ROWS;   // of the next tile to copy
     auto copy = [&](int i) {
-        const int head = kvh * a.group + i / per_head, j0 = (first + i % per_head) * ROWS;
         const int last = min(w.len - 1 - j0, ROWS - 1);
         const uint32_t at = lds0 + (uint32_t)(i & 1) * (2 * TILE);
         const T* qp = static_cast<const T*>(a.q) + (long long)(w.start + j0) * a.sq.token + head * a.sq.head;
@@ -166,13 +187,18 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
             // kept in the order that a result's registers have the rows in
             const int r = threadIdx.x % ROWS / 32 * 32 + L::place(threadIdx.x % 32);
             const long long t = (long long)head * a.T + w.start + j0 + min(r, last);
-            // queries past the end: exp2(. - infinity) leaves nothing of them
-            stat = threadIdx.x < ROWS ? (r <= last ? a.lse[t] * kLog2e : __builtin_inff()) : a.delta[t];
+            // queries past the end: an infinite lse leaves nothing of them
+            stat = threadIdx.x < ROWS ? (r <= last ? a.lse[t] * kLog2e : __builtin_inff()) * -inv_c : -a.delta[t];
+        }
+        j0 += ROWS;
+        if (j0 >= w.len) {
+            j0 = first * ROWS;
+            ++head;
         }
     };
-    copy(0);
+    int here = j0;   // first query of the tile being worked on
+    copy(begin);
 
-    const float c = a.scale * kLog2e;
     Frag<T> kf[KS], vf[KS];
     {
         const long long t = w.start + min(key, w.len - 1);
@@ -185,34 +211,39 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
         }
     }
     const int rlane = L::rows_lane(lane), clane = L::cols_lane(lane), half = L::row_of_half(lane);
-    f32x16 ak[DB] = {}, av[DB] = {};
-    for (int i = 0; i < steps; ++i) {
+    for (int i = begin; i < end; ++i) {
         if (threadIdx.x < 2 * ROWS) stats[i & 1][threadIdx.x / ROWS][threadIdx.x % ROWS] = stat;
         dma_wait();
         __syncthreads();   // tile i is there; everyone is done with the other one
-        if (i + 1 < steps) copy(i + 1);
-        const int j0 = (first + i % per_head) * ROWS;
-        if (keys_left <= 0 || (a.causal && j0 + ROWS - 1 < key0)) continue;
+        const int at = here;
+        here = j0;
+        if (i + 1 < end) copy(i + 1);
+        if (keys_left <= 0 || (a.causal && at + ROWS - 1 < key0)) continue;
         const char* qt = lds + (i & 1) * (2 * TILE) + rlane;
         const char* qc = lds + (i & 1) * (2 * TILE) + clane;
+        const bool edge = a.causal && at < key0 + 31;   // some of the tile's queries come before some of the keys
+#pragma unroll 1
+        for (int qb = 0; qb < ROWS / 32; ++qb, qt += L::row_at(32), qc += L::row_at(32)) {
+            // the products start from -lse log2(e) / c and -delta
+            f32x16 s, dp;
+            const float* st = &stats[i & 1][0][32 * qb + 4 * (lane >> 5)];
 #pragma unroll
-        for (int qb = 0; qb < ROWS / 32; ++qb) {
-            f32x16 s = {}, dp = {};
+            for (int r = 0; r < 16; ++r) s[r] = st[8 * (r >> 2) + (r & 3)];
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                mma(L::rows(qt, 32 * qb, ks), kf[ks], s);
-                mma(L::rows(qt + TILE, 32 * qb, ks), vf[ks], dp);
-            }
-            const float* lse = &stats[i & 1][0][32 * qb + 4 * (lane >> 5)];
-            const float* del = &stats[i & 1][1][32 * qb + 4 * (lane >> 5)];
+            for (int ks = 0; ks < KS; ++ks) mma(L::rows(qt, 0, ks), kf[ks], s);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) dp[r] = st[ROWS + 8 * (r >> 2) + (r & 3)];
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) mma(L::rows(qt + TILE, 0, ks), vf[ks], dp);
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                const int at = 8 * (r >> 2) + (r & 3);
-                float p = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse[at]));
-                float ds = p * (dp[r] - del[at]);
-                if (a.causal && j0 + 32 * qb + L::row_of(r) + half < key) p = ds = 0.f;
-                s[r] = p;
-                dp[r] = ds;
+                s[r] = __builtin_amdgcn_exp2f(s[r] * c);
+                dp[r] *= s[r];
+            }
+            if (edge) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (at + 32 * qb + L::row_of(r) + half < key) s[r] = dp[r] = 0.f;
             }
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -221,26 +252,57 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
                 as_terms(dp, t, ds);
 #pragma unroll
                 for (int db = 0; db < DB; ++db) {
-                    mma(L::cols(qc + TILE, 32 * qb, t, db), p, av[db]);
-                    mma(L::cols(qc, 32 * qb, t, db), ds, ak[db]);
+                    mma(L::cols(qc + TILE, 0, t, db), p, av[db]);
+                    mma(L::cols(qc, 0, t, db), ds, ak[db]);
                 }
             }
         }
     }
-    if (!live) return;
+    store();
+}
+
+// dk and dv from the sums of the splits, in their order; eight channels a thread.
+template <typename T>
+__global__ void __launch_bounds__(256) k_attn_join(Args a) {
+    const long long n = (long long)a.T * a.Hk * a.D, step = (long long)gridDim.x * 256 * 8;
+    for (long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 8; i < 2 * n; i += step) {
+        const bool v = i >= n;
+        const long long at = v ? i - n : i, row = at / a.D;
+        const int c = (int)(at - row * a.D), head = (int)(row % a.Hk);
+        float sum[8] = {};
+        for (int s = 0; s < a.splits; ++s) {
+            float x[4], y[4];
+            load16(a.parts + 2 * s * n + i, x);
+            load16(a.parts + 2 * s * n + i + 4, y);
 #pragma unroll
-    for (int db = 0; db < DB; ++db) {
-        store_tile(dk, db, a.D, lane, ak[db], a.scale);
-        store_tile(dv, db, a.D, lane, av[db], 1.f);
+            for (int j = 0; j < 4; ++j) {
+                sum[j] += x[j];
+                sum[4 + j] += y[j];
+            }
+        }
+        const wtc_attn_strides& st = v ? a.sdv : a.sdk;
+        T* out = static_cast<T*>(v ? a.dv : a.dk) + row / a.Hk * st.token + head * st.head + c;
+#pragma unroll
+        for (int k = 0; k < 8 / kVec<T>; ++k) {
+            float x[kVec<T>];
+#pragma unroll
+            for (int j = 0; j < kVec<T>; ++j) x[j] = sum[k * kVec<T> + j];
+            store16(out + k * kVec<T>, x);
+        }
     }
 }
 
 template <typename T, int DP>
 int run_bwd(const Args& a, hipStream_t st) {
-    const long long gq = slots(a.T, a.n_seq, kDqRows) * a.Hq, gk = slots(a.T, a.n_seq, kDkvKeys) * a.Hk;
-    if (gq >= 1LL << 23 || gk >= 1LL << 23) return WTC_ESHAPE;
+    const long long gq = slots(a.T, a.n_seq, kDqRows) * a.Hq;
+    const long long gk = slots(a.T, a.n_seq, kDkvKeys) * a.Hk * a.splits;
+    if (gq >= kMaxGroups || gk >= kMaxGroups) return WTC_ESHAPE;
     hipLaunchKernelGGL((k_attn_dq<T, DP>), dim3((unsigned)gq), dim3(256), 0, st, a);
     hipLaunchKernelGGL((k_attn_dkv<T, DP>), dim3((unsigned)gk), dim3(256), 0, st, a);
+    if (a.splits > 1) {
+        const long long blocks = (2LL * a.T * a.Hk * a.D / 8 + 255) / 256;
+        hipLaunchKernelGGL((k_attn_join<T>), dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, st, a);
+    }
     return hipGetLastError() == hipSuccess ? WTC_OK : WTC_EHIP;
 }
 

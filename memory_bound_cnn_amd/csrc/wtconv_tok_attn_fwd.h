@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(256, occupancy(kFwd, sizeof(T), DP)) k_attn_fw
 template <typename T, int DP>
 int run_fwd(const Args& a, hipStream_t st) {
     const long long grid = slots(a.T, a.n_seq, kFwdRows) * a.Hq;
-    if (grid >= 1LL << 23) return WTC_ESHAPE;
+    if (grid >= kMaxGroups) return WTC_ESHAPE;
     hipLaunchKernelGGL((k_attn_fwd<T, DP>), dim3((unsigned)grid), dim3(256), 0, st, a);
     return hipGetLastError() == hipSuccess ? WTC_OK : WTC_EHIP;
 }
