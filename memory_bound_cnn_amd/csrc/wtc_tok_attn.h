@@ -65,24 +65,37 @@ __device__ __forceinline__ void as_terms(const f32x16& c, int s, Frag<float>& f)
 }
 
 // A tile of rows in shared memory, as it is copied there: groups of 1024 bytes
-// (kGroup whole rows, what one instruction copies), 32 bytes between groups.
-// Lane l of an A tile stands for row place(l) of 32, not for row l: its low
-// bits choose the group, so that lanes next to each other read addresses 32
-// bytes (then 128, ..) apart modulo the banks, with no chunks to permute, and
-// every read of a tile is one register plus a constant.  place() moves bits, so
-// place(a + b) = place(a) + place(b) where a and b share no bit, and row_at()
-// likewise.  Results whose rows are rows of the tile have them in that order.
+// (kGroup whole rows, what one instruction copies), kPad bytes between groups.
+// Lane l of an A tile stands for row place(l) of 32, not for row l: place()
+// sends the bits of l to bits of the row so that lanes next to each other read
+// different banks (256 bytes wide), rows() and cols() alike, and every read of
+// a tile is one register plus a constant: place(a + b) = place(a) + place(b)
+// where a and b share no bit, and row_at() likewise.  Results whose rows are
+// rows of the tile have them in that order.
+//   Bits 0 and 1 of l are the four rows of 64 bytes that cols() reads at once
+// (bfloat16): they step by 64 bytes or more.  Bit 2 is the wave's half in
+// cols().  Bits 0 to 3 are what rows() reads at once, 16 bytes a lane; where
+// bit 3 steps by a multiple of 256 bytes, rows with that bit set have their
+// 16-byte chunks swapped in pairs (kSwap).
 template <typename T, int DP>
 struct Tile {
     static constexpr int kRowBytes = (DP == 96 ? 128 : DP) * (int)sizeof(T);
     static constexpr int kChunks = kRowBytes / 16;     // of 16 bytes; a power of two
     static constexpr int kGroup = 1024 / kRowBytes;    // rows of a group: 2 .. 16
-    static constexpr int kGroups = 32 / kGroup;        // groups of 32 rows
-    static constexpr int kStride = 1024 + 32;
+    static constexpr int kPad = kRowBytes == 512 ? 16 : 32;
+    static constexpr int kStride = 1024 + kPad;
+    static constexpr int kSwap = sizeof(T) == 2 ? (kRowBytes == 256 ? 1 : kRowBytes == 128 ? 2 : 4) : 0;   // a bit of the row
     static constexpr int bytes(int rows) { return rows / kGroup * kStride; }
-    static_assert(kGroup >= 2 && kGroup <= 16, "place() splits 32 rows into groups");
 
-    static constexpr __host__ __device__ int place(int l) { return (l % kGroups) * kGroup + l / kGroups; }
+    // The row bits that bits 0 .. 4 of l go to.  Rows of 64 bytes: the group is
+    // bit 4 of the row; 128: bits 3 and 4; 256: bits 2 to 4; 512: bits 1 to 4.
+    static constexpr __host__ __device__ int place(int l) {
+        constexpr int to[4][5] = {{0, 1, 4, 2, 3}, {0, 4, 3, 1, 2}, {3, 4, 2, 0, 1}, {1, 2, 4, 3, 0}};
+        constexpr int k = kRowBytes == 64 ? 0 : kRowBytes == 128 ? 1 : kRowBytes == 256 ? 2 : 3;
+        int r = 0;
+        for (int b = 0; b < 5; ++b) r |= ((l >> b) & 1) << to[k][b];
+        return r;
+    }
     static constexpr __host__ __device__ int row_at(int r) { return r / kGroup * kStride + r % kGroup * kRowBytes; }
 
     // Copies rows j0 .. j0 + ROWS - 1 of a matrix into the tile at byte address
@@ -95,8 +108,8 @@ struct Tile {
                                                 int chunks, int wave, int lane) {
         constexpr int CALLS = ROWS / kGroup / WAVES;
         static_assert(ROWS % (kGroup * WAVES) == 0, "whole groups");
-        const int r = lane / kChunks;
-        const uint32_t c = (uint32_t)min(lane % kChunks, chunks - 1) * 16u;
+        const int r = lane / kChunks;   // of the group
+        const uint32_t c = (uint32_t)min((lane % kChunks) ^ (r & kSwap ? 1 : 0), chunks - 1) * 16u;
         if (last >= ROWS - 1) {
             const uint32_t off = (uint32_t)r * row_bytes + c;
 #pragma unroll
@@ -121,7 +134,10 @@ struct Tile {
     }
 
     // The lane's part of the addresses that rows() and cols() read.
-    static __device__ __forceinline__ int rows_lane(int lane) { return row_at(place(lane & 31)) + (lane >> 5) * 8 * (int)sizeof(T); }
+    static __device__ __forceinline__ int rows_lane(int lane) {
+        const int r = place(lane & 31);
+        return row_at(r) + (((lane >> 5) * 8 * (int)sizeof(T)) ^ (r & kSwap ? 16 : 0));
+    }
     static __device__ __forceinline__ int cols_lane(int lane) {
         if constexpr (sizeof(T) == 2)
             return row_at(place(4 * (lane >> 5) + ((lane & 15) >> 2))) + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
@@ -148,17 +164,19 @@ struct Tile {
     }
 
     // Rows r0 + place(16 s + the turned order), of column 32 db + lane % 32: an
-    // A tile whose rows are columns of the matrix.  p = tile + cols_lane().
+    // A tile whose rows are columns of the matrix.  p = tile + cols_lane(), and
+    // swap = cols_swap(), to the other chunk of a pair, for the rows of l's bit 3.
     // bfloat16: 16 lanes read 4 rows of 16 columns and get them transposed, 4
     // rows of a column each.
-    static __device__ __forceinline__ Frag<T> cols(const char* p, int r0, int s, int db) {
+    static __device__ __forceinline__ int cols_swap(int lane) { return lane & 2 ? -16 : 16; }
+    static __device__ __forceinline__ Frag<T> cols(const char* p, int swap, int r0, int s, int db) {
         p += row_at(r0) + 32 * db * (int)sizeof(T);
         Frag<T> f;
         if constexpr (sizeof(T) == 2) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (__attribute__((address_space(3))) s16x4*)(lds_char*)(p + row_at(place(16 * s + 8 * k))));
+                    (__attribute__((address_space(3))) s16x4*)(lds_char*)(p + k * swap + row_at(place(16 * s + 8 * k))));
                 const u32x2 u = __builtin_bit_cast(u32x2, t);
                 f.v[2 * k] = u[0];
                 f.v[2 * k + 1] = u[1];

@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(256, occupancy(kDq, sizeof(T), DP)) k_attn_dq(
         if (live && lane < 32) a.delta[stat] = delta;   // for the other kernel
     }
     const float lse2 = a.lse[stat] * kLog2e;
-    const int rlane = L::rows_lane(lane), clane = L::cols_lane(lane), half = L::row_of_half(lane);
+    const int rlane = L::rows_lane(lane), clane = L::cols_lane(lane), half = L::row_of_half(lane), swap = L::cols_swap(lane);
     f32x16 acc[DB] = {};
     for (int j = 0; j < tiles; ++j) {
         dma_wait();
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(256, occupancy(kDq, sizeof(T), DP)) k_attn_dq(
                 Frag<T> ds;
                 as_terms(s, t, ds);
 #pragma unroll
-                for (int db = 0; db < DB; ++db) mma(L::cols(kc, 32 * kb, t, db), ds, acc[db]);
+                for (int db = 0; db < DB; ++db) mma(L::cols(kc, swap, 32 * kb, t, db), ds, acc[db]);
             }
         }
     }
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
             vf[ks] = row_terms(vrow, ks, a.D, lane, 1.f);
         }
     }
-    const int rlane = L::rows_lane(lane), clane = L::cols_lane(lane), half = L::row_of_half(lane);
+    const int rlane = L::rows_lane(lane), clane = L::cols_lane(lane), half = L::row_of_half(lane), swap = L::cols_swap(lane);
     for (int i = begin; i < end; ++i) {
         if (threadIdx.x < 2 * ROWS) stats[i & 1][threadIdx.x / ROWS][threadIdx.x % ROWS] = stat;
         dma_wait();
@@ -252,8 +252,8 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
                 as_terms(dp, t, ds);
 #pragma unroll
                 for (int db = 0; db < DB; ++db) {
-                    mma(L::cols(qc + TILE, 0, t, db), p, av[db]);
-                    mma(L::cols(qc, 0, t, db), ds, ak[db]);
+                    mma(L::cols(qc + TILE, swap, 0, t, db), p, av[db]);
+                    mma(L::cols(qc, swap, 0, t, db), ds, ak[db]);
                 }
             }
         }

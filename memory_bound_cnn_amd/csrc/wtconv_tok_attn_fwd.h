@@ -64,7 +64,8 @@ __global__ void __launch_bounds__(256, occupancy(kFwd, sizeof(T), DP)) k_attn_fw
     copy(0);
 
     // a negative scale is taken into Q, so that the largest product is the largest logit
-    const float c = fabsf(a.scale) * kLog2e;
+    // (and no scale below 2^-100, a zero one: it must not meet the infinity of a masked product)
+    const float c = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-100f);
     Frag<T> q[KS];
     {
         const T* qrow = static_cast<const T*>(a.q) + (long long)(w.start + min(row, w.len - 1)) * a.sq.token + head * a.sq.head;
@@ -72,7 +73,7 @@ __global__ void __launch_bounds__(256, occupancy(kFwd, sizeof(T), DP)) k_attn_fw
         for (int ks = 0; ks < KS; ++ks) q[ks] = row_terms(qrow, ks, a.D, lane, a.scale < 0.f ? -1.f : 1.f);
     }
     f32x16 o[DB] = {};
-    const int rlane = L::rows_lane(lane), clane = L::cols_lane(lane), half = L::row_of_half(lane);
+    const int rlane = L::rows_lane(lane), clane = L::cols_lane(lane), half = L::row_of_half(lane), swap = L::cols_swap(lane);
     float m = -__builtin_inff(), mc = 0.f, l = 0.f;   // mc = m c, finite
     for (int j = 0; j < tiles; ++j) {
         dma_wait();
@@ -118,9 +119,7 @@ __global__ void __launch_bounds__(256, occupancy(kFwd, sizeof(T), DP)) k_attn_fw
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                const bool seen = !edge || s[kb][r] != -__builtin_inff();
-                const float p = __builtin_amdgcn_exp2f(fmaf(s[kb][r], c, -mc));
-                s[kb][r] = seen ? p : 0.f;   // a zero scale leaves no infinity to vanish
+                s[kb][r] = __builtin_amdgcn_exp2f(fmaf(s[kb][r], c, -mc));
                 sum += s[kb][r];
             }
         l += sum;
@@ -131,7 +130,7 @@ __global__ void __launch_bounds__(256, occupancy(kFwd, sizeof(T), DP)) k_attn_fw
                 Frag<T> p;
                 as_terms(s[kb], t, p);
 #pragma unroll
-                for (int db = 0; db < DB; ++db) mma(L::cols(vt, 32 * kb, t, db), p, o[db]);
+                for (int db = 0; db < DB; ++db) mma(L::cols(vt, swap, 32 * kb, t, db), p, o[db]);
             }
     }
     if (!live) return;
