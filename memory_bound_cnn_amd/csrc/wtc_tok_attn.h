@@ -274,7 +274,7 @@ __device__ __forceinline__ void store_tile(T* row, int db, int D, int lane, cons
 enum Kernel { kFwd, kDq, kDkv };
 constexpr int occupancy(Kernel k, int elem, int dp) {
     if (elem == 4) return dp <= 64 ? 2 : 1;
-    return 2;
+    return dp > 64 ? 2 : dp > 32 && k != kFwd ? 3 : 4;
 }
 
 constexpr long long kMaxGroups = 1LL << 23;   // workgroups of a launch: 2^31 threads

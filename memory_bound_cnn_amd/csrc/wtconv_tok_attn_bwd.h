@@ -17,8 +17,15 @@ namespace attn {
 constexpr int kDqRows = 128;   // queries of a workgroup, 32 a wave
 constexpr int kDqKeys = 64;    // keys of a tile
 constexpr int kDkvKeys = 128;  // keys of a workgroup, 32 a wave
-template <typename T>
-constexpr int kDkvRows = sizeof(T) == 2 ? 64 : 32;   // queries of a tile
+// Queries of a tile, and whether the wave's 32 rows of V wait in shared memory
+// instead of registers.  128 channels of bfloat16 need 64 registers for K and V
+// beside 128 for the sums and 32 for S and dP, more than the 256 that leave two
+// waves on a vector unit; with V (32 KB) and tiles of 32 queries (33 KB) shared
+// memory holds two workgroups as well.
+template <typename T, int DP>
+constexpr bool kDkvHoldV = sizeof(T) == 2 && DP == 128;
+template <typename T, int DP>
+constexpr int kDkvRows = sizeof(T) == 2 && !kDkvHoldV<T, DP> ? 64 : 32;
 
 template <typename T, int DP>
 __global__ void __launch_bounds__(256, occupancy(kDq, sizeof(T), DP)) k_attn_dq(Args a) {
@@ -124,10 +131,12 @@ __global__ void __launch_bounds__(256, occupancy(kDq, sizeof(T), DP)) k_attn_dq(
 template <typename T, int DP>
 __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dkv(Args a) {
     using L = Tile<T, DP>;
-    constexpr int KS = DP / 16, DB = DP / 32, ROWS = kDkvRows<T>, TILE = L::bytes(ROWS);
+    constexpr int KS = DP / 16, DB = DP / 32, ROWS = kDkvRows<T, DP>, TILE = L::bytes(ROWS);
     __shared__ __align__(16) char lds[4 * TILE];   // 2 x (Q tile, dO tile)
     __shared__ __align__(16) float stats[2][2][ROWS];   // 2 x what S and dP of the tile's queries start from
-    static_assert(4 * TILE + 4 * ROWS * 4 <= 160 * 1024, "shared memory");
+    constexpr bool HOLD = kDkvHoldV<T, DP>;
+    __shared__ Frag<T> held[HOLD ? 4 * KS * 64 : 1];   // V of the four waves
+    static_assert(4 * TILE + 4 * ROWS * 4 + (HOLD ? 4 * KS * 64 * (int)sizeof(Frag<T>) : 0) <= 160 * 1024, "shared memory");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int kvh = blockIdx.x % a.Hk, split = blockIdx.x / a.Hk % a.splits;
     const int slot = blockIdx.x / a.Hk / a.splits;   // early tiles have the most queries when causal: they go first
@@ -199,7 +208,8 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
     int here = j0;   // first query of the tile being worked on
     copy(begin);
 
-    Frag<T> kf[KS], vf[KS];
+    Frag<T> kf[KS], vf[HOLD ? 1 : KS];
+    Frag<T>* mine = held + (HOLD ? wave * KS * 64 + lane : 0);
     {
         const long long t = w.start + min(key, w.len - 1);
         const T* krow = static_cast<const T*>(a.k) + t * a.sk.token + kvh * a.sk.head;
@@ -207,7 +217,10 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             kf[ks] = row_terms(krow, ks, a.D, lane, 1.f);
-            vf[ks] = row_terms(vrow, ks, a.D, lane, 1.f);
+            if constexpr (HOLD)
+                mine[64 * ks] = row_terms(vrow, ks, a.D, lane, 1.f);   // read by this lane alone: no barrier
+            else
+                vf[ks] = row_terms(vrow, ks, a.D, lane, 1.f);
         }
     }
     const int rlane = L::rows_lane(lane), clane = L::cols_lane(lane), half = L::row_of_half(lane), swap = L::cols_swap(lane);
@@ -231,10 +244,12 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
             for (int r = 0; r < 16; ++r) s[r] = st[8 * (r >> 2) + (r & 3)];
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) mma(L::rows(qt, 0, ks), kf[ks], s);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int r = 0; r < 16; ++r) dp[r] = st[ROWS + 8 * (r >> 2) + (r & 3)];
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) mma(L::rows(qt + TILE, 0, ks), vf[ks], dp);
+            for (int ks = 0; ks < KS; ++ks) mma(L::rows(qt + TILE, 0, ks), HOLD ? mine[64 * ks] : vf[HOLD ? 0 : ks], dp);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 s[r] = __builtin_amdgcn_exp2f(s[r] * c);
