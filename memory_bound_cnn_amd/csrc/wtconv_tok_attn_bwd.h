@@ -34,9 +34,8 @@ __global__ void __launch_bounds__(256, occupancy(kDq, sizeof(T), DP)) k_attn_dq(
     __shared__ __align__(16) char lds[4 * TILE];   // 2 x (K tile, V tile)
     static_assert(4 * TILE <= 160 * 1024, "shared memory");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n_slots = gridDim.x / a.Hq, head = blockIdx.x % a.Hq;
-    const int slot = n_slots - 1 - blockIdx.x / a.Hq;   // late tiles have the most keys when causal: they go first
-    const Work w = find_work<kDqRows>(a, slot, lane);
+    const int head = blockIdx.x % a.Hq;
+    const Work w = find_work<kDqRows, true>(a, blockIdx.x / a.Hq, lane);
     if (w.none) return;
     const int row0 = w.tile * kDqRows + wave * 32, row = row0 + (lane & 31);
     const int rows_left = w.len - row0;
@@ -139,8 +138,7 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
     static_assert(4 * TILE + 4 * ROWS * 4 + (HOLD ? 4 * KS * 64 * (int)sizeof(Frag<T>) : 0) <= 160 * 1024, "shared memory");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int kvh = blockIdx.x % a.Hk, split = blockIdx.x / a.Hk % a.splits;
-    const int slot = blockIdx.x / a.Hk / a.splits;   // early tiles have the most queries when causal: they go first
-    const Work w = find_work<kDkvKeys>(a, slot, lane);
+    const Work w = find_work<kDkvKeys, false>(a, blockIdx.x / a.Hk / a.splits, lane);
     if (w.none) return;
     const int key0 = w.tile * kDkvKeys + wave * 32, key = key0 + (lane & 31);
     const int keys_left = w.len - key0;

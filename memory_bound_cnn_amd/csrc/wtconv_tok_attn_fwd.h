@@ -30,9 +30,8 @@ __global__ void __launch_bounds__(256, occupancy(kFwd, sizeof(T), DP)) k_attn_fw
     __shared__ __align__(16) char lds[4 * TILE];   // 2 x (K tile, V tile)
     static_assert(4 * TILE <= 160 * 1024, "shared memory");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n_slots = gridDim.x / a.Hq, head = blockIdx.x % a.Hq;
-    const int slot = n_slots - 1 - blockIdx.x / a.Hq;   // late tiles have the most keys when causal: they go first
-    const Work w = find_work<kFwdRows>(a, slot, lane);
+    const int head = blockIdx.x % a.Hq;
+    const Work w = find_work<kFwdRows, true>(a, blockIdx.x / a.Hq, lane);
     if (w.none) return;
     const int row0 = w.tile * kFwdRows + wave * 32, row = row0 + (lane & 31);   // inside the segment
     const int rows_left = w.len - row0;                                         // <= 0: this wave has none
