@@ -51,8 +51,8 @@ class _RMSNorm(torch.autograd.Function):
         xr = _rows(x)
         y, h, rstd, _ = tb.wtconv_rms_norm_forward(xr, weight, None if residual is None else _rows(residual), eps,
                                                    want_rstd=True)
-        y = y.view(x.shape)
-        h = None if h is None else h.view(x.shape)
+        if x.dim() != 2:
+            y, h = y.view(x.shape), None if h is None else h.view(x.shape)
         ctx.eps = eps
         ctx.set_materialize_grads(False)
         ctx.save_for_backward(x if h is None else h, weight, rstd)
@@ -63,9 +63,10 @@ class _RMSNorm(torch.autograd.Function):
         h, weight, rstd = ctx.saved_tensors
         if dy is None:
             return dh, None, dh, None
-        dx, dw = tb.wtconv_rms_norm_backward(_rows(dy), None if dh is None else _rows(dh).contiguous(), _rows(h),
-                                             weight, rstd, ctx.eps)
-        dx = dx.view(h.shape)
+        dx, dw = tb._rms_norm_backward(_rows(dy), None if dh is None else _rows(dh).contiguous(), _rows(h), weight,
+                                       rstd, ctx.eps)
+        if h.dim() != 2:
+            dx = dx.view(h.shape)
         return dx, dw, dx if ctx.needs_input_grad[2] else None, None
 
 
@@ -108,8 +109,9 @@ class _Rotary(torch.autograd.Function):
     @staticmethod
     def backward(ctx, g):
         positions, inv_freq = ctx.saved_tensors
-        return tb.wtconv_rotary(_dense(g), positions, inv_freq, ctx.sections, ctx.interleaved, inverse=True), \
-            None, None, None, None
+        dx = tb._rotary(_dense(g), positions, inv_freq, ctx.sections, ctx.interleaved, True,
+                        torch.empty(g.shape, dtype=g.dtype, device=g.device))
+        return dx, None, None, None, None
 
 
 def rotary(x, positions, inv_freq, sections, interleaved=False):
@@ -154,7 +156,7 @@ class _Attention(torch.autograd.Function):
     @staticmethod
     def backward(ctx, g):
         q, k, v, out, lse, cu_seqlens = ctx.saved_tensors
-        return tb.wtconv_attention_backward(q, k, v, out, lse, _heads(g), cu_seqlens, ctx.causal, ctx.scale) + \
+        return tb._attention_backward(q, k, v, out, lse, _heads(g), cu_seqlens, ctx.causal, ctx.scale) + \
             (None, None, None)
 
 
@@ -190,9 +192,9 @@ class _RotaryAttention(torch.autograd.Function):
         qkv, qk, out, lse, positions, inv_freq, cu_seqlens = ctx.saved_tensors
         d = torch.empty(qkv.shape, dtype=qkv.dtype, device=qkv.device)
         dqk = d[:, :Hq + Hk]
-        tb.wtconv_attention_backward(qk[:, :Hq], qk[:, Hq:], qkv[:, Hq + Hk:], out, lse, _heads(g), cu_seqlens, causal,
-                                     scale, grads=(d[:, :Hq], d[:, Hq:Hq + Hk], d[:, Hq + Hk:]))
-        tb.wtconv_rotary(dqk, positions, inv_freq, sections, interleaved, inverse=True, out=dqk)
+        tb._attention_backward(qk[:, :Hq], qk[:, Hq:], qkv[:, Hq + Hk:], out, lse, _heads(g), cu_seqlens, causal, scale,
+                               grads=(d[:, :Hq], d[:, Hq:Hq + Hk], d[:, Hq + Hk:]))
+        tb._rotary(dqk, positions, inv_freq, sections, interleaved, True, dqk)
         return (d,) + (None,) * 9
 
 
@@ -220,7 +222,9 @@ class _Dropout(torch.autograd.Function):
     @staticmethod
     def backward(ctx, g):
         rng, = ctx.saved_tensors
-        dx = tb.wtconv_dropout(g.contiguous(), ctx.p, rng) if ctx.needs_input_grad[0] else None
+        dx = None
+        if ctx.needs_input_grad[0]:
+            dx = tb._dropout(g.contiguous(), ctx.p, rng, None, torch.empty(g.shape, dtype=g.dtype, device=g.device))
         return dx, None, None, g if ctx.needs_input_grad[3] else None
 
 
