@@ -3,19 +3,23 @@
     python -m memory_bound_cnn_amd.build
 
 Every HIP source is compiled with packed-FP32 instructions disabled; the
-objects are linked into memory_bound_cnn_amd/libwtconv.so.
+objects are linked into memory_bound_cnn_amd/libwtconv.so.  The PyTorch module
+of the token operators, host code alone, is linked to it as _tokens.so.
 """
 import concurrent.futures
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libwtconv.so")
+TORCH_OUT = os.path.join(HERE, "_tokens.so")
 OBJDIR = os.path.join(HERE, "_build")
 ARCH = os.environ.get("WTC_OFFLOAD_ARCH", "gfx950")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+CXX = os.environ.get("CXX", "g++")
 
 COMMON = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
@@ -42,21 +46,43 @@ def _compile(src):
     return obj, r.stderr
 
 
+def _compile_torch():
+    """The object file of the PyTorch module and what it is linked with."""
+    import torch
+    base = os.path.dirname(torch.__file__)
+    obj = os.path.join(OBJDIR, "wtconv_tok_torch.cpp.o")
+    inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(HIPCC)), "include")]
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           "-DTORCH_EXTENSION_NAME=_tokens", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    cmd += ["-I" + d for d in inc] + ["-c", os.path.join(CSRC, "wtconv_tok_torch.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{CXX} failed for wtconv_tok_torch.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj, ["-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip"]
+
+
+def _link(cmd, out):
+    r = subprocess.run(cmd + ["-o", out + ".tmp"], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(out + ".tmp", out)
+
+
 def build(verbose=False):
     os.makedirs(OBJDIR, exist_ok=True)
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 4)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
+        torch_part = ex.submit(_compile_torch)
         results = list(ex.map(_compile, SOURCES))
     objs = [o for o, _ in results]
     if verbose:
         for _, err in results:
             if err.strip():
                 print(err, file=sys.stderr)
-    tmp = OUT + ".tmp"
-    cmd = [HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", "-o", tmp] + objs
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, OUT)
+    _link([HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}"] + objs, OUT)
+    obj, libs = torch_part.result()
+    _link([CXX, "-shared", "-fPIC", obj, "-L" + HERE, "-l:" + os.path.basename(OUT), "-Wl,-rpath,$ORIGIN"] + libs,
+          TORCH_OUT)
     return OUT
 
 

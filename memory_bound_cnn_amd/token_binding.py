@@ -7,7 +7,6 @@ contiguous, other strides are passed on.  Outputs are new tensors unless given.
 """
 
 import ctypes
-import functools
 
 import torch
 
@@ -117,12 +116,6 @@ def _activation(t, name, dims):
     return _DTYPE[t.dtype]
 
 
-# Each entry point checks its arguments; the functions with a leading underscore
-# are what it runs after that, and what the backward passes of tokens.py call on
-# tensors that the forward pass has checked (a backward pass runs on a thread of
-# its own, where every line of Python costs twice as much).
-
-
 def wtconv_rms_norm_forward(x, weight, residual=None, eps=1e-6, fp8=False, want_rstd=False):
     """(y, h, rstd, scale) for x [rows, C]: h is None without a residual, rstd
     unless wanted, scale unless fp8 (y is then float8_e4m3fn)."""
@@ -146,7 +139,7 @@ def wtconv_rms_norm_backward(dy, dh, h, weight, rstd, eps=1e-6, workspace=None):
     """(dx, dw): dx is the gradient of x and of the residual.  h: the norm's
     input (x where there was no residual); dh: the gradient reaching h by its
     other use, or None."""
-    _activation(h, "h", 2)
+    dtype = _activation(h, "h", 2)
     rows, C = h.shape
     dev = h.device
     _check(dy, "dy", h.dtype, dev, h.shape)
@@ -154,22 +147,10 @@ def wtconv_rms_norm_backward(dy, dh, h, weight, rstd, eps=1e-6, workspace=None):
         _check(dh, "dh", h.dtype, dev, h.shape, True)
     _check(weight, "weight", torch.float32, dev, (C,), True)
     _check(rstd, "rstd", torch.float32, dev, (rows,), True)
-    return _rms_norm_backward(dy, dh, h, weight, rstd, eps, workspace)
-
-
-@functools.lru_cache(maxsize=256)
-def _rms_workspace(rows, C, dtype):
-    d = wtc_rms_desc(rows, 0, 0, 0, C, dtype, 0, 0.0)
-    return _load().wtconv_rms_norm_backward_workspace(ctypes.addressof(d))
-
-
-def _rms_norm_backward(dy, dh, h, weight, rstd, eps, workspace=None):
-    rows, C = h.shape
-    dtype, dev = _DTYPE[h.dtype], h.device
     dx = torch.empty((rows, C), dtype=h.dtype, device=dev)
     dw = torch.empty(C, dtype=torch.float32, device=dev)
-    ws, size = _workspace(_rms_workspace(rows, C, dtype), dev, workspace)
     d = wtc_rms_desc(rows, h.stride(0), 0, dy.stride(0), C, dtype, 0, eps)
+    ws, size = _workspace(_load().wtconv_rms_norm_backward_workspace(ctypes.addressof(d)), dev, workspace)
     _call("wtconv_rms_norm_backward", dev, ctypes.addressof(d), dy.data_ptr(), _ptr(dh), h.data_ptr(),
           weight.data_ptr(), rstd.data_ptr(), dx.data_ptr(), dw.data_ptr(), _ptr(ws), size)
     return dx, dw
@@ -179,7 +160,7 @@ def wtconv_rotary(x, positions, inv_freq, sections, interleaved=False, inverse=F
     """x [T, heads, D] with its pairs turned.  positions [T, axes] int32,
     sections: pairs of each axis, inv_freq [sum(sections)] float32.  out may be
     x itself."""
-    _activation(x, "x", 3)
+    dtype = _activation(x, "x", 3)
     T, heads, D = x.shape
     dev = x.device
     axes, P = len(sections), sum(sections)
@@ -193,14 +174,9 @@ def wtconv_rotary(x, positions, inv_freq, sections, interleaved=False, inverse=F
         _check(out, "out", x.dtype, dev, x.shape)
         if out.data_ptr() == x.data_ptr() and out.stride() != x.stride():
             raise ValueError("out shares x's memory with other strides")
-    return _rotary(x, positions, inv_freq, sections, interleaved, inverse, out)
-
-
-def _rotary(x, positions, inv_freq, sections, interleaved, inverse, out):
-    T, heads, D = x.shape
-    d = wtc_rotary_desc(T, x.stride(0), x.stride(1), out.stride(0), out.stride(1), heads, D, _DTYPE[x.dtype],
-                        len(sections), tuple(sections), interleaved, inverse)
-    _call("wtconv_rotary", x.device, ctypes.addressof(d), x.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(),
+    d = wtc_rotary_desc(T, x.stride(0), x.stride(1), out.stride(0), out.stride(1), heads, D, dtype, axes,
+                        tuple(sections), interleaved, inverse)
+    _call("wtconv_rotary", dev, ctypes.addressof(d), x.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(),
           out.data_ptr())
     return out
 
@@ -208,7 +184,7 @@ def _rotary(x, positions, inv_freq, sections, interleaved, inverse, out):
 def wtconv_dropout(x, p, rng, residual=None, out=None):
     """residual + x kept with probability 1 - p and divided by it.  rng: int64
     [2] on the device, seed and offset; x, residual, out contiguous."""
-    _activation(x, "x", x.dim())
+    dtype = _activation(x, "x", x.dim())
     dev = x.device
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
@@ -219,16 +195,12 @@ def wtconv_dropout(x, p, rng, residual=None, out=None):
         out = torch.empty_like(x)
     else:
         _check(out, "out", x.dtype, dev, x.shape, True)
-    return _dropout(x, p, rng, residual, out)
-
-
-def _dropout(x, p, rng, residual, out):
-    _call("wtconv_dropout", x.device, x.numel(), _DTYPE[x.dtype], p, x.data_ptr(), _ptr(residual), rng.data_ptr(), out.data_ptr())
+    _call("wtconv_dropout", dev, x.numel(), dtype, p, x.data_ptr(), _ptr(residual), rng.data_ptr(), out.data_ptr())
     return out
 
 
-def _check_attention(q, k, v, cu_seqlens):
-    _activation(q, "q", 3)
+def _attn_desc(q, k, v, cu_seqlens, causal, scale):
+    dtype = _activation(q, "q", 3)
     T, Hq, D = q.shape
     dev = q.device
     Hk = k.shape[1] if k.dim() == 3 else 0
@@ -239,12 +211,7 @@ def _check_attention(q, k, v, cu_seqlens):
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise ValueError("cu_seqlens must be [n + 1]")
     _check(cu_seqlens, "cu_seqlens", torch.int32, dev, cu_seqlens.shape, True)
-
-
-def _attn_desc(q, k, v, cu_seqlens, causal, scale):
-    T, Hq, D = q.shape
-    d = wtc_attn_desc(T, cu_seqlens.shape[0] - 1, Hq, k.shape[1], D, _DTYPE[q.dtype], causal,
-                      D ** -0.5 if scale is None else scale)
+    d = wtc_attn_desc(T, cu_seqlens.shape[0] - 1, Hq, Hk, D, dtype, causal, D ** -0.5 if scale is None else scale)
     d.q, d.k, d.v = q.stride()[:2], k.stride()[:2], v.stride()[:2]
     return d
 
@@ -252,7 +219,6 @@ def _attn_desc(q, k, v, cu_seqlens, causal, scale):
 def wtconv_attention_forward(q, k, v, cu_seqlens, causal=False, scale=None, want_lse=False, out=None):
     """(out, lse) for q [T, Hq, D], k and v [T, Hk, D]; lse [Hq, T] float32 or
     None.  scale: 1 / sqrt(D) unless given."""
-    _check_attention(q, k, v, cu_seqlens)
     d = _attn_desc(q, k, v, cu_seqlens, causal, scale)
     dev = q.device
     if out is None:
@@ -270,22 +236,15 @@ def wtconv_attention_backward(q, k, v, out, lse, dout, cu_seqlens, causal=False,
                               workspace=None):
     """(dq, dk, dv).  grads: the tensors to write them to (q's, k's and v's
     shapes, any strides that the library takes), or None."""
-    _check_attention(q, k, v, cu_seqlens)
+    d = _attn_desc(q, k, v, cu_seqlens, causal, scale)
     dev = q.device
     _check(out, "out", q.dtype, dev, q.shape)
     _check(dout, "dout", q.dtype, dev, q.shape)
     _check(lse, "lse", torch.float32, dev, (q.shape[1], q.shape[0]), True)
-    if grads is not None:
-        for g, t, name in zip(grads, (q, k, v), ("dq", "dk", "dv")):
-            _check(g, name, q.dtype, dev, t.shape)
-    return _attention_backward(q, k, v, out, lse, dout, cu_seqlens, causal, scale, grads, workspace)
-
-
-def _attention_backward(q, k, v, out, lse, dout, cu_seqlens, causal, scale, grads=None, workspace=None):
-    d = _attn_desc(q, k, v, cu_seqlens, causal, scale)
-    dev = q.device
     if grads is None:
         grads = tuple(torch.empty(t.shape, dtype=q.dtype, device=dev) for t in (q, k, v))
+    for g, t, name in zip(grads, (q, k, v), ("dq", "dk", "dv")):
+        _check(g, name, q.dtype, dev, t.shape)
     dq, dk, dv = grads
     d.o, d.g, d.dq, d.dk, d.dv = (t.stride()[:2] for t in (out, dout, dq, dk, dv))
     ws, size = _workspace(_load().wtconv_attention_backward_workspace(ctypes.addressof(d)), dev, workspace)

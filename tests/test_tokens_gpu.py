@@ -336,7 +336,7 @@ def attn_check(q, k, v, cu, causal=False, scale=None, train=True, what=""):
         r, b, lse = attention_ref(q, k, v, cu, causal, sc, dout if train else None, 0.0 if dtype == "fp32" else u)
         for n, t in got.items():
             within(t, r[n], 1.02 * (b[n] + u * (r[n].abs() + b[n])) + 1e-30, f"{what} {n}")
-        _, ls = tb.wtconv_attention_forward(tokens._heads(q), tokens._heads(k), tokens._heads(v), cu, causal, scale,
+        _, ls = tb.wtconv_attention_forward(q.contiguous(), k.contiguous(), v.contiguous(), cu, causal, scale,
                                             want_lse=True)
         fin = torch.isfinite(lse)
         assert torch.equal(torch.isposinf(ls), ~fin)
@@ -566,6 +566,51 @@ def test_token_block_trains_and_repeats():
     x2 = x.detach().clone()
     x2[49:] += 1
     assert torch.equal(m(x2, pos, cu)[:49], a[:49])
+
+
+def test_second_derivatives_are_refused():
+    x, w = torch.randn(4, 16, device=DEV, requires_grad=True), torch.ones(16, device=DEV, requires_grad=True)
+    y = tokens.rms_norm(x, w)
+    dy = torch.randn(4, 16, device=DEV, requires_grad=True)
+    with pytest.raises(RuntimeError, match="first derivatives only"):
+        torch.autograd.grad(y, x, dy, create_graph=True)
+    q = torch.randn(5, 2, 32, device=DEV, requires_grad=True)
+    cu = torch.tensor([0, 5], dtype=torch.int32, device=DEV)
+    g = torch.randn(5, 2, 32, device=DEV, requires_grad=True)
+    with pytest.raises(RuntimeError, match="first derivatives only"):
+        torch.autograd.grad(tokens.attention(q, q, q, cu), q, g, create_graph=True)
+
+
+def test_entry_points_refuse():
+    """Device tensors of wrong types, shapes and places, through the public functions."""
+    x, w = torch.zeros(4, 16, device=DEV), torch.ones(16, device=DEV)
+    cu = torch.tensor([0, 4], dtype=torch.int32, device=DEV)
+    pos, f = torch.zeros(4, 1, dtype=torch.int32, device=DEV), torch.ones(8, device=DEV)
+    x3 = x.view(4, 1, 16)
+    for call, message in (
+            (lambda: tokens.rms_norm(x.half(), w), "expected float32 or bfloat16"),
+            (lambda: tokens.rms_norm(x, w[:8]), "weight has shape"),
+            (lambda: tokens.rms_norm(x, w.bfloat16()), "weight has dtype"),
+            (lambda: tokens.rms_norm(x, w.cpu()), "weight must be a CUDA tensor"),
+            (lambda: tokens.rms_norm(x, w, x.bfloat16()), "residual has dtype"),
+            (lambda: tokens.rms_norm_fp8(x.clone().requires_grad_(), w), "no gradient"),
+            (lambda: tokens.rotary(x3, pos, f, (9,)), "pairs do not fit"),
+            (lambda: tokens.rotary(x3, pos, f, (4,)), "inv_freq has shape"),
+            (lambda: tokens.rotary(x3, pos.long(), f, (8,)), "positions has dtype"),
+            (lambda: tokens.rotary(x3, pos, f, ()), "axes are supported"),
+            (lambda: tokens.rotary(x, pos, f, (8,)), "expected 3 axes"),
+            (lambda: tokens.attention(x3, x3, x3, cu.long()), "cu_seqlens has dtype"),
+            (lambda: tokens.attention(x3, x3, x3[:3], cu), "v has shape"),
+            (lambda: tokens.attention(x3, x3.expand(4, 2, 16), x3.expand(4, 2, 16), cu), "do not divide"),
+            (lambda: tokens.attention(x3, x3, x3.bfloat16(), cu), "v has dtype"),
+            (lambda: tokens.dropout(x, 1.5, torch.zeros(2, dtype=torch.int64, device=DEV)), "no probability"),
+            (lambda: tokens.dropout(x, 0.5, torch.zeros(2, device=DEV)), "rng has dtype"),
+            (lambda: tokens.dropout(x, 0.5, torch.zeros(2, dtype=torch.int64, device=DEV), x[:2]), "residual has shape")):
+        with pytest.raises(ValueError, match=message):
+            call()
+    x60 = torch.zeros(4, 1, 60, device=DEV)
+    with pytest.raises(RuntimeError, match="shape outside the supported limits"):
+        tokens.attention(x60, x60, x60, cu)
 
 
 def test_operators_replay_in_a_graph():
