@@ -9,8 +9,12 @@
 // registers 8 s .. 8 s + 7 of a result are, as a B tile, the terms
 //   16 s + 4 h + {0, 1, 2, 3} and 16 s + 8 + 4 h + {0, 1, 2, 3}     ("turned" order)
 // and the A tile of that product is read from shared memory in this order.
-// bfloat16 takes one v_mfma_f32_32x32x16_bf16 a tile, float32 eight
-// v_mfma_f32_32x32x2_f32, whose two terms are the same i of both halves.
+// bfloat16 takes one v_mfma_f32_32x32x16_bf16 a tile (32 cycles).  A float32
+// is the sum of three bfloat16 (8 of its 24 bits each, split exactly), and its
+// product six of theirs: the three left out are below 2^-24 of it, so this is
+// float32's own precision in 192 cycles, where the float32 instructions take
+// 512 (4 sequences of 2048 tokens, 12 heads of 64: forward, dq, dk and dv 425,
+// 608 and 832 us with those, 259, 404 and 538 so).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -22,7 +26,7 @@ namespace wtc {
 namespace attn {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -40,7 +44,7 @@ struct Frag<uint16_t> {
 };
 template <>
 struct Frag<float> {
-    f32x8 v;
+    u32x4 v[3];   // high, middle and low parts
 };
 
 __device__ __forceinline__ void mma(const Frag<uint16_t>& a, const Frag<uint16_t>& b, f32x16& c) {
@@ -48,8 +52,42 @@ __device__ __forceinline__ void mma(const Frag<uint16_t>& a, const Frag<uint16_t
                                                 0, 0, 0);
 }
 __device__ __forceinline__ void mma(const Frag<float>& a, const Frag<float>& b, f32x16& c) {
+    auto part = [&](int i, int j) {
+        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a.v[i]),
+                                                    __builtin_bit_cast(bf16x8, b.v[j]), c, 0, 0, 0);
+    };
+    part(0, 2);
+    part(2, 0);
+    part(1, 1);
+    part(0, 1);
+    part(1, 0);
+    part(0, 0);
+}
+
+// Two float32 to the pairs of their parts; each difference is exact.
+__device__ __forceinline__ void split(float a, float b, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+    hi = bf16x2_rne(a, b);
+    a -= __builtin_bit_cast(float, hi << 16);
+    b -= __builtin_bit_cast(float, hi & 0xFFFF0000u);
+    mid = bf16x2_rne(a, b);
+    a -= __builtin_bit_cast(float, mid << 16);
+    b -= __builtin_bit_cast(float, mid & 0xFFFF0000u);
+    lo = bf16x2_rne(a, b);
+}
+__device__ __forceinline__ Frag<float> split8(const f32x4& x, const f32x4& y) {
+    Frag<float> f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a.v[i], b.v[i], c, 0, 0, 0);
+    for (int i = 0; i < 4; ++i) {
+        uint32_t h, m, l;
+        if (i < 2)
+            split(x[2 * i], x[2 * i + 1], h, m, l);
+        else
+            split(y[2 * i - 4], y[2 * i - 3], h, m, l);
+        f.v[0][i] = h;
+        f.v[1][i] = m;
+        f.v[2][i] = l;
+    }
+    return f;
 }
 
 // Registers 8 s .. 8 s + 7 of a result as the terms of a B tile.  bfloat16:
@@ -60,68 +98,102 @@ __device__ __forceinline__ void as_terms(const f32x16& c, int s, Frag<uint16_t>&
     for (int i = 0; i < 4; ++i) f.v[i] = bf16x2_rne(c[8 * s + 2 * i], c[8 * s + 2 * i + 1]);
 }
 __device__ __forceinline__ void as_terms(const f32x16& c, int s, Frag<float>& f) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f.v[i] = c[8 * s + i];
+    f = split8(f32x4{c[8 * s], c[8 * s + 1], c[8 * s + 2], c[8 * s + 3]},
+               f32x4{c[8 * s + 4], c[8 * s + 5], c[8 * s + 6], c[8 * s + 7]});
 }
 
-// A tile of rows in shared memory, as it is copied there: groups of 1024 bytes
-// (kGroup whole rows, what one instruction copies), kPad bytes between groups.
-// Lane l of an A tile stands for row place(l) of 32, not for row l: place()
+// A tile of ROWS rows in shared memory: groups of 1024 bytes (kGroup whole
+// rows of 16-bit channels, what one copying instruction moves), 32 bytes
+// between groups; float32 has three such parts, one after another.
+//   Lane l of an A tile stands for row place(l) of 32, not for row l: place()
 // sends the bits of l to bits of the row so that lanes next to each other read
 // different banks (256 bytes wide), rows() and cols() alike, and every read of
 // a tile is one register plus a constant: place(a + b) = place(a) + place(b)
 // where a and b share no bit, and row_at() likewise.  Results whose rows are
 // rows of the tile have them in that order.
-//   Bits 0 and 1 of l are the four rows of 64 bytes that cols() reads at once
-// (bfloat16): they step by 64 bytes or more.  Bit 2 is the wave's half in
-// cols().  Bits 0 to 3 are what rows() reads at once, 16 bytes a lane; where
-// bit 3 steps by a multiple of 256 bytes, rows with that bit set have their
-// 16-byte chunks swapped in pairs (kSwap).
-template <typename T, int DP>
+//   Bits 0 and 1 of l are the four rows of 64 bytes that cols() reads at once:
+// they step by 64 bytes or more.  Bit 2 is the wave's half in cols().  Bits 0
+// to 3 are what rows() reads at once, 16 bytes a lane; bit 3 steps by 256
+// bytes, so rows with that bit set have their 16-byte chunks swapped in pairs
+// (kSwap).
+template <typename T, int DP, int ROWS>
 struct Tile {
-    static constexpr int kRowBytes = (DP == 96 ? 128 : DP) * (int)sizeof(T);
-    static constexpr int kChunks = kRowBytes / 16;     // of 16 bytes; a power of two
-    static constexpr int kGroup = 1024 / kRowBytes;    // rows of a group: 2 .. 16
-    static constexpr int kPad = kRowBytes == 512 ? 16 : 32;
-    static constexpr int kStride = 1024 + kPad;
-    static constexpr int kSwap = sizeof(T) == 2 ? (kRowBytes == 256 ? 1 : kRowBytes == 128 ? 2 : 4) : 0;   // a bit of the row
-    static constexpr int bytes(int rows) { return rows / kGroup * kStride; }
+    static constexpr int kParts = sizeof(T) == 2 ? 1 : 3;
+    static constexpr int kRowBytes = (DP == 96 ? 128 : DP) * 2;
+    static constexpr int kChunks = kRowBytes / 16;     // of 8 channels; a power of two
+    static constexpr int kGroup = 1024 / kRowBytes;    // rows of a group: 4, 8 or 16
+    static constexpr int kStride = 1024 + 32;
+    static constexpr int kSwap = kRowBytes == 256 ? 1 : kRowBytes == 128 ? 2 : 4;   // a bit of the row
+    static constexpr int kPart = ROWS / kGroup * kStride;
+    static constexpr int kBytes = kParts * kPart;
 
     // The row bits that bits 0 .. 4 of l go to.  Rows of 64 bytes: the group is
-    // bit 4 of the row; 128: bits 3 and 4; 256: bits 2 to 4; 512: bits 1 to 4.
+    // bit 4 of the row; 128: bits 3 and 4; 256: bits 2 to 4.
     static constexpr __host__ __device__ int place(int l) {
-        constexpr int to[4][5] = {{0, 1, 4, 2, 3}, {0, 4, 3, 1, 2}, {3, 4, 2, 0, 1}, {1, 2, 4, 3, 0}};
-        constexpr int k = kRowBytes == 64 ? 0 : kRowBytes == 128 ? 1 : kRowBytes == 256 ? 2 : 3;
+        constexpr int to[3][5] = {{0, 1, 4, 2, 3}, {0, 4, 3, 1, 2}, {3, 4, 2, 0, 1}};
+        constexpr int k = kRowBytes == 64 ? 0 : kRowBytes == 128 ? 1 : 2;
         int r = 0;
         for (int b = 0; b < 5; ++b) r |= ((l >> b) & 1) << to[k][b];
         return r;
     }
     static constexpr __host__ __device__ int row_at(int r) { return r / kGroup * kStride + r % kGroup * kRowBytes; }
 
-    // Copies rows j0 .. j0 + ROWS - 1 of a matrix into the tile at byte address
-    // `dst` of shared memory: rows past `last` repeat row `last`, chunks past
-    // the head's channels its last chunk, so that nothing outside the sequence
-    // is read (those places meet zeros or are not used).  `base` points at row
-    // j0.  Asynchronous: the caller waits with dma_wait() and a barrier.
-    template <int ROWS, int WAVES>
-    static __device__ __forceinline__ void copy(uint32_t dst, const char* base, uint32_t row_bytes, int last,
-                                                int chunks, int wave, int lane) {
-        constexpr int CALLS = ROWS / kGroup / WAVES;
-        static_assert(ROWS % (kGroup * WAVES) == 0, "whole groups");
-        const int r = lane / kChunks;   // of the group
-        const uint32_t c = (uint32_t)min((lane % kChunks) ^ (r & kSwap ? 1 : 0), chunks - 1) * 16u;
-        if (last >= ROWS - 1) {
-            const uint32_t off = (uint32_t)r * row_bytes + c;
+    // Rows j0 .. j0 + ROWS - 1 of a matrix on their way into the tile, which
+    // commit() ends: a barrier then makes them visible.  Rows past `last`
+    // repeat row `last`, chunks past the head's channels its last chunk, so
+    // that nothing outside the sequence is read (those places meet zeros or are
+    // not used).  `base` points at row j0, `dst` is the tile's byte address in
+    // shared memory, `chunks` the head's channels / 8.  The workgroup has four
+    // waves.  bfloat16 is copied by the memory system; float32 passes through
+    // registers, where it is split, once for all the waves that read it.
+    static constexpr int kUnits = sizeof(T) == 2 ? 1 : (ROWS * kChunks + 255) / 256;   // of 8 channels, a thread
+    struct Load {
+        f32x4 v[kUnits][2];
+    };
+    static __device__ __forceinline__ void issue(Load& load, uint32_t dst, const char* base, uint32_t row_bytes, int last,
+                                                 int chunks, int wave, int lane) {
+        if constexpr (sizeof(T) == 2) {
+            constexpr int CALLS = ROWS / kGroup / 4;
+            static_assert(ROWS % (kGroup * 4) == 0, "whole groups");
+            const int r = lane / kChunks;   // of the group
+            const uint32_t c = (uint32_t)min((lane % kChunks) ^ (r & kSwap ? 1 : 0), chunks - 1) * 16u;
+            if (last >= ROWS - 1) {
+                const uint32_t off = (uint32_t)r * row_bytes + c;
 #pragma unroll
-            for (int i = 0; i < CALLS; ++i) {
-                const int g = wave * CALLS + i;
-                dma(dst + (uint32_t)(g * kStride), base + (size_t)(uint32_t)(g * kGroup) * row_bytes, off);
+                for (int i = 0; i < CALLS; ++i) {
+                    const int g = wave * CALLS + i;
+                    dma(dst + (uint32_t)(g * kStride), base + (size_t)(uint32_t)(g * kGroup) * row_bytes, off);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < CALLS; ++i) {
+                    const int g = wave * CALLS + i;
+                    dma(dst + (uint32_t)(g * kStride), base, (uint32_t)min(g * kGroup + r, last) * row_bytes + c);
+                }
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < CALLS; ++i) {
-                const int g = wave * CALLS + i;
-                dma(dst + (uint32_t)(g * kStride), base, (uint32_t)min(g * kGroup + r, last) * row_bytes + c);
+            for (int i = 0; i < kUnits; ++i) {
+                const int u = 256 * i + 64 * wave + lane;   // past the last row: not committed
+                const char* p = base + (uint32_t)min(u / kChunks, last) * row_bytes +
+                                (uint32_t)min(u % kChunks, chunks - 1) * 32u;
+                load.v[i][0] = *reinterpret_cast<const f32x4*>(p);
+                load.v[i][1] = *reinterpret_cast<const f32x4*>(p + 16);
+            }
+        }
+    }
+    static __device__ __forceinline__ void commit(const Load& load, char* tile, int wave, int lane) {
+        if constexpr (sizeof(T) == 2) {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        } else {
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i) {
+                const int u = 256 * i + 64 * wave + lane, r = u / kChunks;
+                if (ROWS * kChunks % 256 != 0 && u >= ROWS * kChunks) break;
+                const Frag<float> f = split8(load.v[i][0], load.v[i][1]);
+                char* p = tile + row_at(r) + (((u % kChunks) ^ (r & kSwap ? 1 : 0)) << 4);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) *reinterpret_cast<u32x4*>(p + k * kPart) = f.v[k];
             }
         }
     }
@@ -136,29 +208,22 @@ struct Tile {
     // The lane's part of the addresses that rows() and cols() read.
     static __device__ __forceinline__ int rows_lane(int lane) {
         const int r = place(lane & 31);
-        return row_at(r) + (((lane >> 5) * 8 * (int)sizeof(T)) ^ (r & kSwap ? 16 : 0));
+        return row_at(r) + (((lane >> 5) * 16) ^ (r & kSwap ? 16 : 0));
     }
     static __device__ __forceinline__ int cols_lane(int lane) {
-        if constexpr (sizeof(T) == 2)
-            return row_at(place(4 * (lane >> 5) + ((lane & 15) >> 2))) + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
-        return row_at(place(4 * (lane >> 5))) + (lane & 31) * 4;
+        return row_at(place(4 * (lane >> 5) + ((lane & 15) >> 2))) + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
     }
 
     // Terms 16 ks + 8 h .. + 7 of row r0 + place(lane % 32), r0 a multiple of
     // 32: an A tile whose rows are rows of the matrix.  p = tile + rows_lane().
     static __device__ __forceinline__ Frag<T> rows(const char* p, int r0, int ks) {
-        p += row_at(r0) + 16 * ks * (int)sizeof(T);
+        p += row_at(r0) + 32 * ks;
         Frag<T> f;
         if constexpr (sizeof(T) == 2) {
             f.v = *reinterpret_cast<const u32x4*>(p);
         } else {
-            const u32x4 lo = *reinterpret_cast<const u32x4*>(p), hi = *reinterpret_cast<const u32x4*>(p + 16);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t l = lo[i], u = hi[i];
-                f.v[i] = __builtin_bit_cast(float, l);
-                f.v[4 + i] = __builtin_bit_cast(float, u);
-            }
+            for (int k = 0; k < 3; ++k) f.v[k] = *reinterpret_cast<const u32x4*>(p + k * kPart);
         }
         return f;
     }
@@ -166,25 +231,29 @@ struct Tile {
     // Rows r0 + place(16 s + the turned order), of column 32 db + lane % 32: an
     // A tile whose rows are columns of the matrix.  p = tile + cols_lane(), and
     // swap = cols_swap(), to the other chunk of a pair, for the rows of l's bit 3.
-    // bfloat16: 16 lanes read 4 rows of 16 columns and get them transposed, 4
-    // rows of a column each.
+    // 16 lanes read 4 rows of 16 columns and get them transposed, 4 rows of a
+    // column each.
     static __device__ __forceinline__ int cols_swap(int lane) { return lane & 2 ? -16 : 16; }
+    static __device__ __forceinline__ u32x4 cols_part(const char* p, int swap, int s) {
+        u32x4 v;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) s16x4*)(lds_char*)(p + k * swap + row_at(place(16 * s + 8 * k))));
+            const u32x2 u = __builtin_bit_cast(u32x2, t);
+            v[2 * k] = u[0];
+            v[2 * k + 1] = u[1];
+        }
+        return v;
+    }
     static __device__ __forceinline__ Frag<T> cols(const char* p, int swap, int r0, int s, int db) {
-        p += row_at(r0) + 32 * db * (int)sizeof(T);
+        p += row_at(r0) + 64 * db;
         Frag<T> f;
         if constexpr (sizeof(T) == 2) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (__attribute__((address_space(3))) s16x4*)(lds_char*)(p + k * swap + row_at(place(16 * s + 8 * k))));
-                const u32x2 u = __builtin_bit_cast(u32x2, t);
-                f.v[2 * k] = u[0];
-                f.v[2 * k + 1] = u[1];
-            }
+            f.v = cols_part(p, swap, s);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                f.v[i] = *reinterpret_cast<const float*>(p + row_at(place(16 * s + 8 * (i >> 2) + (i & 3))));
+            for (int k = 0; k < 3; ++k) f.v[k] = cols_part(p + k * kPart, swap, s);
         }
         return f;
     }
@@ -195,9 +264,6 @@ struct Tile {
 };
 
 __device__ __forceinline__ uint32_t lds_address(const void* p) { return (uint32_t)(uintptr_t)(lds_char*)p; }
-
-// Waits for this wave's copies; a barrier then makes all waves' visible.
-__device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // Terms 16 ks + 8 h .. + 7 of one row in device memory (D channels, the others
 // zero), times `sign` (+1 or -1): a B tile whose columns are rows of the matrix.
@@ -211,25 +277,33 @@ __device__ __forceinline__ Frag<T> row_terms(const T* row, int ks, int D, int la
         if (sign < 0.f) u ^= 0x80008000u;
         f.v = u;
     } else {
-        f.v = f32x8{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (c < D) f.v = *reinterpret_cast<const f32x8*>(row + c) * sign;
+        f32x4 x = {0.f, 0.f, 0.f, 0.f}, y = x;
+        if (c < D) {
+            x = *reinterpret_cast<const f32x4*>(row + c) * sign;
+            y = *reinterpret_cast<const f32x4*>(row + c + 4) * sign;
+        }
+        f = split8(x, y);
     }
     return f;
 }
 
-__device__ __forceinline__ float dot(const Frag<uint16_t>& a, const Frag<uint16_t>& b) {
+// The lane's half of the terms of a . b, rows of D channels in device memory.
+template <typename T, int KS>
+__device__ __forceinline__ float half_dot(const T* a, const T* b, int D, int lane) {
     float v = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v = fmaf(__builtin_bit_cast(float, a.v[i] << 16), __builtin_bit_cast(float, b.v[i] << 16), v);
-        v = fmaf(__builtin_bit_cast(float, a.v[i] & 0xFFFF0000u), __builtin_bit_cast(float, b.v[i] & 0xFFFF0000u), v);
+    for (int ks = 0; ks < KS; ++ks) {
+        const int c = 16 * ks + 8 * (lane >> 5);
+        if (c >= D) continue;
+#pragma unroll
+        for (int k = 0; k < 8; k += kVec<T>) {
+            float x[kVec<T>], y[kVec<T>];
+            load16(a + c + k, x);
+            load16(b + c + k, y);
+#pragma unroll
+            for (int i = 0; i < kVec<T>; ++i) v = fmaf(x[i], y[i], v);
+        }
     }
-    return v;
-}
-__device__ __forceinline__ float dot(const Frag<float>& a, const Frag<float>& b) {
-    float v = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v = fmaf(a.v[i], b.v[i], v);
     return v;
 }
 
@@ -257,7 +331,6 @@ __device__ __forceinline__ void store4(T* row, int db, int g, int D, int lane, f
     if constexpr (sizeof(T) == 2) {
         *reinterpret_cast<u32x2*>(row + at) = u32x2{bf16x2_rne(a, b), bf16x2_rne(c, d)};
     } else {
-        typedef float f32x4 __attribute__((ext_vector_type(4)));
         *reinterpret_cast<f32x4*>(row + at) = f32x4{a, b, c, d};
     }
 }

@@ -15,7 +15,8 @@ namespace wtc {
 namespace attn {
 
 constexpr int kDqRows = 128;   // queries of a workgroup, 32 a wave
-constexpr int kDqKeys = 64;    // keys of a tile
+template <typename T>
+constexpr int kDqKeys = sizeof(T) == 2 ? 64 : 32;   // keys of a tile
 constexpr int kDkvKeys = 128;  // keys of a workgroup, 32 a wave
 // Queries of a tile, and whether the wave's 32 rows of V wait in shared memory
 // instead of registers.  128 channels of bfloat16 need 64 registers for K and V
@@ -29,8 +30,9 @@ constexpr int kDkvRows = sizeof(T) == 2 && !kDkvHoldV<T, DP> ? 64 : 32;
 
 template <typename T, int DP>
 __global__ void __launch_bounds__(256, occupancy(kDq, sizeof(T), DP)) k_attn_dq(Args a) {
-    using L = Tile<T, DP>;
-    constexpr int KS = DP / 16, DB = DP / 32, TILE = L::bytes(kDqKeys);
+    constexpr int KEYS = kDqKeys<T>, KB = KEYS / 32, KS = DP / 16, DB = DP / 32;
+    using L = Tile<T, DP, KEYS>;
+    constexpr int TILE = L::kBytes;
     __shared__ __align__(16) char lds[4 * TILE];   // 2 x (K tile, V tile)
     static_assert(4 * TILE <= 160 * 1024, "shared memory");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -50,18 +52,19 @@ __global__ void __launch_bounds__(256, occupancy(kDq, sizeof(T), DP)) k_attn_dq(
         }
         return;
     }
-    const int kvh = head / a.group, chunks = a.D * (int)sizeof(T) / 16;
+    const int kvh = head / a.group, chunks = a.D / 8;
     const char* kbase = reinterpret_cast<const char*>(static_cast<const T*>(a.k) + (long long)w.start * a.sk.token + kvh * a.sk.head);
     const char* vbase = reinterpret_cast<const char*>(static_cast<const T*>(a.v) + (long long)w.start * a.sv.token + kvh * a.sv.head);
     const uint32_t krow = (uint32_t)a.sk.token * sizeof(T), vrow = (uint32_t)a.sv.token * sizeof(T);
     const int keys = a.causal ? min(w.len, (w.tile + 1) * kDqRows) : w.len;
-    const int tiles = (keys + kDqKeys - 1) / kDqKeys;
+    const int tiles = (keys + KEYS - 1) / KEYS;
     const uint32_t lds0 = lds_address(lds);
+    typename L::Load kload, vload;
     auto copy = [&](int j) {
-        const int j0 = j * kDqKeys, last = min(w.len - 1 - j0, kDqKeys - 1);
+        const int j0 = j * KEYS, last = min(w.len - 1 - j0, KEYS - 1);
         const uint32_t at = lds0 + (uint32_t)(j & 1) * (2 * TILE);
-        L::template copy<kDqKeys, 4>(at, kbase + (long long)j0 * krow, krow, last, chunks, wave, lane);
-        L::template copy<kDqKeys, 4>(at + TILE, vbase + (long long)j0 * vrow, vrow, last, chunks, wave, lane);
+        L::issue(kload, at, kbase + (long long)j0 * krow, krow, last, chunks, wave, lane);
+        L::issue(vload, at + TILE, vbase + (long long)j0 * vrow, vrow, last, chunks, wave, lane);
     };
     copy(0);
 
@@ -77,26 +80,26 @@ __global__ void __launch_bounds__(256, occupancy(kDq, sizeof(T), DP)) k_attn_dq(
         for (int ks = 0; ks < KS; ++ks) {
             q[ks] = row_terms(qrow, ks, a.D, lane, 1.f);
             g[ks] = row_terms(grow, ks, a.D, lane, 1.f);
-            delta += dot(g[ks], row_terms(orow, ks, a.D, lane, 1.f));
         }
-        delta = both_sum(delta);
+        delta = both_sum(half_dot<T, KS>(grow, orow, a.D, lane));
         if (live && lane < 32) a.delta[stat] = delta;   // for the other kernel
     }
     const float lse2 = a.lse[stat] * kLog2e;
     const int rlane = L::rows_lane(lane), clane = L::cols_lane(lane), half = L::row_of_half(lane), swap = L::cols_swap(lane);
     f32x16 acc[DB] = {};
     for (int j = 0; j < tiles; ++j) {
-        dma_wait();
+        L::commit(kload, lds + (j & 1) * (2 * TILE), wave, lane);
+        L::commit(vload, lds + (j & 1) * (2 * TILE) + TILE, wave, lane);
         __syncthreads();   // tile j is there; everyone is done with the other one
         if (j + 1 < tiles) copy(j + 1);
-        const int j0 = j * kDqKeys;
+        const int j0 = j * KEYS;
         if (rows_left <= 0 || (a.causal && j0 > row0 + 31)) continue;
         const char* kt = lds + (j & 1) * (2 * TILE) + rlane;
         const char* kc = lds + (j & 1) * (2 * TILE) + clane;
         const int limit = a.causal ? min(w.len - 1, row) : w.len - 1;
-        const bool edge = j0 + kDqKeys - 1 > (a.causal ? min(w.len - 1, row0) : w.len - 1);
+        const bool edge = j0 + KEYS - 1 > (a.causal ? min(w.len - 1, row0) : w.len - 1);
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
+        for (int kb = 0; kb < KB; ++kb) {
             f32x16 s = {}, dp = {};
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
@@ -129,8 +132,9 @@ __global__ void __launch_bounds__(256, occupancy(kDq, sizeof(T), DP)) k_attn_dq(
 
 template <typename T, int DP>
 __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dkv(Args a) {
-    using L = Tile<T, DP>;
-    constexpr int KS = DP / 16, DB = DP / 32, ROWS = kDkvRows<T, DP>, TILE = L::bytes(ROWS);
+    constexpr int ROWS = kDkvRows<T, DP>, KS = DP / 16, DB = DP / 32;
+    using L = Tile<T, DP, ROWS>;
+    constexpr int TILE = L::kBytes;
     __shared__ __align__(16) char lds[4 * TILE];   // 2 x (Q tile, dO tile)
     __shared__ __align__(16) float stats[2][2][ROWS];   // 2 x what S and dP of the tile's queries start from
     constexpr bool HOLD = kDkvHoldV<T, DP>;
@@ -169,7 +173,7 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
         store();
         return;
     }
-    const int chunks = a.D * (int)sizeof(T) / 16;
+    const int chunks = a.D / 8;
     const uint32_t qrow = (uint32_t)a.sq.token * sizeof(T), grow = (uint32_t)a.sg.token * sizeof(T);
     const int first = a.causal ? w.tile * kDkvKeys / ROWS : 0;   // the first query tile that sees these keys
     const int per_head = (w.len + ROWS - 1) / ROWS - first, all = per_head * a.group;
@@ -182,14 +186,15 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
     // no scale below 2^-100 (a zero one): what it multiplies is then lost beside lse, as it should be
     const float c = copysignf(fmaxf(fabsf(a.scale) * kLog2e, 0x1p-100f), a.scale), inv_c = 1.f / c;
     float stat = 0.f;   // of the tile copied last, on its way to shared memory
+    typename L::Load qload, gload;
     int head = kvh * a.group + begin / per_head, j0 = (first + begin % per_head) * ROWS;   // of the next tile to copy
     auto copy = [&](int i) {
         const int last = min(w.len - 1 - j0, ROWS - 1);
         const uint32_t at = lds0 + (uint32_t)(i & 1) * (2 * TILE);
         const T* qp = static_cast<const T*>(a.q) + (long long)(w.start + j0) * a.sq.token + head * a.sq.head;
         const T* gp = static_cast<const T*>(a.g) + (long long)(w.start + j0) * a.sg.token + head * a.sg.head;
-        L::template copy<ROWS, 4>(at, reinterpret_cast<const char*>(qp), qrow, last, chunks, wave, lane);
-        L::template copy<ROWS, 4>(at + TILE, reinterpret_cast<const char*>(gp), grow, last, chunks, wave, lane);
+        L::issue(qload, at, reinterpret_cast<const char*>(qp), qrow, last, chunks, wave, lane);
+        L::issue(gload, at + TILE, reinterpret_cast<const char*>(gp), grow, last, chunks, wave, lane);
         if (threadIdx.x < 2 * ROWS) {
             // kept in the order that a result's registers have the rows in
             const int r = threadIdx.x % ROWS / 32 * 32 + L::place(threadIdx.x % 32);
@@ -224,7 +229,8 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
     const int rlane = L::rows_lane(lane), clane = L::cols_lane(lane), half = L::row_of_half(lane), swap = L::cols_swap(lane);
     for (int i = begin; i < end; ++i) {
         if (threadIdx.x < 2 * ROWS) stats[i & 1][threadIdx.x / ROWS][threadIdx.x % ROWS] = stat;
-        dma_wait();
+        L::commit(qload, lds + (i & 1) * (2 * TILE), wave, lane);
+        L::commit(gload, lds + (i & 1) * (2 * TILE) + TILE, wave, lane);
         __syncthreads();   // tile i is there; everyone is done with the other one
         const int at = here;
         here = j0;

@@ -16,7 +16,8 @@ namespace wtc {
 namespace attn {
 
 constexpr int kFwdRows = 128;   // queries of a workgroup
-constexpr int kFwdKeys = 64;    // keys of a tile
+template <typename T>
+constexpr int kFwdKeys = sizeof(T) == 2 ? 64 : 32;   // keys of a tile
 
 // The running maximum is raised, and the sums rescaled, only when a tile
 // exceeds it by more than this many powers of two: P then reaches 2^8 instead
@@ -25,8 +26,9 @@ constexpr float kRaise = 8.f;
 
 template <typename T, int DP>
 __global__ void __launch_bounds__(256, occupancy(kFwd, sizeof(T), DP)) k_attn_fwd(Args a) {
-    using L = Tile<T, DP>;
-    constexpr int KS = DP / 16, DB = DP / 32, TILE = L::bytes(kFwdKeys);
+    constexpr int KEYS = kFwdKeys<T>, KB = KEYS / 32, KS = DP / 16, DB = DP / 32;
+    using L = Tile<T, DP, KEYS>;
+    constexpr int TILE = L::kBytes;
     __shared__ __align__(16) char lds[4 * TILE];   // 2 x (K tile, V tile)
     static_assert(4 * TILE <= 160 * 1024, "shared memory");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -47,18 +49,19 @@ __global__ void __launch_bounds__(256, occupancy(kFwd, sizeof(T), DP)) k_attn_fw
         }
         return;
     }
-    const int kvh = head / a.group, chunks = a.D * (int)sizeof(T) / 16;
+    const int kvh = head / a.group, chunks = a.D / 8;
     const char* kbase = reinterpret_cast<const char*>(static_cast<const T*>(a.k) + (long long)w.start * a.sk.token + kvh * a.sk.head);
     const char* vbase = reinterpret_cast<const char*>(static_cast<const T*>(a.v) + (long long)w.start * a.sv.token + kvh * a.sv.head);
     const uint32_t krow = (uint32_t)a.sk.token * sizeof(T), vrow = (uint32_t)a.sv.token * sizeof(T);
     const int keys = a.causal ? min(w.len, (w.tile + 1) * kFwdRows) : w.len;
-    const int tiles = (keys + kFwdKeys - 1) / kFwdKeys;
+    const int tiles = (keys + KEYS - 1) / KEYS;
     const uint32_t lds0 = lds_address(lds);
+    typename L::Load kload, vload;
     auto copy = [&](int j) {
-        const int j0 = j * kFwdKeys, last = min(w.len - 1 - j0, kFwdKeys - 1);
+        const int j0 = j * KEYS, last = min(w.len - 1 - j0, KEYS - 1);
         const uint32_t at = lds0 + (uint32_t)(j & 1) * (2 * TILE);
-        L::template copy<kFwdKeys, 4>(at, kbase + (long long)j0 * krow, krow, last, chunks, wave, lane);
-        L::template copy<kFwdKeys, 4>(at + TILE, vbase + (long long)j0 * vrow, vrow, last, chunks, wave, lane);
+        L::issue(kload, at, kbase + (long long)j0 * krow, krow, last, chunks, wave, lane);
+        L::issue(vload, at + TILE, vbase + (long long)j0 * vrow, vrow, last, chunks, wave, lane);
     };
     copy(0);
 
@@ -75,34 +78,35 @@ __global__ void __launch_bounds__(256, occupancy(kFwd, sizeof(T), DP)) k_attn_fw
     const int rlane = L::rows_lane(lane), clane = L::cols_lane(lane), half = L::row_of_half(lane), swap = L::cols_swap(lane);
     float m = -__builtin_inff(), mc = 0.f, l = 0.f;   // mc = m c, finite
     for (int j = 0; j < tiles; ++j) {
-        dma_wait();
+        L::commit(kload, lds + (j & 1) * (2 * TILE), wave, lane);
+        L::commit(vload, lds + (j & 1) * (2 * TILE) + TILE, wave, lane);
         __syncthreads();   // tile j is there; everyone is done with the other one
         if (j + 1 < tiles) copy(j + 1);
-        const int j0 = j * kFwdKeys;
+        const int j0 = j * KEYS;
         if (rows_left <= 0 || (a.causal && j0 > row0 + 31)) continue;   // nothing of this tile for this wave
         const char* kt = lds + (j & 1) * (2 * TILE) + rlane;
         const char* vt = lds + (j & 1) * (2 * TILE) + TILE + clane;
         // waves in a product go before waves in a softmax, whose vector work then
         // runs beside it (4 x 4096 tokens, 12 heads of 64: 251 -> 242 us)
         __builtin_amdgcn_s_setprio(1);
-        f32x16 s[2] = {};
+        f32x16 s[KB] = {};
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb) mma(L::rows(kt, 32 * kb, ks), q[ks], s[kb]);
+            for (int kb = 0; kb < KB; ++kb) mma(L::rows(kt, 32 * kb, ks), q[ks], s[kb]);
         __builtin_amdgcn_s_setprio(0);
         const int limit = a.causal ? min(w.len - 1, row) : w.len - 1;   // last key this query sees
-        const bool edge = j0 + kFwdKeys - 1 > (a.causal ? min(w.len - 1, row0) : w.len - 1);
+        const bool edge = j0 + KEYS - 1 > (a.causal ? min(w.len - 1, row0) : w.len - 1);
         if (edge) {
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb)
+            for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
                     if (j0 + 32 * kb + L::row_of(r) + half > limit) s[kb][r] = -__builtin_inff();
         }
         float top = s[0][0];
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
+        for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
             for (int r = 0; r < 16; ++r) top = fmaxf(top, s[kb][r]);
         top = both_max(top);
@@ -119,7 +123,7 @@ __global__ void __launch_bounds__(256, occupancy(kFwd, sizeof(T), DP)) k_attn_fw
         }
         float sum = 0.f;
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
+        for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 s[kb][r] = __builtin_amdgcn_exp2f(fmaf(s[kb][r], c, -mc));
@@ -128,7 +132,7 @@ __global__ void __launch_bounds__(256, occupancy(kFwd, sizeof(T), DP)) k_attn_fw
         l += sum;
         __builtin_amdgcn_s_setprio(2);
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
+        for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 Frag<T> p;
