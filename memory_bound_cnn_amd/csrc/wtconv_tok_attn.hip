@@ -20,21 +20,23 @@ Args args_of(const wtc_attn_desc* d, const void* q, const void* k, const void* v
 }
 
 // Splits of a key tile's queries.  With few key tiles (few heads of k and v, a
-// short pack) or long causal sequences, whose first tiles have twice the mean
-// tile's queries, one workgroup a tile leaves most of the chip waiting for the
-// longest: up to 16 of them share a tile until there are four workgroups for
-// each compute unit, eight when causal, with kLeast query tiles each at the
-// pack's mean length.  Measured (dk and dv with their join): causal 3 sequences
-// of 3500 to 8192 tokens, 16 heads on 4 of 128 channels, 1654 us unsplit, 991
-// in 4; 48 images of 49 to 1024 tokens, 6 heads of 64 channels (1440 tiles),
-// 138 us unsplit, 168 in 2.
-constexpr int kLeast = 4, kMostSplits = 16;
+// short pack), or causal ones, whose first have twice the mean tile's queries,
+// one workgroup a tile leaves most of the chip waiting for the longest: several
+// share it where there are fewer than kWanted tiles (twice as many causal
+// ones: 512 workgroups run at once), with kLeast query tiles each at the pack's
+// mean length.  Their sums cost 8 bytes written and read a channel and split.
+// Measured, dk and dv with their join: causal 3 sequences of 3500 to 8192
+// tokens, 16 heads on 4 of 128 channels (552 tiles), 843 us in 4, 795 in 2;
+// causal 4 of 2000 to 4096, 8 heads of 96 (800 tiles), 164 us whole, 198 in 2;
+// float32 32 of 196, 6 heads on 3 of 64 (192 tiles), 56 us whole, 53 in 2, 60
+// in 3.
+constexpr int kWanted = 512, kWantedCausal = 1100, kLeast = 6, kMostSplits = 16;
 int dkv_splits(const wtc_attn_desc* d) {
     if (d->T == 0 || d->n_seq == 0) return 1;
     const long long mean = (d->T + d->n_seq - 1) / d->n_seq, rows = d->dtype == WTC_BF16 ? 64 : 32;
-    const long long tiles = (mean + 127) / 128 * d->n_seq * d->Hk, wanted = d->causal ? 2048 : 1024;
+    const long long tiles = (mean + 127) / 128 * d->n_seq * d->Hk, wanted = d->causal ? kWantedCausal : kWanted;
     const long long steps = (mean + rows - 1) / rows * (d->Hq / d->Hk) / (d->causal ? 2 : 1);
-    long long s = (wanted + tiles - 1) / tiles;
+    long long s = (wanted + tiles / 2) / tiles;
     if (s > steps / kLeast) s = steps / kLeast;
     return (int)(s < 1 ? 1 : s > kMostSplits ? kMostSplits : s);
 }
