@@ -61,10 +61,10 @@ __global__ void __launch_bounds__(256, occupancy(kDq, sizeof(T), DP)) k_attn_dq(
     const uint32_t lds0 = lds_address(lds);
     typename L::Load kload, vload;
     auto copy = [&](int j) {
-        const int j0 = j * KEYS, last = min(w.len - 1 - j0, KEYS - 1);
+        const int j0 = j * KEYS, end = min(w.len - 1 - j0, KEYS - 1);
         const uint32_t at = lds0 + (uint32_t)(j & 1) * (2 * TILE);
-        L::issue(kload, at, kbase + (long long)j0 * krow, krow, last, chunks, wave, lane);
-        L::issue(vload, at + TILE, vbase + (long long)j0 * vrow, vrow, last, chunks, wave, lane);
+        L::issue(kload, at, kbase + (long long)j0 * krow, krow, end, chunks, wave, lane);
+        L::issue(vload, at + TILE, vbase + (long long)j0 * vrow, vrow, end, chunks, wave, lane);
     };
     copy(0);
 
@@ -86,7 +86,10 @@ __global__ void __launch_bounds__(256, occupancy(kDq, sizeof(T), DP)) k_attn_dq(
     }
     const float lse2 = a.lse[stat] * kLog2e;
     const int rlane = L::rows_lane(lane), clane = L::cols_lane(lane), half = L::row_of_half(lane), swap = L::cols_swap(lane);
-    f32x16 acc[DB] = {};
+    const int last = a.causal ? min(w.len - 1, row0 + 31) : w.len - 1;   // last key that any of the wave's queries sees
+    f32x16 acc[DB] = {}, minus;   // dP starts from -delta
+#pragma unroll
+    for (int r = 0; r < 16; ++r) minus[r] = -delta;
     for (int j = 0; j < tiles; ++j) {
         L::commit(kload, lds + (j & 1) * (2 * TILE), wave, lane);
         L::commit(vload, lds + (j & 1) * (2 * TILE) + TILE, wave, lane);
@@ -100,7 +103,8 @@ __global__ void __launch_bounds__(256, occupancy(kDq, sizeof(T), DP)) k_attn_dq(
         const bool edge = j0 + KEYS - 1 > (a.causal ? min(w.len - 1, row0) : w.len - 1);
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
-            f32x16 s = {}, dp = {};
+            if (kb > 0 && j0 + 32 * kb > last) break;   // no pair in this block
+            f32x16 s = {}, dp = minus;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 mma(L::rows(kt, 32 * kb, ks), q[ks], s);
@@ -109,7 +113,7 @@ __global__ void __launch_bounds__(256, occupancy(kDq, sizeof(T), DP)) k_attn_dq(
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 const float p = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse2));
-                s[r] = p * (dp[r] - delta);
+                s[r] = p * dp[r];
             }
             if (edge) {
 #pragma unroll
