@@ -263,6 +263,14 @@ struct Tile {
     static __device__ __forceinline__ int row_of_half(int lane) { return place(4) * (lane >> 5); }
 };
 
+// v, but what is derived from it is not kept in registers over a loop: a
+// register too many there is stored away, and its reload waits for every copy
+// that is on its way.
+__device__ __forceinline__ int anew(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
 __device__ __forceinline__ uint32_t lds_address(const void* p) { return (uint32_t)(uintptr_t)(lds_char*)p; }
 
 // Terms 16 ks + 8 h .. + 7 of one row in device memory (D channels, the others
@@ -356,6 +364,7 @@ struct Args {
     const void *q, *k, *v, *o, *g;
     const int* cu;
     void *out, *dq, *dk, *dv;
+    void* low;   // what was rounded off the output, [T, Hq, D] bfloat16, or null
     float *lse, *delta, *parts;
     int splits;   // of a key tile's queries in the backward pass; their sums in parts when there are several
     int T, n_seq, Hq, Hk, group, D, causal;

@@ -27,11 +27,11 @@ int launch_dropout(long long n, int dtype, unsigned least, const void* x, const 
                    const unsigned long long* rng, void* y, void* stream);
 
 int launch_attn_forward(const wtc_attn_desc* d, const void* q, const void* k, const void* v, const int* cu, void* out,
-                        float* lse, void* stream);
+                        float* lse, void* out_low, void* stream);
 // workspace: rowsum(dout * out) [Hq, T], and the partial sums of dk and dv
 size_t attn_backward_bytes(const wtc_attn_desc* d);
 int launch_attn_backward(const wtc_attn_desc* d, const void* q, const void* k, const void* v, const void* out,
-                         const float* lse, const void* dout, const int* cu, void* dq, void* dk, void* dv,
+                         const float* lse, const void* out_low, const void* dout, const int* cu, void* dq, void* dk, void* dv,
                          void* workspace, void* stream);
 
 }  // namespace wtc

@@ -58,6 +58,11 @@ int check_strides(const wtc_attn_desc* d, const wtc_attn_strides& s, const void*
     return s.token > WTC_ATTN_MAX_TOKEN_STRIDE ? WTC_ESHAPE : WTC_OK;
 }
 
+int check_low(const wtc_attn_desc* d, const void* low) {
+    if (!low) return WTC_OK;
+    return d->dtype != WTC_BF16 ? WTC_EDTYPE : aligned(low, 16) ? WTC_OK : WTC_EINVAL;
+}
+
 int first_error(std::initializer_list<int> all) {
     for (int s : all)
         if (s != WTC_OK) return s;
@@ -120,15 +125,15 @@ int wtconv_dropout(long long n, int dtype, double p, const void* x, const void* 
 }
 
 int wtconv_attention_forward(const wtc_attn_desc* d, const void* q, const void* k, const void* v,
-                             const int* cu_seqlens, void* out, float* lse, void* stream) {
+                             const int* cu_seqlens, void* out, float* lse, void* out_low, void* stream) {
     const int st = check_attn(d);
     if (st != WTC_OK) return st;
     if (d->T == 0) return WTC_OK;
     if (!q || !k || !v || !cu_seqlens || !out) return WTC_EINVAL;
     const int bad = first_error({check_strides(d, d->q, q), check_strides(d, d->k, k), check_strides(d, d->v, v),
-                                 check_strides(d, d->o, out)});
+                                 check_strides(d, d->o, out), check_low(d, out_low)});
     if (bad != WTC_OK) return bad;
-    return launch_attn_forward(d, q, k, v, cu_seqlens, out, lse, stream);
+    return launch_attn_forward(d, q, k, v, cu_seqlens, out, lse, out_low, stream);
 }
 
 size_t wtconv_attention_backward_workspace(const wtc_attn_desc* d) {
@@ -137,7 +142,7 @@ size_t wtconv_attention_backward_workspace(const wtc_attn_desc* d) {
 }
 
 int wtconv_attention_backward(const wtc_attn_desc* d, const void* q, const void* k, const void* v, const void* out,
-                              const float* lse, const void* dout, const int* cu_seqlens, void* dq, void* dk, void* dv,
+                              const float* lse, const void* out_low, const void* dout, const int* cu_seqlens, void* dq, void* dk, void* dv,
                               void* workspace, size_t workspace_bytes, void* stream) {
     const int st = check_attn(d);
     if (st != WTC_OK) return st;
@@ -145,10 +150,10 @@ int wtconv_attention_backward(const wtc_attn_desc* d, const void* q, const void*
     if (!q || !k || !v || !out || !lse || !dout || !cu_seqlens || !dq || !dk || !dv) return WTC_EINVAL;
     const int bad = first_error({check_strides(d, d->q, q), check_strides(d, d->k, k), check_strides(d, d->v, v),
                                  check_strides(d, d->o, out), check_strides(d, d->g, dout), check_strides(d, d->dq, dq),
-                                 check_strides(d, d->dk, dk), check_strides(d, d->dv, dv)});
+                                 check_strides(d, d->dk, dk), check_strides(d, d->dv, dv), check_low(d, out_low)});
     if (bad != WTC_OK) return bad;
     if (!workspace || workspace_bytes < wtconv_attention_backward_workspace(d)) return WTC_EWORKSPACE;
-    return launch_attn_backward(d, q, k, v, out, lse, dout, cu_seqlens, dq, dk, dv, workspace, stream);
+    return launch_attn_backward(d, q, k, v, out, lse, out_low, dout, cu_seqlens, dq, dk, dv, workspace, stream);
 }
 
 }  // extern "C"

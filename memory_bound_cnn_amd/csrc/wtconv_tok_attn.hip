@@ -51,20 +51,22 @@ size_t attn_backward_bytes(const wtc_attn_desc* d) {
 }
 
 int launch_attn_forward(const wtc_attn_desc* d, const void* q, const void* k, const void* v, const int* cu, void* out,
-                        float* lse, void* stream) {
+                        float* lse, void* out_low, void* stream) {
     attn::Args a = attn::args_of(d, q, k, v, cu);
     a.out = out;
     a.lse = lse;
+    a.low = out_low;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     return d->dtype == WTC_BF16 ? attn::fwd_bf16(a, st) : attn::fwd_fp32(a, st);
 }
 
 int launch_attn_backward(const wtc_attn_desc* d, const void* q, const void* k, const void* v, const void* out,
-                         const float* lse, const void* dout, const int* cu, void* dq, void* dk, void* dv,
+                         const float* lse, const void* out_low, const void* dout, const int* cu, void* dq, void* dk, void* dv,
                          void* workspace, void* stream) {
     attn::Args a = attn::args_of(d, q, k, v, cu);
     a.o = out;
     a.g = dout;
+    a.low = const_cast<void*>(out_low);
     a.lse = const_cast<float*>(lse);
     a.delta = static_cast<float*>(workspace);
     a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + attn::delta_bytes(d));

@@ -81,7 +81,11 @@ __global__ void __launch_bounds__(256, occupancy(kDq, sizeof(T), DP)) k_attn_dq(
             q[ks] = row_terms(qrow, ks, a.D, lane, 1.f);
             g[ks] = row_terms(grow, ks, a.D, lane, 1.f);
         }
-        delta = both_sum(half_dot<T, KS>(grow, orow, a.D, lane));
+        delta = half_dot<T, KS>(grow, orow, a.D, lane);
+        // with the bits that were rounded off out: 8 of them alone move dS by as much as its own rounding
+        if (sizeof(T) == 2 && a.low)
+            delta += half_dot<T, KS>(grow, static_cast<const T*>(a.low) + (t * a.Hq + head) * a.D, a.D, lane);
+        delta = both_sum(delta);
         if (live && lane < 32) a.delta[stat] = delta;   // for the other kernel
     }
     const float lse2 = a.lse[stat] * kLog2e;
@@ -140,8 +144,11 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
     using L = Tile<T, DP, ROWS>;
     constexpr int TILE = L::kBytes;
     __shared__ __align__(16) char lds[4 * TILE];   // 2 x (Q tile, dO tile)
-    __shared__ __align__(16) float stats[2][2][ROWS];   // 2 x what S and dP of the tile's queries start from
+    __shared__ __align__(16) float stats[2][2][ROWS];   // 2 x -lse log2(e), over c where S starts from it, and -delta of the tile's queries
     constexpr bool HOLD = kDkvHoldV<T, DP>;
+    // S starts from -lse log2(e) / c and dP from -delta, which saves their subtraction.  Not S in
+    // float32: it is then rounded at lse's size (dk and dv 2.5 times the error)
+    constexpr bool START = sizeof(T) == 2;
     __shared__ Frag<T> held[HOLD ? 4 * KS * 64 : 1];   // V of the four waves
     static_assert(4 * TILE + 4 * ROWS * 4 + (HOLD ? 4 * KS * 64 * (int)sizeof(Frag<T>) : 0) <= 160 * 1024, "shared memory");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -204,7 +211,7 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
             const int r = threadIdx.x % ROWS / 32 * 32 + L::place(threadIdx.x % 32);
             const long long t = (long long)head * a.T + w.start + j0 + min(r, last);
             // queries past the end: an infinite lse leaves nothing of them
-            stat = threadIdx.x < ROWS ? (r <= last ? a.lse[t] * kLog2e : __builtin_inff()) * -inv_c : -a.delta[t];
+            stat = threadIdx.x < ROWS ? (r <= last ? a.lse[t] * kLog2e : __builtin_inff()) * (START ? -inv_c : -1.f) : -a.delta[t];
         }
         j0 += ROWS;
         if (j0 >= w.len) {
@@ -230,7 +237,7 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
                 vf[ks] = row_terms(vrow, ks, a.D, lane, 1.f);
         }
     }
-    const int rlane = L::rows_lane(lane), clane = L::cols_lane(lane), half = L::row_of_half(lane), swap = L::cols_swap(lane);
+    const int rlane = L::rows_lane(lane), clane = L::cols_lane(lane), swap = L::cols_swap(lane);
     for (int i = begin; i < end; ++i) {
         if (threadIdx.x < 2 * ROWS) stats[i & 1][threadIdx.x / ROWS][threadIdx.x % ROWS] = stat;
         L::commit(qload, lds + (i & 1) * (2 * TILE), wave, lane);
@@ -245,11 +252,14 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
         const bool edge = a.causal && at < key0 + 31;   // some of the tile's queries come before some of the keys
 #pragma unroll 1
         for (int qb = 0; qb < ROWS / 32; ++qb, qt += L::row_at(32), qc += L::row_at(32)) {
-            // the products start from -lse log2(e) / c and -delta
             f32x16 s, dp;
             const float* st = &stats[i & 1][0][32 * qb + 4 * (lane >> 5)];
+            if constexpr (START) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) s[r] = st[8 * (r >> 2) + (r & 3)];
+                for (int r = 0; r < 16; ++r) s[r] = st[8 * (r >> 2) + (r & 3)];
+            } else {
+                s = f32x16{};
+            }
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) mma(L::rows(qt, 0, ks), kf[ks], s);
             __builtin_amdgcn_sched_barrier(0);
@@ -260,13 +270,14 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                s[r] = __builtin_amdgcn_exp2f(s[r] * c);
+                s[r] = __builtin_amdgcn_exp2f(START ? s[r] * c : fmaf(s[r], c, st[8 * (r >> 2) + (r & 3)]));
                 dp[r] *= s[r];
             }
             if (edge) {
+                const int l = anew(lane), seen = key0 + (l & 31) - at - 32 * qb - L::row_of_half(l);
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    if (at + 32 * qb + L::row_of(r) + half < key) s[r] = dp[r] = 0.f;
+                    if (L::row_of(r) < seen) s[r] = dp[r] = 0.f;
             }
 #pragma unroll
             for (int t = 0; t < 2; ++t) {

@@ -147,6 +147,17 @@ __global__ void __launch_bounds__(256, occupancy(kFwd, sizeof(T), DP)) k_attn_fw
     const float inv = 1.f / l;
 #pragma unroll
     for (int db = 0; db < DB; ++db) store_tile(out, db, a.D, lane, o[db], inv);
+    if constexpr (sizeof(T) == 2) {
+        if (a.low) {
+            T* low = static_cast<T*>(a.low) + ((long long)(w.start + row) * a.Hq + head) * a.D;
+#pragma unroll
+            for (int db = 0; db < DB; ++db) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) o[db][r] = o[db][r] * inv - as_stored<T>(o[db][r] * inv);
+                store_tile(low, db, a.D, lane, o[db], 1.f);
+            }
+        }
+    }
     if (lse && lane < 32) *lse = (mc + log2f(l)) * kLn2;
 }
 

@@ -257,22 +257,25 @@ void attn_check(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor&
     TORCH_CHECK_VALUE(cu.dim() == 1 && cu.size(0) >= 1, "cu_seqlens must be [n + 1]");
     check(cu, "cu_seqlens", at::kInt, q, cu.sizes());
 }
-std::tuple<Tensor, Tensor> attn_forward(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& cu,
+struct AttnOut {
+    Tensor o, lse, low;   // lse, low: kept for the backward pass (low: what was rounded off o, bfloat16)
+};
+AttnOut attn_forward(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& cu,
                                         const Setting& s, bool keep) {
     wtc_attn_desc d = attn_desc(q, k, v, cu, s);
-    const Tensor o = empty(q.sizes(), q), lse = keep ? empty({q.size(1), q.size(0)}, q, at::kFloat) : Tensor();
-    d.o = strides(o);
+    const AttnOut r = {empty(q.sizes(), q), keep ? empty({q.size(1), q.size(0)}, q, at::kFloat) : Tensor(),
+                       keep && q.scalar_type() == at::kBFloat16 ? empty(q.sizes(), q) : Tensor()};
+    d.o = strides(r.o);
     const On on(q);
-    raise_on(wtconv_attention_forward(&d, in(q), in(k), in(v), in_as<int>(cu), out(o), static_cast<float*>(out(lse)),
-                                      on.stream),
+    raise_on(wtconv_attention_forward(&d, in(q), in(k), in(v), in_as<int>(cu), out(r.o), static_cast<float*>(out(r.lse)),
+                                      out(r.low), on.stream),
              "wtconv_attention_forward");
-    return {o, lse};
+    return r;
 }
-void attn_backward(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& o, const Tensor& lse,
-                   const Tensor& g, const Tensor& cu, const Setting& s, const Tensor& dq, const Tensor& dk,
+void attn_backward(const Tensor& q, const Tensor& k, const Tensor& v, const AttnOut& f, const Tensor& g, const Tensor& cu, const Setting& s, const Tensor& dq, const Tensor& dk,
                    const Tensor& dv) {
     wtc_attn_desc d = attn_desc(q, k, v, cu, s);
-    d.o = strides(o);
+    d.o = strides(f.o);
     d.g = strides(g);
     d.dq = strides(dq);
     d.dk = strides(dk);
@@ -280,7 +283,7 @@ void attn_backward(const Tensor& q, const Tensor& k, const Tensor& v, const Tens
     const size_t bytes = wtconv_attention_backward_workspace(&d);
     const Tensor ws = workspace(bytes, q);
     const On on(q);
-    raise_on(wtconv_attention_backward(&d, in(q), in(k), in(v), in(o), in_as<float>(lse), in(g), in_as<int>(cu),
+    raise_on(wtconv_attention_backward(&d, in(q), in(k), in(v), in(f.o), in_as<float>(f.lse), in(f.low), in(g), in_as<int>(cu),
                                        out(dq), out(dk), out(dv), out(ws), bytes, on.stream),
              "wtconv_attention_backward");
 }
@@ -290,17 +293,17 @@ struct Attention : torch::autograd::Function<Attention> {
     static Tensor forward(AutogradContext* ctx, const Tensor& q0, const Tensor& k0, const Tensor& v0, const Tensor& cu,
                           bool causal, double scale) {
         const Tensor q = heads(q0), k = heads(k0), v = heads(v0);
-        const auto [o, lse] = attn_forward(q, k, v, cu, {causal, scale}, true);
-        ctx->save_for_backward({q, k, v, o, lse, cu});
+        const AttnOut f = attn_forward(q, k, v, cu, {causal, scale}, true);
+        ctx->save_for_backward({q, k, v, f.o, f.lse, f.low, cu});
         ctx->saved_data["causal"] = causal;
         ctx->saved_data["scale"] = scale;
-        return o;
+        return f.o;
     }
     static variable_list backward(AutogradContext* ctx, const variable_list& g) {
         once(g);
         const variable_list s = ctx->get_saved_variables();
         const Tensor dq = empty(s[0].sizes(), s[0]), dk = empty(s[1].sizes(), s[0]), dv = empty(s[2].sizes(), s[0]);
-        attn_backward(s[0], s[1], s[2], s[3], s[4], heads(g[0]), s[5],
+        attn_backward(s[0], s[1], s[2], {s[3], s[4], s[5]}, heads(g[0]), s[6],
                       {ctx->saved_data["causal"].toBool(), ctx->saved_data["scale"].toDouble()}, dq, dk, dv);
         return {dq, dk, dv, Tensor(), Tensor(), Tensor()};
     }
@@ -315,7 +318,7 @@ Tensor attention(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor
     attn_check(q, k, v, cu);
     const double s = scale_of(scale, q);
     if (wants_grad(q, k, v)) return Attention::apply(q, k, v, cu, causal, s);
-    return std::get<0>(attn_forward(heads(q), heads(k), heads(v), cu, {causal, s}, false));
+    return attn_forward(heads(q), heads(k), heads(v), cu, {causal, s}, false).o;
 }
 
 struct RotaryAttention : torch::autograd::Function<RotaryAttention> {
@@ -326,16 +329,16 @@ struct RotaryAttention : torch::autograd::Function<RotaryAttention> {
                           bool causal, double scale) {
         const Tensor qkv = heads(qkv0), qk = empty({qkv.size(0), Hq + Hk, qkv.size(2)}, qkv);
         rotary_run(qkv.narrow(1, 0, Hq + Hk), qk, positions, inv_freq, sections, interleaved, false);
-        const auto [o, lse] = attn_forward(qk.narrow(1, 0, Hq), qk.narrow(1, Hq, Hk), qkv.narrow(1, Hq + Hk, Hk), cu,
-                                           {causal, scale}, true);
-        ctx->save_for_backward({qkv, qk, o, lse, cu, positions, inv_freq});
+        const AttnOut f = attn_forward(qk.narrow(1, 0, Hq), qk.narrow(1, Hq, Hk), qkv.narrow(1, Hq + Hk, Hk), cu,
+                                       {causal, scale}, true);
+        ctx->save_for_backward({qkv, qk, f.o, f.lse, f.low, cu, positions, inv_freq});
         ctx->saved_data["Hq"] = Hq;
         ctx->saved_data["Hk"] = Hk;
         ctx->saved_data["sections"] = sections;
         ctx->saved_data["interleaved"] = interleaved;
         ctx->saved_data["causal"] = causal;
         ctx->saved_data["scale"] = scale;
-        return o;
+        return f.o;
     }
     static variable_list backward(AutogradContext* ctx, const variable_list& g) {
         once(g);
@@ -344,10 +347,10 @@ struct RotaryAttention : torch::autograd::Function<RotaryAttention> {
         const int64_t Hq = at["Hq"].toInt(), Hk = at["Hk"].toInt();
         const Tensor &qkv = s[0], &qk = s[1];
         const Tensor d = empty(qkv.sizes(), qkv), dqk = d.narrow(1, 0, Hq + Hk);
-        attn_backward(qk.narrow(1, 0, Hq), qk.narrow(1, Hq, Hk), qkv.narrow(1, Hq + Hk, Hk), s[2], s[3], heads(g[0]), s[4],
+        attn_backward(qk.narrow(1, 0, Hq), qk.narrow(1, Hq, Hk), qkv.narrow(1, Hq + Hk, Hk), {s[2], s[3], s[4]}, heads(g[0]), s[5],
                       {at["causal"].toBool(), at["scale"].toDouble()}, d.narrow(1, 0, Hq), d.narrow(1, Hq, Hk),
                       d.narrow(1, Hq + Hk, Hk));
-        rotary_run(dqk, dqk, s[5], s[6], at["sections"].toIntVector(), at["interleaved"].toBool(), true);
+        rotary_run(dqk, dqk, s[6], s[7], at["sections"].toIntVector(), at["interleaved"].toBool(), true);
         variable_list r(10);
         r[0] = d;
         return r;

@@ -58,8 +58,8 @@ def _load():
                 ("wtconv_rms_norm_backward", [_P] * 9 + [_SZ, _P]),
                 ("wtconv_rotary", [_P] * 6),
                 ("wtconv_dropout", [_LL, _I, ctypes.c_double] + [_P] * 5),
-                ("wtconv_attention_forward", [_P] * 8),
-                ("wtconv_attention_backward", [_P] * 12 + [_SZ, _P])):
+                ("wtconv_attention_forward", [_P] * 9),
+                ("wtconv_attention_backward", [_P] * 13 + [_SZ, _P])):
             f = getattr(lib, name)
             f.restype, f.argtypes = _I, args
         for name in ("wtconv_rms_norm_backward_workspace", "wtconv_attention_backward_workspace"):
@@ -216,30 +216,35 @@ def _attn_desc(q, k, v, cu_seqlens, causal, scale):
     return d
 
 
-def wtconv_attention_forward(q, k, v, cu_seqlens, causal=False, scale=None, want_lse=False, out=None):
+def wtconv_attention_forward(q, k, v, cu_seqlens, causal=False, scale=None, want_lse=False, out=None, out_low=None):
     """(out, lse) for q [T, Hq, D], k and v [T, Hk, D]; lse [Hq, T] float32 or
-    None.  scale: 1 / sqrt(D) unless given."""
+    None.  scale: 1 / sqrt(D) unless given.  out_low: a contiguous bfloat16
+    tensor of q's shape for what is rounded off out, or None."""
     d = _attn_desc(q, k, v, cu_seqlens, causal, scale)
     dev = q.device
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=dev)
     else:
         _check(out, "out", q.dtype, dev, q.shape)
+    if out_low is not None:
+        _check(out_low, "out_low", torch.bfloat16, dev, q.shape, True)
     lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=dev) if want_lse else None
     d.o = out.stride()[:2]
     _call("wtconv_attention_forward", dev, ctypes.addressof(d), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-          cu_seqlens.data_ptr(), out.data_ptr(), _ptr(lse))
+          cu_seqlens.data_ptr(), out.data_ptr(), _ptr(lse), _ptr(out_low))
     return out, lse
 
 
 def wtconv_attention_backward(q, k, v, out, lse, dout, cu_seqlens, causal=False, scale=None, grads=None,
-                              workspace=None):
-    """(dq, dk, dv).  grads: the tensors to write them to (q's, k's and v's
+                              workspace=None, out_low=None):
+    """(dq, dk, dv).  out_low: as the forward pass left it, or None.  grads: the tensors to write them to (q's, k's and v's
     shapes, any strides that the library takes), or None."""
     d = _attn_desc(q, k, v, cu_seqlens, causal, scale)
     dev = q.device
     _check(out, "out", q.dtype, dev, q.shape)
     _check(dout, "dout", q.dtype, dev, q.shape)
+    if out_low is not None:
+        _check(out_low, "out_low", torch.bfloat16, dev, q.shape, True)
     _check(lse, "lse", torch.float32, dev, (q.shape[1], q.shape[0]), True)
     if grads is None:
         grads = tuple(torch.empty(t.shape, dtype=q.dtype, device=dev) for t in (q, k, v))
@@ -249,6 +254,6 @@ def wtconv_attention_backward(q, k, v, out, lse, dout, cu_seqlens, causal=False,
     d.o, d.g, d.dq, d.dk, d.dv = (t.stride()[:2] for t in (out, dout, dq, dk, dv))
     ws, size = _workspace(_load().wtconv_attention_backward_workspace(ctypes.addressof(d)), dev, workspace)
     _call("wtconv_attention_backward", dev, ctypes.addressof(d), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-          out.data_ptr(), lse.data_ptr(), dout.data_ptr(), cu_seqlens.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+          out.data_ptr(), lse.data_ptr(), _ptr(out_low), dout.data_ptr(), cu_seqlens.data_ptr(), dq.data_ptr(), dk.data_ptr(),
           dv.data_ptr(), _ptr(ws), size)
     return dq, dk, dv

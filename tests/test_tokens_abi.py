@@ -129,8 +129,8 @@ ATTN_BAD = [
 @pytest.mark.parametrize("kw,status", ATTN_BAD)
 def test_attention_rejects(kw, status):
     lib, d = tb._load(), attn(**kw)
-    assert lib.wtconv_attention_forward(ref(d), P, P, P, P, P, P, None) == status
-    assert lib.wtconv_attention_backward(ref(d), P, P, P, P, P, P, P, P, P, P, P, 1 << 62, None) == status
+    assert lib.wtconv_attention_forward(ref(d), P, P, P, P, P, P, None, None) == status
+    assert lib.wtconv_attention_backward(ref(d), P, P, P, P, P, None, P, P, P, P, P, P, 1 << 62, None) == status
 
 
 def test_attention_rejects_pointers_and_workspaces():
@@ -138,23 +138,27 @@ def test_attention_rejects_pointers_and_workspaces():
     for at in range(5):
         args = [P] * 6
         args[at] = None
-        assert lib.wtconv_attention_forward(ref(d), *args, None) == EINVAL
+        assert lib.wtconv_attention_forward(ref(d), *args, None, None) == EINVAL
         if at != 3:    # cu_seqlens is int32
             args[at] = ODD
-            assert lib.wtconv_attention_forward(ref(d), *args, None) == EINVAL
+            assert lib.wtconv_attention_forward(ref(d), *args, None, None) == EINVAL
+    assert lib.wtconv_attention_forward(ref(d), *[P] * 6, ODD, None) == EINVAL
+    assert lib.wtconv_attention_forward(ref(attn(dtype=0)), *[P] * 6, P, None) == EDTYPE   # nothing is rounded off
     need = lib.wtconv_attention_backward_workspace(ref(d))
     assert need == 256    # 4 heads x 5 tokens x 4 bytes, to the next 256
-    for at in range(10):
-        args = [P] * 10
+    for at in range(11):
+        if at == 5:    # out_low may be NULL
+            continue
+        args = [P] * 11
         args[at] = None
         assert lib.wtconv_attention_backward(ref(d), *args, P, need, None) == EINVAL
-    assert lib.wtconv_attention_backward(ref(d), *[P] * 10, P, need - 1, None) == EWORKSPACE
-    assert lib.wtconv_attention_backward(ref(d), *[P] * 10, None, need, None) == EWORKSPACE
+    assert lib.wtconv_attention_backward(ref(d), *[P] * 11, P, need - 1, None) == EWORKSPACE
+    assert lib.wtconv_attention_backward(ref(d), *[P] * 11, None, need, None) == EWORKSPACE
     for name in ("g", "dq", "dk", "dv"):
         bad = attn(**{name: (256, 63)})
-        assert lib.wtconv_attention_backward(ref(bad), *[P] * 10, P, need, None) == EINVAL
-    assert lib.wtconv_attention_forward(None, P, P, P, P, P, P, None) == EINVAL
-    assert lib.wtconv_attention_forward(ref(attn(T=0)), None, None, None, None, None, None, None) == binding.WTC_OK
+        assert lib.wtconv_attention_backward(ref(bad), *[P] * 11, P, need, None) == EINVAL
+    assert lib.wtconv_attention_forward(None, P, P, P, P, P, P, None, None) == EINVAL
+    assert lib.wtconv_attention_forward(ref(attn(T=0)), *[None] * 8) == binding.WTC_OK
 
 
 def test_python_entry_points_refuse_host_tensors():
