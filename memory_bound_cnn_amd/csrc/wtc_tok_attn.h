@@ -330,25 +330,44 @@ __device__ __forceinline__ float both_sum(float v) {
     return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
 }
 
-// Registers 4 g .. 4 g + 3 of the result tile `db` of a transposed output:
-// channels 32 db + 8 g + 4 h .. + 3 of the lane's row.
-template <typename T>
-__device__ __forceinline__ void store4(T* row, int db, int g, int D, int lane, float a, float b, float c, float d) {
-    const int at = 32 * db + 8 * g + 4 * (lane >> 5);
-    if (at >= D) return;
-    if constexpr (sizeof(T) == 2) {
-        *reinterpret_cast<u32x2*>(row + at) = u32x2{bf16x2_rne(a, b), bf16x2_rne(c, d)};
-    } else {
-        *reinterpret_cast<f32x4*>(row + at) = f32x4{a, b, c, d};
+// Stores a wave's 32 rows from the result tiles of a transposed output (lane:
+// row lane % 32, channels 32 db + 8 (r / 4) + 4 h + r % 4), times `factor`:
+// rows 0 .. rows - 1 of D channels, `stride` elements apart.  They pass through
+// shared memory, a place of the wave's own (`at`, kRowsScratch bytes that
+// nothing else uses now), so that a store has whole rows of 16-byte chunks
+// instead of 8 bytes of 32 rows each.
+template <typename T, int DP>
+constexpr int kScratchRow = DP * (int)sizeof(T) + 16;   // 16 bytes more: rows begin in different banks
+template <typename T, int DP>
+constexpr int kRowsScratch = 32 * kScratchRow<T, DP>;
+
+template <typename T, int DP>
+__device__ __forceinline__ void store_rows(char* at, T* out, long long stride, int rows, int D, int lane,
+                                           const f32x16 (&c)[DP / 32], float factor) {
+    constexpr int ROW = kScratchRow<T, DP>, CH = DP * (int)sizeof(T) / 16;
+    asm volatile("" ::: "memory");
+    char* p = at + (lane & 31) * ROW + (lane >> 5) * 4 * (int)sizeof(T);
+#pragma unroll
+    for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const f32x4 v = f32x4{c[db][4 * g], c[db][4 * g + 1], c[db][4 * g + 2], c[db][4 * g + 3]} * factor;
+            char* to = p + (32 * db + 8 * g) * (int)sizeof(T);
+            if constexpr (sizeof(T) == 2)
+                *reinterpret_cast<u32x2*>(to) = u32x2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
+            else
+                *reinterpret_cast<f32x4*>(to) = v;
+        }
+    asm volatile("" ::: "memory");   // a wave's own accesses to shared memory stay in order
+#pragma unroll
+    for (int i = 0; i < 32 * CH / 64; ++i) {
+        const int u = 64 * i + lane, r = u / CH, k = u % CH;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(at + r * ROW + 16 * k);
+        if (r < rows && k * kVec<T> < D) *reinterpret_cast<u32x4*>(out + r * stride + k * kVec<T>) = v;
     }
 }
-template <typename T>
-__device__ __forceinline__ void store_tile(T* row, int db, int D, int lane, const f32x16& c, float factor) {
-#pragma unroll
-    for (int g = 0; g < 4; ++g)
-        store4(row, db, g, D, lane, c[4 * g] * factor, c[4 * g + 1] * factor, c[4 * g + 2] * factor,
-               c[4 * g + 3] * factor);
-}
+
+constexpr int max_of(int a, int b) { return a > b ? a : b; }
 
 // Workgroups (of four waves, one on each vector unit) that the registers of a
 // compute unit hold at least.

@@ -42,14 +42,13 @@ __global__ void __launch_bounds__(256, occupancy(kDq, sizeof(T), DP)) k_attn_dq(
     const int row0 = w.tile * kDqRows + wave * 32, row = row0 + (lane & 31);
     const int rows_left = w.len - row0;
     const bool live = row < w.len;
-    T* dq = static_cast<T*>(a.dq) + (long long)(w.start + row) * a.sdq.token + head * a.sdq.head;
+    T* dq = static_cast<T*>(a.dq) + (long long)(w.start + row0) * a.sdq.token + head * a.sdq.head;
+    char* scratch = lds + wave * kRowsScratch<T, DP>;
+    static_assert(4 * kRowsScratch<T, DP> <= 4 * TILE, "the tiles' place serves for storing");
     const long long stat = (long long)head * a.T + w.start + min(row, w.len - 1);
     if (w.pad) {
-        if (live) {
-            f32x16 zero = {};
-#pragma unroll
-            for (int db = 0; db < DB; ++db) store_tile(dq, db, a.D, lane, zero, 0.f);
-        }
+        const f32x16 zero[DB] = {};
+        store_rows<T, DP>(scratch, dq, a.sdq.token, rows_left, a.D, lane, zero, 0.f);
         return;
     }
     const int kvh = head / a.group, chunks = a.D / 8;
@@ -133,9 +132,8 @@ __global__ void __launch_bounds__(256, occupancy(kDq, sizeof(T), DP)) k_attn_dq(
             }
         }
     }
-    if (!live) return;
-#pragma unroll
-    for (int db = 0; db < DB; ++db) store_tile(dq, db, a.D, lane, acc[db], a.scale);
+    __syncthreads();   // everyone is done with the tiles
+    if (rows_left > 0) store_rows<T, DP>(scratch, dq, a.sdq.token, rows_left, a.D, lane, acc, a.scale);
 }
 
 template <typename T, int DP>
@@ -143,14 +141,14 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
     constexpr int ROWS = kDkvRows<T, DP>, KS = DP / 16, DB = DP / 32;
     using L = Tile<T, DP, ROWS>;
     constexpr int TILE = L::kBytes;
-    __shared__ __align__(16) char lds[4 * TILE];   // 2 x (Q tile, dO tile)
-    __shared__ __align__(16) float stats[2][2][ROWS];   // 2 x -lse log2(e), over c where S starts from it, and -delta of the tile's queries
     constexpr bool HOLD = kDkvHoldV<T, DP>;
+    constexpr int LDS = max_of(4 * TILE + (HOLD ? 4 * KS * 64 * (int)sizeof(Frag<T>) : 0), 4 * kRowsScratch<float, DP>);
+    __shared__ __align__(16) char lds[LDS];   // 2 x (Q tile, dO tile), then V of the four waves
+    __shared__ __align__(16) float stats[2][2][ROWS];   // 2 x -lse log2(e), over c where S starts from it, and -delta of the tile's queries
     // S starts from -lse log2(e) / c and dP from -delta, which saves their subtraction.  Not S in
     // float32: it is then rounded at lse's size (dk and dv 2.5 times the error)
     constexpr bool START = sizeof(T) == 2;
-    __shared__ Frag<T> held[HOLD ? 4 * KS * 64 : 1];   // V of the four waves
-    static_assert(4 * TILE + 4 * ROWS * 4 + (HOLD ? 4 * KS * 64 * (int)sizeof(Frag<T>) : 0) <= 160 * 1024, "shared memory");
+    static_assert(LDS + 4 * ROWS * 4 <= 160 * 1024, "shared memory");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int kvh = blockIdx.x % a.Hk, split = blockIdx.x / a.Hk % a.splits;
     const Work w = find_work<kDkvKeys, false>(a, blockIdx.x / a.Hk / a.splits, lane);
@@ -159,27 +157,24 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
     const int keys_left = w.len - key0;
     const bool live = key < w.len;
     f32x16 ak[DB] = {}, av[DB] = {};
-    auto store = [&] {
-        if (!live) return;
-        const long long t = w.start + key;
+    auto store = [&] {   // no tile is read any more
+        if (keys_left <= 0) return;
+        const long long t = w.start + key0;
         if (a.splits == 1) {
-            T* dk = static_cast<T*>(a.dk) + t * a.sdk.token + kvh * a.sdk.head;
-            T* dv = static_cast<T*>(a.dv) + t * a.sdv.token + kvh * a.sdv.head;
-#pragma unroll
-            for (int db = 0; db < DB; ++db) {
-                store_tile(dk, db, a.D, lane, ak[db], a.scale);
-                store_tile(dv, db, a.D, lane, av[db], 1.f);
-            }
+            char* scratch = lds + wave * kRowsScratch<T, DP>;
+            store_rows<T, DP>(scratch, static_cast<T*>(a.dk) + t * a.sdk.token + kvh * a.sdk.head, a.sdk.token, keys_left, a.D,
+                              lane, ak, a.scale);
+            store_rows<T, DP>(scratch, static_cast<T*>(a.dv) + t * a.sdv.token + kvh * a.sdv.head, a.sdv.token, keys_left, a.D,
+                              lane, av, 1.f);
         } else {
-            const long long n = (long long)a.T * a.Hk * a.D;
-            float* dk = a.parts + 2 * split * n + (t * a.Hk + kvh) * a.D;
-#pragma unroll
-            for (int db = 0; db < DB; ++db) {
-                store_tile(dk, db, a.D, lane, ak[db], a.scale);
-                store_tile(dk + n, db, a.D, lane, av[db], 1.f);
-            }
+            const long long n = (long long)a.T * a.Hk * a.D, row = (long long)a.Hk * a.D;
+            float* dk = a.parts + 2 * split * n + t * row + kvh * a.D;
+            char* scratch = lds + wave * kRowsScratch<float, DP>;
+            store_rows<float, DP>(scratch, dk, row, keys_left, a.D, lane, ak, a.scale);
+            store_rows<float, DP>(scratch, dk + n, row, keys_left, a.D, lane, av, 1.f);
         }
     };
+    static_assert(4 * kRowsScratch<float, DP> <= LDS, "the tiles' place serves for storing");
     if (w.pad) {
         store();
         return;
@@ -223,7 +218,7 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
     copy(begin);
 
     Frag<T> kf[KS], vf[HOLD ? 1 : KS];
-    Frag<T>* mine = held + (HOLD ? wave * KS * 64 + lane : 0);
+    Frag<T>* mine = reinterpret_cast<Frag<T>*>(lds + 4 * TILE) + wave * KS * 64 + lane;   // V's place with HOLD
     {
         const long long t = w.start + min(key, w.len - 1);
         const T* krow = static_cast<const T*>(a.k) + t * a.sk.token + kvh * a.sk.head;
@@ -292,6 +287,7 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
             }
         }
     }
+    __syncthreads();   // everyone is done with the tiles
     store();
 }
 

@@ -38,15 +38,14 @@ __global__ void __launch_bounds__(256, occupancy(kFwd, sizeof(T), DP)) k_attn_fw
     const int row0 = w.tile * kFwdRows + wave * 32, row = row0 + (lane & 31);   // inside the segment
     const int rows_left = w.len - row0;                                         // <= 0: this wave has none
     const bool live = row < w.len;
-    T* out = static_cast<T*>(a.out) + (long long)(w.start + row) * a.so.token + head * a.so.head;
+    T* out = static_cast<T*>(a.out) + (long long)(w.start + row0) * a.so.token + head * a.so.head;
+    char* scratch = lds + wave * kRowsScratch<T, DP>;
+    static_assert(4 * kRowsScratch<T, DP> <= 4 * TILE, "the tiles' place serves for storing");
     float* lse = a.lse ? a.lse + (long long)head * a.T + w.start + row : nullptr;
     if (w.pad) {
-        if (live) {
-            f32x16 zero = {};
-#pragma unroll
-            for (int db = 0; db < DB; ++db) store_tile(out, db, a.D, lane, zero, 0.f);
-            if (lse && lane < 32) *lse = __builtin_inff();
-        }
+        const f32x16 zero[DB] = {};
+        store_rows<T, DP>(scratch, out, a.so.token, rows_left, a.D, lane, zero, 0.f);
+        if (lse && live && lane < 32) *lse = __builtin_inff();
         return;
     }
     const int kvh = head / a.group, chunks = a.D / 8;
@@ -142,23 +141,22 @@ __global__ void __launch_bounds__(256, occupancy(kFwd, sizeof(T), DP)) k_attn_fw
             }
         __builtin_amdgcn_s_setprio(0);
     }
-    if (!live) return;
     l = both_sum(l);
     const float inv = 1.f / l;
-#pragma unroll
-    for (int db = 0; db < DB; ++db) store_tile(out, db, a.D, lane, o[db], inv);
+    if (lse && live && lane < 32) *lse = (mc + log2f(l)) * kLn2;
+    __syncthreads();   // everyone is done with the tiles
+    if (rows_left <= 0) return;
+    store_rows<T, DP>(scratch, out, a.so.token, rows_left, a.D, lane, o, inv);
     if constexpr (sizeof(T) == 2) {
         if (a.low) {
-            T* low = static_cast<T*>(a.low) + ((long long)(w.start + row) * a.Hq + head) * a.D;
 #pragma unroll
-            for (int db = 0; db < DB; ++db) {
+            for (int db = 0; db < DB; ++db)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) o[db][r] = o[db][r] * inv - as_stored<T>(o[db][r] * inv);
-                store_tile(low, db, a.D, lane, o[db], 1.f);
-            }
+            store_rows<T, DP>(scratch, static_cast<T*>(a.low) + ((long long)(w.start + row0) * a.Hq + head) * a.D,
+                              (long long)a.Hq * a.D, rows_left, a.D, lane, o, 1.f);
         }
     }
-    if (lse && lane < 32) *lse = (mc + log2f(l)) * kLn2;
 }
 
 template <typename T, int DP>
