@@ -638,3 +638,13 @@ def test_operators_replay_in_a_graph():
         torch.cuda.synchronize()
         for a, b in zip(outs, step()):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_hybrid_network_learns(dtype):
+    """WTConv stage, packed token blocks and their gradients together: the loss
+    of eight images, seen 30 times, falls well below that of a guess."""
+    from memory_bound_cnn_amd import hybrid
+    losses = hybrid.train(steps=30, dtype=dtype, log=None)
+    assert all(math.isfinite(v) for v in losses)
+    assert losses[-1] < 0.5 * losses[0], losses
