@@ -24,24 +24,31 @@ __device__ __forceinline__ T from_f32(float v) {
         return v;
 }
 
+// 16 bytes of elements as they lie in memory: half the registers of their
+// float32 values when they are bfloat16, for loads that are on their way.
+template <typename T>
+struct Raw {
+    u32x4_any u;
+};
+template <typename T>
+__device__ __forceinline__ void unpack(const Raw<T>& r, float (&v)[kVec<T>]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t e = r.u[i];   // a value of its own: a vector's element is no object to cast the bits of
+        if constexpr (sizeof(T) == 2) {
+            v[2 * i] = __builtin_bit_cast(float, e << 16);
+            v[2 * i + 1] = __builtin_bit_cast(float, e & 0xFFFF0000u);
+        } else {
+            v[i] = __builtin_bit_cast(float, e);
+        }
+    }
+}
+
 // 16 bytes at any element address: gfx950 reads and writes them with one
 // instruction whatever their alignment.
 template <typename T>
 __device__ __forceinline__ void load16(const T* p, float (&v)[kVec<T>]) {
-    const u32x4_any u = *reinterpret_cast<const u32x4_any*>(p);
-    if constexpr (sizeof(T) == 2) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __builtin_bit_cast(float, u[i] << 16);
-            v[2 * i + 1] = __builtin_bit_cast(float, u[i] & 0xFFFF0000u);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t e = u[i];   // a value of its own: a vector's element is no object to cast the bits of
-            v[i] = __builtin_bit_cast(float, e);
-        }
-    }
+    unpack(Raw<T>{*reinterpret_cast<const u32x4_any*>(p)}, v);
 }
 
 template <typename T>
@@ -58,6 +65,20 @@ __device__ __forceinline__ void store16(T* p, const float (&v)[kVec<T>]) {
 }
 
 // The first n (0 .. kVec) elements; the others are zero, and not touched in memory.
+template <typename T>
+__device__ __forceinline__ Raw<T> load_raw(const T* p, int n) {
+    if (n >= kVec<T>) return {*reinterpret_cast<const u32x4_any*>(p)};
+    Raw<T> r = {{0u, 0u, 0u, 0u}};
+#pragma unroll
+    for (int i = 0; i < kVec<T>; ++i)
+        if (i < n) {
+            if constexpr (sizeof(T) == 2)
+                r.u[i / 2] |= (uint32_t)p[i] << (16 * (i % 2));
+            else
+                r.u[i] = __builtin_bit_cast(uint32_t, p[i]);
+        }
+    return r;
+}
 template <typename T>
 __device__ __forceinline__ void load_part(const T* p, int n, float (&v)[kVec<T>]) {
     if (n >= kVec<T>) {
