@@ -149,9 +149,13 @@ typedef struct {
  * rounded off out (bfloat16 only), kept for a backward pass whose row sums of
  * dout . out then have 16 bits of out.  Tensors are 16-byte aligned.  A value that is not finite
  * never reaches another sequence; inside its sequence it may reach every row.
+ * The workspace holds partial results where a short pack's keys are split over
+ * workgroups (0 bytes, and NULL is taken, where they are not).
  * WTC_ESHAPE: more than about 2^30 / Hq tokens (2^23 workgroups). */
+size_t wtconv_attention_forward_workspace(const wtc_attn_desc* d);
 int wtconv_attention_forward(const wtc_attn_desc* d, const void* q, const void* k, const void* v,
-                             const int* cu_seqlens, void* out, float* lse, void* out_low, void* stream);
+                             const int* cu_seqlens, void* out, float* lse, void* out_low, void* workspace,
+                             size_t workspace_bytes, void* stream);
 
 /* dq, dk, dv from dout and the forward pass's out, lse and out_low (or NULL);
  * dk and dv are summed over the q heads of their group.  Fixed summation order. */

@@ -384,8 +384,11 @@ struct Args {
     const int* cu;
     void *out, *dq, *dk, *dv;
     void* low;   // what was rounded off the output, [T, Hq, D] bfloat16, or null
-    float *lse, *delta, *parts;
-    int splits;   // of a key tile's queries in the backward pass; their sums in parts when there are several
+    float *lse, *delta;
+    int q_splits, k_splits;   // of a query tile's keys, of a key tile's queries; with several, their results:
+    float* parts;             // sums [split][T, heads, D] (dk and dv: [split][2][T, heads, D])
+    float* stat;              // forward: maximum c, log2, and sum of exp2, [split][2][row_floats]
+    long long row_floats;
     int T, n_seq, Hq, Hk, group, D, causal;
     float scale;
     wtc_attn_strides sq, sk, sv, so, sg, sdq, sdk, sdv;
@@ -496,6 +499,12 @@ __device__ __forceinline__ Work find_work(const Args& a, int slot, int lane) {
     return w;
 }
 inline long long slots(long long T, int n_seq, int size) { return T / size + n_seq + 2; }
+
+// workgroups of 256 for a join of splits, which strides over what is left
+inline unsigned join_groups(long long threads) {
+    const long long groups = (threads + 255) / 256;
+    return (unsigned)(groups < 8192 ? groups : 8192);
+}
 
 }  // namespace attn
 }  // namespace wtc

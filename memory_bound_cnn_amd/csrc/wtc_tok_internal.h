@@ -26,10 +26,11 @@ int launch_rotary(const wtc_rotary_desc* d, const void* x, const int* pos, const
 int launch_dropout(long long n, int dtype, unsigned least, const void* x, const void* r,
                    const unsigned long long* rng, void* y, void* stream);
 
-int launch_attn_forward(const wtc_attn_desc* d, const void* q, const void* k, const void* v, const int* cu, void* out,
-                        float* lse, void* out_low, void* stream);
-// workspace: rowsum(dout * out) [Hq, T], and the partial sums of dk and dv
+// workspaces: the splits' partial results; backward also rowsum(dout * out) [Hq, T]
+size_t attn_forward_bytes(const wtc_attn_desc* d);
 size_t attn_backward_bytes(const wtc_attn_desc* d);
+int launch_attn_forward(const wtc_attn_desc* d, const void* q, const void* k, const void* v, const int* cu, void* out,
+                        float* lse, void* out_low, void* workspace, void* stream);
 int launch_attn_backward(const wtc_attn_desc* d, const void* q, const void* k, const void* v, const void* out,
                          const float* lse, const void* out_low, const void* dout, const int* cu, void* dq, void* dk, void* dv,
                          void* workspace, void* stream);

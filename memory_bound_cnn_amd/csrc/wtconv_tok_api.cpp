@@ -124,8 +124,14 @@ int wtconv_dropout(long long n, int dtype, double p, const void* x, const void* 
     return launch_dropout(n, dtype, (unsigned)std::nearbyint(p * 65536.0), x, residual, rng, y, stream);
 }
 
+size_t wtconv_attention_forward_workspace(const wtc_attn_desc* d) {
+    if (check_attn(d) != WTC_OK) return 0;
+    return attn_forward_bytes(d);
+}
+
 int wtconv_attention_forward(const wtc_attn_desc* d, const void* q, const void* k, const void* v,
-                             const int* cu_seqlens, void* out, float* lse, void* out_low, void* stream) {
+                             const int* cu_seqlens, void* out, float* lse, void* out_low, void* workspace,
+                             size_t workspace_bytes, void* stream) {
     const int st = check_attn(d);
     if (st != WTC_OK) return st;
     if (d->T == 0) return WTC_OK;
@@ -133,7 +139,9 @@ int wtconv_attention_forward(const wtc_attn_desc* d, const void* q, const void* 
     const int bad = first_error({check_strides(d, d->q, q), check_strides(d, d->k, k), check_strides(d, d->v, v),
                                  check_strides(d, d->o, out), check_low(d, out_low)});
     if (bad != WTC_OK) return bad;
-    return launch_attn_forward(d, q, k, v, cu_seqlens, out, lse, out_low, stream);
+    const size_t need = attn_forward_bytes(d);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return WTC_EWORKSPACE;
+    return launch_attn_forward(d, q, k, v, cu_seqlens, out, lse, out_low, workspace, stream);
 }
 
 size_t wtconv_attention_backward_workspace(const wtc_attn_desc* d) {

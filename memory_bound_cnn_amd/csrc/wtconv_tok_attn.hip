@@ -19,43 +19,64 @@ Args args_of(const wtc_attn_desc* d, const void* q, const void* k, const void* v
     return a;
 }
 
-// Splits of a key tile's queries.  With few key tiles (few heads of k and v, a
-// short pack), or causal ones, whose first have twice the mean tile's queries,
-// one workgroup a tile leaves most of the chip waiting for the longest: several
-// share it where there are fewer than kWanted tiles (twice as many causal
-// ones: 512 workgroups run at once), with kLeast query tiles each at the pack's
-// mean length.  Their sums cost 8 bytes written and read a channel and split.
-// Measured, dk and dv with their join: causal 3 sequences of 3500 to 8192
-// tokens, 16 heads on 4 of 128 channels (552 tiles), 843 us in 4, 795 in 2;
-// causal 4 of 2000 to 4096, 8 heads of 96 (800 tiles), 164 us whole, 198 in 2;
-// float32 32 of 196, 6 heads on 3 of 64 (192 tiles), 56 us whole, 53 in 2, 60
-// in 3.
-constexpr int kWanted = 512, kWantedCausal = 1100, kLeast = 6, kMostSplits = 16;
-int dkv_splits(const wtc_attn_desc* d) {
+// Splits of a tile's other side.  With few tiles (few heads, a short pack), or
+// causal ones, whose longest have twice the mean tile's work, one workgroup a
+// tile leaves most of the chip waiting for the longest: several share it, as
+// many as keep their number within `wanted`, with kLeast tiles of the other side
+// each at the pack's mean length.  Partial results cost 8 bytes written and read
+// a channel and split.  Measured, with the joins, bfloat16, whole and split:
+//   8192 tokens, 1 head of 64 (64 tiles): forward 112 us, 39 in 8; dq 129, 48
+//   2 x 2000..2048, 6 of 64 (192 tiles): forward 35.3 us, 32.9 in 2; dq 41.5, 41.8
+//   3 x 1024, 12 of 64 (288 tiles): forward 26.2 us, 30.9 in 2; dq 34.6, 39.4
+//   causal 2 x 3100, 8 on 2 of 64 (400 tiles): forward 52 us, 45 in 2; dq 63, 53
+//   causal 4096, 16 of 128 (512 tiles): forward 103 us, 104 in 2; dq 134, 148
+//   causal 3 x 3500..8192, 16 on 4 of 128 (552 key tiles): dk and dv 843 us in 4, 795 in 2
+//   causal 4 x 2000..4096, 8 of 96 (800 key tiles): dk and dv 164 us, 198 in 2
+constexpr int kWanted = 512, kWantedCausal = 820, kWantedCausalKeys = 1150, kLeast = 6, kMostSplits = 16;
+int splits_of(const wtc_attn_desc* d, int wanted, int heads, int together) {
     if (d->T == 0 || d->n_seq == 0) return 1;
     const long long mean = (d->T + d->n_seq - 1) / d->n_seq, rows = d->dtype == WTC_BF16 ? 64 : 32;
-    const long long tiles = (mean + 127) / 128 * d->n_seq * d->Hk, wanted = d->causal ? kWantedCausal : kWanted;
-    const long long steps = (mean + rows - 1) / rows * (d->Hq / d->Hk) / (d->causal ? 2 : 1);
-    long long s = (wanted + tiles / 2) / tiles;
-    if (s > steps / kLeast) s = steps / kLeast;
+    const long long tiles = (mean + 127) / 128 * d->n_seq * heads;
+    const long long steps = (mean + rows - 1) / rows * together / (d->causal ? 2 : 1);
+    const long long s = wanted / tiles < steps / kLeast ? wanted / tiles : steps / kLeast;
     return (int)(s < 1 ? 1 : s > kMostSplits ? kMostSplits : s);
 }
+// of a query tile's keys (forward, dq)
+int query_splits(const wtc_attn_desc* d) { return splits_of(d, d->causal ? kWantedCausal : kWanted, d->Hq, 1); }
+// of a key tile's queries, the heads' of its group (dk, dv)
+int key_splits(const wtc_attn_desc* d) {
+    return splits_of(d, d->causal ? kWantedCausalKeys : kWanted, d->Hk, d->Hq / d->Hk);
+}
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
-size_t delta_bytes(const wtc_attn_desc* d) { return align256((size_t)d->Hq * (size_t)d->T * sizeof(float)); }
+size_t row_floats(const wtc_attn_desc* d) { return align256((size_t)d->Hq * (size_t)d->T * sizeof(float)); }
+size_t part_bytes(const wtc_attn_desc* d, int splits, int heads) {
+    return splits > 1 ? sizeof(float) * splits * (size_t)d->T * heads * d->D : 0;
+}
 }  // namespace
 }  // namespace attn
 
+// the splits' outputs, and the maximum and the sum of their rows
+size_t attn_forward_bytes(const wtc_attn_desc* d) {
+    const int s = attn::query_splits(d);
+    return s > 1 ? 2 * s * attn::row_floats(d) + attn::part_bytes(d, s, d->Hq) : 0;
+}
+// delta, then the splits' sums of dq, whose place those of dk and dv take afterwards
 size_t attn_backward_bytes(const wtc_attn_desc* d) {
-    const int s = attn::dkv_splits(d);
-    return attn::delta_bytes(d) + (s > 1 ? sizeof(float) * 2 * s * (size_t)d->T * d->Hk * d->D : 0);
+    const size_t q = attn::part_bytes(d, attn::query_splits(d), d->Hq);
+    const size_t kv = 2 * attn::part_bytes(d, attn::key_splits(d), d->Hk);
+    return attn::row_floats(d) + (q > kv ? q : kv);
 }
 
 int launch_attn_forward(const wtc_attn_desc* d, const void* q, const void* k, const void* v, const int* cu, void* out,
-                        float* lse, void* out_low, void* stream) {
+                        float* lse, void* out_low, void* workspace, void* stream) {
     attn::Args a = attn::args_of(d, q, k, v, cu);
     a.out = out;
     a.lse = lse;
     a.low = out_low;
+    a.q_splits = attn::query_splits(d);
+    a.row_floats = (long long)(attn::row_floats(d) / sizeof(float));
+    a.stat = static_cast<float*>(workspace);
+    a.parts = a.stat + (workspace ? 2 * a.q_splits * a.row_floats : 0);
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     return d->dtype == WTC_BF16 ? attn::fwd_bf16(a, st) : attn::fwd_fp32(a, st);
 }
@@ -69,8 +90,9 @@ int launch_attn_backward(const wtc_attn_desc* d, const void* q, const void* k, c
     a.low = const_cast<void*>(out_low);
     a.lse = const_cast<float*>(lse);
     a.delta = static_cast<float*>(workspace);
-    a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + attn::delta_bytes(d));
-    a.splits = attn::dkv_splits(d);
+    a.parts = a.delta + attn::row_floats(d) / sizeof(float);
+    a.q_splits = attn::query_splits(d);
+    a.k_splits = attn::key_splits(d);
     a.dq = dq; a.dk = dk; a.dv = dv;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     return d->dtype == WTC_BF16 ? attn::bwd_bf16(a, st) : attn::bwd_fp32(a, st);

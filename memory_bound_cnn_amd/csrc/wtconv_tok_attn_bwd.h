@@ -6,7 +6,15 @@
 // of one that would have to add dQ into memory from many workgroups in an
 // order that changes: dQ by query tiles (3 products a tile: S^T, dP^T, dQ^T),
 // dK and dV by key tiles, over the q heads of their group (4 products: S, dP,
-// dV^T, dK^T).  P is recomputed in both from the stored lse.
+// dV^T, dK^T).  P is recomputed in both from the stored lse.  With few tiles
+// both are split as the forward pass is, and their partial sums joined.
+//
+// Bound by the matrix units with the exponentials and roundings between their
+// products.  bfloat16, dq and dk/dv: 48 images of 49 to 1024 tokens, 6 heads of
+// 64, 76 and 86 us (650 and 765 TFLOP/s of the products each makes); 4 x 4096,
+// 12 heads of 64, 303 and 408 us (1020, 1010); causal 3 x 3500..8192, 16 heads on
+// 4 of 128, 495 and 755 us (1045, 915) with 27 us of joins; float32 32 x 196, 6
+// heads on 3 of 64, 39 and 45 us (73, 84) with 7 us of joins.
 #pragma once
 
 #include "wtc_tok_attn.h"
@@ -32,23 +40,32 @@ template <typename T, int DP>
 __global__ void __launch_bounds__(256, occupancy(kDq, sizeof(T), DP)) k_attn_dq(Args a) {
     constexpr int KEYS = kDqKeys<T>, KB = KEYS / 32, KS = DP / 16, DB = DP / 32;
     using L = Tile<T, DP, KEYS>;
-    constexpr int TILE = L::kBytes;
-    __shared__ __align__(16) char lds[4 * TILE];   // 2 x (K tile, V tile)
-    static_assert(4 * TILE <= 160 * 1024, "shared memory");
+    constexpr int TILE = L::kBytes, LDS = max_of(4 * TILE, 4 * kRowsScratch<float, DP>);
+    __shared__ __align__(16) char lds[LDS];   // 2 x (K tile, V tile); then a place to store from
+    static_assert(LDS <= 160 * 1024, "shared memory");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int head = blockIdx.x % a.Hq;
-    const Work w = find_work<kDqRows, true>(a, blockIdx.x / a.Hq, lane);
+    const int head = blockIdx.x % a.Hq, split = blockIdx.x / a.Hq % a.q_splits;
+    const Work w = find_work<kDqRows, true>(a, blockIdx.x / a.Hq / a.q_splits, lane);
     if (w.none) return;
     const int row0 = w.tile * kDqRows + wave * 32, row = row0 + (lane & 31);
     const int rows_left = w.len - row0;
     const bool live = row < w.len;
-    T* dq = static_cast<T*>(a.dq) + (long long)(w.start + row0) * a.sdq.token + head * a.sdq.head;
-    char* scratch = lds + wave * kRowsScratch<T, DP>;
-    static_assert(4 * kRowsScratch<T, DP> <= 4 * TILE, "the tiles' place serves for storing");
+    f32x16 acc[DB] = {};
+    auto store = [&] {   // no tile is read any more
+        if (rows_left <= 0) return;
+        const long long t = w.start + row0;
+        if (a.q_splits == 1) {
+            store_rows<T, DP>(lds + wave * kRowsScratch<T, DP>, static_cast<T*>(a.dq) + t * a.sdq.token + head * a.sdq.head,
+                              a.sdq.token, rows_left, a.D, lane, acc, a.scale);
+        } else {
+            const long long step = (long long)a.Hq * a.D, n = a.T * step;
+            store_rows<float, DP>(lds + wave * kRowsScratch<float, DP>, a.parts + split * n + t * step + head * a.D, step,
+                                  rows_left, a.D, lane, acc, a.scale);
+        }
+    };
     const long long stat = (long long)head * a.T + w.start + min(row, w.len - 1);
     if (w.pad) {
-        const f32x16 zero[DB] = {};
-        store_rows<T, DP>(scratch, dq, a.sdq.token, rows_left, a.D, lane, zero, 0.f);
+        store();
         return;
     }
     const int kvh = head / a.group, chunks = a.D / 8;
@@ -57,15 +74,16 @@ __global__ void __launch_bounds__(256, occupancy(kDq, sizeof(T), DP)) k_attn_dq(
     const uint32_t krow = (uint32_t)a.sk.token * sizeof(T), vrow = (uint32_t)a.sv.token * sizeof(T);
     const int keys = a.causal ? min(w.len, (w.tile + 1) * kDqRows) : w.len;
     const int tiles = (keys + KEYS - 1) / KEYS;
+    const int begin = (int)((long long)tiles * split / a.q_splits), end = (int)((long long)tiles * (split + 1) / a.q_splits);
     const uint32_t lds0 = lds_address(lds);
     typename L::Load kload, vload;
     auto copy = [&](int j) {
-        const int j0 = j * KEYS, end = min(w.len - 1 - j0, KEYS - 1);
+        const int j0 = j * KEYS, there = min(w.len - 1 - j0, KEYS - 1);
         const uint32_t at = lds0 + (uint32_t)(j & 1) * (2 * TILE);
-        L::issue(kload, at, kbase + (long long)j0 * krow, krow, end, chunks, wave, lane);
-        L::issue(vload, at + TILE, vbase + (long long)j0 * vrow, vrow, end, chunks, wave, lane);
+        L::issue(kload, at, kbase + (long long)j0 * krow, krow, there, chunks, wave, lane);
+        L::issue(vload, at + TILE, vbase + (long long)j0 * vrow, vrow, there, chunks, wave, lane);
     };
-    copy(0);
+    if (begin < end) copy(begin);
 
     const float c = a.scale * kLog2e;
     Frag<T> q[KS], g[KS];
@@ -85,19 +103,19 @@ __global__ void __launch_bounds__(256, occupancy(kDq, sizeof(T), DP)) k_attn_dq(
         if (sizeof(T) == 2 && a.low)
             delta += half_dot<T, KS>(grow, static_cast<const T*>(a.low) + (t * a.Hq + head) * a.D, a.D, lane);
         delta = both_sum(delta);
-        if (live && lane < 32) a.delta[stat] = delta;   // for the other kernel
+        if (split == 0 && live && lane < 32) a.delta[stat] = delta;   // for the other kernel
     }
     const float lse2 = a.lse[stat] * kLog2e;
     const int rlane = L::rows_lane(lane), clane = L::cols_lane(lane), half = L::row_of_half(lane), swap = L::cols_swap(lane);
     const int last = a.causal ? min(w.len - 1, row0 + 31) : w.len - 1;   // last key that any of the wave's queries sees
-    f32x16 acc[DB] = {}, minus;   // dP starts from -delta
+    f32x16 minus;   // dP starts from -delta
 #pragma unroll
     for (int r = 0; r < 16; ++r) minus[r] = -delta;
-    for (int j = 0; j < tiles; ++j) {
+    for (int j = begin; j < end; ++j) {
         L::commit(kload, lds + (j & 1) * (2 * TILE), wave, lane);
         L::commit(vload, lds + (j & 1) * (2 * TILE) + TILE, wave, lane);
         __syncthreads();   // tile j is there; everyone is done with the other one
-        if (j + 1 < tiles) copy(j + 1);
+        if (j + 1 < end) copy(j + 1);
         const int j0 = j * KEYS;
         if (rows_left <= 0 || (a.causal && j0 > row0 + 31)) continue;
         const char* kt = lds + (j & 1) * (2 * TILE) + rlane;
@@ -133,7 +151,7 @@ __global__ void __launch_bounds__(256, occupancy(kDq, sizeof(T), DP)) k_attn_dq(
         }
     }
     __syncthreads();   // everyone is done with the tiles
-    if (rows_left > 0) store_rows<T, DP>(scratch, dq, a.sdq.token, rows_left, a.D, lane, acc, a.scale);
+    store();
 }
 
 template <typename T, int DP>
@@ -150,8 +168,8 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
     constexpr bool START = sizeof(T) == 2;
     static_assert(LDS + 4 * ROWS * 4 <= 160 * 1024, "shared memory");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int kvh = blockIdx.x % a.Hk, split = blockIdx.x / a.Hk % a.splits;
-    const Work w = find_work<kDkvKeys, false>(a, blockIdx.x / a.Hk / a.splits, lane);
+    const int kvh = blockIdx.x % a.Hk, split = blockIdx.x / a.Hk % a.k_splits;
+    const Work w = find_work<kDkvKeys, false>(a, blockIdx.x / a.Hk / a.k_splits, lane);
     if (w.none) return;
     const int key0 = w.tile * kDkvKeys + wave * 32, key = key0 + (lane & 31);
     const int keys_left = w.len - key0;
@@ -160,7 +178,7 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
     auto store = [&] {   // no tile is read any more
         if (keys_left <= 0) return;
         const long long t = w.start + key0;
-        if (a.splits == 1) {
+        if (a.k_splits == 1) {
             char* scratch = lds + wave * kRowsScratch<T, DP>;
             store_rows<T, DP>(scratch, static_cast<T*>(a.dk) + t * a.sdk.token + kvh * a.sdk.head, a.sdk.token, keys_left, a.D,
                               lane, ak, a.scale);
@@ -183,7 +201,7 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
     const uint32_t qrow = (uint32_t)a.sq.token * sizeof(T), grow = (uint32_t)a.sg.token * sizeof(T);
     const int first = a.causal ? w.tile * kDkvKeys / ROWS : 0;   // the first query tile that sees these keys
     const int per_head = (w.len + ROWS - 1) / ROWS - first, all = per_head * a.group;
-    const int begin = (int)((long long)all * split / a.splits), end = (int)((long long)all * (split + 1) / a.splits);
+    const int begin = (int)((long long)all * split / a.k_splits), end = (int)((long long)all * (split + 1) / a.k_splits);
     if (begin == end) {
         store();
         return;
@@ -291,48 +309,57 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
     store();
 }
 
-// dk and dv from the sums of the splits, in their order; eight channels a thread.
+// Gradients from the splits' sums, in their order: `arrays` of them [T, heads,
+// D], a split's one after another.  Eight channels a thread.
+struct Join {
+    const float* parts;
+    int splits, arrays, heads, D;
+    long long n;   // T heads D
+    void* to[2];
+    wtc_attn_strides st[2];
+};
 template <typename T>
-__global__ void __launch_bounds__(256) k_attn_join(Args a) {
-    const long long n = (long long)a.T * a.Hk * a.D, step = (long long)gridDim.x * 256 * 8;
-    for (long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 8; i < 2 * n; i += step) {
-        const bool v = i >= n;
-        const long long at = v ? i - n : i, row = at / a.D;
-        const int c = (int)(at - row * a.D), head = (int)(row % a.Hk);
+__global__ void __launch_bounds__(256) k_attn_join(Join a) {
+    const long long step = (long long)gridDim.x * 256 * 8;
+    for (long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 8; i < a.arrays * a.n; i += step) {
+        const int which = i >= a.n;
+        const long long at = i - which * a.n, row = at / a.D;
+        const int c = (int)(at - row * a.D), head = (int)(row % a.heads);
         float sum[8] = {};
         for (int s = 0; s < a.splits; ++s) {
             float x[4], y[4];
-            load16(a.parts + 2 * s * n + i, x);
-            load16(a.parts + 2 * s * n + i + 4, y);
+            load16(a.parts + s * a.arrays * a.n + i, x);
+            load16(a.parts + s * a.arrays * a.n + i + 4, y);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 sum[j] += x[j];
                 sum[4 + j] += y[j];
             }
         }
-        const wtc_attn_strides& st = v ? a.sdv : a.sdk;
-        T* out = static_cast<T*>(v ? a.dv : a.dk) + row / a.Hk * st.token + head * st.head + c;
+        T* out = static_cast<T*>(a.to[which]) + row / a.heads * a.st[which].token + head * a.st[which].head + c;
 #pragma unroll
-        for (int k = 0; k < 8 / kVec<T>; ++k) {
-            float x[kVec<T>];
+        for (int k = 0; k < 8; k += kVec<T>) {
+            float v[kVec<T>];
 #pragma unroll
-            for (int j = 0; j < kVec<T>; ++j) x[j] = sum[k * kVec<T> + j];
-            store16(out + k * kVec<T>, x);
+            for (int j = 0; j < kVec<T>; ++j) v[j] = sum[k + j];
+            store16(out + k, v);
         }
     }
+}
+template <typename T>
+void run_join(const Join& j, hipStream_t st) {
+    hipLaunchKernelGGL((k_attn_join<T>), dim3(join_groups(j.arrays * j.n / 8)), dim3(256), 0, st, j);
 }
 
 template <typename T, int DP>
 int run_bwd(const Args& a, hipStream_t st) {
-    const long long gq = slots(a.T, a.n_seq, kDqRows) * a.Hq;
-    const long long gk = slots(a.T, a.n_seq, kDkvKeys) * a.Hk * a.splits;
+    const long long gq = slots(a.T, a.n_seq, kDqRows) * a.Hq * a.q_splits;
+    const long long gk = slots(a.T, a.n_seq, kDkvKeys) * a.Hk * a.k_splits;
     if (gq >= kMaxGroups || gk >= kMaxGroups) return WTC_ESHAPE;
     hipLaunchKernelGGL((k_attn_dq<T, DP>), dim3((unsigned)gq), dim3(256), 0, st, a);
+    if (a.q_splits > 1) run_join<T>({a.parts, a.q_splits, 1, a.Hq, a.D, (long long)a.T * a.Hq * a.D, {a.dq, nullptr}, {a.sdq, {}}}, st);
     hipLaunchKernelGGL((k_attn_dkv<T, DP>), dim3((unsigned)gk), dim3(256), 0, st, a);
-    if (a.splits > 1) {
-        const long long blocks = (2LL * a.T * a.Hk * a.D / 8 + 255) / 256;
-        hipLaunchKernelGGL((k_attn_join<T>), dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, st, a);
-    }
+    if (a.k_splits > 1) run_join<T>({a.parts, a.k_splits, 2, a.Hk, a.D, (long long)a.T * a.Hk * a.D, {a.dk, a.dv}, {a.sdk, a.sdv}}, st);
     return hipGetLastError() == hipSuccess ? WTC_OK : WTC_EHIP;
 }
 

@@ -8,6 +8,16 @@
 // has 32 of the 64 products of one query: the maximum and the sum take one
 // exchange between the two halves of the wave, the scale of the running sums is
 // the lane's own, and P^T feeds O^T = V^T P^T from the registers it is in.
+//
+// Where a pack has few query tiles, several workgroups share the keys of one;
+// their sums, maxima and sums of exponentials go to a workspace and a second
+// kernel joins them.
+//
+// Bound by the matrix units and, about as long again, the exponentials and
+// roundings between the two products.  bfloat16, 48 images of 49 to 1024 tokens,
+// 6 heads of 64: 55 us (600 TFLOP/s); 4 x 4096, 12 heads of 64: 233 us (885); causal 3 x
+// 3500..8192, 16 heads on 4 of 128: 358 us (965); float32, in six products of
+// bfloat16 parts, 32 x 196, 6 heads on 3 of 64: 27 us (70).
 #pragma once
 
 #include "wtc_tok_attn.h"
@@ -28,21 +38,33 @@ template <typename T, int DP>
 __global__ void __launch_bounds__(256, occupancy(kFwd, sizeof(T), DP)) k_attn_fwd(Args a) {
     constexpr int KEYS = kFwdKeys<T>, KB = KEYS / 32, KS = DP / 16, DB = DP / 32;
     using L = Tile<T, DP, KEYS>;
-    constexpr int TILE = L::kBytes;
-    __shared__ __align__(16) char lds[4 * TILE];   // 2 x (K tile, V tile)
-    static_assert(4 * TILE <= 160 * 1024, "shared memory");
+    constexpr int TILE = L::kBytes, LDS = max_of(4 * TILE, 4 * kRowsScratch<float, DP>);
+    __shared__ __align__(16) char lds[LDS];   // 2 x (K tile, V tile); then a place to store from
+    static_assert(LDS <= 160 * 1024, "shared memory");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int head = blockIdx.x % a.Hq;
-    const Work w = find_work<kFwdRows, true>(a, blockIdx.x / a.Hq, lane);
+    const int head = blockIdx.x % a.Hq, split = blockIdx.x / a.Hq % a.q_splits;
+    const Work w = find_work<kFwdRows, true>(a, blockIdx.x / a.Hq / a.q_splits, lane);
     if (w.none) return;
     const int row0 = w.tile * kFwdRows + wave * 32, row = row0 + (lane & 31);   // inside the segment
     const int rows_left = w.len - row0;                                         // <= 0: this wave has none
     const bool live = row < w.len;
     T* out = static_cast<T*>(a.out) + (long long)(w.start + row0) * a.so.token + head * a.so.head;
     char* scratch = lds + wave * kRowsScratch<T, DP>;
-    static_assert(4 * kRowsScratch<T, DP> <= 4 * TILE, "the tiles' place serves for storing");
-    float* lse = a.lse ? a.lse + (long long)head * a.T + w.start + row : nullptr;
+    const long long stat = (long long)head * a.T + w.start + row;
+    float* lse = a.lse ? a.lse + stat : nullptr;
+    // a split's row: the maximum (times c) that its sums are over, and the sum of
+    // its exponentials; inf and 0 for a token of no sequence, -inf and 0 where the
+    // split has nothing for the row
+    auto store_stat = [&](float top, float sum) {
+        if (!live || lane >= 32) return;
+        a.stat[2 * split * a.row_floats + stat] = top;
+        a.stat[(2 * split + 1) * a.row_floats + stat] = sum;
+    };
     if (w.pad) {
+        if (a.q_splits > 1) {
+            store_stat(__builtin_inff(), 0.f);
+            return;
+        }
         const f32x16 zero[DB] = {};
         store_rows<T, DP>(scratch, out, a.so.token, rows_left, a.D, lane, zero, 0.f);
         if (lse && live && lane < 32) *lse = __builtin_inff();
@@ -54,6 +76,11 @@ __global__ void __launch_bounds__(256, occupancy(kFwd, sizeof(T), DP)) k_attn_fw
     const uint32_t krow = (uint32_t)a.sk.token * sizeof(T), vrow = (uint32_t)a.sv.token * sizeof(T);
     const int keys = a.causal ? min(w.len, (w.tile + 1) * kFwdRows) : w.len;
     const int tiles = (keys + KEYS - 1) / KEYS;
+    const int begin = (int)((long long)tiles * split / a.q_splits), end = (int)((long long)tiles * (split + 1) / a.q_splits);
+    if (begin == end) {
+        store_stat(-__builtin_inff(), 0.f);
+        return;
+    }
     const uint32_t lds0 = lds_address(lds);
     typename L::Load kload, vload;
     auto copy = [&](int j) {
@@ -62,7 +89,7 @@ __global__ void __launch_bounds__(256, occupancy(kFwd, sizeof(T), DP)) k_attn_fw
         L::issue(kload, at, kbase + (long long)j0 * krow, krow, last, chunks, wave, lane);
         L::issue(vload, at + TILE, vbase + (long long)j0 * vrow, vrow, last, chunks, wave, lane);
     };
-    copy(0);
+    copy(begin);
 
     // a negative scale is taken into Q, so that the largest product is the largest logit
     // (and no scale below 2^-100, a zero one: it must not meet the infinity of a masked product)
@@ -76,11 +103,11 @@ __global__ void __launch_bounds__(256, occupancy(kFwd, sizeof(T), DP)) k_attn_fw
     f32x16 o[DB] = {};
     const int rlane = L::rows_lane(lane), clane = L::cols_lane(lane), half = L::row_of_half(lane), swap = L::cols_swap(lane);
     float m = -__builtin_inff(), mc = 0.f, l = 0.f;   // mc = m c, finite
-    for (int j = 0; j < tiles; ++j) {
+    for (int j = begin; j < end; ++j) {
         L::commit(kload, lds + (j & 1) * (2 * TILE), wave, lane);
         L::commit(vload, lds + (j & 1) * (2 * TILE) + TILE, wave, lane);
         __syncthreads();   // tile j is there; everyone is done with the other one
-        if (j + 1 < tiles) copy(j + 1);
+        if (j + 1 < end) copy(j + 1);
         const int j0 = j * KEYS;
         if (rows_left <= 0 || (a.causal && j0 > row0 + 31)) continue;   // nothing of this tile for this wave
         const char* kt = lds + (j & 1) * (2 * TILE) + rlane;
@@ -142,6 +169,15 @@ __global__ void __launch_bounds__(256, occupancy(kFwd, sizeof(T), DP)) k_attn_fw
         __builtin_amdgcn_s_setprio(0);
     }
     l = both_sum(l);
+    if (a.q_splits > 1) {
+        store_stat(m == -__builtin_inff() ? m : mc, l);
+        __syncthreads();   // everyone is done with the tiles
+        if (rows_left <= 0) return;
+        const long long step = (long long)a.Hq * a.D, n = a.T * step;
+        store_rows<float, DP>(lds + wave * kRowsScratch<float, DP>, a.parts + split * n + (w.start + row0) * step + head * a.D,
+                              step, rows_left, a.D, lane, o, 1.f);
+        return;
+    }
     const float inv = 1.f / l;
     if (lse && live && lane < 32) *lse = (mc + log2f(l)) * kLn2;
     __syncthreads();   // everyone is done with the tiles
@@ -159,11 +195,57 @@ __global__ void __launch_bounds__(256, occupancy(kFwd, sizeof(T), DP)) k_attn_fw
     }
 }
 
+// The splits' outputs joined: each weighed by 2^(its maximum - the largest one),
+// over the sum of the sums so weighed.  Eight channels a thread.
+template <typename T>
+__global__ void __launch_bounds__(256) k_attn_join_out(Args a) {
+    const int units = a.D / 8;
+    const long long rows = (long long)a.T * a.Hq, n = rows * a.D, step = (long long)gridDim.x * 256;
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < rows * units; i += step) {
+        const long long row = i / units, t = row / a.Hq;
+        const int c = (int)(i - row * units) * 8, head = (int)(row - t * a.Hq);
+        const float* stat = a.stat + (long long)head * a.T + t;
+        float top = -__builtin_inff(), sum = 0.f, o[8] = {};
+        for (int s = 0; s < a.q_splits; ++s) top = fmaxf(top, stat[2 * s * a.row_floats]);
+        for (int s = 0; s < a.q_splits; ++s) {
+            const float l = stat[(2 * s + 1) * a.row_floats];
+            if (l == 0.f) continue;   // nothing for this row, and nothing stored where the split has no keys
+            const float weight = __builtin_amdgcn_exp2f(stat[2 * s * a.row_floats] - top);
+            sum = fmaf(weight, l, sum);
+            float x[4], y[4];
+            load16(a.parts + s * n + row * a.D + c, x);
+            load16(a.parts + s * n + row * a.D + c + 4, y);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                o[j] = fmaf(weight, x[j], o[j]);
+                o[4 + j] = fmaf(weight, y[j], o[4 + j]);
+            }
+        }
+        const bool pad = top == __builtin_inff() && sum == 0.f;   // a token of no sequence
+        const float inv = pad ? 0.f : 1.f / sum;
+        if (a.lse && c == 0) a.lse[(long long)head * a.T + t] = pad ? top : (top + log2f(sum)) * kLn2;
+        T* out = static_cast<T*>(a.out) + t * a.so.token + head * a.so.head + c;
+#pragma unroll
+        for (int k = 0; k < 8; k += kVec<T>) {
+            float v[kVec<T>], low[kVec<T>];
+#pragma unroll
+            for (int j = 0; j < kVec<T>; ++j) {
+                v[j] = o[k + j] * inv;
+                low[j] = v[j] - as_stored<T>(v[j]);
+            }
+            store16(out + k, v);
+            if (sizeof(T) == 2 && a.low) store16(static_cast<T*>(a.low) + row * a.D + c + k, low);
+        }
+    }
+}
+
 template <typename T, int DP>
 int run_fwd(const Args& a, hipStream_t st) {
-    const long long grid = slots(a.T, a.n_seq, kFwdRows) * a.Hq;
+    const long long grid = slots(a.T, a.n_seq, kFwdRows) * a.Hq * a.q_splits;
     if (grid >= kMaxGroups) return WTC_ESHAPE;
     hipLaunchKernelGGL((k_attn_fwd<T, DP>), dim3((unsigned)grid), dim3(256), 0, st, a);
+    if (a.q_splits > 1)
+        hipLaunchKernelGGL((k_attn_join_out<T>), dim3(join_groups((long long)a.T * a.Hq * a.D / 8)), dim3(256), 0, st, a);
     return hipGetLastError() == hipSuccess ? WTC_OK : WTC_EHIP;
 }
 

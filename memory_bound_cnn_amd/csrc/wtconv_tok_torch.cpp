@@ -266,9 +266,11 @@ AttnOut attn_forward(const Tensor& q, const Tensor& k, const Tensor& v, const Te
     const AttnOut r = {empty(q.sizes(), q), keep ? empty({q.size(1), q.size(0)}, q, at::kFloat) : Tensor(),
                        keep && q.scalar_type() == at::kBFloat16 ? empty(q.sizes(), q) : Tensor()};
     d.o = strides(r.o);
+    const size_t bytes = wtconv_attention_forward_workspace(&d);
+    const Tensor ws = workspace(bytes, q);
     const On on(q);
     raise_on(wtconv_attention_forward(&d, in(q), in(k), in(v), in_as<int>(cu), out(r.o), static_cast<float*>(out(r.lse)),
-                                      out(r.low), on.stream),
+                                      out(r.low), out(ws), bytes, on.stream),
              "wtconv_attention_forward");
     return r;
 }

@@ -58,11 +58,12 @@ def _load():
                 ("wtconv_rms_norm_backward", [_P] * 9 + [_SZ, _P]),
                 ("wtconv_rotary", [_P] * 6),
                 ("wtconv_dropout", [_LL, _I, ctypes.c_double] + [_P] * 5),
-                ("wtconv_attention_forward", [_P] * 9),
+                ("wtconv_attention_forward", [_P] * 9 + [_SZ, _P]),
                 ("wtconv_attention_backward", [_P] * 13 + [_SZ, _P])):
             f = getattr(lib, name)
             f.restype, f.argtypes = _I, args
-        for name in ("wtconv_rms_norm_backward_workspace", "wtconv_attention_backward_workspace"):
+        for name in ("wtconv_rms_norm_backward_workspace", "wtconv_attention_forward_workspace",
+                     "wtconv_attention_backward_workspace"):
             f = getattr(lib, name)
             f.restype, f.argtypes = _SZ, [_P]
         _lib = lib
@@ -216,7 +217,8 @@ def _attn_desc(q, k, v, cu_seqlens, causal, scale):
     return d
 
 
-def wtconv_attention_forward(q, k, v, cu_seqlens, causal=False, scale=None, want_lse=False, out=None, out_low=None):
+def wtconv_attention_forward(q, k, v, cu_seqlens, causal=False, scale=None, want_lse=False, out=None, out_low=None,
+                             workspace=None):
     """(out, lse) for q [T, Hq, D], k and v [T, Hk, D]; lse [Hq, T] float32 or
     None.  scale: 1 / sqrt(D) unless given.  out_low: a contiguous bfloat16
     tensor of q's shape for what is rounded off out, or None."""
@@ -230,8 +232,9 @@ def wtconv_attention_forward(q, k, v, cu_seqlens, causal=False, scale=None, want
         _check(out_low, "out_low", torch.bfloat16, dev, q.shape, True)
     lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=dev) if want_lse else None
     d.o = out.stride()[:2]
+    ws, size = _workspace(_load().wtconv_attention_forward_workspace(ctypes.addressof(d)), dev, workspace)
     _call("wtconv_attention_forward", dev, ctypes.addressof(d), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-          cu_seqlens.data_ptr(), out.data_ptr(), _ptr(lse), _ptr(out_low))
+          cu_seqlens.data_ptr(), out.data_ptr(), _ptr(lse), _ptr(out_low), _ptr(ws), size)
     return out, lse
 
 

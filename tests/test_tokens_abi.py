@@ -129,7 +129,7 @@ ATTN_BAD = [
 @pytest.mark.parametrize("kw,status", ATTN_BAD)
 def test_attention_rejects(kw, status):
     lib, d = tb._load(), attn(**kw)
-    assert lib.wtconv_attention_forward(ref(d), P, P, P, P, P, P, None, None) == status
+    assert lib.wtconv_attention_forward(ref(d), P, P, P, P, P, P, None, P, 1 << 62, None) == status
     assert lib.wtconv_attention_backward(ref(d), P, P, P, P, P, None, P, P, P, P, P, P, 1 << 62, None) == status
 
 
@@ -138,12 +138,12 @@ def test_attention_rejects_pointers_and_workspaces():
     for at in range(5):
         args = [P] * 6
         args[at] = None
-        assert lib.wtconv_attention_forward(ref(d), *args, None, None) == EINVAL
+        assert lib.wtconv_attention_forward(ref(d), *args, None, None, 0, None) == EINVAL
         if at != 3:    # cu_seqlens is int32
             args[at] = ODD
-            assert lib.wtconv_attention_forward(ref(d), *args, None, None) == EINVAL
-    assert lib.wtconv_attention_forward(ref(d), *[P] * 6, ODD, None) == EINVAL
-    assert lib.wtconv_attention_forward(ref(attn(dtype=0)), *[P] * 6, P, None) == EDTYPE   # nothing is rounded off
+            assert lib.wtconv_attention_forward(ref(d), *args, None, None, 0, None) == EINVAL
+    assert lib.wtconv_attention_forward(ref(d), *[P] * 6, ODD, None, 0, None) == EINVAL
+    assert lib.wtconv_attention_forward(ref(attn(dtype=0)), *[P] * 6, P, None, 0, None) == EDTYPE   # nothing is rounded off
     need = lib.wtconv_attention_backward_workspace(ref(d))
     assert need == 256    # 4 heads x 5 tokens x 4 bytes, to the next 256
     for at in range(11):
@@ -157,8 +157,14 @@ def test_attention_rejects_pointers_and_workspaces():
     for name in ("g", "dq", "dk", "dv"):
         bad = attn(**{name: (256, 63)})
         assert lib.wtconv_attention_backward(ref(bad), *[P] * 11, P, need, None) == EINVAL
-    assert lib.wtconv_attention_forward(None, P, P, P, P, P, P, None, None) == EINVAL
-    assert lib.wtconv_attention_forward(ref(attn(T=0)), *[None] * 8) == binding.WTC_OK
+    assert lib.wtconv_attention_forward(None, P, P, P, P, P, P, None, None, 0, None) == EINVAL
+    assert lib.wtconv_attention_forward(ref(attn(T=0)), *[None] * 8, 0, None) == binding.WTC_OK
+    # a long sequence of one head is split over workgroups, whose results need a place
+    d = attn(T=8192, Hq=1, Hk=1)
+    need = lib.wtconv_attention_forward_workspace(ref(d))
+    assert need > 0
+    assert lib.wtconv_attention_forward(ref(d), *[P] * 6, None, P, need - 1, None) == EWORKSPACE
+    assert lib.wtconv_attention_forward(ref(d), *[P] * 6, None, None, need, None) == EWORKSPACE
 
 
 def test_python_entry_points_refuse_host_tensors():

@@ -368,6 +368,23 @@ def test_attention(lens, Hq, Hk, D, causal, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("cu,Hq,Hk,D", [([0, 1500], 1, 1, 64), ([0, 1300], 2, 1, 128), ([3, 3, 1200, 1290], 1, 1, 32),
+                                        ([0, 1000, 1003, 1900], 2, 2, 104), ([7, 2610], 2, 1, 64),
+                                        ([0, 1, 4000], 1, 1, 128)])
+def test_attention_split(cu, Hq, Hk, D, causal, dtype):
+    """Few long sequences and heads: a tile's other side is split over
+    workgroups, some of which have nothing of a short sequence or of the tokens
+    of none."""
+    q, k, v, _ = pack([cu[-1] + 20], Hq, Hk, D, dtype, seed=cu[-1])
+    cu = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    if cu[-1] - cu[0] > 2000 and not causal:
+        d = tb._attn_desc(q, k, v, cu, causal, None)
+        assert tb._load().wtconv_attention_forward_workspace(tb.ctypes.addressof(d)) > 0
+    attn_check(q, k, v, cu, causal, what=f"split {cu.tolist()}")
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
 def test_attention_scales(scale, dtype):
     q, k, v, cu = pack([70, 131], 2, 1, 64, dtype, seed=1)
