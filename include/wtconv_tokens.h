@@ -147,8 +147,9 @@ typedef struct {
  * each row's sum of exp (+infinity for tokens of no sequence), kept for the
  * backward pass.  out_low [T, Hq, D] bfloat16 contiguous or NULL: what was
  * rounded off out (bfloat16 only), kept for a backward pass whose row sums of
- * dout . out then have 16 bits of out.  Tensors are 16-byte aligned.  A value that is not finite
- * never reaches another sequence; inside its sequence it may reach every row.
+ * dout . out then have 16 bits of out.  Tensors are 16-byte aligned.  A value
+ * that is not finite never reaches another sequence; inside its sequence it may
+ * reach every row.
  * The workspace holds partial results where a short pack's keys are split over
  * workgroups (0 bytes, and NULL is taken, where they are not).
  * WTC_ESHAPE: more than about 2^30 / Hq tokens (2^23 workgroups). */
@@ -161,8 +162,8 @@ int wtconv_attention_forward(const wtc_attn_desc* d, const void* q, const void* 
  * dk and dv are summed over the q heads of their group.  Fixed summation order. */
 size_t wtconv_attention_backward_workspace(const wtc_attn_desc* d);
 int wtconv_attention_backward(const wtc_attn_desc* d, const void* q, const void* k, const void* v, const void* out,
-                              const float* lse, const void* out_low, const void* dout, const int* cu_seqlens, void* dq, void* dk, void* dv,
-                              void* workspace, size_t workspace_bytes, void* stream);
+                              const float* lse, const void* out_low, const void* dout, const int* cu_seqlens,
+                              void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

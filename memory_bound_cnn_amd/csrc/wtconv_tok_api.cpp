@@ -150,8 +150,8 @@ size_t wtconv_attention_backward_workspace(const wtc_attn_desc* d) {
 }
 
 int wtconv_attention_backward(const wtc_attn_desc* d, const void* q, const void* k, const void* v, const void* out,
-                              const float* lse, const void* out_low, const void* dout, const int* cu_seqlens, void* dq, void* dk, void* dv,
-                              void* workspace, size_t workspace_bytes, void* stream) {
+                              const float* lse, const void* out_low, const void* dout, const int* cu_seqlens,
+                              void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes, void* stream) {
     const int st = check_attn(d);
     if (st != WTC_OK) return st;
     if (d->T == 0) return WTC_OK;

@@ -78,11 +78,14 @@ bool wants_grad(const Ts&... ts) {
 }
 bool wants_grad_opt(const OptTensor& t) { return t && wants_grad(*t); }
 
-// A gradient's own gradient would have to be written down; without this it would silently be zero.
-void once(const variable_list& grads) {
-    if (at::GradMode::is_enabled())
-        for (const Tensor& g : grads)
-            TORCH_CHECK(!g.defined() || !g.requires_grad(), "the token operators have first derivatives only");
+// A gradient's own gradient would have to be written down; without this it
+// would silently be zero: that by the output's gradient, and where the operator
+// is not linear, that by its inputs.
+void once(const variable_list& grads, bool linear) {
+    if (!at::GradMode::is_enabled()) return;   // create_graph
+    TORCH_CHECK(linear, "the token operators have first derivatives only");
+    for (const Tensor& g : grads)
+        TORCH_CHECK(!g.defined() || !g.requires_grad(), "the token operators have first derivatives only");
 }
 
 // [rows, C] with a contiguous last axis; a view where t allows it.
@@ -127,7 +130,7 @@ struct RmsNorm : torch::autograd::Function<RmsNorm> {
         return {o.y, o.h};
     }
     static variable_list backward(AutogradContext* ctx, const variable_list& g) {
-        once(g);
+        once(g, false);
         const variable_list s = ctx->get_saved_variables();
         const Tensor dh = g.size() > 1 ? g[1] : Tensor();
         if (!g[0].defined()) return {dh, Tensor(), dh, Tensor()};
@@ -203,7 +206,7 @@ struct Rotary : torch::autograd::Function<Rotary> {
         return rotary_forward(x, positions, inv_freq, sections, interleaved, false);
     }
     static variable_list backward(AutogradContext* ctx, const variable_list& g) {
-        once(g);
+        once(g, true);
         const variable_list s = ctx->get_saved_variables();
         return {rotary_forward(g[0], s[0], s[1], ctx->saved_data["sections"].toIntVector(),
                                ctx->saved_data["interleaved"].toBool(), true),
@@ -260,8 +263,8 @@ void attn_check(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor&
 struct AttnOut {
     Tensor o, lse, low;   // lse, low: kept for the backward pass (low: what was rounded off o, bfloat16)
 };
-AttnOut attn_forward(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& cu,
-                                        const Setting& s, bool keep) {
+AttnOut attn_forward(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& cu, const Setting& s,
+                     bool keep) {
     wtc_attn_desc d = attn_desc(q, k, v, cu, s);
     const AttnOut r = {empty(q.sizes(), q), keep ? empty({q.size(1), q.size(0)}, q, at::kFloat) : Tensor(),
                        keep && q.scalar_type() == at::kBFloat16 ? empty(q.sizes(), q) : Tensor()};
@@ -274,8 +277,8 @@ AttnOut attn_forward(const Tensor& q, const Tensor& k, const Tensor& v, const Te
              "wtconv_attention_forward");
     return r;
 }
-void attn_backward(const Tensor& q, const Tensor& k, const Tensor& v, const AttnOut& f, const Tensor& g, const Tensor& cu, const Setting& s, const Tensor& dq, const Tensor& dk,
-                   const Tensor& dv) {
+void attn_backward(const Tensor& q, const Tensor& k, const Tensor& v, const AttnOut& f, const Tensor& g,
+                   const Tensor& cu, const Setting& s, const Tensor& dq, const Tensor& dk, const Tensor& dv) {
     wtc_attn_desc d = attn_desc(q, k, v, cu, s);
     d.o = strides(f.o);
     d.g = strides(g);
@@ -291,7 +294,7 @@ void attn_backward(const Tensor& q, const Tensor& k, const Tensor& v, const Attn
 }
 
 struct Attention : torch::autograd::Function<Attention> {
-    // Saves its inputs, its output and one float per query and head.
+    // Saves its inputs, its output (with what was rounded off it) and one float per query and head.
     static Tensor forward(AutogradContext* ctx, const Tensor& q0, const Tensor& k0, const Tensor& v0, const Tensor& cu,
                           bool causal, double scale) {
         const Tensor q = heads(q0), k = heads(k0), v = heads(v0);
@@ -302,7 +305,7 @@ struct Attention : torch::autograd::Function<Attention> {
         return f.o;
     }
     static variable_list backward(AutogradContext* ctx, const variable_list& g) {
-        once(g);
+        once(g, false);
         const variable_list s = ctx->get_saved_variables();
         const Tensor dq = empty(s[0].sizes(), s[0]), dk = empty(s[1].sizes(), s[0]), dv = empty(s[2].sizes(), s[0]);
         attn_backward(s[0], s[1], s[2], {s[3], s[4], s[5]}, heads(g[0]), s[6],
@@ -323,16 +326,26 @@ Tensor attention(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor
     return attn_forward(heads(q), heads(k), heads(v), cu, {causal, s}, false).o;
 }
 
+// the q and k heads of a projection, turned, and the attention of it
+Tensor turned(const Tensor& qkv, int64_t n, const Tensor& positions, const Tensor& inv_freq,
+              const std::vector<int64_t>& sections, bool interleaved) {
+    const Tensor qk = empty({qkv.size(0), n, qkv.size(2)}, qkv);
+    rotary_run(qkv.narrow(1, 0, n), qk, positions, inv_freq, sections, interleaved, false);
+    return qk;
+}
+AttnOut turned_forward(const Tensor& qkv, const Tensor& qk, int64_t Hq, int64_t Hk, const Tensor& cu, const Setting& s,
+                       bool keep) {
+    return attn_forward(qk.narrow(1, 0, Hq), qk.narrow(1, Hq, Hk), qkv.narrow(1, Hq + Hk, Hk), cu, s, keep);
+}
+
 struct RotaryAttention : torch::autograd::Function<RotaryAttention> {
     // rotary on q and k, then attention, on one projection: the gradients are
     // written where the projection's are wanted, and turned back there.
     static Tensor forward(AutogradContext* ctx, const Tensor& qkv0, int64_t Hq, int64_t Hk, const Tensor& positions,
                           const Tensor& inv_freq, std::vector<int64_t> sections, const Tensor& cu, bool interleaved,
                           bool causal, double scale) {
-        const Tensor qkv = heads(qkv0), qk = empty({qkv.size(0), Hq + Hk, qkv.size(2)}, qkv);
-        rotary_run(qkv.narrow(1, 0, Hq + Hk), qk, positions, inv_freq, sections, interleaved, false);
-        const AttnOut f = attn_forward(qk.narrow(1, 0, Hq), qk.narrow(1, Hq, Hk), qkv.narrow(1, Hq + Hk, Hk), cu,
-                                       {causal, scale}, true);
+        const Tensor qkv = heads(qkv0), qk = turned(qkv, Hq + Hk, positions, inv_freq, sections, interleaved);
+        const AttnOut f = turned_forward(qkv, qk, Hq, Hk, cu, {causal, scale}, true);
         ctx->save_for_backward({qkv, qk, f.o, f.lse, f.low, cu, positions, inv_freq});
         ctx->saved_data["Hq"] = Hq;
         ctx->saved_data["Hk"] = Hk;
@@ -343,14 +356,14 @@ struct RotaryAttention : torch::autograd::Function<RotaryAttention> {
         return f.o;
     }
     static variable_list backward(AutogradContext* ctx, const variable_list& g) {
-        once(g);
+        once(g, false);
         const variable_list s = ctx->get_saved_variables();
         auto& at = ctx->saved_data;
         const int64_t Hq = at["Hq"].toInt(), Hk = at["Hk"].toInt();
         const Tensor &qkv = s[0], &qk = s[1];
         const Tensor d = empty(qkv.sizes(), qkv), dqk = d.narrow(1, 0, Hq + Hk);
-        attn_backward(qk.narrow(1, 0, Hq), qk.narrow(1, Hq, Hk), qkv.narrow(1, Hq + Hk, Hk), {s[2], s[3], s[4]}, heads(g[0]), s[5],
-                      {at["causal"].toBool(), at["scale"].toDouble()}, d.narrow(1, 0, Hq), d.narrow(1, Hq, Hk),
+        attn_backward(qk.narrow(1, 0, Hq), qk.narrow(1, Hq, Hk), qkv.narrow(1, Hq + Hk, Hk), {s[2], s[3], s[4]},
+                      heads(g[0]), s[5], {at["causal"].toBool(), at["scale"].toDouble()}, d.narrow(1, 0, Hq), d.narrow(1, Hq, Hk),
                       d.narrow(1, Hq + Hk, Hk));
         rotary_run(dqk, dqk, s[6], s[7], at["sections"].toIntVector(), at["interleaved"].toBool(), true);
         variable_list r(10);
@@ -368,8 +381,12 @@ Tensor rotary_attention(const Tensor& qkv, int64_t Hq, int64_t Hk, const Tensor&
     rotary_check(qkv, positions, inv_freq, sections);
     TORCH_CHECK_VALUE(cu.dim() == 1 && cu.size(0) >= 1, "cu_seqlens must be [n + 1]");
     check(cu, "cu_seqlens", at::kInt, qkv, cu.sizes());
-    return RotaryAttention::apply(qkv, Hq, Hk, positions, inv_freq, sections, cu, interleaved, causal,
-                                  scale_of(scale, qkv));
+    const double s = scale_of(scale, qkv);
+    if (wants_grad(qkv))
+        return RotaryAttention::apply(qkv, Hq, Hk, positions, inv_freq, sections, cu, interleaved, causal, s);
+    const Tensor x = heads(qkv);
+    return turned_forward(x, turned(x, Hq + Hk, positions, inv_freq, sections, interleaved), Hq, Hk, cu, {causal, s},
+                          false).o;
 }
 
 // ------------------------------------------------------------------ dropout
@@ -391,7 +408,7 @@ struct Dropout : torch::autograd::Function<Dropout> {
         return dropout_forward(x, p, rng, residual.value_or(Tensor()));
     }
     static variable_list backward(AutogradContext* ctx, const variable_list& g) {
-        once(g);
+        once(g, true);
         Tensor dx;
         if (ctx->needs_input_grad(0))
             dx = dropout_forward(g[0], ctx->saved_data["p"].toDouble(), ctx->get_saved_variables()[0], Tensor());

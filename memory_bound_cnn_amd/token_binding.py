@@ -240,8 +240,9 @@ def wtconv_attention_forward(q, k, v, cu_seqlens, causal=False, scale=None, want
 
 def wtconv_attention_backward(q, k, v, out, lse, dout, cu_seqlens, causal=False, scale=None, grads=None,
                               workspace=None, out_low=None):
-    """(dq, dk, dv).  out_low: as the forward pass left it, or None.  grads: the tensors to write them to (q's, k's and v's
-    shapes, any strides that the library takes), or None."""
+    """(dq, dk, dv).  out_low: as the forward pass left it, or None.  grads: the
+    tensors to write them to (q's, k's and v's shapes, any strides that the
+    library takes), or None."""
     d = _attn_desc(q, k, v, cu_seqlens, causal, scale)
     dev = q.device
     _check(out, "out", q.dtype, dev, q.shape)

@@ -598,6 +598,37 @@ def test_second_derivatives_are_refused():
         torch.autograd.grad(tokens.attention(q, q, q, cu), q, g, create_graph=True)
 
 
+def test_second_derivatives_by_the_inputs_are_refused():
+    """An output's gradient that needs none itself: the norm's and the
+    attention's gradients depend on their inputs all the same, those of the
+    rotation and of dropout do not."""
+    x, w = torch.randn(4, 16, device=DEV, requires_grad=True), torch.ones(16, device=DEV)
+    with pytest.raises(RuntimeError, match="first derivatives only"):
+        torch.autograd.grad(tokens.rms_norm(x, w).sum(), x, create_graph=True)
+    q = torch.randn(5, 3, 32, device=DEV, requires_grad=True)
+    cu, pos = torch.tensor([0, 5], dtype=torch.int32, device=DEV), torch.zeros(5, 1, dtype=torch.int32, device=DEV)
+    f, rng = tokens.rotary_frequencies((4,), device=DEV), torch.zeros(2, dtype=torch.int64, device=DEV)
+    with pytest.raises(RuntimeError, match="first derivatives only"):
+        torch.autograd.grad(tokens.attention(q, q, q, cu).sum(), q, create_graph=True)
+    with pytest.raises(RuntimeError, match="first derivatives only"):
+        torch.autograd.grad(tokens.rotary_attention(q, 1, 1, pos, f, (4,), cu).sum(), q, create_graph=True)
+    for y in (tokens.rotary(q, pos, f, (4,)), tokens.dropout(q, 0.5, rng)):
+        torch.autograd.grad(y.sum(), q, create_graph=True)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rotary_attention_without_gradients_is_the_same(dtype):
+    """Without gradients nothing is kept for them; the outputs are the same bits."""
+    qkv = torch.randn(300, 8, 64, device=DEV, dtype=dtype, requires_grad=True)
+    cu = torch.tensor([0, 7, 300], dtype=torch.int32, device=DEV)
+    pos = torch.arange(300, device=DEV, dtype=torch.int32)[:, None].contiguous()
+    f = tokens.rotary_frequencies((32,), device=DEV)
+    y = tokens.rotary_attention(qkv, 4, 2, pos, f, (32,), cu, causal=True)
+    with torch.no_grad():
+        z = tokens.rotary_attention(qkv, 4, 2, pos, f, (32,), cu, causal=True)
+    assert y.requires_grad and not z.requires_grad and torch.equal(y, z)
+
+
 def test_entry_points_refuse():
     """Device tensors of wrong types, shapes and places, through the public functions."""
     x, w = torch.zeros(4, 16, device=DEV), torch.ones(16, device=DEV)
