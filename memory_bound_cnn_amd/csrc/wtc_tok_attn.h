@@ -14,7 +14,7 @@
 // product six of theirs: the three left out are below 2^-24 of it, so this is
 // float32's own precision in 192 cycles, where the float32 instructions take
 // 512 (4 sequences of 2048 tokens, 12 heads of 64: forward, dq, dk and dv 425,
-// 608 and 832 us with those, 259, 404 and 538 so).
+// 608 and 832 us with those, 271, 420 and 600 so).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -403,9 +403,9 @@ struct Args {
 // orders count the work in tiles: with w(L) = the tiles that come before all
 // those of L tiles' work, the slot's L is found by bisection, with no plan on
 // the host.  Measured against the order of the sequences (forward, dq, dk and
-// dv): 48 images of 49 to 1024 tokens, 6 heads of 64 channels, 62 / 82 / 113 ->
-// 56 / 75 / 97 us; 4 causal sequences of 2000 to 4096, 8 heads of 96, 102 / 134
-// / 169 -> 90 / 122 / 175; equal lengths the same within 2 %.
+// dv): 48 images of 49 to 1024 tokens, 6 heads of 64 channels, 65 / 85 / 104 ->
+// 56 / 78 / 87 us; 4 causal sequences of 2000 to 4096, 8 heads of 96, 129 / 165
+// / 204 -> 104 / 136 / 175; equal lengths the same within 3 %.
 //   More segments: segment s may use the slots from floor(start / SIZE) + s on.
 // That leaves ceil(length / SIZE) slots at least to each, and a slot's segment
 // is found by searching cu_seqlens itself, 63 segments at a time.

@@ -209,7 +209,13 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
     const uint32_t lds0 = lds_address(lds);
     // no scale below 2^-100 (a zero one): what it multiplies is then lost beside lse, as it should be
     const float c = copysignf(fmaxf(fabsf(a.scale) * kLog2e, 0x1p-100f), a.scale), inv_c = 1.f / c;
-    float stat = 0.f;   // of the tile copied last, on its way to shared memory
+    // lse (the first ROWS threads) or delta (the next) of a query of the tile copied last, on its way to
+    // shared memory, in the order that a result's registers have the rows in.  It is left as it was loaded
+    // until the tile itself is waited for.
+    float stat = 0.f;
+    int stat_last = 0;
+    const bool is_lse = threadIdx.x < ROWS;
+    const int stat_row = threadIdx.x % ROWS / 32 * 32 + L::place(threadIdx.x % 32);
     typename L::Load qload, gload;
     int head = kvh * a.group + begin / per_head, j0 = (first + begin % per_head) * ROWS;   // of the next tile to copy
     auto copy = [&](int i) {
@@ -220,11 +226,9 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
         L::issue(qload, at, reinterpret_cast<const char*>(qp), qrow, last, chunks, wave, lane);
         L::issue(gload, at + TILE, reinterpret_cast<const char*>(gp), grow, last, chunks, wave, lane);
         if (threadIdx.x < 2 * ROWS) {
-            // kept in the order that a result's registers have the rows in
-            const int r = threadIdx.x % ROWS / 32 * 32 + L::place(threadIdx.x % 32);
-            const long long t = (long long)head * a.T + w.start + j0 + min(r, last);
-            // queries past the end: an infinite lse leaves nothing of them
-            stat = threadIdx.x < ROWS ? (r <= last ? a.lse[t] * kLog2e : __builtin_inff()) * (START ? -inv_c : -1.f) : -a.delta[t];
+            const long long t = (long long)head * a.T + w.start + j0 + min(stat_row, last);
+            stat = (is_lse ? a.lse : a.delta)[t];
+            stat_last = last;
         }
         j0 += ROWS;
         if (j0 >= w.len) {
@@ -252,7 +256,11 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
     }
     const int rlane = L::rows_lane(lane), clane = L::cols_lane(lane), swap = L::cols_swap(lane);
     for (int i = begin; i < end; ++i) {
-        if (threadIdx.x < 2 * ROWS) stats[i & 1][threadIdx.x / ROWS][threadIdx.x % ROWS] = stat;
+        if (threadIdx.x < 2 * ROWS) {
+            // queries past the end: an infinite lse leaves nothing of them
+            const float lse = stat_row <= stat_last ? stat * kLog2e : __builtin_inff();
+            stats[i & 1][threadIdx.x / ROWS][threadIdx.x % ROWS] = is_lse ? lse * (START ? -inv_c : -1.f) : -stat;
+        }
         L::commit(qload, lds + (i & 1) * (2 * TILE), wave, lane);
         L::commit(gload, lds + (i & 1) * (2 * TILE) + TILE, wave, lane);
         __syncthreads();   // tile i is there; everyone is done with the other one
