@@ -184,7 +184,10 @@ struct Tile {
     }
     static __device__ __forceinline__ void commit(const Load& load, char* tile, int wave, int lane) {
         if constexpr (sizeof(T) == 2) {
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            // every load; as a builtin, so that the compiler knows that its own are done, too, and adds no wait
+            // for what a loop issues after it
+            __builtin_amdgcn_s_waitcnt(0x0F70);
+            asm volatile("" ::: "memory");
         } else {
 #pragma unroll
             for (int i = 0; i < kUnits; ++i) {
@@ -273,44 +276,74 @@ __device__ __forceinline__ int anew(int v) {
 
 __device__ __forceinline__ uint32_t lds_address(const void* p) { return (uint32_t)(uintptr_t)(lds_char*)p; }
 
-// Terms 16 ks + 8 h .. + 7 of one row in device memory (D channels, the others
-// zero), times `sign` (+1 or -1): a B tile whose columns are rows of the matrix.
+// 8 channels from c on of a row of D in device memory; zeros from D on.  Read
+// with no branch, so that the loads of a row are on their way together.
 template <typename T>
-__device__ __forceinline__ Frag<T> row_terms(const T* row, int ks, int D, int lane, float sign) {
-    const int c = 16 * ks + 8 * (lane >> 5);
-    Frag<T> f;
-    if constexpr (sizeof(T) == 2) {
-        u32x4 u = {0u, 0u, 0u, 0u};
-        if (c < D) u = *reinterpret_cast<const u32x4*>(row + c);
-        if (sign < 0.f) u ^= 0x80008000u;
-        f.v = u;
-    } else {
-        f32x4 x = {0.f, 0.f, 0.f, 0.f}, y = x;
-        if (c < D) {
-            x = *reinterpret_cast<const f32x4*>(row + c) * sign;
-            y = *reinterpret_cast<const f32x4*>(row + c + 4) * sign;
-        }
-        f = split8(x, y);
-    }
-    return f;
+struct Eight {
+    u32x4 u[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Eight<T> load_eight(const T* row, int c) {
+    Eight<T> x;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) x.u[i] = reinterpret_cast<const u32x4*>(row + c)[i];
+    return x;
 }
 
-// The lane's half of the terms of a . b, rows of D channels in device memory.
+// Terms 16 ks + 8 h .. + 7, ks < KS, of one row (D > 16 KS - 32 channels, the
+// others zero), times `sign` (+1 or -1): B tiles whose columns are rows of the
+// matrix.
 template <typename T, int KS>
-__device__ __forceinline__ float half_dot(const T* a, const T* b, int D, int lane) {
-    float v = 0.f;
+__device__ __forceinline__ void row_terms(const T* row, int D, int lane, float sign, Frag<T> (&f)[KS]) {
+    Eight<T> x[KS];
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
         const int c = 16 * ks + 8 * (lane >> 5);
-        if (c >= D) continue;
+        x[ks] = load_eight(row, ks < KS - 2 || c < D ? c : 0);
+    }
 #pragma unroll
-        for (int k = 0; k < 8; k += kVec<T>) {
-            float x[kVec<T>], y[kVec<T>];
-            load16(a + c + k, x);
-            load16(b + c + k, y);
+    for (int ks = 0; ks < KS; ++ks) {
+        const int c = 16 * ks + 8 * (lane >> 5);
 #pragma unroll
-            for (int i = 0; i < kVec<T>; ++i) v = fmaf(x[i], y[i], v);
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+            if (ks >= KS - 2 && c >= D) x[ks].u[i] = u32x4{0u, 0u, 0u, 0u};
+            if (sign < 0.f) x[ks].u[i] ^= sizeof(T) == 2 ? 0x80008000u : 0x80000000u;
         }
+        if constexpr (sizeof(T) == 2)
+            f[ks].v = x[ks].u[0];
+        else
+            f[ks] = split8(__builtin_bit_cast(f32x4, x[ks].u[0]), __builtin_bit_cast(f32x4, x[ks].u[1]));
+    }
+}
+
+// The lane's half of the terms of a . b, rows of D > 16 KS - 32 channels in
+// device memory.
+template <typename T, int KS>
+__device__ __forceinline__ float half_dot(const T* a, const T* b, int D, int lane) {
+    Eight<T> x[KS], y[KS];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+        const int c = 16 * ks + 8 * (lane >> 5), at = ks < KS - 2 || c < D ? c : 0;
+        x[ks] = load_eight(a, at);
+        y[ks] = load_eight(b, at);
+    }
+    float v = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+        float part = 0.f;
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t p = x[ks].u[i][j], q = y[ks].u[i][j];
+                if constexpr (sizeof(T) == 2) {
+                    part = fmaf(__builtin_bit_cast(float, p << 16), __builtin_bit_cast(float, q << 16), part);
+                    part = fmaf(__builtin_bit_cast(float, p & 0xFFFF0000u), __builtin_bit_cast(float, q & 0xFFFF0000u), part);
+                } else {
+                    part = fmaf(__builtin_bit_cast(float, p), __builtin_bit_cast(float, q), part);
+                }
+            }
+        v += ks < KS - 2 || 16 * ks + 8 * (lane >> 5) < D ? part : 0.f;
     }
     return v;
 }
@@ -438,7 +471,8 @@ __device__ __forceinline__ Work find_work(const Args& a, int slot, int lane) {
     const int segments = a.n_seq + 2;
     Work w;
     if (segments <= 64) {
-        const int start = bound_of(a, lane), len = max(bound_of(a, lane + 1) - start, 0);   // 0 past the last one
+        const int start = bound_of(a, lane), next = __shfl_down(start, 1);
+        const int len = max((lane < 63 ? next : a.T) - start, 0);   // 0 past the last one
         const bool pad = lane == 0 || lane == segments - 1;
         const int tiles = (len + SIZE - 1) / SIZE, real = pad ? 0 : tiles;
         auto before = [&](int L) {   // tiles of more than L tiles' work

@@ -88,16 +88,14 @@ __global__ void __launch_bounds__(256, occupancy(kDq, sizeof(T), DP)) k_attn_dq(
     const float c = a.scale * kLog2e;
     Frag<T> q[KS], g[KS];
     float delta = 0.f;
+    const float lse = a.lse[stat];
     {
         const long long t = w.start + min(row, w.len - 1);
         const T* qrow = static_cast<const T*>(a.q) + t * a.sq.token + head * a.sq.head;
         const T* grow = static_cast<const T*>(a.g) + t * a.sg.token + head * a.sg.head;
         const T* orow = static_cast<const T*>(a.o) + t * a.so.token + head * a.so.head;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            q[ks] = row_terms(qrow, ks, a.D, lane, 1.f);
-            g[ks] = row_terms(grow, ks, a.D, lane, 1.f);
-        }
+        row_terms(qrow, a.D, lane, 1.f, q);
+        row_terms(grow, a.D, lane, 1.f, g);
         delta = half_dot<T, KS>(grow, orow, a.D, lane);
         // with the bits that were rounded off out: 8 of them alone move dS by as much as its own rounding
         if (sizeof(T) == 2 && a.low)
@@ -105,7 +103,7 @@ __global__ void __launch_bounds__(256, occupancy(kDq, sizeof(T), DP)) k_attn_dq(
         delta = both_sum(delta);
         if (split == 0 && live && lane < 32) a.delta[stat] = delta;   // for the other kernel
     }
-    const float lse2 = a.lse[stat] * kLog2e;
+    const float lse2 = lse * kLog2e;
     const int rlane = L::rows_lane(lane), clane = L::cols_lane(lane), half = L::row_of_half(lane), swap = L::cols_swap(lane);
     const int last = a.causal ? min(w.len - 1, row0 + 31) : w.len - 1;   // last key that any of the wave's queries sees
     f32x16 minus;   // dP starts from -delta
@@ -239,19 +237,17 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
     int here = j0;   // first query of the tile being worked on
     copy(begin);
 
-    Frag<T> kf[KS], vf[HOLD ? 1 : KS];
-    Frag<T>* mine = reinterpret_cast<Frag<T>*>(lds + 4 * TILE) + wave * KS * 64 + lane;   // V's place with HOLD
+    Frag<T> kf[KS], vf[KS];   // with HOLD, V waits in shared memory
+    Frag<T>* mine = reinterpret_cast<Frag<T>*>(lds + 4 * TILE) + wave * KS * 64 + lane;   // its place there
     {
         const long long t = w.start + min(key, w.len - 1);
         const T* krow = static_cast<const T*>(a.k) + t * a.sk.token + kvh * a.sk.head;
         const T* vrow = static_cast<const T*>(a.v) + t * a.sv.token + kvh * a.sv.head;
+        row_terms(krow, a.D, lane, 1.f, kf);
+        row_terms(vrow, a.D, lane, 1.f, vf);
+        if constexpr (HOLD) {
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            kf[ks] = row_terms(krow, ks, a.D, lane, 1.f);
-            if constexpr (HOLD)
-                mine[64 * ks] = row_terms(vrow, ks, a.D, lane, 1.f);   // read by this lane alone: no barrier
-            else
-                vf[ks] = row_terms(vrow, ks, a.D, lane, 1.f);
+            for (int ks = 0; ks < KS; ++ks) mine[64 * ks] = vf[ks];   // read by this lane alone: no barrier
         }
     }
     const int rlane = L::rows_lane(lane), clane = L::cols_lane(lane), swap = L::cols_swap(lane);
@@ -287,7 +283,7 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
 #pragma unroll
             for (int r = 0; r < 16; ++r) dp[r] = st[ROWS + 8 * (r >> 2) + (r & 3)];
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) mma(L::rows(qt + TILE, 0, ks), HOLD ? mine[64 * ks] : vf[HOLD ? 0 : ks], dp);
+            for (int ks = 0; ks < KS; ++ks) mma(L::rows(qt + TILE, 0, ks), HOLD ? mine[64 * ks] : vf[ks], dp);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int r = 0; r < 16; ++r) {

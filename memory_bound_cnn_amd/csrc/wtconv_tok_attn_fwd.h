@@ -97,8 +97,7 @@ __global__ void __launch_bounds__(256, occupancy(kFwd, sizeof(T), DP)) k_attn_fw
     Frag<T> q[KS];
     {
         const T* qrow = static_cast<const T*>(a.q) + (long long)(w.start + min(row, w.len - 1)) * a.sq.token + head * a.sq.head;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) q[ks] = row_terms(qrow, ks, a.D, lane, a.scale < 0.f ? -1.f : 1.f);
+        row_terms(qrow, a.D, lane, a.scale < 0.f ? -1.f : 1.f, q);
     }
     f32x16 o[DB] = {};
     const int rlane = L::rows_lane(lane), clane = L::cols_lane(lane), half = L::row_of_half(lane), swap = L::cols_swap(lane);
