@@ -14,7 +14,7 @@
 // product six of theirs: the three left out are below 2^-24 of it, so this is
 // float32's own precision in 192 cycles, where the float32 instructions take
 // 512 (4 sequences of 2048 tokens, 12 heads of 64: forward, dq, dk and dv 425,
-// 608 and 832 us with those, 271, 420 and 600 so).
+// 608 and 832 us with those, 251, 382 and 512 so).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -453,15 +453,22 @@ __device__ __forceinline__ int bound_of(const Args& a, int s) {
     return min(max(a.cu[s - 1], 0), a.T);
 }
 
-// Sum over the wave, the same in every lane.
-__device__ __forceinline__ int wave_sum(int v) {
-    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);   // row_shr 1, 2, 4, 8
-    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row_bcast 15 into rows 1 and 3
-    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // row_bcast 31 into rows 2 and 3
+// Sum and maximum over the wave of values that are not negative, the same in every lane.
+template <typename F>
+__device__ __forceinline__ int wave_join(int v, const F& f) {
+    v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false));   // row_shr 1, 2, 4, 8
+    v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false));
+    v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false));
+    v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false));
+    v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false));   // row_bcast 15 into rows 1 and 3
+    v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false));   // row_bcast 31 into rows 2 and 3
     return __builtin_amdgcn_readlane(v, 63);
+}
+__device__ __forceinline__ int wave_sum(int v) {
+    return wave_join(v, [](int x, int y) { return x + y; });
+}
+__device__ __forceinline__ int wave_max(int v) {
+    return wave_join(v, [](int x, int y) { return max(x, y); });
 }
 
 // LATE: when causal, a sequence's late tiles have the most work (its queries
@@ -478,7 +485,7 @@ __device__ __forceinline__ Work find_work(const Args& a, int slot, int lane) {
         auto before = [&](int L) {   // tiles of more than L tiles' work
             return wave_sum(real > L ? (a.causal ? real - L : real) : 0);
         };
-        int lo = 0, hi = a.T / SIZE + 1, above = 0;   // the slot's work is in lo + 1 .. hi; above = before(hi)
+        int lo = 0, hi = wave_max(real), above = 0;   // the slot's work is in lo + 1 .. hi; above = before(hi)
         const int all = before(0);
         int at;
         if (slot < all) {

@@ -11,10 +11,10 @@
 //
 // Bound by the matrix units with the exponentials and roundings between their
 // products.  bfloat16, dq and dk/dv: 48 images of 49 to 1024 tokens, 6 heads of
-// 64, 76 and 86 us (650 and 765 TFLOP/s of the products each makes); 4 x 4096,
-// 12 heads of 64, 303 and 408 us (1020, 1010); causal 3 x 3500..8192, 16 heads on
-// 4 of 128, 495 and 755 us (1045, 915) with 27 us of joins; float32 32 x 196, 6
-// heads on 3 of 64, 39 and 45 us (73, 84) with 7 us of joins.
+// 64, 69 and 84 us (715 and 780 TFLOP/s of the products each makes); 4 x 4096,
+// 12 heads of 64, 303 and 411 us (1020, 1000); causal 3 x 3500..8192, 16 heads on
+// 4 of 128, 481 and 680 us (1075, 1015) with 26 us of joins; float32 32 x 196, 6
+// heads on 3 of 64, 35 and 43.5 us (81, 87) with 7 us of joins.
 #pragma once
 
 #include "wtc_tok_attn.h"

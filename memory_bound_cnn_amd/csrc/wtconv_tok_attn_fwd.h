@@ -15,9 +15,9 @@
 //
 // Bound by the matrix units and, about as long again, the exponentials and
 // roundings between the two products.  bfloat16, 48 images of 49 to 1024 tokens,
-// 6 heads of 64: 55 us (600 TFLOP/s); 4 x 4096, 12 heads of 64: 233 us (885); causal 3 x
+// 6 heads of 64: 54 us (610 TFLOP/s); 4 x 4096, 12 heads of 64: 233 us (885); causal 3 x
 // 3500..8192, 16 heads on 4 of 128: 358 us (965); float32, in six products of
-// bfloat16 parts, 32 x 196, 6 heads on 3 of 64: 27 us (70).
+// bfloat16 parts, 32 x 196, 6 heads on 3 of 64: 25 us (75).
 #pragma once
 
 #include "wtc_tok_attn.h"
