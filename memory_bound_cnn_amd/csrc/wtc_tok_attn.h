@@ -184,10 +184,10 @@ struct Tile {
     }
     static __device__ __forceinline__ void commit(const Load& load, char* tile, int wave, int lane) {
         if constexpr (sizeof(T) == 2) {
-            // every load; as a builtin, so that the compiler knows that its own are done, too, and adds no wait
-            // for what a loop issues after it
-            __builtin_amdgcn_s_waitcnt(0x0F70);
-            asm volatile("" ::: "memory");
+            // the builtin tells the compiler that its own loads are done as well: it then adds no wait for them in a
+            // loop, where it would also be one for the copies.  It knows nothing of the copies, hence the other.
+            __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         } else {
 #pragma unroll
             for (int i = 0; i < kUnits; ++i) {

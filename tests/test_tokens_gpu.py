@@ -451,6 +451,57 @@ def test_attention_keeps_sequences_apart(dtype):
             assert torch.equal(a[lo:hi], b[lo:hi])
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
+def test_attention_split_scales(scale, dtype):
+    q, k, v, cu = pack([1600], 1, 1, 64, dtype, seed=21)
+    attn_check(q, k, v, cu, False, scale, what=f"split scale {scale}")
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_attention_split_rising_maxima(dtype):
+    """Parts of the keys whose maxima lie far apart: the weights of most vanish."""
+    q, k, v, cu = pack([1600], 1, 1, 64, dtype, seed=22)
+    k = (k.float().abs() * torch.linspace(0.01, 6, 1600, device=DEV)[:, None, None]).to(k.dtype)
+    q = q.float().abs().to(q.dtype)
+    attn_check(q, k, v, cu, False, what="split rising")
+    attn_check(q, k.flip(0).contiguous(), v, cu, False, what="split falling")
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_attention_split_keeps_sequences_apart(dtype):
+    """As above for sequences whose keys are split: not even through a
+    workspace that held NaN, on another stream, and into outputs with strides."""
+    q, k, v, _ = pack([1700], 1, 1, 64, dtype, seed=23)
+    cu = torch.tensor([5, 805, 1690], dtype=torch.int32, device=DEV)
+    dout = normal(gen(24), *q.shape, dtype=q.dtype)
+
+    def all_of(q, k, v, dout, wide):
+        d = tb._attn_desc(q, k, v, cu, False, None)
+        need = [f(tb.ctypes.addressof(d)) for f in (tb._load().wtconv_attention_forward_workspace,
+                                                    tb._load().wtconv_attention_backward_workspace)]
+        assert need[0] > 0
+        ws = [torch.full((n // 4 + 1,), float("nan"), device=DEV).view(torch.uint8) for n in need]
+        out = torch.full((q.shape[0], 1, 64 + wide), 7.0, device=DEV, dtype=q.dtype)[..., :64]
+        _, lse = tb.wtconv_attention_forward(q, k, v, cu, False, want_lse=True, out=out, workspace=ws[0])
+        return (out, lse.t()) + tb.wtconv_attention_backward(q, k, v, out, lse, dout, cu, False, workspace=ws[1])
+
+    clean = all_of(*(t.contiguous() for t in (q, k, v, dout)), 0)
+    assert not clean[0][:5].any() and not clean[0][1690:].any() and torch.isposinf(clean[1][:5]).all()
+    bad = [t.contiguous().clone() for t in (q, k, v, dout)]
+    for i, t in enumerate(bad):
+        t[:5] = float("nan")
+        t[1690:] = float("inf")
+        t[900 + 300 * i % 700] = float("nan") if i % 2 else float("-inf")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = all_of(*bad, 8)
+    torch.cuda.current_stream().wait_stream(s)
+    for a, b in zip(clean, got):
+        assert torch.equal(a[5:805], b[5:805]) and torch.equal(a[:5], b[:5]) and torch.equal(a[1690:], b[1690:])
+
+
 def test_attention_repeatable_and_other_streams():
     q, k, v, cu = pack([300, 41, 777], 4, 2, 64, "bf16", seed=7)
     dout = normal(gen(8), *q.shape, dtype=q.dtype)
