@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(256, occupancy(kDq, sizeof(T), DP)) k_attn_dq(
         if (rows_left <= 0 || (a.causal && j0 > row0 + 31)) continue;
         const char* kt = lds + (j & 1) * (2 * TILE) + rlane;
         const char* kc = lds + (j & 1) * (2 * TILE) + clane;
-        const int limit = a.causal ? min(w.len - 1, row) : w.len - 1;
+        const int seen = (a.causal ? min(w.len - 1, row) : w.len - 1) - j0 - half;
         const bool edge = j0 + KEYS - 1 > (a.causal ? min(w.len - 1, row0) : w.len - 1);
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(256, occupancy(kDq, sizeof(T), DP)) k_attn_dq(
             if (edge) {
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    if (j0 + 32 * kb + L::row_of(r) + half > limit) s[r] = 0.f;
+                    if (32 * kb + L::row_of(r) > seen) s[r] = 0.f;
             }
 #pragma unroll
             for (int t = 0; t < 2; ++t) {

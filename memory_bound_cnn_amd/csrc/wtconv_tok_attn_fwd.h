@@ -120,14 +120,14 @@ __global__ void __launch_bounds__(256, occupancy(kFwd, sizeof(T), DP)) k_attn_fw
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) mma(L::rows(kt, 32 * kb, ks), q[ks], s[kb]);
         __builtin_amdgcn_s_setprio(0);
-        const int limit = a.causal ? min(w.len - 1, row) : w.len - 1;   // last key this query sees
+        const int seen = (a.causal ? min(w.len - 1, row) : w.len - 1) - j0 - half;   // last key of the tile that this query sees
         const bool edge = j0 + KEYS - 1 > (a.causal ? min(w.len - 1, row0) : w.len - 1);
         if (edge) {
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    if (j0 + 32 * kb + L::row_of(r) + half > limit) s[kb][r] = -__builtin_inff();
+                    if (32 * kb + L::row_of(r) > seen) s[kb][r] = -__builtin_inff();
         }
         float top = s[0][0];
 #pragma unroll
