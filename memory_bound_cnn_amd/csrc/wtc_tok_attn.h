@@ -294,8 +294,7 @@ __device__ __forceinline__ Eight<T> load_eight(const T* row, int c) {
 // others zero), times `sign` (+1 or -1): B tiles whose columns are rows of the
 // matrix.
 template <typename T, int KS>
-__device__ __forceinline__ void row_terms(const T* row, int D, int lane, float sign, Frag<T> (&f)[KS]) {
-    Eight<T> x[KS];
+__device__ __forceinline__ void load_row(const T* row, int D, int lane, float sign, Eight<T> (&x)[KS]) {
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
         const int c = 16 * ks + 8 * (lane >> 5);
@@ -309,11 +308,28 @@ __device__ __forceinline__ void row_terms(const T* row, int D, int lane, float s
             if (ks >= KS - 2 && c >= D) x[ks].u[i] = u32x4{0u, 0u, 0u, 0u};
             if (sign < 0.f) x[ks].u[i] ^= sizeof(T) == 2 ? 0x80008000u : 0x80000000u;
         }
-        if constexpr (sizeof(T) == 2)
-            f[ks].v = x[ks].u[0];
-        else
-            f[ks] = split8(__builtin_bit_cast(f32x4, x[ks].u[0]), __builtin_bit_cast(f32x4, x[ks].u[1]));
     }
+}
+template <typename T>
+__device__ __forceinline__ Frag<T> terms_of(const Eight<T>& x) {
+    if constexpr (sizeof(T) == 2)
+        return Frag<T>{x.u[0]};
+    else
+        return split8(__builtin_bit_cast(f32x4, x.u[0]), __builtin_bit_cast(f32x4, x.u[1]));
+}
+template <typename T, int KS>
+__device__ __forceinline__ void row_terms(const T* row, int D, int lane, float sign, Frag<T> (&f)[KS]) {
+    Eight<T> x[KS];
+    load_row(row, D, lane, sign, x);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) f[ks] = terms_of<T>(x[ks]);
+}
+// The same kept as they were loaded, and split anew at each use.
+template <typename T>
+__device__ __forceinline__ Frag<T> terms_anew(Eight<T> x) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) asm volatile("" : "+v"(x.u[i]));
+    return terms_of<T>(x);
 }
 
 // The lane's half of the terms of a . b, rows of D > 16 KS - 32 channels in

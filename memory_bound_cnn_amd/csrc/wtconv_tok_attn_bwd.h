@@ -158,6 +158,10 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
     using L = Tile<T, DP, ROWS>;
     constexpr int TILE = L::kBytes;
     constexpr bool HOLD = kDkvHoldV<T, DP>;
+    // 128 channels of float32: 96 registers each for K's and V's terms are 42 more than there are.  Kept as
+    // they were loaded they take 64, and the split runs beside the products (4 causal sequences of 500 to 1024,
+    // 8 heads: 117 -> 111 us; at 96 channels, which have the registers, 594 -> 640 us for 4 x 2048).
+    constexpr bool RAW = sizeof(T) == 4 && DP > 96;
     constexpr int LDS = max_of(4 * TILE + (HOLD ? 4 * KS * 64 * (int)sizeof(Frag<T>) : 0), 4 * kRowsScratch<float, DP>);
     __shared__ __align__(16) char lds[LDS];   // 2 x (Q tile, dO tile), then V of the four waves
     __shared__ __align__(16) float stats[2][2][ROWS];   // 2 x -lse log2(e), over c where S starts from it, and -delta of the tile's queries
@@ -238,13 +242,19 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
     copy(begin);
 
     Frag<T> kf[KS], vf[KS];   // with HOLD, V waits in shared memory
+    Eight<T> kr[KS], vr[KS];   // with RAW, both are held as they were loaded
     Frag<T>* mine = reinterpret_cast<Frag<T>*>(lds + 4 * TILE) + wave * KS * 64 + lane;   // its place there
     {
         const long long t = w.start + min(key, w.len - 1);
         const T* krow = static_cast<const T*>(a.k) + t * a.sk.token + kvh * a.sk.head;
         const T* vrow = static_cast<const T*>(a.v) + t * a.sv.token + kvh * a.sv.head;
-        row_terms(krow, a.D, lane, 1.f, kf);
-        row_terms(vrow, a.D, lane, 1.f, vf);
+        if constexpr (RAW) {
+            load_row(krow, a.D, lane, 1.f, kr);
+            load_row(vrow, a.D, lane, 1.f, vr);
+        } else {
+            row_terms(krow, a.D, lane, 1.f, kf);
+            row_terms(vrow, a.D, lane, 1.f, vf);
+        }
         if constexpr (HOLD) {
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) mine[64 * ks] = vf[ks];   // read by this lane alone: no barrier
@@ -278,12 +288,12 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
                 s = f32x16{};
             }
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) mma(L::rows(qt, 0, ks), kf[ks], s);
+            for (int ks = 0; ks < KS; ++ks) mma(L::rows(qt, 0, ks), RAW ? terms_anew<T>(kr[ks]) : kf[ks], s);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int r = 0; r < 16; ++r) dp[r] = st[ROWS + 8 * (r >> 2) + (r & 3)];
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) mma(L::rows(qt + TILE, 0, ks), HOLD ? mine[64 * ks] : vf[ks], dp);
+            for (int ks = 0; ks < KS; ++ks) mma(L::rows(qt + TILE, 0, ks), HOLD ? mine[64 * ks] : RAW ? terms_anew<T>(vr[ks]) : vf[ks], dp);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
