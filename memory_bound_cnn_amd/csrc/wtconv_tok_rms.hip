@@ -13,9 +13,9 @@
 // in registers over those rows, and one record of C floats per workgroup is
 // joined in a fixed order by a second kernel.  Rows on their way are held as
 // they lie in memory.  Measured: 65536 x 192 bfloat16 with residual 16.5 us
-// forward (6.1 TB/s; it fits the last-level cache) and 22.2 backward, 8192 x
+// forward (6.1 TB/s; it fits the last-level cache) and 18.2 backward, 8192 x
 // 4096 42.3 and 45.7 us (6.4 and 5.9 TB/s), 100003 x 387 float32 without 58.9
-// and 91.7 us (5.3 and 5.1 TB/s), 49 x 768 5.2 us.
+// and 91.7 us (5.3 and 5.1 TB/s), 49 x 768 4.5 us.
 //
 // The norm is of the sum as the residual stream stores it: the backward pass
 // then reads h alone, and its gradient is that of what was computed.
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(G > 256 ? G : 256) k_rms_backward(RmsArgs a) {
     constexpr int V = kVec<T>, THREADS = G > 256 ? G : 256, RPB = THREADS / G;
     constexpr int WIDTH = G * NV * V;   // >= C
     // The next row is read while this one is worked on, where that leaves three waves on a vector
-    // unit: 8192 x 4096 bfloat16 48.2 -> 45.7 us, but 65536 x 192 (three vectors) 22.2 -> 23.8
+    // unit, which three vectors do not: 8192 x 4096 bfloat16 48.2 -> 45.7 us
     constexpr bool AHEAD = NV <= 2 && G <= 256;
     __shared__ float red[16];
     __shared__ float join[G <= 64 ? 4 * WIDTH : 1];   // dw sums of the four waves
@@ -276,19 +276,29 @@ __global__ void __launch_bounds__(1024) k_rms_join(const float* __restrict__ par
 // The group of G lanes and the NV vectors per lane for a row of n 16-byte
 // vectors: the first of these shapes, in the order of G * NV, that holds it.
 // Where two have the same G * NV the wider group stands here (longer runs of
-// consecutive addresses).
+// consecutive addresses).  Those marked `many` leave no lane idle in rows of 24,
+// 48 and 96 vectors, and are for forward passes of kManyVectors and more, as
+// bfloat16 (without, with the residual): 65536 x 192 9.5 and 16.5 us, 11.4 and
+// 17.0 without them, 25088 x 384 8.4 and 13.3, 9.9 and 13.4; but 49 x 768 4.0
+// and 5.4, 3.7 and 4.5 without.  Nor for the backward pass, whose registers they
+// fill: 22.2 us, 18.2 without them, and 18.0, 15.2.
 struct RmsShape {
     int G, NV;
+    bool many;
 };
-constexpr RmsShape kRmsShapes[] = {{2, 1},  {4, 1},  {8, 1},  {16, 1},  {8, 3},   {32, 1},  {16, 3},   {64, 1},   {32, 3},
-                                   {64, 2}, {64, 3}, {64, 4}, {256, 2}, {256, 3}, {256, 4}, {1024, 2}, {1024, 3}, {1024, 4}};
+constexpr long long kManyVectors = 1 << 17;
+constexpr RmsShape kRmsShapes[] = {{2, 1, false},    {4, 1, false},    {8, 1, false},   {16, 1, false}, {8, 3, true},
+                                   {32, 1, false},   {16, 3, true},    {64, 1, false},  {32, 3, true},  {64, 2, false},
+                                   {64, 3, false},   {64, 4, false},   {256, 2, false}, {256, 3, false}, {256, 4, false},
+                                   {1024, 2, false}, {1024, 3, false}, {1024, 4, false}};
 constexpr int kRmsShapeCount = (int)(sizeof(kRmsShapes) / sizeof(kRmsShapes[0]));
 static_assert(1024 * 4 * kVec<float> >= WTC_RMS_MAX_C && 1024 * 2 * kVec<uint16_t> >= WTC_RMS_MAX_C, "the longest row");
 
-int rms_shape(int C, int dtype) {
+int rms_shape(int C, int dtype, long long forward_rows) {
     const int V = dtype == WTC_BF16 ? kVec<uint16_t> : kVec<float>;
+    const bool many = forward_rows * ((C + V - 1) / V) >= kManyVectors;
     int i = 0;
-    while (kRmsShapes[i].G * kRmsShapes[i].NV * V < C) ++i;
+    while (kRmsShapes[i].G * kRmsShapes[i].NV * V < C || (kRmsShapes[i].many && !many)) ++i;
     return i;
 }
 
@@ -320,14 +330,15 @@ struct BackwardLaunch {
     int parts;
     template <typename T, int G, int NV>
     void operator()() const {
-        hipLaunchKernelGGL((k_rms_backward<T, G, NV>), dim3((unsigned)parts), dim3(G > 256 ? G : 256), 0, st, a);
+        if constexpr (G >= 64 || NV == 1)   // the others are for the forward pass
+            hipLaunchKernelGGL((k_rms_backward<T, G, NV>), dim3((unsigned)parts), dim3(G > 256 ? G : 256), 0, st, a);
     }
 };
 
 }  // namespace
 
 int rms_backward_parts(const wtc_rms_desc* d) {
-    const int G = kRmsShapes[rms_shape(d->C, d->dtype)].G, rpb = (G > 256 ? G : 256) / G;
+    const int G = kRmsShapes[rms_shape(d->C, d->dtype, 0)].G, rpb = (G > 256 ? G : 256) / G;
     // a row to a workgroup: fewer, whose records of C floats are much of the traffic
     const long long blocks = (d->rows + rpb - 1) / rpb, most = G > 64 ? kRmsMaxParts / 2 : kRmsMaxParts;
     return (int)(blocks < most ? blocks : most);
@@ -340,7 +351,7 @@ int launch_rms_forward(const wtc_rms_desc* d, const void* x, const void* r, cons
     a.rows = d->rows; a.x_stride = d->x_stride; a.r_stride = d->r_stride;
     a.C = d->C; a.eps = d->eps; a.inv_C = 1.f / (float)d->C;
     const ForwardLaunch f = {a, reinterpret_cast<hipStream_t>(stream)};
-    const int at = rms_shape(d->C, d->dtype);
+    const int at = rms_shape(d->C, d->dtype, d->rows);
     if (d->dtype == WTC_BF16)
         rms_dispatch<uint16_t>(at, f);
     else
@@ -358,7 +369,7 @@ int launch_rms_backward(const wtc_rms_desc* d, const void* dy, const void* dh, c
     const int n = rms_backward_parts(d);
     if (n > 0) {
         const BackwardLaunch f = {a, st, n};
-        const int at = rms_shape(d->C, d->dtype);
+        const int at = rms_shape(d->C, d->dtype, 0);
         if (d->dtype == WTC_BF16)
             rms_dispatch<uint16_t>(at, f);
         else

@@ -44,7 +44,8 @@ def rms_ref(x, w, r, eps):
 
 
 RMS_SHAPES = [(1, 1), (1, 768), (3, 7), (5, 8), (49, 96), (130, 33), (257, 192), (7, 387), (300, 64), (64, 1024),
-              (33, 1025), (9, 2048), (11, 2056), (5, 4100), (3, 8192), (2, 16384), (4, 5000), (1000, 16), (31, 640)]
+              (33, 1025), (9, 2048), (11, 2056), (5, 4100), (3, 8192), (2, 16384), (4, 5000), (1000, 16), (31, 640),
+              (5600, 192), (5601, 91), (2803, 381), (1400, 768)]   # the last four: other shapes of lanes and vectors
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
@@ -82,7 +83,8 @@ def test_rms_norm_forward_backward(rows, C, residual, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
-@pytest.mark.parametrize("rows,C", [(1, 1), (49, 768), (7, 387), (130, 33), (5, 4100), (3, 16384), (64, 24)])
+@pytest.mark.parametrize("rows,C", [(1, 1), (49, 768), (7, 387), (130, 33), (5, 4100), (3, 16384), (64, 24),
+                                    (5600, 192), (2803, 381), (1400, 768)])
 def test_rms_norm_fp8(rows, C, dtype):
     """The scale to float32, the values to half a step of e4m3 (three bits after
     the leading one; 2^-9 below 2^-6) plus the rounding of y and its scale."""
