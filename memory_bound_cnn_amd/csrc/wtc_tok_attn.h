@@ -200,9 +200,10 @@ struct Tile {
             }
         }
     }
-    // 16 bytes a lane from base + off to 1024 consecutive bytes at dst.
+    // 16 bytes a lane from base + off to 1024 consecutive bytes at dst.  A scalar register that a vector instruction
+    // wrote may be an address five instructions later; the compiler sees to that outside of asm only.
     static __device__ __forceinline__ void dma(uint32_t dst, const char* base, uint32_t off) {
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2"
                      :
                      : "s"(__builtin_amdgcn_readfirstlane(dst)), "v"(off), "s"(base)
                      : "memory");
