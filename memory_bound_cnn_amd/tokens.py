@@ -12,6 +12,11 @@ current stream and have gradients (first ones only), except ``rms_norm_fp8``.
 They go through the extension module ``_tokens`` (csrc/wtconv_tok_torch.cpp),
 which is loaded by the first call and must have been built; ``token_binding``
 has the same kernels without gradients, as the C functions.
+
+Steps of small packs wait for the host, and most of that for PyTorch's handing
+the backward pass to a thread of its own: within
+``torch.autograd.set_multithreading_enabled(False)`` a forward and a backward
+pass of 8 tokens take 32 us (norm) and 31 us (attention) instead of 75 and 72.
 """
 
 import torch
