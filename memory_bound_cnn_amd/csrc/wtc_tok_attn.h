@@ -206,7 +206,7 @@ struct Tile {
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2"
                      :
                      : "s"(__builtin_amdgcn_readfirstlane(dst)), "v"(off), "s"(base)
-                     : "memory");
+                     : "m0", "memory");
     }
 
     // The lane's part of the addresses that rows() and cols() read.
