@@ -125,7 +125,13 @@ class TokenBlock(torch.nn.Module):
         h = x + dropout(proj(attention(rotary(qkv(norm(x))))))
         out = h + dropout(down(gelu(up(norm(h)))))
     x [T, C], C = heads * D; kv_heads heads of k and v; sections: rotary pairs
-    of each position axis (half of D / 2 each for images unless given)."""
+    of each position axis (half of D / 2 each for images unless given).
+
+    What a pass drops follows from a key that it draws from PyTorch's generator
+    of the block's device: ``torch.manual_seed`` sets it, every block and pass
+    gets its own, and activation checkpointing, which restores that generator,
+    drops the same elements again.  seed tells blocks apart whose generators
+    are in the same state (the ranks of a job that all started from one)."""
 
     def __init__(self, channels, heads, kv_heads=None, sections=None, hidden=None, p=0.0, causal=False, seed=0,
                  device=None, dtype=torch.bfloat16):
@@ -142,19 +148,21 @@ class TokenBlock(torch.nn.Module):
         self.up = torch.nn.Linear(channels, hidden or 4 * channels, **f)
         self.down = torch.nn.Linear(hidden or 4 * channels, channels, **f)
         self.register_buffer("inv_freq", rotary_frequencies(self.sections, device=device))
-        self.register_buffer("rng", torch.tensor([seed, 0], device=device))
+        # generator words of the latest pass: its key, and the offset after those of its two dropouts (0 and 1)
+        self.register_buffer("rng", torch.tensor([0, 2], device=device))
+        self.register_buffer("_to_words", torch.tensor([[seed, -2], [seed, -1]], device=device), persistent=False)
 
-    def _dropout(self, x, residual):
-        if not self.training or self.p == 0.0:
-            return residual + x
-        rng = self.rng.clone()   # this call's words; the next one takes another offset
-        self.rng[1] += 1
-        return dropout(x, self.p, rng, residual)
+    def _dropout(self, x, residual, rng):
+        return residual + x if rng is None else dropout(x, self.p, rng, residual)
 
     def forward(self, x, positions, cu_seqlens):
         T = x.shape[0]
+        rng = (None, None)
+        if self.training and self.p > 0.0:
+            self.rng[0].random_()
+            rng = self.rng + self._to_words   # new memory: it is saved for the backward pass
         qkv = self.qkv(self.norm1(x)).view(T, -1, self.D)
         a = rotary_attention(qkv, self.heads, self.kv_heads, positions, self.inv_freq, self.sections, cu_seqlens,
                              causal=self.causal)
-        h = self._dropout(self.proj(a.reshape(T, -1)), x)
-        return self._dropout(self.down(torch.nn.functional.gelu(self.up(self.norm2(h)))), h)
+        h = self._dropout(self.proj(a.reshape(T, -1)), x, rng[0])
+        return self._dropout(self.down(torch.nn.functional.gelu(self.up(self.norm2(h)))), h, rng[1])

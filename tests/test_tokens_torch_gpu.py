@@ -1,0 +1,79 @@
+"""The token operators inside PyTorch's own machinery: activation checkpointing,
+captured graphs, forward-mode derivatives, traces."""
+
+import pytest
+import torch
+from torch.utils.checkpoint import checkpoint
+
+from memory_bound_cnn_amd import tokens
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def block_and_input(**kw):
+    torch.manual_seed(0)
+    m = tokens.TokenBlock(64, 2, kv_heads=1, p=0.3, device=DEV, dtype=torch.float32, **kw)
+    pos, cu = tokens.image_positions([(5, 7), (4, 9)], device=DEV)
+    return m, torch.randn(71, 64, device=DEV), pos, cu
+
+
+# ------------------------------------------------------------------ the block's dropout
+@pytest.mark.parametrize("reentrant", [False, True])
+def test_checkpointed_block_has_the_blocks_gradients(reentrant):
+    m, x, pos, cu = block_and_input()
+
+    def gradients(call):
+        torch.manual_seed(1)
+        m.zero_grad()
+        t = x.clone().requires_grad_()
+        y = call(t)
+        y.square().sum().backward()
+        return [y.detach(), t.grad] + [p.grad.clone() for p in m.parameters()]
+
+    want = gradients(lambda t: m(t, pos, cu))
+    got = gradients(lambda t: checkpoint(m, t, pos, cu, use_reentrant=reentrant))
+    assert not torch.equal(want[0], m.eval()(x, pos, cu))
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+
+
+def test_block_in_a_graph_drops_other_elements_each_replay():
+    """Dropout's words come from the generator in every replay; what is not
+    dropped is the eager result of the same words."""
+    m, x, pos, cu = block_and_input()
+    seen = []
+    call = tokens.dropout
+
+    def watched(t, p, rng, residual=None):
+        seen.append(rng)
+        return call(t, p, rng, residual)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s), torch.no_grad():
+        m(x, pos, cu)
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    tokens.dropout = watched
+    try:
+        with torch.no_grad(), torch.cuda.graph(graph):
+            out = m(x, pos, cu)
+    finally:
+        tokens.dropout = call
+    assert len(seen) == 2
+    keys = set()
+    for i in range(3):
+        x.copy_(torch.randn(71, 64, device=DEV))
+        graph.replay()
+        torch.cuda.synchronize()
+        keys.add(int(seen[0][0]))
+        words = iter(w.clone() for w in seen)
+        try:
+            tokens.dropout = lambda t, p, rng, residual=None: call(t, p, next(words), residual)
+            with torch.no_grad():
+                want = m(x, pos, cu)
+        finally:
+            tokens.dropout = call
+        assert torch.equal(out, want)
+    assert len(keys) == 3
