@@ -6,6 +6,7 @@
 // The gradients are C++ nodes because a backward pass runs on a thread of
 // PyTorch's own: with Python nodes a step of a small norm spent 128 us on the
 // host, two thirds of it there.
+#include <c10/core/AutogradState.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/extension.h>
@@ -78,6 +79,15 @@ bool wants_grad(const Ts&... ts) {
 }
 bool wants_grad_opt(const OptTensor& t) { return t && wants_grad(*t); }
 
+// A tangent that came with an input would silently not leave with the output.
+bool has_tangent(const Tensor& t) { return t.defined() && t._fw_grad(0).defined(); }
+bool has_tangent(const OptTensor& t) { return t && has_tangent(*t); }
+template <typename... Ts>
+void refuse_tangents(const Ts&... ts) {
+    TORCH_CHECK(!(... || has_tangent(ts)) || !c10::AutogradState::get_tls_state().get_fw_grad_mode(),
+                "the token operators have no forward-mode derivatives");
+}
+
 // A gradient's own gradient would have to be written down; without this it
 // would silently be zero: that by the output's gradient, and where the operator
 // is not linear, that by its inputs.
@@ -149,6 +159,7 @@ struct RmsNorm : torch::autograd::Function<RmsNorm> {
 };
 
 std::tuple<Tensor, OptTensor> rms_norm(const Tensor& x, const Tensor& weight, const OptTensor& residual, double eps) {
+    refuse_tangents(x, weight, residual);
     if (wants_grad(x, weight) || wants_grad_opt(residual)) {
         const variable_list o = RmsNorm::apply(x, weight, residual, eps);
         return {o[0], residual ? OptTensor(o[1]) : std::nullopt};
@@ -159,6 +170,7 @@ std::tuple<Tensor, OptTensor> rms_norm(const Tensor& x, const Tensor& weight, co
 
 std::tuple<Tensor, Tensor, OptTensor> rms_norm_fp8(const Tensor& x, const Tensor& weight, const OptTensor& residual,
                                                    double eps) {
+    refuse_tangents(x, weight, residual);
     TORCH_CHECK_VALUE(!wants_grad(x, weight) && !wants_grad_opt(residual),
                       "rms_norm_fp8 has no gradient; call it under torch.no_grad()");
     const Rms o = rms_forward(x, weight, residual, eps, false, true);
@@ -216,6 +228,7 @@ struct Rotary : torch::autograd::Function<Rotary> {
 
 Tensor rotary(const Tensor& x, const Tensor& positions, const Tensor& inv_freq, std::vector<int64_t> sections,
               bool interleaved) {
+    refuse_tangents(x, inv_freq);
     rotary_check(x, positions, inv_freq, sections);
     if (wants_grad(x)) return Rotary::apply(x, positions, inv_freq, sections, interleaved);
     return rotary_forward(x, positions, inv_freq, sections, interleaved, false);
@@ -320,6 +333,7 @@ double scale_of(std::optional<double> scale, const Tensor& q) {
 
 Tensor attention(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& cu, bool causal,
                  std::optional<double> scale) {
+    refuse_tangents(q, k, v);
     attn_check(q, k, v, cu);
     const double s = scale_of(scale, q);
     if (wants_grad(q, k, v)) return Attention::apply(q, k, v, cu, causal, s);
@@ -375,6 +389,7 @@ struct RotaryAttention : torch::autograd::Function<RotaryAttention> {
 Tensor rotary_attention(const Tensor& qkv, int64_t Hq, int64_t Hk, const Tensor& positions, const Tensor& inv_freq,
                         std::vector<int64_t> sections, const Tensor& cu, bool interleaved, bool causal,
                         std::optional<double> scale) {
+    refuse_tangents(qkv, inv_freq);
     TORCH_CHECK_VALUE(Hq >= 1 && Hk >= 1 && Hq % Hk == 0, Hq, " heads of q do not divide into ", Hk, " of k and v");
     activation(qkv, "qkv", 3);
     TORCH_CHECK_VALUE(qkv.size(1) == Hq + 2 * Hk, "qkv has ", qkv.size(1), " heads, expected ", Hq + 2 * Hk);
@@ -417,6 +432,7 @@ struct Dropout : torch::autograd::Function<Dropout> {
 };
 
 Tensor dropout(const Tensor& x, double p, const Tensor& rng, const OptTensor& residual) {
+    refuse_tangents(x, residual);
     activation(x, "x", -1);
     check_residual(x, residual);
     check(rng, "rng", at::kLong, x, {2});

@@ -77,3 +77,44 @@ def test_block_in_a_graph_drops_other_elements_each_replay():
             tokens.dropout = call
         assert torch.equal(out, want)
     assert len(keys) == 3
+
+
+# ------------------------------------------------------------------ forward-mode derivatives
+def operator_calls():
+    """{name: (call, its activations)}"""
+    g = torch.Generator(device=DEV).manual_seed(0)
+    n = lambda *s: torch.randn(*s, generator=g, device=DEV)
+    w, rng = 1 + 0.1 * n(32), torch.tensor([3, 4], device=DEV)
+    pos, cu = tokens.image_positions([(3, 5), (4, 4)], device=DEV)
+    f = tokens.rotary_frequencies((8, 8), device=DEV)
+    return {
+        "rms_norm": (lambda x, w: tokens.rms_norm(x, w), (n(31, 32), w)),
+        "rms_norm residual": (lambda x, w, r: tokens.rms_norm(x, w, r), (n(31, 32), w, n(31, 32))),
+        "rms_norm_fp8": (lambda x, w, r: tokens.rms_norm_fp8(x, w, r)[:2], (n(31, 32), w, n(31, 32))),
+        "rotary": (lambda x: tokens.rotary(x, pos, f, (8, 8)), (n(31, 2, 32),)),
+        "attention": (lambda q, k, v: tokens.attention(q, k, v, cu), (n(31, 4, 32), n(31, 2, 32), n(31, 2, 32))),
+        "rotary_attention": (lambda x: tokens.rotary_attention(x, 4, 2, pos, f, (8, 8), cu), (n(31, 8, 32),)),
+        "dropout": (lambda x: tokens.dropout(x, 0.5, rng), (n(31, 32),)),
+        "dropout residual": (lambda x, r: tokens.dropout(x, 0.5, rng, r), (n(31, 32), n(31, 32))),
+    }
+
+
+CALLS = ["rms_norm", "rms_norm residual", "rms_norm_fp8", "rotary", "attention", "rotary_attention", "dropout",
+         "dropout residual"]
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_forward_mode_derivatives_are_refused(name):
+    """By every activation alone, whether it requires a gradient or not."""
+    import torch.autograd.forward_ad as fwd
+    call, args = operator_calls()[name]
+    for i in range(len(args)):
+        for requires in (False, True):
+            with fwd.dual_level():
+                a = [t.clone() for t in args]
+                if requires and name != "rms_norm_fp8":
+                    a[i].requires_grad_()
+                a[i] = fwd.make_dual(a[i], torch.ones_like(a[i]))
+                with pytest.raises(RuntimeError, match="forward-mode"):
+                    call(*a)
+    call(*args)
