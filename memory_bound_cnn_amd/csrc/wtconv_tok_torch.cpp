@@ -12,6 +12,7 @@
 #include <torch/extension.h>
 
 #include <cmath>
+#include <limits>
 #include <optional>
 #include <tuple>
 #include <vector>
@@ -98,6 +99,16 @@ void once(const variable_list& grads, bool linear) {
         TORCH_CHECK(!g.defined() || !g.requires_grad(), "the token operators have first derivatives only");
 }
 
+// Sizes that the library takes as int.
+int narrow(int64_t n, const char* what) {
+    TORCH_CHECK_VALUE(n <= std::numeric_limits<int>::max(), what, ": ", n, " do not fit 32 bits");
+    return (int)n;
+}
+int sequences(const Tensor& cu) {
+    TORCH_CHECK_VALUE(cu.dim() == 1 && cu.size(0) >= 1, "cu_seqlens must be [n + 1]");
+    return narrow(cu.size(0), "entries of cu_seqlens") - 1;
+}
+
 // [rows, C] with a contiguous last axis; a view where t allows it.
 Tensor rows(const Tensor& t) {
     const Tensor r = t.dim() == 2 ? t : t.reshape({-1, t.size(-1)});
@@ -112,7 +123,7 @@ Rms rms_forward(const Tensor& x, const Tensor& weight, const OptTensor& residual
     TORCH_CHECK_VALUE(x.dim() >= 1, "x has no axis");
     check_residual(x, residual);
     const int dtype = activation(x, "x", -1);
-    const int64_t C = x.size(-1);
+    const int C = narrow(x.size(-1), "channels of x");
     check(weight, "weight", at::kFloat, x, {C});
     const Tensor xr = rows(x), rr = residual ? rows(*residual) : Tensor();
     const int64_t n = xr.size(0);
@@ -121,7 +132,7 @@ Rms rms_forward(const Tensor& x, const Tensor& weight, const OptTensor& residual
     if (residual) o.h = empty(x.sizes(), x);
     if (keep) o.rstd = empty({n}, x, at::kFloat);
     if (fp8) o.scale = empty(x.sizes().slice(0, x.dim() - 1), x, at::kFloat);
-    const wtc_rms_desc d = {n, xr.stride(0), residual ? rr.stride(0) : 0, 0, (int)C, dtype, fp8, (float)eps};
+    const wtc_rms_desc d = {n, xr.stride(0), residual ? rr.stride(0) : 0, 0, C, dtype, fp8, (float)eps};
     const On on(x);
     raise_on(wtconv_rms_norm_forward(&d, in(xr), in(rr), in_as<float>(weight), out(o.y), out(o.h),
                                      static_cast<float*>(out(o.rstd)), static_cast<float*>(out(o.scale)), on.stream),
@@ -145,8 +156,9 @@ struct RmsNorm : torch::autograd::Function<RmsNorm> {
         const Tensor dh = g.size() > 1 ? g[1] : Tensor();
         if (!g[0].defined()) return {dh, Tensor(), dh, Tensor()};
         const Tensor h = rows(s[0]), dy = rows(g[0]), dhr = dh.defined() ? rows(dh).contiguous() : Tensor();
-        const int64_t n = h.size(0), C = h.size(1);
-        const wtc_rms_desc d = {n, h.stride(0), 0, dy.stride(0), (int)C, h.scalar_type() == at::kFloat ? WTC_FP32 : WTC_BF16,
+        const int64_t n = h.size(0);
+        const int C = (int)h.size(1);   // as the forward pass took it
+        const wtc_rms_desc d = {n, h.stride(0), 0, dy.stride(0), C, h.scalar_type() == at::kFloat ? WTC_FP32 : WTC_BF16,
                                 0, 0.f};
         const size_t bytes = wtconv_rms_norm_backward_workspace(&d);
         const Tensor dx = empty(s[0].sizes(), h), dw = empty({C}, h, at::kFloat), ws = workspace(bytes, h);
@@ -191,6 +203,8 @@ void rotary_run(const Tensor& x, const Tensor& y, const Tensor& positions, const
 void rotary_check(const Tensor& x, const Tensor& positions, const Tensor& inv_freq,
                   const std::vector<int64_t>& sections) {
     activation(x, "x", 3);
+    narrow(x.size(1), "heads of x");
+    narrow(x.size(2), "channels of a head of x");
     TORCH_CHECK_VALUE(!sections.empty() && sections.size() <= WTC_ROTARY_MAX_AXES, sections.size(), " sections: 1 to ",
                       WTC_ROTARY_MAX_AXES, " axes are supported");
     int64_t P = 0;
@@ -252,7 +266,7 @@ struct Setting {
 wtc_attn_desc attn_desc(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& cu, const Setting& s) {
     wtc_attn_desc d = {};
     d.T = q.size(0);
-    d.n_seq = (int)cu.size(0) - 1;
+    d.n_seq = sequences(cu);
     d.Hq = (int)q.size(1);
     d.Hk = (int)k.size(1);
     d.D = (int)q.size(2);
@@ -266,11 +280,13 @@ wtc_attn_desc attn_desc(const Tensor& q, const Tensor& k, const Tensor& v, const
 }
 void attn_check(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& cu) {
     activation(q, "q", 3);
+    narrow(q.size(1), "heads of q");
+    narrow(q.size(2), "channels of a head of q");
     const int64_t Hk = k.dim() == 3 ? k.size(1) : 0;
     check(k, "k", q.scalar_type(), q, {q.size(0), Hk, q.size(2)}, false);
     check(v, "v", q.scalar_type(), q, {q.size(0), Hk, q.size(2)}, false);
     TORCH_CHECK_VALUE(Hk >= 1 && q.size(1) % Hk == 0, q.size(1), " heads of q do not divide into ", Hk, " of k and v");
-    TORCH_CHECK_VALUE(cu.dim() == 1 && cu.size(0) >= 1, "cu_seqlens must be [n + 1]");
+    sequences(cu);
     check(cu, "cu_seqlens", at::kInt, q, cu.sizes());
 }
 struct AttnOut {
@@ -394,7 +410,7 @@ Tensor rotary_attention(const Tensor& qkv, int64_t Hq, int64_t Hk, const Tensor&
     activation(qkv, "qkv", 3);
     TORCH_CHECK_VALUE(qkv.size(1) == Hq + 2 * Hk, "qkv has ", qkv.size(1), " heads, expected ", Hq + 2 * Hk);
     rotary_check(qkv, positions, inv_freq, sections);
-    TORCH_CHECK_VALUE(cu.dim() == 1 && cu.size(0) >= 1, "cu_seqlens must be [n + 1]");
+    sequences(cu);
     check(cu, "cu_seqlens", at::kInt, qkv, cu.sizes());
     const double s = scale_of(scale, qkv);
     if (wants_grad(qkv))

@@ -88,6 +88,12 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _narrow(name, *sizes):
+    """Sizes that the library takes as int: ctypes would take them modulo 2^32."""
+    if any(n >= 1 << 31 for n in sizes):
+        raise ValueError(f"{name}: a size of {max(sizes)} does not fit 32 bits")
+
+
 def _check(t, name, dtype, device, shape, contiguous=False):
     """A device tensor of this type and shape whose last axis is contiguous
     (all of it, if asked)."""
@@ -104,15 +110,17 @@ def _check(t, name, dtype, device, shape, contiguous=False):
         raise ValueError(f"the last axis of {name} must be contiguous")
 
 
-def _activation(t, name, dims):
-    """An activation: its storage type, checked."""
+def _activation(t, name, dims=None):
+    """An activation: its storage type, checked; any shape unless dims is given."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in _DTYPE:
         raise ValueError(f"{name} has dtype {t.dtype}, expected float32 or bfloat16")
-    if t.dim() != dims:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {dims} axes")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    if dims is not None:
+        if t.dim() != dims:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {dims} axes")
+        _narrow(name, *t.shape[1:])
+    if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"the last axis of {name} must be contiguous")
     return _DTYPE[t.dtype]
 
@@ -185,7 +193,7 @@ def wtconv_rotary(x, positions, inv_freq, sections, interleaved=False, inverse=F
 def wtconv_dropout(x, p, rng, residual=None, out=None):
     """residual + x kept with probability 1 - p and divided by it.  rng: int64
     [2] on the device, seed and offset; x, residual, out contiguous."""
-    dtype = _activation(x, "x", x.dim())
+    dtype = _activation(x, "x")
     dev = x.device
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
@@ -211,6 +219,7 @@ def _attn_desc(q, k, v, cu_seqlens, causal, scale):
         raise ValueError(f"{Hq} heads of q do not divide into {Hk} of k and v")
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise ValueError("cu_seqlens must be [n + 1]")
+    _narrow("cu_seqlens", *cu_seqlens.shape)
     _check(cu_seqlens, "cu_seqlens", torch.int32, dev, cu_seqlens.shape, True)
     d = wtc_attn_desc(T, cu_seqlens.shape[0] - 1, Hq, Hk, D, dtype, causal, D ** -0.5 if scale is None else scale)
     d.q, d.k, d.v = q.stride()[:2], k.stride()[:2], v.stride()[:2]

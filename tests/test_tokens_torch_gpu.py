@@ -118,3 +118,27 @@ def test_forward_mode_derivatives_are_refused(name):
                 with pytest.raises(RuntimeError, match="forward-mode"):
                     call(*a)
     call(*args)
+
+
+# ------------------------------------------------------------------ sizes
+def test_sizes_beyond_32_bits_are_refused():
+    """Not taken modulo 2^32: each of these would pass as a small one."""
+    from memory_bound_cnn_amd import token_binding as tb
+    big = (1 << 32) + 8
+    x = torch.zeros(1, device=DEV, dtype=torch.bfloat16)
+    w, f, cu = torch.ones(8, device=DEV), torch.ones(2, device=DEV), torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+    pos, cus = torch.zeros(1, 1, dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV).expand(big)
+    small = x.expand(1, 8, 8)
+    for call in (lambda: tokens.rms_norm(x.expand(1, big), w), lambda: tokens.rms_norm_fp8(x.expand(1, big), w),
+                 lambda: tokens.rotary(x.expand(1, big, 8), pos, f, (2,)),
+                 lambda: tokens.rotary(x.expand(1, 8, big), pos, f, (2,)),
+                 lambda: tokens.attention(x.expand(1, big, 8), small, small, cu),
+                 lambda: tokens.attention(x.expand(1, 8, big), x.expand(1, 8, big), x.expand(1, 8, big), cu),
+                 lambda: tokens.attention(small, small, small, cus),
+                 lambda: tokens.rotary_attention(x.expand(1, big, 8), big - 4, 2, pos, f, (2,), cu),
+                 lambda: tb.wtconv_rms_norm_forward(x.expand(1, big), w),
+                 lambda: tb.wtconv_rotary(x.expand(1, big, 1), pos, f[:0], (0,)),
+                 lambda: tb.wtconv_attention_forward(x.expand(1, big, 1), x.expand(1, 8, 1), x.expand(1, 8, 1), cu),
+                 lambda: tb.wtconv_attention_forward(x.expand(1, 8, 1), x.expand(1, 8, 1), x.expand(1, 8, 1), cus)):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
