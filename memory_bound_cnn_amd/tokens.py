@@ -11,7 +11,9 @@ current stream and have gradients (first ones only), except ``rms_norm_fp8``.
 
 They go through the extension module ``_tokens`` (csrc/wtconv_tok_torch.cpp),
 which is loaded by the first call and must have been built; ``token_binding``
-has the same kernels without gradients, as the C functions.
+has the same kernels without gradients, as the C functions.  The module
+registers them as ``torch.ops.wtconv_tokens``, which is what traces hold: load
+it (any call does) before running one that was saved.
 
 Steps of small packs wait for the host, and most of that for PyTorch's handing
 the backward pass to a thread of its own: within
@@ -43,15 +45,16 @@ def rms_norm(x, weight, residual=None, eps=1e-6):
     """y = h / sqrt(mean(h^2) + eps) * weight over the last axis, h = x +
     residual in x's type.  Returns y, or (y, h) with a residual.  x [..., C]
     float32 or bfloat16, weight [C] float32."""
-    y, h = (_ops or _load()).rms_norm(x, weight, residual, eps)
-    return y if residual is None else (y, h)
+    y, *h = (_ops or _load()).rms_norm(x, weight, residual, eps)
+    return (y, *h) if h else y
 
 
 def rms_norm_fp8(x, weight, residual=None, eps=1e-6):
     """:func:`rms_norm` with its result in 8 bits: (y8, scale, h), y = y8 *
     scale[..., None] with y8 float8_e4m3fn and one float32 scale per row; h is
     None without a residual.  No gradient."""
-    return (_ops or _load()).rms_norm_fp8(x, weight, residual, eps)
+    y, scale, *h = (_ops or _load()).rms_norm_fp8(x, weight, residual, eps)
+    return y, scale, h[0] if h else None
 
 
 def rotary(x, positions, inv_freq, sections, interleaved=False):

@@ -142,3 +142,81 @@ def test_sizes_beyond_32_bits_are_refused():
                  lambda: tb.wtconv_attention_forward(x.expand(1, 8, 1), x.expand(1, 8, 1), x.expand(1, 8, 1), cus)):
         with pytest.raises(ValueError, match="32 bits"):
             call()
+
+
+# ------------------------------------------------------------------ traces
+def flat(r):
+    return [t for t in (r if isinstance(r, tuple) else (r,)) if t is not None]
+
+
+def compare(got, want):
+    assert len(flat(got)) == len(flat(want))
+    for a, b in zip(flat(got), flat(want)):
+        assert a.dtype == b.dtype and torch.equal(a.float(), b.float())
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_traced_functions_compute(name):
+    """A TorchScript trace and a make_fx graph hold the operator: on other
+    inputs they give what a call gives."""
+    from torch.fx.experimental.proxy_tensor import make_fx
+    call, args = operator_calls()[name]
+    others = [t.flip(0) * 2 for t in args]
+    want = call(*others)
+    for traced in (torch.jit.trace(lambda *a: tuple(flat(call(*a))), args, check_trace=False),
+                   make_fx(lambda *a: tuple(flat(call(*a))))(*args)):
+        compare(call(*args), call(*args))     # memory that a trace must not find its answer in
+        compare(traced(*others), want)
+
+
+@pytest.mark.parametrize("name", [n for n in CALLS if n != "rms_norm_fp8"])
+def test_traced_gradients_compute(name):
+    """The gradient of a traced function, and a graph of a function that takes gradients."""
+    from torch.fx.experimental.proxy_tensor import make_fx
+    call, args = operator_calls()[name]
+    others = [t.flip(0) * 2 for t in args]
+
+    def gradients(f, a):
+        a = [t.detach().requires_grad_() for t in a]
+        return torch.autograd.grad(sum(t.float().square().sum() for t in flat(f(*a))), a)
+
+    want = gradients(call, others)
+    traced = torch.jit.trace(lambda *a: tuple(flat(call(*a))), args, check_trace=False)
+    compare(gradients(traced, others), want)
+    compare(make_fx(lambda *a: gradients(call, a))(*args)(*others), want)
+
+
+def test_parts_of_a_gradient_check_their_arguments():
+    """A graph may call them with any tensors."""
+    tokens._load()
+    o = torch.ops.wtconv_tokens
+    x, w, s = torch.randn(5, 32, device=DEV), torch.ones(32, device=DEV), torch.ones(5, device=DEV)
+    x3, cu, pos = x.view(5, 1, 32), torch.tensor([0, 5], dtype=torch.int32, device=DEV), torch.zeros(5, 1, dtype=torch.int32, device=DEV)
+    f = tokens.rotary_frequencies((4,), device=DEV)
+    kept = o._attention_forward(x3, x3, x3, cu, False, None)
+    qkv, qk = x3.expand(5, 3, 32).contiguous(), x3.expand(5, 2, 32).contiguous()
+    for call in (lambda: o._rms_norm_backward(x, None, x, w, s[:4]), lambda: o._rms_norm_backward(x[:4], None, x, w, s),
+                 lambda: o._rms_norm_backward(x, x[:4], x, w, s), lambda: o._rms_norm_backward(x, None, x, w[:31], s),
+                 lambda: o._rms_norm_backward(x.bfloat16(), None, x, w, s), lambda: o._rms_norm_backward(x.cpu(), None, x.cpu(), w, s),
+                 lambda: o._rotary_backward(x3, pos[:4], f, (4,), False), lambda: o._rotary_backward(x3, pos, f, (17,), False),
+                 lambda: o._attention_backward(x3, x3, x3, x3[:4], kept, cu, False, None),
+                 lambda: o._attention_backward(x3[:4], x3, x3, x3, kept, cu, False, None),
+                 lambda: o._attention_backward(x3, x3, x3, x3, [kept[0]], cu, False, None),
+                 lambda: o._attention_backward(x3, x3, x3, x3, [kept[0][:4], kept[1]], cu, False, None),
+                 lambda: o._attention_backward(x3, x3, x3, x3, [kept[0], kept[1][:, :4]], cu, False, None),
+                 lambda: o._attention_backward(x3, x3, x3, x3, [*kept, x3], cu, False, None),
+                 lambda: o._rotary_attention_backward(x3, qkv, qk[:, :1], kept, 1, 1, pos, f, (4,), cu, False, False, None),
+                 lambda: o._rotary_attention_backward(x3, qkv[:, :2], qk, kept, 1, 1, pos, f, (4,), cu, False, False, None)):
+        with pytest.raises(ValueError):
+            call()
+    dy = x.clone().requires_grad_()
+    dx, _ = o._rms_norm_backward(dy, None, x, w, s)
+    with pytest.raises(RuntimeError, match="not implemented"):
+        dx.sum().backward()
+
+
+def test_lazily_negated_inputs():
+    """Memory that stands for its negative (as the imaginary part of a conjugate does)."""
+    x, w = torch.randn(5, 32, device=DEV), torch.ones(32, device=DEV)
+    assert torch.equal(tokens.rms_norm(torch._neg_view(x), w), tokens.rms_norm(-x, w))
+    assert torch.equal(tokens.dropout(torch._neg_view(x), 0.0, torch.zeros(2, dtype=torch.int64, device=DEV)), -x)
