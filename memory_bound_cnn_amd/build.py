@@ -4,10 +4,12 @@
 
 Every HIP source is compiled with packed-FP32 instructions disabled; the
 objects are linked into memory_bound_cnn_amd/libwtconv.so.  The PyTorch module
-of the token operators, host code alone, is linked to it as _tokens.so.
+of the token operators, host code alone, is linked to it as _tokens.so; it is
+left out where there is no PyTorch for ROCm, which the library does not need.
 """
 import concurrent.futures
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -19,7 +21,7 @@ TORCH_OUT = os.path.join(HERE, "_tokens.so")
 OBJDIR = os.path.join(HERE, "_build")
 ARCH = os.environ.get("WTC_OFFLOAD_ARCH", "gfx950")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
-CXX = os.environ.get("CXX", "g++")
+CXX = os.environ.get("CXX") or ("g++" if shutil.which("g++") else os.path.join(os.path.dirname(HIPCC), "amdclang++"))
 
 COMMON = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
@@ -47,8 +49,14 @@ def _compile(src):
 
 
 def _compile_torch():
-    """The object file of the PyTorch module and what it is linked with."""
-    import torch
+    """The object file of the PyTorch module and what it is linked with; None
+    without a PyTorch for ROCm."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    if torch.version.hip is None:
+        return None
     base = os.path.dirname(torch.__file__)
     obj = os.path.join(OBJDIR, "wtconv_tok_torch.cpp.o")
     inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
@@ -80,6 +88,9 @@ def build(verbose=False):
             if err.strip():
                 print(err, file=sys.stderr)
     _link([HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}"] + objs, OUT)
+    if torch_part.result() is None:
+        print("no PyTorch for ROCm here: _tokens.so (the token operators' PyTorch module) is not built", file=sys.stderr)
+        return OUT
     obj, libs = torch_part.result()
     _link([CXX, "-shared", "-fPIC", obj, "-L" + HERE, "-l:" + os.path.basename(OUT), "-Wl,-rpath,$ORIGIN"] + libs,
           TORCH_OUT)
