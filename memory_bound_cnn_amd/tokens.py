@@ -111,13 +111,25 @@ def image_positions(sizes, device=None):
 
 
 # ------------------------------------------------------------------ modules
+def _keep_dtype(fn):
+    """A module's conversion that leaves types alone: what the operators take as
+    float32 is not rounded by ``module.to(torch.bfloat16)``."""
+    def convert(t):
+        new = fn(t)
+        return new if new.dtype == t.dtype else t.to(new.device)
+    return convert
+
+
 class RMSNorm(torch.nn.Module):
-    """:func:`rms_norm` with its weight."""
+    """:func:`rms_norm` with its weight, which stays float32."""
 
     def __init__(self, channels, eps=1e-6, device=None):
         super().__init__()
         self.eps = eps
         self.weight = torch.nn.Parameter(torch.ones(channels, dtype=torch.float32, device=device))
+
+    def _apply(self, fn, recurse=True):
+        return super()._apply(_keep_dtype(fn), recurse)
 
     def forward(self, x, residual=None):
         return rms_norm(x, self.weight, residual, self.eps)
@@ -155,8 +167,16 @@ class TokenBlock(torch.nn.Module):
         self.register_buffer("rng", torch.tensor([0, 2], device=device))
         self.register_buffer("_to_words", torch.tensor([[seed, -2], [seed, -1]], device=device), persistent=False)
 
+    def _apply(self, fn, recurse=True):
+        inv_freq = self.inv_freq
+        super()._apply(fn, recurse)
+        self.inv_freq = _keep_dtype(fn)(inv_freq)
+        return self
+
     def _dropout(self, x, residual, rng):
-        return residual + x if rng is None else dropout(x, self.p, rng, residual)
+        if rng is None:
+            return residual + x
+        return dropout(x.to(residual.dtype), self.p, rng, residual)   # another type under autocast
 
     def forward(self, x, positions, cu_seqlens):
         T = x.shape[0]

@@ -16,6 +16,7 @@ def plain(monkeypatch):
     words = []
 
     def dropout(x, p, rng, residual=None):
+        assert residual is None or residual.dtype == x.dtype
         words.append(tuple(rng.tolist()))
         g = torch.Generator().manual_seed(hash(words[-1]) % (1 << 62))
         kept = x * (torch.rand(x.shape, generator=g) >= p) / (1 - p)
@@ -87,3 +88,32 @@ def test_the_generator_decides(plain):
         torch.manual_seed(seed)
         out.append(m(x, None, None))
     assert torch.equal(out[0], out[1]) and not torch.equal(out[0], out[2])
+
+
+def test_norms_and_frequencies_stay_float32(plain):
+    """The operators take float32 parameters whatever the activations' type; a
+    conversion of the module must not round them either."""
+    torch.manual_seed(0)
+    m = block()
+    with torch.no_grad():
+        m.norm1.weight.add_(torch.randn(C) * 0.1)
+    weight, f = m.norm1.weight.clone(), m.inv_freq.clone()
+    for convert in (lambda: m.to(torch.bfloat16), lambda: m.bfloat16(), lambda: m.double(), lambda: m.to(torch.bfloat16)):
+        assert convert() is m
+        assert m.norm1.weight.dtype == m.inv_freq.dtype == torch.float32 and isinstance(m.norm1.weight, torch.nn.Parameter)
+        assert torch.equal(m.norm1.weight, weight) and torch.equal(m.inv_freq, f)
+        assert "inv_freq" in m.state_dict()
+    assert m.qkv.weight.dtype == torch.bfloat16 and m.rng.dtype == torch.int64
+    assert m(torch.randn(T, C, dtype=torch.bfloat16), None, None).dtype == torch.bfloat16
+    n = tokens.RMSNorm(C).to("meta", torch.bfloat16)
+    assert n.weight.dtype == torch.float32 and n.weight.is_meta
+
+
+@pytest.mark.parametrize("train", [False, True])
+def test_block_under_autocast(plain, train):
+    m, x = block().train(train), torch.randn(T, C)
+    with torch.autocast("cpu", torch.bfloat16):
+        y = m(x, None, None)
+    assert y.dtype == torch.float32
+    y.sum().backward()
+    assert all(p.grad is not None and torch.isfinite(p.grad).all() for p in m.parameters())
