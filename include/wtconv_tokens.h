@@ -58,7 +58,9 @@ typedef struct {
  * NULL (kept for the backward pass).
  * fp8 = 1: y is one byte per element (e4m3, largest value 448), scale [rows]
  *   scale = max(max_c |y| / 448, 2^-100),   y8 = e4m3(y / scale)
- * (an all-zero row has y8 = 0).  scale is NULL when fp8 = 0. */
+ * (an all-zero row has y8 = 0; the quotient is y times scale's rounded
+ * reciprocal, within two roundings of float32 before the 8 bits' own; a NaN is
+ * no maximum: it stays a NaN in y8 alone).  scale is NULL when fp8 = 0. */
 int wtconv_rms_norm_forward(const wtc_rms_desc* d, const void* x, const void* residual, const float* weight, void* y,
                             void* h, float* rstd, float* scale, void* stream);
 
@@ -149,7 +151,11 @@ typedef struct {
  * rounded off out (bfloat16 only), kept for a backward pass whose row sums of
  * dout . out then have 16 bits of out.  Tensors are 16-byte aligned.  A value
  * that is not finite never reaches another sequence; inside its sequence it may
- * reach every row.
+ * reach every row.  float32 values above bfloat16's largest (3.3895e38) count as
+ * infinite, and results that an infinity would leave infinite may be NaN.
+ * Speed: with few tiles (heads and 128 queries) a tile's keys are shared by
+ * workgroups when the mean length T / n_seq is long; leave out empty sequences
+ * and those of few tokens where one long sequence should be.
  * The workspace holds partial results where a short pack's keys are split over
  * workgroups (0 bytes, and NULL is taken, where they are not).
  * WTC_ESHAPE: more than about 2^30 / Hq tokens (2^23 workgroups). */

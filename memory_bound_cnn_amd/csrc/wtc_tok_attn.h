@@ -385,7 +385,10 @@ __device__ __forceinline__ float both_sum(float v) {
 // rows 0 .. rows - 1 of D channels, `stride` elements apart.  They pass through
 // shared memory, a place of the wave's own (`at`, kRowsScratch bytes that
 // nothing else uses now), so that a store has whole rows of 16-byte chunks
-// instead of 8 bytes of 32 rows each.
+// instead of 8 bytes of 32 rows each.  The 8-byte writes of bfloat16 rows on
+// their way in are the only accesses that meet a bank twice: 53 cycles for a
+// wave's 32 rows of 64 channels (SQ_LDS_BANK_CONFLICT counts them once in dq,
+// twice in the forward pass with out_low and in dk and dv), float32's none in 128.
 template <typename T, int DP>
 constexpr int kScratchRow = DP * (int)sizeof(T) + 16;   // 16 bytes more: rows begin in different banks
 template <typename T, int DP>

@@ -32,6 +32,14 @@ Args args_of(const wtc_attn_desc* d, const void* q, const void* k, const void* v
 //   causal 4096, 16 of 128 (512 tiles): forward 103 us, 104 in 2; dq 134, 148
 //   causal 3 x 3500..8192, 16 on 4 of 128 (552 key tiles): dk and dv 843 us in 4, 795 in 2
 //   causal 4 x 2000..4096, 8 of 96 (800 key tiles): dk and dv 164 us, 198 in 2
+// Around kWantedCausalKeys (split in 2 up to 575 key tiles), the backward pass:
+//   causal 8192, 9 to 12 of 128 (576, 640, 704, 768): 605, 633, 663, 688 us, 584, 624, 681, 720 in 2
+//   causal 4 x 3000, 6 and 7 of 96 (576, 672): 188, 199 us, 207, 229 in 2
+//   causal 8 x 2048, 5 of 64 (640): 111 us, 131 in 2; 4 x 4096, 5 of 64 (640): 204, 204
+// The lengths themselves are on the device: the rule knows their mean, with empty
+// sequences counted.  One of 8192 tokens and one head takes 43 us forward and 95
+// backward alone, but 113 and 331 beside 63 empty ones, 15 of one token or 61 of
+// 64, where it is not split.
 constexpr int kWanted = 512, kWantedCausal = 820, kWantedCausalKeys = 1150, kLeast = 6, kMostSplits = 16;
 int splits_of(const wtc_attn_desc* d, int wanted, int heads, int together) {
     if (d->T == 0 || d->n_seq == 0) return 1;

@@ -10,11 +10,12 @@
 // both are split as the forward pass is, and their partial sums joined.
 //
 // Bound by the matrix units with the exponentials and roundings between their
-// products.  bfloat16, dq and dk/dv: 48 images of 49 to 1024 tokens, 6 heads of
-// 64, 69 and 84 us (715 and 780 TFLOP/s of the products each makes); 4 x 4096,
-// 12 heads of 64, 303 and 411 us (1020, 1000); causal 3 x 3500..8192, 16 heads on
-// 4 of 128, 481 and 680 us (1075, 1015) with 26 us of joins; float32 32 x 196, 6
-// heads on 3 of 64, 35 and 43.5 us (81, 87) with 7 us of joins.
+// products.  Means of 20 training steps (the fastest up to 18 % less),
+// bfloat16, dq and dk/dv: 48 images of 49 to 1024 tokens, 6 heads of 64, 83 and
+// 103 us (595 and 635 TFLOP/s of the products each makes); 4 x 4096, 12 heads of
+// 64, 320 and 441 us (965, 935); causal 3 x 3500..8192, 16 heads on 4 of 128, 501
+// and 717 us (1035, 965) with 26 us of joins; float32 32 x 196, 6 heads on 3 of
+// 64, 36 and 44 us (79, 85) with 7 us of joins.
 #pragma once
 
 #include "wtc_tok_attn.h"
@@ -165,8 +166,9 @@ __global__ void __launch_bounds__(256, occupancy(kDkv, sizeof(T), DP)) k_attn_dk
     constexpr int LDS = max_of(4 * TILE + (HOLD ? 4 * KS * 64 * (int)sizeof(Frag<T>) : 0), 4 * kRowsScratch<float, DP>);
     __shared__ __align__(16) char lds[LDS];   // 2 x (Q tile, dO tile), then V of the four waves
     __shared__ __align__(16) float stats[2][2][ROWS];   // 2 x -lse log2(e), over c where S starts from it, and -delta of the tile's queries
-    // S starts from -lse log2(e) / c and dP from -delta, which saves their subtraction.  Not S in
-    // float32: it is then rounded at lse's size (dk and dv 2.5 times the error)
+    // S starts from -lse log2(e) / c and dP from -delta, which saves their subtraction.  S is then rounded at
+    // lse's size: P is off by |lse| log2(e) 2^-24, less than its rounding to bfloat16 (2^-8) up to |lse| = 2^15.
+    // Not so in float32 (dk and dv 2.5 times the error)
     constexpr bool START = sizeof(T) == 2;
     static_assert(LDS + 4 * ROWS * 4 <= 160 * 1024, "shared memory");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);

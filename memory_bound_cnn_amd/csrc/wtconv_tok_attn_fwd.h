@@ -14,10 +14,11 @@
 // kernel joins them.
 //
 // Bound by the matrix units and, about as long again, the exponentials and
-// roundings between the two products.  bfloat16, 48 images of 49 to 1024 tokens,
-// 6 heads of 64: 54 us (610 TFLOP/s); 4 x 4096, 12 heads of 64: 233 us (885); causal 3 x
-// 3500..8192, 16 heads on 4 of 128: 358 us (965); float32, in six products of
-// bfloat16 parts, 32 x 196, 6 heads on 3 of 64: 25 us (75).
+// roundings between the two products.  Means of 20 training steps (the
+// fastest up to 18 % less): bfloat16, 48 images of 49 to 1024 tokens, 6 heads of
+// 64: 66 us (500 TFLOP/s); 4 x 4096, 12 heads of 64: 253 us (815); causal 3 x
+// 3500..8192, 16 heads on 4 of 128: 374 us (925); float32, in six products of
+// bfloat16 parts, 32 x 196, 6 heads on 3 of 64: 26 us (71).
 #pragma once
 
 #include "wtc_tok_attn.h"

@@ -7,8 +7,8 @@
 // 32 x 32 bits, which run at a quarter of the vector rate: with 32 bits for
 // each element they alone would take longer than the 6 bytes an element moves
 // (bfloat16 with a residual).  The bound is device memory, 3 N e bytes with a
-// residual and 2 N e without: 100663296 bfloat16 103 and 69.5 us (5.9 and 5.8
-// TB/s), 50331648 float32 109 and 71 (5.6 and 5.7).
+// residual and 2 N e without.  Means of 20 training steps: 100663296 bfloat16 109
+// and 76 us (5.5 and 5.3 TB/s), 50331648 float32 114 and 69 (5.3 and 5.9).
 #include <hip/hip_runtime.h>
 
 #include "wtc_tok_device.h"

@@ -12,10 +12,11 @@
 // registers, so that it is read once per workgroup; the backward pass sums dw
 // in registers over those rows, and one record of C floats per workgroup is
 // joined in a fixed order by a second kernel.  Rows on their way are held as
-// they lie in memory.  Measured: 65536 x 192 bfloat16 with residual 16.5 us
-// forward (6.1 TB/s; it fits the last-level cache) and 18.2 backward, 8192 x
-// 4096 42.3 and 45.7 us (6.4 and 5.9 TB/s), 100003 x 387 float32 without 58.9
-// and 91.7 us (5.3 and 5.1 TB/s), 49 x 768 4.5 us.
+// they lie in memory.  Measured, means of 20 training steps: 65536 x 192
+// bfloat16 with residual 17.5 us forward (5.8 TB/s; it fits the last-level
+// cache) and 19.4 backward, 8192 x 4096 46.5 and 46.9 us (5.8 and 5.7 TB/s),
+// 100003 x 387 float32 without 57.6 and 99.2 us (5.4 and 4.7 TB/s), 49 x 768
+// 4.6 us.
 //
 // The norm is of the sum as the residual stream stores it: the backward pass
 // then reads h alone, and its gradient is that of what was computed.
@@ -280,7 +281,12 @@ __global__ void __launch_bounds__(1024) k_rms_join(const float* __restrict__ par
 // 48 and 96 vectors, and are for forward passes of kManyVectors and more, as
 // bfloat16 (without, with the residual): 65536 x 192 9.5 and 16.5 us, 11.4 and
 // 17.0 without them, 25088 x 384 8.4 and 13.3, 9.9 and 13.4; but 49 x 768 4.0
-// and 5.4, 3.7 and 4.5 without.  Nor for the backward pass, whose registers they
+// and 5.4, 3.7 and 4.5 without.  Around kManyVectors, 192 channels in a graph:
+// 5461 rows (2^17 vectors) 3.8 and 5.2, 3.3 and 4.0 without, 8192 rows 3.5 and
+// 4.6, 3.6 and 4.6, 10922 rows 4.1 and 5.8, 4.3 and 5.6, 21845 rows 5.3 and 8.5,
+// 5.8 and 7.8, 87381 rows 11.9 and 24.7, 13.4 and 24.8: the two meet between 2^17
+// and 2^18 without a residual, and with one do not differ by more than 0.8 us
+// from there on.  Nor for the backward pass, whose registers they
 // fill: 22.2 us, 18.2 without them, and 18.0, 15.2.
 struct RmsShape {
     int G, NV;

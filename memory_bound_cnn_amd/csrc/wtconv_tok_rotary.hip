@@ -7,7 +7,7 @@
 // tables.  A thread takes the pairs of one 16-byte vector: kVec pairs whose
 // halves lie P apart, or kVec / 2 neighbouring pairs; channels past the pairs
 // are copied by further threads.  Heads are split over blockIdx.y where tokens
-// alone do not fill the chip.  25088 tokens x 12 heads of 64 bfloat16 16.2 us (4.8
+// alone do not fill the chip.  25088 tokens x 12 heads of 64 bfloat16 16.8 us (4.6
 // TB/s), 65537 x 10 of 128 float32 with three axes 129 us (5.2 TB/s).
 #include <hip/hip_runtime.h>
 
