@@ -220,3 +220,33 @@ def test_lazily_negated_inputs():
     x, w = torch.randn(5, 32, device=DEV), torch.ones(32, device=DEV)
     assert torch.equal(tokens.rms_norm(torch._neg_view(x), w), tokens.rms_norm(-x, w))
     assert torch.equal(tokens.dropout(torch._neg_view(x), 0.0, torch.zeros(2, dtype=torch.int64, device=DEV)), -x)
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_function_transforms_compute_or_refuse(name):
+    """vmap gives what a loop gives where it gives anything; grad and jvp of
+    torch.func, which the gradients are not written for, raise."""
+    call, args = operator_calls()[name]
+    first = lambda *a: flat(call(*a))[0].float()
+    try:
+        got = torch.func.vmap(first)(*(torch.stack([a, a * 2]) for a in args))
+    except RuntimeError:
+        got = None
+    for i in range(2 if got is not None else 0):
+        assert torch.equal(got[i], first(*(a * (i + 1) for a in args)))
+    with pytest.raises((RuntimeError, ValueError)):
+        torch.func.grad(lambda *a: first(*a).sum())(*args)
+    with pytest.raises(RuntimeError, match="forward-mode"):
+        torch.func.jvp(first, args, tuple(torch.ones_like(a) for a in args))
+
+
+def test_float32_block_trains_under_autocast_and_a_converted_one_in_bfloat16():
+    for convert, autocast, dtype in ((False, True, torch.float32), (True, False, torch.bfloat16)):
+        m, x, pos, cu = block_and_input()
+        if convert:
+            m, x = m.to(torch.bfloat16), x.bfloat16()
+        with torch.autocast("cuda", torch.bfloat16, enabled=autocast):
+            y = m(x, pos, cu)
+        assert y.dtype == dtype
+        y.float().square().mean().backward()
+        assert all(p.grad is not None and p.grad.dtype == p.dtype and torch.isfinite(p.grad).all() for p in m.parameters())
