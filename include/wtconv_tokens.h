@@ -11,6 +11,11 @@
  *   attention  softmax(scale Q K^T) V inside each sequence of a pack, full or
  *              causal, grouped heads, forward and backward
  *   dropout    keep / drop from a counter-based generator, no stored mask
+ *   layer_norm y = (h - mean_c h) / sqrt(var_c h + eps) * weight + bias, forward and backward
+ *   gated_scan a gated linear recurrence along each sequence of a pack, forward and
+ *              backward, and for one more token of each sequence
+ *   expert_*   tokens sorted by expert, their rows brought there and back, and the
+ *              products of each expert's rows, forward and backward
  *
  * Conventions (those of wtconv.h):
  *   - Tensor pointers are DEVICE pointers owned by the caller.  Nothing is
@@ -170,6 +175,151 @@ size_t wtconv_attention_backward_workspace(const wtc_attn_desc* d);
 int wtconv_attention_backward(const wtc_attn_desc* d, const void* q, const void* k, const void* v, const void* out,
                               const float* lse, const void* out_low, const void* dout, const int* cu_seqlens,
                               void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Layer norm over rows
+ * ---------------------------------------------------------------------- */
+typedef struct {
+    long long rows;               /* >= 0                                              */
+    long long x_stride, r_stride; /* row strides of x (backward: of h) and the residual */
+    long long g_stride;           /* backward: row stride of dy                         */
+    int C;                        /* channels, 1 .. WTC_RMS_MAX_C                       */
+    int dtype;                    /* wtc_dtype of x, residual, h, y, dy, dh, dx         */
+    float eps;                    /* >= 0                                               */
+} wtc_layer_desc;
+
+/* h = x + residual rounded to the storage type (without residual h = x and the
+ * argument h is NULL);
+ *   m = mean_c h,  s = 1 / sqrt(mean_c (h - m)^2 + eps),  y = (h - m) s weight + bias.
+ * weight and bias [C] float32, bias may be NULL; y and h [rows, C] contiguous;
+ * stats [rows, 2] float32 (m and s, kept for the backward pass) or NULL,
+ * 8-byte aligned. */
+int wtconv_layer_norm_forward(const wtc_layer_desc* d, const void* x, const void* residual, const float* weight,
+                              const float* bias, void* y, void* h, float* stats, void* stream);
+
+/* Given dy and (or NULL) dh, the gradient that reaches h by its other use:
+ *   xh = (h - m) s,  u = dy weight,  dx = dh + s (u - mean_c u - xh mean_c(u xh)),
+ *   dw = sum over rows of dy xh,  db = sum over rows of dy (db may be NULL).
+ * dx [rows, C] contiguous is the gradient of x and of the residual alike; dh
+ * contiguous; dw, db [C]. */
+size_t wtconv_layer_norm_backward_workspace(const wtc_layer_desc* d);
+int wtconv_layer_norm_backward(const wtc_layer_desc* d, const void* dy, const void* dh, const void* h, const float* weight,
+                               const float* stats, void* dx, float* dw, float* db, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/* ------------------------------------------------------------------------
+ * Gated linear recurrence over packed sequences
+ * ---------------------------------------------------------------------- */
+#define WTC_SCAN_MAX_C (1 << 20)
+
+typedef struct {
+    long long T;                  /* tokens of the pack, >= 0, < 2^31 - 2^10             */
+    long long x_stride, f_stride; /* row strides of x and the gate                       */
+    long long g_stride;           /* backward: row stride of dy                          */
+    int n_seq;                    /* sequences, >= 0, <= 2^24                            */
+    int C;                        /* channels, 1 .. WTC_SCAN_MAX_C                       */
+    int dtype;                    /* wtc_dtype of x, gate, y, dy, dx, dgate              */
+    int reverse;                  /* 1: from each sequence's last token to its first     */
+} wtc_scan_desc;
+
+/* a = 1 / (1 + exp(-gate)), and along each sequence
+ *   h_t = a_t h_(t-1) + (1 - a_t) x_t,  y_t = h_t,
+ * from h = state[s] (state [n_seq, C] float32, NULL: zeros).  last [n_seq, C]
+ * float32 or NULL: h after the sequence's final token (the first token with
+ * reverse); a sequence with no token has state[s] there.  cu_seqlens as for
+ * attention; tokens of no sequence get zeros.  y [T, C] contiguous.  kept or
+ * NULL: what the backward pass needs, wtconv_gated_scan_kept() float32.  h is
+ * float32 throughout.  A value that is not finite never reaches another sequence.
+ * state and last must not overlap. */
+size_t wtconv_gated_scan_kept(const wtc_scan_desc* d);
+size_t wtconv_gated_scan_workspace(const wtc_scan_desc* d);   /* of both passes; 0 bytes, and NULL is taken, for short packs */
+int wtconv_gated_scan_forward(const wtc_scan_desc* d, const void* x, const void* gate, const int* cu_seqlens,
+                              const float* state, void* y, float* last, float* kept, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* Given dy, and dlast [n_seq, C] float32 or NULL (zeros):
+ *   dh_t = dy_t + a_(t+1) dh_(t+1)  (dlast after the final token),
+ *   dx = (1 - a) dh,  dgate = dh (h_(t-1) - x) a (1 - a),  dstate[s] = a dh of its first token.
+ * dx, dgate [T, C] contiguous; dstate [n_seq, C] float32 or NULL. */
+int wtconv_gated_scan_backward(const wtc_scan_desc* d, const void* x, const void* gate, const int* cu_seqlens,
+                               const float* state, const float* kept, const void* dy, const float* dlast, void* dx, void* dgate,
+                               float* dstate, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One more token of each of d->T sequences (d->n_seq and d->reverse are not
+ * looked at): state_out = a state + (1 - a) x, y = state_out as stored.  state,
+ * state_out [T, C] float32 contiguous; state_out may be state. */
+int wtconv_gated_scan_step(const wtc_scan_desc* d, const void* x, const void* gate, const float* state, void* y,
+                           float* state_out, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Tokens sorted by expert
+ * ---------------------------------------------------------------------- */
+#define WTC_EXPERTS_MAX 512
+
+/* experts [n] int32: the expert of each pair of a token and one of its choices
+ * (pair p = t k + j); a number outside of 0 .. E - 1 is no expert.  The pairs in
+ * the order of the experts, those of one in the order of p:
+ *   slot [n]: each pair's place in that order, -1 for pairs of no expert;
+ *   pair [n]: the pair at each place, -1 past the last one;
+ *   cu_experts [E + 1]: expert e's places are cu_experts[e] up to cu_experts[e + 1].
+ * 0 <= n < 2^31 - 2^16, 1 <= E <= WTC_EXPERTS_MAX. */
+size_t wtconv_expert_order_workspace(long long n, int E);
+int wtconv_expert_order(long long n, int E, const int* experts, int* slot, int* pair, int* cu_experts, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+#define WTC_ROWS_MAX_C 65536
+
+typedef struct {
+    long long T;                  /* tokens, >= 0                                        */
+    long long x_stride, r_stride; /* row strides of what is by token, and of the rows read */
+    int k;                        /* choices of a token, >= 1; T k < 2^31 - 2^16         */
+    int E;                        /* experts, 1 .. WTC_EXPERTS_MAX                       */
+    int C;                        /* channels, 1 .. WTC_ROWS_MAX_C                       */
+    int dtype;                    /* wtc_dtype of the activations                        */
+} wtc_rows_desc;
+
+/* rows[slot[t, j]] = x[t]; zeros to the rows from cu_experts[E] on.  rows [T k, C]
+ * contiguous.  slot [T, k] and cu_experts as wtconv_expert_order gave them (a slot
+ * outside of 0 .. T k - 1 is none). */
+int wtconv_expert_gather(const wtc_rows_desc* d, const void* x, const int* slot, const int* cu_experts, void* rows,
+                         void* stream);
+/* y[t] = sum_j weights[t, j] rows[slot[t, j]], added in the order of j in float32;
+ * weights [T, k] float32, or NULL for ones (gather's gradient).  y [T, C] contiguous. */
+int wtconv_expert_combine(const wtc_rows_desc* d, const void* rows, const float* weights, const int* slot, void* y,
+                          void* stream);
+/* drows[slot[t, j]] = weights[t, j] dy[t] (zeros from cu_experts[E] on), dweights[t, j] =
+ * dy[t] . rows[slot[t, j]] (0 for pairs of no expert).  drows [T k, C], dweights [T, k] contiguous. */
+int wtconv_expert_combine_backward(const wtc_rows_desc* d, const void* dy, const void* rows, const float* weights,
+                                   const int* slot, const int* cu_experts, void* drows, float* dweights, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The experts' products
+ * ---------------------------------------------------------------------- */
+#define WTC_EXPERT_MAX_STRIDE (1 << 22)
+
+typedef struct {
+    long long R;                  /* rows, >= 0, < 2^31 - 2^16                           */
+    long long x_stride, g_stride; /* row strides of x and dy: multiples of 16 bytes,
+                                     <= WTC_EXPERT_MAX_STRIDE                            */
+    int E;                        /* experts, 1 .. WTC_EXPERTS_MAX                       */
+    int K, N;                     /* channels in and out: multiples of 8, 8 .. 65536     */
+    int dtype;                    /* wtc_dtype of all tensors but cu_experts             */
+} wtc_expert_desc;
+
+/* y[r] = weight[e] x[r] + bias[e] for the rows cu_experts[e] <= r < cu_experts[e + 1]
+ * of each expert, zeros for the rows of none.  weight [E, N, K], bias [E, N] or NULL,
+ * y [R, N]: contiguous.  cu_experts [E + 1] int32, non-decreasing; entries are clamped
+ * to 0 .. R on the device.  Sums are float32.  All tensors are 16-byte aligned. */
+int wtconv_expert_linear_forward(const wtc_expert_desc* d, const void* x, const void* weight, const void* bias,
+                                 const int* cu_experts, void* y, void* stream);
+/* dx[r] = dy[r] weight[e]; zeros for the rows of no expert.  dx [R, K] contiguous. */
+int wtconv_expert_linear_input_grad(const wtc_expert_desc* d, const void* dy, const void* weight, const int* cu_experts,
+                                    void* dx, void* stream);
+/* dweight[e] = sum of dy[r] x[r]^T and dbias[e] = sum of dy[r] (or NULL) over the rows
+ * of expert e; zeros for an expert with none. */
+size_t wtconv_expert_linear_weight_grad_workspace(const wtc_expert_desc* d);
+int wtconv_expert_linear_weight_grad(const wtc_expert_desc* d, const void* dy, const void* x, const int* cu_experts,
+                                     void* dweight, void* dbias, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

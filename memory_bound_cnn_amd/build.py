@@ -36,7 +36,9 @@ SOURCES = ["wtconv_fused.hip", "wtconv_fused_k1.hip", "wtconv_fused_k3.hip", "wt
            "wtconv_fused_s_dw.hip",
            "wtconv_tiny.hip", "wtconv_lane.hip", "wtconv_unfused.hip", "wtconv_top.hip", "wtconv_layout.hip", "wtconv_noalloc.hip", "wtconv_corr.hip", "wtconv_api.cpp", "wtconv_plan.cpp",
            "wtconv_tok_rms.hip", "wtconv_tok_rotary.hip", "wtconv_tok_dropout.hip", "wtconv_tok_attn.hip",
-           "wtconv_tok_attn_bf16.hip", "wtconv_tok_attn_fp32.hip", "wtconv_tok_api.cpp"]
+           "wtconv_tok_attn_bf16.hip", "wtconv_tok_attn_fp32.hip", "wtconv_tok_layer.hip", "wtconv_tok_scan.hip",
+           "wtconv_tok_expert.hip", "wtconv_tok_product.hip", "wtconv_tok_product_bf16.hip", "wtconv_tok_product_fp32.hip",
+           "wtconv_tok_api.cpp"]
 
 
 def _compile(src):

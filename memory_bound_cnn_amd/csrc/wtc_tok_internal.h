@@ -35,4 +35,35 @@ int launch_attn_backward(const wtc_attn_desc* d, const void* q, const void* k, c
                          const float* lse, const void* out_low, const void* dout, const int* cu, void* dq, void* dk, void* dv,
                          void* workspace, void* stream);
 
+int layer_backward_parts(const wtc_layer_desc* d);
+int launch_layer_forward(const wtc_layer_desc* d, const void* x, const void* r, const float* w, const float* b, void* y,
+                         void* h, float* stats, void* stream);
+int launch_layer_backward(const wtc_layer_desc* d, const void* dy, const void* dh, const void* h, const float* w,
+                          const float* stats, void* dx, float* dw, float* db, float* parts, void* stream);
+
+// Gated recurrence: tokens of a tile, at whose start the forward pass keeps the state for the backward pass
+constexpr int kScanTile = 128;
+size_t scan_workspace(const wtc_scan_desc* d);
+int launch_scan_forward(const wtc_scan_desc* d, const void* x, const void* f, const int* cu, const float* state, void* y,
+                        float* last, float* kept, void* workspace, void* stream);
+int launch_scan_backward(const wtc_scan_desc* d, const void* x, const void* f, const int* cu, const float* state,
+                         const float* kept, const void* dy, const float* dlast, void* dx, void* df, float* dstate,
+                         void* workspace, void* stream);
+int launch_scan_step(const wtc_scan_desc* d, const void* x, const void* f, const float* state, void* y, float* out,
+                     void* stream);
+
+size_t order_workspace(long long n, int E);
+int launch_expert_order(long long n, int E, const int* experts, int* slot, int* pair, int* cu, void* workspace, void* stream);
+int launch_rows_gather(const wtc_rows_desc* d, const void* x, const int* slot, const int* cu, void* rows, void* stream);
+int launch_rows_sum(const wtc_rows_desc* d, const void* rows, const float* weights, const int* slot, void* y, void* stream);
+int launch_rows_sum_backward(const wtc_rows_desc* d, const void* dy, const void* rows, const float* weights, const int* slot,
+                             const int* cu, void* drows, float* dweights, void* stream);
+
+size_t expert_weights_workspace(const wtc_expert_desc* d);
+int launch_expert_forward(const wtc_expert_desc* d, const void* x, const void* w, const void* b, const int* cu, void* y,
+                          void* stream);
+int launch_expert_input_grad(const wtc_expert_desc* d, const void* dy, const void* w, const int* cu, void* dx, void* stream);
+int launch_expert_weight_grad(const wtc_expert_desc* d, const void* dy, const void* x, const int* cu, void* dw, void* db,
+                              void* workspace, void* stream);
+
 }  // namespace wtc

@@ -1,0 +1,255 @@
+// Building blocks of the experts' products (wtconv_tok_product*.hip): tiles of
+// matrices in shared memory and their products on the matrix cores.
+//
+// A workgroup makes a tile of the output, rows i by columns j (consecutive in
+// memory), as 32 x 32 blocks.  The matrix instruction's A operand is the one
+// with the columns and its B operand the one with the rows, so that a lane owns
+// one row of the output (i = lane % 32) and register r is column
+// 8 (r / 4) + 4 h + r % 4, h = lane / 32: four consecutive ones at a time.
+//   An operand lies in memory with its terms (what is summed over) along the
+// rows or across them:
+//   Along   a row of the tile is a row of the output's (or a column's) 128 bytes
+//           of terms; a lane reads 16 bytes of its row.
+//   Across  a row of the tile is one term, its 16-byte chunks are rows (columns)
+//           of the output; bfloat16 is read with the transposing instruction,
+//           float32 a value at a time.
+// A step takes 128 bytes of terms.  Tiles are copied by the memory system 1024
+// consecutive bytes of shared memory at a time, and the chunks of a row are
+// permuted on that way so that reads meet no bank twice.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "wtc_tok_device.h"
+#include "wtc_tok_internal.h"
+
+namespace wtc {
+namespace product {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) char lds_char;
+
+template <typename T>
+constexpr int kTerms = 128 / (int)sizeof(T);   // of a step
+// A lane's terms of one read: 8 bfloat16 or 4 float32, of the two halves 16 or 8.
+template <typename T>
+constexpr int kRead = 2 * kVec<T>;
+template <typename T>
+constexpr int kReads = kTerms<T> / kRead<T>;   // 4
+
+__device__ __forceinline__ void mma(const u32x4& a, const u32x4& b, f32x16& c, uint16_t) {
+    c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ void mma(const u32x4& a, const u32x4& b, f32x16& c, float) {
+    const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(x[i], y[i], c, 0, 0, 0);
+}
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) { return (uint32_t)(uintptr_t)(lds_char*)p; }
+
+// 16 bytes a lane from base + off to 1024 consecutive bytes at dst.  A scalar register that a vector instruction
+// wrote may be an address five instructions later; the compiler sees to that outside of asm only.
+__device__ __forceinline__ void copy1024(uint32_t dst, const char* base, uint32_t off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane(dst)), "v"(off), "s"(base)
+                 : "m0", "memory");
+}
+
+// N rows (or columns) of an operand whose terms lie along its rows.
+template <typename T, int N, int WAVES>
+struct Along {
+    static constexpr int kBytes = N * 128, kCopies = kBytes / 1024 / WAVES;
+    static_assert(kBytes % (1024 * WAVES) == 0, "whole copies");
+    // bytes from the operand's first row to the lane's part of each copy; rows past `last` repeat it
+    uint32_t off[kCopies];
+    int unit[kCopies];      // the chunk of the row
+    __device__ __forceinline__ void place(uint32_t row_bytes, int last, int wave, int lane) {
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+            const int r = (wave * kCopies + i) * 8 + lane / 8;
+            unit[i] = (lane % 8) ^ ((r >> 1) & 7);
+            off[i] = (uint32_t)min(r, last) * row_bytes + unit[i] * 16;
+        }
+    }
+    // base: the step's first term of the operand's first row; chunks: of terms that are there, if fewer than 8
+    __device__ __forceinline__ void copy(uint32_t dst, const char* base, int chunks, int wave) const {
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+            const uint32_t back = chunks < 8 && unit[i] >= chunks ? (uint32_t)(unit[i] - chunks + 1) * 16 : 0;
+            copy1024(dst + (wave * kCopies + i) * 1024, base, off[i] - back);
+        }
+    }
+    __device__ static __forceinline__ int lane_part(int lane) { return (lane & 31) * 128; }
+    // 16 bytes of terms of row r0 + lane % 32, r0 a multiple of 32
+    __device__ static __forceinline__ u32x4 read(const char* tile, int part, int r0, int at, int lane) {
+        const int unit = (2 * at + (lane >> 5)) ^ ((lane >> 1) & 7);
+        return *reinterpret_cast<const u32x4*>(tile + part + r0 * 128 + unit * 16);
+    }
+};
+
+// The same of an operand whose terms lie across: a row of the tile is one term
+// with N of the output's rows (or columns).
+template <typename T, int N, int WAVES>
+struct Across {
+    static constexpr int kRow = N * (int)sizeof(T), kChunks = kRow / 16;
+    static constexpr int kBytes = kTerms<T> * kRow, kCopies = kBytes / 1024 / WAVES;
+    static constexpr int kRowsEach = 1024 / kRow > 0 ? 1024 / kRow : 1;
+    static_assert(kBytes % (1024 * WAVES) == 0 && 1024 % kRow == 0 && kRow >= 256, "whole copies, and chunks to permute");
+    // the permutation of a row's chunks: bfloat16 by 64 bytes, with the four terms of one
+    // transposing read; float32 by 128 bytes, with the halves of the wave
+    static __device__ __forceinline__ int turn(int term) {
+        return sizeof(T) == 2 ? (term & 3) << 2 : ((term >> 2) & 1) << 3;
+    }
+    uint32_t unit[kCopies];   // bytes along the row
+    int term[kCopies];
+    __device__ __forceinline__ void place(int last_chunk, int wave, int lane) {
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+            term[i] = (wave * kCopies + i) * kRowsEach + lane / kChunks;
+            unit[i] = (uint32_t)min((lane % kChunks) ^ turn(term[i]), last_chunk) * 16;
+        }
+    }
+    // base: the step's first term of the operand's first row (column); last: the last term that is there
+    __device__ __forceinline__ void copy(uint32_t dst, const char* base, uint32_t row_bytes, int last, int wave) const {
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i)
+            copy1024(dst + (wave * kCopies + i) * 1024, base, (uint32_t)min(term[i], last) * row_bytes + unit[i]);
+    }
+    // The lane's part: of the terms it reads first, and its column's.
+    __device__ static __forceinline__ int lane_part(int lane) {
+        if constexpr (sizeof(T) == 2) return (8 * (lane >> 5) + ((lane & 15) >> 2)) * kRow + (lane & 3) * 8;
+        return 4 * (lane >> 5) * kRow + (lane & 3) * 4;
+    }
+    // The terms of row (column) r0 + lane % 32
+    __device__ static __forceinline__ u32x4 read(const char* tile, int part, int r0, int at, int lane) {
+        u32x4 v;
+        if constexpr (sizeof(T) == 2) {
+            const int c = (r0 / 8 + ((lane >> 4) & 1) * 2) ^ turn((lane & 15) >> 2);   // the last bit is in `part`
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (__attribute__((address_space(3))) s16x4*)(lds_char*)(tile + part + (16 * at + 4 * k) * kRow + c * 16));
+                const u32x2 u = __builtin_bit_cast(u32x2, t);
+                v[2 * k] = u[0];
+                v[2 * k + 1] = u[1];
+            }
+        } else {
+            const int c = (r0 / 4 + ((lane & 31) >> 2)) ^ turn(4 * (lane >> 5));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = *reinterpret_cast<const uint32_t*>(tile + part + (8 * at + i) * kRow + c * 16);
+        }
+        return v;
+    }
+};
+
+// Zeros the terms from `there` on (counted from the step's first).
+template <typename T>
+__device__ __forceinline__ u32x4 cut(u32x4 v, int at, int there, int lane) {
+    const int first = kRead<T> * at + kVec<T> * (lane >> 5);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 2) {
+            if (first + 2 * i >= there)
+                v[i] = 0;
+            else if (first + 2 * i + 1 >= there)
+                v[i] &= 0xFFFFu;
+        } else {
+            if (first + i >= there) v[i] = 0;
+        }
+    }
+    return v;
+}
+
+// ------------------------------------------------------------------ work
+// The rows of a tile: SIZE of one expert's, or of no expert's (before the first's, after the last's).
+struct Rows {
+    int expert;   // -1: rows of none
+    int start, count;
+};
+// Segment s = 0 .. E + 1 of the rows: those before the first expert's, the experts', those after the last's.
+__device__ __forceinline__ int segment_begin(const int* cu, int E, int R, int s) {
+    if (s <= 0) return 0;
+    if (s >= E + 2) return R;
+    return min(max(cu[s - 1], 0), R);
+}
+// Segment s may use the tiles from floor(begin / SIZE) + s on, which leaves it
+// ceil(rows / SIZE) at least; whose a tile is, is found by searching cu, 64
+// segments at a time.  count = 0: a tile of none.
+template <int SIZE>
+__device__ __forceinline__ Rows find_rows(const int* cu, int E, int R, int slot, int lane) {
+    int lo = 0, hi = E + 2;   // the segment is in lo .. hi - 1
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 63) / 64, s = lo + lane * step;
+        const bool at = s < hi && segment_begin(cu, E, R, s < hi ? s : hi) / SIZE + s <= slot;
+        const int n = __builtin_popcountll(__builtin_amdgcn_ballot_w64(at)), k = n > 0 ? n - 1 : 0;
+        lo += k * step;
+        hi = min(hi, lo + step);
+    }
+    const int b = segment_begin(cu, E, R, lo), e = segment_begin(cu, E, R, lo + 1), tile = slot - (b / SIZE + lo);
+    Rows r;
+    r.expert = lo == 0 || lo == E + 1 ? -1 : lo - 1;
+    r.start = b + tile * SIZE;
+    r.count = tile < 0 ? 0 : min(max(e - b - tile * SIZE, 0), SIZE);
+    return r;
+}
+inline long long row_slots(long long R, int E, int size) { return R / size + E + 2; }
+
+// The number of a workgroup, counted so that those of one XCD (every eighth)
+// are next to each other.
+__device__ __forceinline__ int spread(int id, int all) {
+    const int each = all / 8, more = all % 8, x = id % 8;
+    return x * each + min(x, more) + id / 8;
+}
+
+// ------------------------------------------------------------------ output
+// Stores 32 rows by 32 NB columns of a wave from its blocks (see above) through
+// shared memory (`at`, kStoreBytes of the wave's own), so that a store has whole
+// rows of 16-byte chunks.  Rows `rows` and more, and columns `columns` and more,
+// are not there.  bias: of the wave's first column, or null.
+template <typename T, int NB>
+constexpr int kStoreRow = 32 * NB * (int)sizeof(T) + 16;
+template <typename T, int NB>
+constexpr int kStoreBytes = 32 * kStoreRow<T, NB>;
+
+template <typename T, int NB>
+__device__ __forceinline__ void store_block(char* at, T* out, long long stride, int rows, int columns, const T* bias, int lane,
+                                            const f32x16 (&c)[NB]) {
+    constexpr int ROW = kStoreRow<T, NB>, CH = 32 * NB * (int)sizeof(T) / 16;
+    asm volatile("" ::: "memory");
+    char* p = at + (lane & 31) * ROW + (lane >> 5) * 4 * (int)sizeof(T);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            f32x4 v = {c[nb][4 * g], c[nb][4 * g + 1], c[nb][4 * g + 2], c[nb][4 * g + 3]};
+            const int j = 32 * nb + 8 * g + 4 * (lane >> 5);
+            if (bias && j < columns) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] += to_f32(bias[j + i]);
+            }
+            char* to = p + (32 * nb + 8 * g) * (int)sizeof(T);
+            if constexpr (sizeof(T) == 2)
+                *reinterpret_cast<u32x2*>(to) = u32x2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
+            else
+                *reinterpret_cast<f32x4*>(to) = v;
+        }
+    asm volatile("" ::: "memory");   // a wave's own accesses to shared memory stay in order
+#pragma unroll
+    for (int i = 0; i < 32 * CH / 64; ++i) {
+        const int u = 64 * i + lane, r = u / CH, k = u % CH;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(at + r * ROW + 16 * k);
+        if (r < rows && k * kVec<T> < columns) *reinterpret_cast<u32x4*>(out + r * stride + k * kVec<T>) = v;
+    }
+    asm volatile("" ::: "memory");
+}
+
+}  // namespace product
+}  // namespace wtc

@@ -1,0 +1,281 @@
+// The experts' products, of the rows x[r] of each expert e (rows cu[e] to
+// cu[e + 1] - 1) with its weights W[e] [N, K]:
+//   k_product_rows, forward   y[r]  = W[e] x[r] + b[e]          terms K, columns N
+//   k_product_rows, back      dx[r] = dy[r] W[e]                 terms N, columns K
+//   k_product_weights         dW[e] = sum_r dy[r] x[r]^T,  db[e] = sum_r dy[r]
+//
+// Bound by the matrix units.  A workgroup's tiles of the two operands are
+// copied to shared memory STAGES - 1 steps ahead of their products.
+#pragma once
+
+#include "wtc_tok_product.h"
+
+namespace wtc {
+namespace product {
+
+struct Args {
+    const void *x, *w, *b;      // x: dy in the backward pass
+    const void* g;              // k_product_weights: dy, beside x
+    const int* cu;
+    void* y;                    // dx, dW
+    void* db;
+    float* parts;               // k_product_weights, split: [splits][E][N][K], then [splits][E][N]
+    long long x_stride, g_stride, slots;
+    int R, E, K, N, splits;
+};
+
+// Waits until at most N of the wave's copies are on their way.
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void meet() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// The products of one step: NB blocks of columns by MB of rows, from the wave's first.
+template <typename T, int NB, int MB, typename Cols, typename RowsOp>
+__device__ __forceinline__ void step(const char* cols, const char* rows, int cpart, int rpart, int col0, int row0, int lane,
+                                     bool partial, int there, f32x16 (&acc)[MB][NB]) {
+#pragma unroll
+    for (int at = 0; at < kReads<T>; ++at) {
+        u32x4 a[NB], b[MB];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) a[nb] = Cols::read(cols, cpart, col0 + 32 * nb, at, lane);
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) b[mb] = RowsOp::read(rows, rpart, row0 + 32 * mb, at, lane);
+        if (partial) {
+            if (at * kRead<T> >= there) break;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) a[nb] = cut<T>(a[nb], at, there, lane);
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb) b[mb] = cut<T>(b[mb], at, there, lane);
+        }
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma(a[nb], b[mb], acc[mb][nb], T{});
+    }
+}
+
+// WM x WN waves of MB x NB blocks each.
+template <typename T, bool BACK, int WM, int WN, int MB, int NB, int STAGES>
+__global__ void __launch_bounds__(64 * WM * WN) k_product_rows(Args a) {
+    constexpr int WAVES = WM * WN, BM = 32 * WM * MB, BN = 32 * WN * NB, TERMS = kTerms<T>;
+    using X = Along<T, BM, WAVES>;
+    using WF = Along<T, BN, WAVES>;
+    using WB = Across<T, BN, WAVES>;
+    constexpr int STAGE = X::kBytes + WF::kBytes, COPIES = X::kCopies + WF::kCopies;
+    static_assert(WF::kBytes == WB::kBytes && WF::kCopies == WB::kCopies, "one size");
+    constexpr int STORE = WAVES * kStoreBytes<T, NB>, LDS = STAGES * STAGE > STORE ? STAGES * STAGE : STORE;
+    static_assert(LDS <= 160 * 1024, "shared memory");
+    __shared__ __align__(16) char lds[LDS];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    const int terms = BACK ? a.N : a.K, columns = BACK ? a.K : a.N, tiles = (columns + BN - 1) / BN;
+    // workgroups next to each other: 8 tiles of rows, then the next columns of those
+    const int id = spread(blockIdx.x, gridDim.x), group = id / (8 * tiles), in = id % (8 * tiles);
+    const int high = min(8, (int)a.slots - 8 * group), col0 = in / high * BN;
+    const Rows r = find_rows<BM>(a.cu, a.E, a.R, 8 * group + in % high, lane);
+    if (r.count == 0) return;
+    f32x16 acc[MB][NB] = {};
+    const bool none = r.expert < 0;
+    const size_t expert = none ? 0 : r.expert;
+    if (!none) {
+        constexpr int SZ = (int)sizeof(T);
+        const uint32_t xrow = (uint32_t)a.x_stride * SZ, wrow = (uint32_t)a.K * SZ;
+        const char* x = static_cast<const char*>(a.x) + (long long)r.start * a.x_stride * SZ;
+        const char* w = static_cast<const char*>(a.w) + expert * a.N * a.K * SZ +
+                        (BACK ? (size_t)col0 * SZ : (size_t)col0 * a.K * SZ);
+        const int here = min(columns - col0, BN);
+        X xt;
+        WF wf;
+        WB wb;
+        xt.place(xrow, r.count - 1, wave, lane);
+        if constexpr (BACK)
+            wb.place(here / kVec<T> - 1, wave, lane);
+        else
+            wf.place(wrow, here - 1, wave, lane);
+        const uint32_t lds0 = lds_address(lds);
+        const int steps = (terms + TERMS - 1) / TERMS;
+        auto copy = [&](int s) {
+            const uint32_t at = lds0 + (uint32_t)(s % STAGES) * STAGE;
+            const int left = terms - s * TERMS;
+            xt.copy(at, x + (size_t)s * 128, left / kVec<T>, wave);
+            if constexpr (BACK)
+                wb.copy(at + X::kBytes, w + (size_t)s * TERMS * wrow, wrow, left - 1, wave);
+            else
+                wf.copy(at + X::kBytes, w + (size_t)s * 128, left / kVec<T>, wave);
+        };
+#pragma unroll
+        for (int s = 0; s < STAGES - 1; ++s)
+            if (s < steps) copy(s);
+        const int xpart = X::lane_part(lane), wpart = BACK ? WB::lane_part(lane) : WF::lane_part(lane);
+        for (int s = 0; s < steps; ++s) {
+            if (s + STAGES - 1 <= steps)
+                wait_copies<(STAGES - 2) * COPIES>();
+            else
+                wait_copies<0>();
+            meet();   // step s is there; everyone is done with the one before it
+            if (s + STAGES - 1 < steps) copy(s + STAGES - 1);
+            const char* at = lds + s % STAGES * STAGE;
+            const int left = terms - s * TERMS;
+            if (left >= TERMS)
+                step<T, NB, MB, typename std::conditional<BACK, WB, WF>::type, X>(at + X::kBytes, at, wpart, xpart, 32 * NB * wn,
+                                                                                  32 * MB * wm, lane, false, 0, acc);
+            else
+                step<T, NB, MB, typename std::conditional<BACK, WB, WF>::type, X>(at + X::kBytes, at, wpart, xpart, 32 * NB * wn,
+                                                                                  32 * MB * wm, lane, true, left, acc);
+        }
+        meet();   // no tile is read any more
+    }
+    const int col = col0 + 32 * NB * wn;
+    const T* bias = BACK || none || !a.b ? nullptr : static_cast<const T*>(a.b) + expert * a.N + col;
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+        const int row = 32 * (MB * wm + mb);
+        if (row >= r.count || col >= columns) break;
+        store_block<T, NB>(lds + wave * kStoreBytes<T, NB>, static_cast<T*>(a.y) + (long long)(r.start + row) * columns + col,
+                           columns, r.count - row, columns - col, bias, lane, acc[mb]);
+    }
+}
+
+template <typename T, int WM, int WN, int MB, int NB, int STAGES>
+__global__ void __launch_bounds__(64 * WM * WN) k_product_weights(Args a) {
+    constexpr int WAVES = WM * WN, BM = 32 * WM * MB, BN = 32 * WN * NB, TERMS = kTerms<T>;
+    using G = Across<T, BM, WAVES>;
+    using X = Across<T, BN, WAVES>;
+    constexpr int STAGE = G::kBytes + X::kBytes, COPIES = G::kCopies + X::kCopies;
+    constexpr int STORE = WAVES * kStoreBytes<float, NB>, LDS = STAGES * STAGE > STORE ? STAGES * STAGE : STORE;
+    static_assert(LDS <= 160 * 1024, "shared memory");
+    __shared__ __align__(16) char lds[LDS];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    const int ktiles = (a.K + BN - 1) / BN, ntiles = (a.N + BM - 1) / BM;
+    int id = spread(blockIdx.x, gridDim.x);
+    const int col0 = id % ktiles * BN;
+    id /= ktiles;
+    const int row0 = id % ntiles * BM;
+    id /= ntiles;
+    const int split = id % a.splits, e = id / a.splits;
+    const int first = segment_begin(a.cu, a.E, a.R, e + 1), count = max(segment_begin(a.cu, a.E, a.R, e + 2) - first, 0);
+    const int all = (count + TERMS - 1) / TERMS;
+    const int begin = (int)((long long)all * split / a.splits), end = (int)((long long)all * (split + 1) / a.splits);
+    f32x16 acc[MB][NB] = {}, sum[MB] = {};
+    const bool sums = a.db && col0 == 0 && wn == 0;
+    constexpr int SZ = (int)sizeof(T);
+    const uint32_t grow = (uint32_t)a.g_stride * SZ, xrow = (uint32_t)a.x_stride * SZ;
+    const char* g = static_cast<const char*>(a.g) + ((long long)first * a.g_stride + row0) * SZ;
+    const char* x = static_cast<const char*>(a.x) + ((long long)first * a.x_stride + col0) * SZ;
+    G gt;
+    X xt;
+    gt.place(min(a.N - row0, BM) / kVec<T> - 1, wave, lane);
+    xt.place(min(a.K - col0, BN) / kVec<T> - 1, wave, lane);
+    const uint32_t lds0 = lds_address(lds);
+    auto copy = [&](int s) {
+        const uint32_t at = lds0 + (uint32_t)((s - begin) % STAGES) * STAGE;
+        const int last = count - 1 - s * TERMS;
+        gt.copy(at, g + (size_t)s * TERMS * grow, grow, last, wave);
+        xt.copy(at + G::kBytes, x + (size_t)s * TERMS * xrow, xrow, last, wave);
+    };
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s)
+        if (begin + s < end) copy(begin + s);
+    const int gpart = G::lane_part(lane), xpart = X::lane_part(lane);
+    const uint32_t one = sizeof(T) == 2 ? 0x3F803F80u : 0x3F800000u;
+    const u32x4 ones = {one, one, one, one};
+    for (int s = begin; s < end; ++s) {
+        if (s + STAGES - 1 <= end)
+            wait_copies<(STAGES - 2) * COPIES>();
+        else
+            wait_copies<0>();
+        meet();
+        if (s + STAGES - 1 < end) copy(s + STAGES - 1);
+        const char* at = lds + (s - begin) % STAGES * STAGE;
+        const int left = count - s * TERMS;
+        if (left >= TERMS)
+            step<T, NB, MB, X, G>(at + G::kBytes, at, xpart, gpart, 32 * NB * wn, 32 * MB * wm, lane, false, 0, acc);
+        else
+            step<T, NB, MB, X, G>(at + G::kBytes, at, xpart, gpart, 32 * NB * wn, 32 * MB * wm, lane, true, left, acc);
+        if (sums) {
+#pragma unroll
+            for (int k = 0; k < kReads<T>; ++k)
+#pragma unroll
+                for (int mb = 0; mb < MB; ++mb) {
+                    u32x4 v = G::read(at, gpart, 32 * (MB * wm + mb), k, lane);
+                    if (left < TERMS) v = cut<T>(v, k, left, lane);
+                    mma(ones, v, sum[mb], T{});
+                }
+        }
+    }
+    meet();
+    const int col = col0 + 32 * NB * wn;
+    const size_t weights = (size_t)a.E * a.N * a.K;
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+        const int row = row0 + 32 * (MB * wm + mb);
+        if (row >= a.N) break;
+        if (sums && lane < 32 && row + lane < a.N) {   // every register of a lane is its row's sum
+            if (a.splits == 1)
+                static_cast<T*>(a.db)[(size_t)e * a.N + row + lane] = from_f32<T>(sum[mb][0]);
+            else
+                a.parts[a.splits * weights + ((size_t)split * a.E + e) * a.N + row + lane] = sum[mb][0];
+        }
+        if (col >= a.K) continue;
+        const size_t to = ((size_t)e * a.N + row) * a.K + col;
+        if (a.splits == 1)
+            store_block<T, NB>(lds + wave * kStoreBytes<T, NB>, static_cast<T*>(a.y) + to, a.K, a.N - row, a.K - col,
+                               static_cast<const T*>(nullptr), lane, acc[mb]);
+        else
+            store_block<float, NB>(lds + wave * kStoreBytes<float, NB>, a.parts + split * weights + to, a.K, a.N - row, a.K - col,
+                                   static_cast<const float*>(nullptr), lane, acc[mb]);
+    }
+}
+
+// The splits' sums in their order: n weights of dW, then m of db.
+template <typename T>
+__global__ void __launch_bounds__(256) k_product_join(Args a, long long n, long long m) {
+    for (long long u = (long long)blockIdx.x * 256 + threadIdx.x; 4 * u < n + m; u += (long long)gridDim.x * 256) {
+        const bool bias = 4 * u >= n;   // n and m are multiples of 8
+        const float* p = a.parts + (bias ? a.splits * n + 4 * u - n : 4 * u);
+        const long long far = bias ? m : n;
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+        for (int s = 0; s < a.splits; ++s) v += *reinterpret_cast<const f32x4*>(p + s * far);
+        T* to = bias ? static_cast<T*>(a.db) + (4 * u - n) : static_cast<T*>(a.y) + 4 * u;
+        if constexpr (sizeof(T) == 2)
+            *reinterpret_cast<u32x2*>(to) = u32x2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
+        else
+            *reinterpret_cast<f32x4*>(to) = v;
+    }
+}
+
+constexpr int kTile = 128;   // rows and columns of a workgroup's tile
+
+template <typename T>
+int run_rows(Args a, bool back, hipStream_t st) {
+    const int columns = back ? a.K : a.N;
+    a.slots = row_slots(a.R, a.E, kTile);
+    const long long groups = a.slots * ((columns + kTile - 1) / kTile);
+    if (groups > (1 << 23)) return WTC_ESHAPE;
+    if (back)
+        hipLaunchKernelGGL((k_product_rows<T, true, 2, 2, 2, 2, 2>), dim3((unsigned)groups), dim3(256), 0, st, a);
+    else
+        hipLaunchKernelGGL((k_product_rows<T, false, 2, 2, 2, 2, 2>), dim3((unsigned)groups), dim3(256), 0, st, a);
+    return hipGetLastError() == hipSuccess ? WTC_OK : WTC_EHIP;
+}
+template <typename T>
+int run_weights(const Args& a, hipStream_t st) {
+    const long long groups = (long long)((a.K + kTile - 1) / kTile) * ((a.N + kTile - 1) / kTile) * a.E * a.splits;
+    if (groups > (1 << 23)) return WTC_ESHAPE;
+    hipLaunchKernelGGL((k_product_weights<T, 2, 2, 2, 2, 2>), dim3((unsigned)groups), dim3(256), 0, st, a);
+    if (a.splits > 1) {
+        const long long n = (long long)a.E * a.N * a.K, m = a.db ? (long long)a.E * a.N : 0, blocks = ((n + m) / 4 + 255) / 256;
+        hipLaunchKernelGGL(k_product_join<T>, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, st, a, n, m);
+    }
+    return hipGetLastError() == hipSuccess ? WTC_OK : WTC_EHIP;
+}
+
+}  // namespace product
+}  // namespace wtc

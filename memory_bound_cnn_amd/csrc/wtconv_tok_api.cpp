@@ -63,6 +63,55 @@ int check_low(const wtc_attn_desc* d, const void* low) {
     return d->dtype != WTC_BF16 ? WTC_EDTYPE : aligned(low, 16) ? WTC_OK : WTC_EINVAL;
 }
 
+int check_layer(const wtc_layer_desc* d) {
+    if (!d) return WTC_EINVAL;
+    if (d->rows < 0 || d->C < 1 || !(d->eps >= 0.f) || std::isinf(d->eps)) return WTC_EINVAL;
+    if (d->x_stride < 0 || d->r_stride < 0 || d->g_stride < 0) return WTC_EINVAL;
+    if (!is_dtype(d->dtype)) return WTC_EDTYPE;
+    if (d->C > WTC_RMS_MAX_C || d->rows >= kMaxTokens) return WTC_ESHAPE;
+    return WTC_OK;
+}
+
+// place and row indices of a tile past the end stay below 2^31
+constexpr long long kMaxScan = kMaxTokens - (1 << 10), kMaxRows = kMaxTokens - (1 << 16);
+
+int check_scan(const wtc_scan_desc* d) {
+    if (!d) return WTC_EINVAL;
+    if (d->T < 0 || d->n_seq < 0 || d->C < 1 || (d->reverse != 0 && d->reverse != 1)) return WTC_EINVAL;
+    if (d->x_stride < 0 || d->f_stride < 0 || d->g_stride < 0) return WTC_EINVAL;
+    if (!is_dtype(d->dtype)) return WTC_EDTYPE;
+    if (d->C > WTC_SCAN_MAX_C || d->T >= kMaxScan || d->n_seq > (1 << 24)) return WTC_ESHAPE;
+    return WTC_OK;
+}
+
+int check_order(long long n, int E) {
+    if (n < 0 || E < 1) return WTC_EINVAL;
+    return n >= kMaxRows || E > WTC_EXPERTS_MAX ? WTC_ESHAPE : WTC_OK;
+}
+
+int check_rows(const wtc_rows_desc* d) {
+    if (!d) return WTC_EINVAL;
+    if (d->T < 0 || d->k < 1 || d->C < 1 || d->x_stride < 0 || d->r_stride < 0) return WTC_EINVAL;
+    if (!is_dtype(d->dtype)) return WTC_EDTYPE;
+    if (d->C > WTC_ROWS_MAX_C || d->T >= kMaxRows) return WTC_ESHAPE;
+    const int st = check_order(d->T * d->k, d->E);
+    if (st != WTC_OK) return st;
+    const long long chunks = ((long long)d->C * elem_bytes(d->dtype) + 15) / 16;
+    return d->T * chunks > (1LL << 33) ? WTC_ESHAPE : WTC_OK;   // 2^23 workgroups
+}
+
+int check_expert(const wtc_expert_desc* d) {
+    if (!d) return WTC_EINVAL;
+    if (d->R < 0 || d->K < 1 || d->N < 1 || d->E < 1) return WTC_EINVAL;
+    if (!is_dtype(d->dtype)) return WTC_EDTYPE;
+    if (d->K % 8 != 0 || d->N % 8 != 0 || d->K > 65536 || d->N > 65536) return WTC_ESHAPE;
+    return d->R >= kMaxRows || d->E > WTC_EXPERTS_MAX ? WTC_ESHAPE : WTC_OK;
+}
+int check_expert_rows(const wtc_expert_desc* d, long long stride, const void* p) {
+    if (stride < 0 || stride % (16 / elem_bytes(d->dtype)) != 0 || !aligned(p, 16)) return WTC_EINVAL;
+    return stride > WTC_EXPERT_MAX_STRIDE ? WTC_ESHAPE : WTC_OK;
+}
+
 int first_error(std::initializer_list<int> all) {
     for (int s : all)
         if (s != WTC_OK) return s;
@@ -162,6 +211,158 @@ int wtconv_attention_backward(const wtc_attn_desc* d, const void* q, const void*
     if (bad != WTC_OK) return bad;
     if (!workspace || workspace_bytes < wtconv_attention_backward_workspace(d)) return WTC_EWORKSPACE;
     return launch_attn_backward(d, q, k, v, out, lse, out_low, dout, cu_seqlens, dq, dk, dv, workspace, stream);
+}
+
+int wtconv_layer_norm_forward(const wtc_layer_desc* d, const void* x, const void* residual, const float* weight,
+                              const float* bias, void* y, void* h, float* stats, void* stream) {
+    const int st = check_layer(d);
+    if (st != WTC_OK) return st;
+    if ((residual != nullptr) != (h != nullptr) || !aligned(stats, 8)) return WTC_EINVAL;
+    if (d->rows == 0) return WTC_OK;
+    if (!x || !weight || !y) return WTC_EINVAL;
+    return launch_layer_forward(d, x, residual, weight, bias, y, h, stats, stream);
+}
+
+size_t wtconv_layer_norm_backward_workspace(const wtc_layer_desc* d) {
+    if (check_layer(d) != WTC_OK) return 0;
+    return (size_t)layer_backward_parts(d) * d->C * 2 * sizeof(float);
+}
+
+int wtconv_layer_norm_backward(const wtc_layer_desc* d, const void* dy, const void* dh, const void* h, const float* weight,
+                               const float* stats, void* dx, float* dw, float* db, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+    const int st = check_layer(d);
+    if (st != WTC_OK) return st;
+    if (!weight || !dw || !aligned(stats, 8)) return WTC_EINVAL;
+    if (d->rows > 0 && (!dy || !h || !stats || !dx)) return WTC_EINVAL;
+    const size_t need = wtconv_layer_norm_backward_workspace(d);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return WTC_EWORKSPACE;
+    return launch_layer_backward(d, dy, dh, h, weight, stats, dx, dw, db, static_cast<float*>(workspace), stream);
+}
+
+size_t wtconv_gated_scan_kept(const wtc_scan_desc* d) {
+    if (check_scan(d) != WTC_OK) return 0;
+    return (size_t)((d->T + kScanTile - 1) / kScanTile) * d->C * sizeof(float);
+}
+
+size_t wtconv_gated_scan_workspace(const wtc_scan_desc* d) {
+    if (check_scan(d) != WTC_OK) return 0;
+    return scan_workspace(d);
+}
+
+int wtconv_gated_scan_forward(const wtc_scan_desc* d, const void* x, const void* gate, const int* cu_seqlens,
+                              const float* state, void* y, float* last, float* kept, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+    const int st = check_scan(d);
+    if (st != WTC_OK) return st;
+    if (d->T == 0 && (d->n_seq == 0 || !last)) return WTC_OK;
+    if (!cu_seqlens || (d->T > 0 && (!x || !gate || !y))) return WTC_EINVAL;
+    const size_t need = scan_workspace(d);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return WTC_EWORKSPACE;
+    if (!aligned(workspace, 8)) return WTC_EINVAL;
+    return launch_scan_forward(d, x, gate, cu_seqlens, state, y, last, kept, workspace, stream);
+}
+
+int wtconv_gated_scan_backward(const wtc_scan_desc* d, const void* x, const void* gate, const int* cu_seqlens,
+                               const float* state, const float* kept, const void* dy, const float* dlast, void* dx, void* dgate,
+                               float* dstate, void* workspace, size_t workspace_bytes, void* stream) {
+    const int st = check_scan(d);
+    if (st != WTC_OK) return st;
+    if (d->T == 0 && (d->n_seq == 0 || !dstate)) return WTC_OK;
+    if (!cu_seqlens || (d->T > 0 && (!x || !gate || !kept || !dy || !dx || !dgate))) return WTC_EINVAL;
+    const size_t need = scan_workspace(d);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return WTC_EWORKSPACE;
+    if (!aligned(workspace, 8)) return WTC_EINVAL;
+    return launch_scan_backward(d, x, gate, cu_seqlens, state, kept, dy, dlast, dx, dgate, dstate, workspace, stream);
+}
+
+int wtconv_gated_scan_step(const wtc_scan_desc* d, const void* x, const void* gate, const float* state, void* y,
+                           float* state_out, void* stream) {
+    const int st = check_scan(d);
+    if (st != WTC_OK) return st;
+    if (d->T == 0) return WTC_OK;
+    if (!x || !gate || !state || !y || !state_out) return WTC_EINVAL;
+    return launch_scan_step(d, x, gate, state, y, state_out, stream);
+}
+
+size_t wtconv_expert_order_workspace(long long n, int E) { return check_order(n, E) != WTC_OK ? 0 : order_workspace(n, E); }
+
+int wtconv_expert_order(long long n, int E, const int* experts, int* slot, int* pair, int* cu_experts, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+    const int st = check_order(n, E);
+    if (st != WTC_OK) return st;
+    if (!cu_experts || (n > 0 && (!experts || !slot || !pair))) return WTC_EINVAL;
+    const size_t need = order_workspace(n, E);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return WTC_EWORKSPACE;
+    if (!aligned(workspace, 4)) return WTC_EINVAL;
+    return launch_expert_order(n, E, experts, slot, pair, cu_experts, workspace, stream);
+}
+
+int wtconv_expert_gather(const wtc_rows_desc* d, const void* x, const int* slot, const int* cu_experts, void* rows,
+                         void* stream) {
+    const int st = check_rows(d);
+    if (st != WTC_OK) return st;
+    if (d->T == 0) return WTC_OK;
+    if (!x || !slot || !cu_experts || !rows) return WTC_EINVAL;
+    return launch_rows_gather(d, x, slot, cu_experts, rows, stream);
+}
+
+int wtconv_expert_combine(const wtc_rows_desc* d, const void* rows, const float* weights, const int* slot, void* y,
+                          void* stream) {
+    const int st = check_rows(d);
+    if (st != WTC_OK) return st;
+    if (d->T == 0) return WTC_OK;
+    if (!rows || !slot || !y) return WTC_EINVAL;
+    return launch_rows_sum(d, rows, weights, slot, y, stream);
+}
+
+int wtconv_expert_combine_backward(const wtc_rows_desc* d, const void* dy, const void* rows, const float* weights,
+                                   const int* slot, const int* cu_experts, void* drows, float* dweights, void* stream) {
+    const int st = check_rows(d);
+    if (st != WTC_OK) return st;
+    if (d->T == 0) return WTC_OK;
+    if (!dy || !rows || !weights || !slot || !cu_experts || !drows || !dweights) return WTC_EINVAL;
+    return launch_rows_sum_backward(d, dy, rows, weights, slot, cu_experts, drows, dweights, stream);
+}
+
+int wtconv_expert_linear_forward(const wtc_expert_desc* d, const void* x, const void* weight, const void* bias,
+                                 const int* cu_experts, void* y, void* stream) {
+    const int st = check_expert(d);
+    if (st != WTC_OK) return st;
+    if (d->R == 0) return WTC_OK;
+    if (!x || !weight || !cu_experts || !y || !aligned(weight, 16) || !aligned(bias, 16) || !aligned(y, 16)) return WTC_EINVAL;
+    const int bad = check_expert_rows(d, d->x_stride, x);
+    if (bad != WTC_OK) return bad;
+    return launch_expert_forward(d, x, weight, bias, cu_experts, y, stream);
+}
+
+int wtconv_expert_linear_input_grad(const wtc_expert_desc* d, const void* dy, const void* weight, const int* cu_experts,
+                                    void* dx, void* stream) {
+    const int st = check_expert(d);
+    if (st != WTC_OK) return st;
+    if (d->R == 0) return WTC_OK;
+    if (!dy || !weight || !cu_experts || !dx || !aligned(weight, 16) || !aligned(dx, 16)) return WTC_EINVAL;
+    const int bad = check_expert_rows(d, d->g_stride, dy);
+    if (bad != WTC_OK) return bad;
+    return launch_expert_input_grad(d, dy, weight, cu_experts, dx, stream);
+}
+
+size_t wtconv_expert_linear_weight_grad_workspace(const wtc_expert_desc* d) {
+    return check_expert(d) != WTC_OK ? 0 : expert_weights_workspace(d);
+}
+
+int wtconv_expert_linear_weight_grad(const wtc_expert_desc* d, const void* dy, const void* x, const int* cu_experts,
+                                     void* dweight, void* dbias, void* workspace, size_t workspace_bytes, void* stream) {
+    const int st = check_expert(d);
+    if (st != WTC_OK) return st;
+    if (!cu_experts || !dweight || !aligned(dweight, 16) || !aligned(dbias, 16)) return WTC_EINVAL;
+    if (d->R > 0 && (!dy || !x)) return WTC_EINVAL;
+    const int bad = first_error({check_expert_rows(d, d->x_stride, x), check_expert_rows(d, d->g_stride, dy)});
+    if (bad != WTC_OK) return bad;
+    const size_t need = expert_weights_workspace(d);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return WTC_EWORKSPACE;
+    if (!aligned(workspace, 16)) return WTC_EINVAL;
+    return launch_expert_weight_grad(d, dy, x, cu_experts, dweight, dbias, workspace, stream);
 }
 
 }  // extern "C"

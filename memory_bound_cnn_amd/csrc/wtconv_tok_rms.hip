@@ -22,8 +22,7 @@
 // then reads h alone, and its gradient is that of what was computed.
 #include <hip/hip_runtime.h>
 
-#include "wtc_tok_device.h"
-#include "wtc_tok_internal.h"
+#include "wtc_tok_rows.h"
 
 namespace wtc {
 namespace {
@@ -41,40 +40,6 @@ struct RmsArgs {
     float eps, inv_C;
 };
 
-// Sum (or maximum) over the G lanes of a row; every lane gets it.  `red`: one
-// float per wave for groups wider than a wave (all threads of the workgroup
-// call it together).
-template <int G, bool MAX>
-__device__ __forceinline__ float group_reduce(float v, float* red) {
-#pragma unroll
-    for (int o = 1; o < (G < 64 ? G : 64); o <<= 1) {
-        const float other = __shfl_xor(v, o);
-        v = MAX ? fmaxf(v, other) : v + other;
-    }
-    if constexpr (G > 64) {
-        const int wave = threadIdx.x >> 6;
-        __syncthreads();   // the previous use of `red` is over
-        if ((threadIdx.x & 63) == 0) red[wave] = v;
-        __syncthreads();
-        v = red[0];
-#pragma unroll
-        for (int i = 1; i < G / 64; ++i) v = MAX ? fmaxf(v, red[i]) : v + red[i];
-    }
-    return v;
-}
-
-// Weights of channels c .. c + V - 1, zero past the last one.
-template <int V>
-__device__ __forceinline__ void load_weight(const RmsArgs& a, int c, float (&w)[V]) {
-#pragma unroll
-    for (int k = 0; k < V; k += 4) {
-        float part[4];
-        load_part(a.w + c + k, a.C - c - k, part);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[k + j] = part[j];
-    }
-}
-
 template <typename T, int G, int NV>
 __global__ void __launch_bounds__(G > 256 ? G : 256) k_rms_forward(RmsArgs a) {
     constexpr int V = kVec<T>, THREADS = G > 256 ? G : 256, RPB = THREADS / G;
@@ -83,7 +48,7 @@ __global__ void __launch_bounds__(G > 256 ? G : 256) k_rms_forward(RmsArgs a) {
     float w[NV][V];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        load_weight<V>(a, (lane + i * G) * V, w[i]);
+        load_weight<V>(a.w, a.C, (lane + i * G) * V, w[i]);
     }
     const long long step = (long long)gridDim.x * RPB;
     Raw<T> xn[NV], rn[NV];   // of the row that comes next
@@ -175,7 +140,7 @@ __global__ void __launch_bounds__(G > 256 ? G : 256) k_rms_backward(RmsArgs a) {
     float w[NV][V], dw[NV][V];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        load_weight<V>(a, (lane + i * G) * V, w[i]);
+        load_weight<V>(a.w, a.C, (lane + i * G) * V, w[i]);
 #pragma unroll
         for (int j = 0; j < V; ++j) dw[i][j] = 0.f;
     }
@@ -253,70 +218,6 @@ __global__ void __launch_bounds__(G > 256 ? G : 256) k_rms_backward(RmsArgs a) {
     }
 }
 
-// dw[c] = sum of the records' c, in a fixed order: 32 threads of a column take
-// every 32nd record, then their sums are joined.
-__global__ void __launch_bounds__(1024) k_rms_join(const float* __restrict__ parts, int n, int C,
-                                                   float* __restrict__ dw) {
-    __shared__ float sums[32][33];
-    const int col = threadIdx.x & 31, part = threadIdx.x >> 5, c = blockIdx.x * 32 + col;
-    float v = 0.f;
-    if (c < C) {
-#pragma unroll 8
-        for (int p = part; p < n; p += 32) v += parts[(size_t)p * C + c];
-    }
-    sums[part][col] = v;
-    __syncthreads();
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        if (part < o) sums[part][col] += sums[part + o][col];
-        __syncthreads();
-    }
-    if (part == 0 && c < C) dw[c] = sums[0][col];
-}
-
-// The group of G lanes and the NV vectors per lane for a row of n 16-byte
-// vectors: the first of these shapes, in the order of G * NV, that holds it.
-// Where two have the same G * NV the wider group stands here (longer runs of
-// consecutive addresses).  Those marked `many` leave no lane idle in rows of 24,
-// 48 and 96 vectors, and are for forward passes of kManyVectors and more, as
-// bfloat16 (without, with the residual): 65536 x 192 9.5 and 16.5 us, 11.4 and
-// 17.0 without them, 25088 x 384 8.4 and 13.3, 9.9 and 13.4; but 49 x 768 4.0
-// and 5.4, 3.7 and 4.5 without.  Around kManyVectors, 192 channels in a graph:
-// 5461 rows (2^17 vectors) 3.8 and 5.2, 3.3 and 4.0 without, 8192 rows 3.5 and
-// 4.6, 3.6 and 4.6, 10922 rows 4.1 and 5.8, 4.3 and 5.6, 21845 rows 5.3 and 8.5,
-// 5.8 and 7.8, 87381 rows 11.9 and 24.7, 13.4 and 24.8: the two meet between 2^17
-// and 2^18 without a residual, and with one do not differ by more than 0.8 us
-// from there on.  Nor for the backward pass, whose registers they
-// fill: 22.2 us, 18.2 without them, and 18.0, 15.2.
-struct RmsShape {
-    int G, NV;
-    bool many;
-};
-constexpr long long kManyVectors = 1 << 17;
-constexpr RmsShape kRmsShapes[] = {{2, 1, false},    {4, 1, false},    {8, 1, false},   {16, 1, false}, {8, 3, true},
-                                   {32, 1, false},   {16, 3, true},    {64, 1, false},  {32, 3, true},  {64, 2, false},
-                                   {64, 3, false},   {64, 4, false},   {256, 2, false}, {256, 3, false}, {256, 4, false},
-                                   {1024, 2, false}, {1024, 3, false}, {1024, 4, false}};
-constexpr int kRmsShapeCount = (int)(sizeof(kRmsShapes) / sizeof(kRmsShapes[0]));
-static_assert(1024 * 4 * kVec<float> >= WTC_RMS_MAX_C && 1024 * 2 * kVec<uint16_t> >= WTC_RMS_MAX_C, "the longest row");
-
-int rms_shape(int C, int dtype, long long forward_rows) {
-    const int V = dtype == WTC_BF16 ? kVec<uint16_t> : kVec<float>;
-    const bool many = forward_rows * ((C + V - 1) / V) >= kManyVectors;
-    int i = 0;
-    while (kRmsShapes[i].G * kRmsShapes[i].NV * V < C || (kRmsShapes[i].many && !many)) ++i;
-    return i;
-}
-
-// f<T, G, NV>() for shape number `at`; shapes past the longest row of T are
-// not compiled.
-template <typename T, int I = 0, typename F>
-void rms_dispatch(int at, const F& f) {
-    if (at == I) f.template operator()<T, kRmsShapes[I].G, kRmsShapes[I].NV>();
-    if constexpr (I + 1 < kRmsShapeCount)
-        if constexpr (kRmsShapes[I].G * kRmsShapes[I].NV * kVec<T> < WTC_RMS_MAX_C) rms_dispatch<T, I + 1>(at, f);
-}
-
 struct ForwardLaunch {
     const RmsArgs& a;
     hipStream_t st;
@@ -343,12 +244,7 @@ struct BackwardLaunch {
 
 }  // namespace
 
-int rms_backward_parts(const wtc_rms_desc* d) {
-    const int G = kRmsShapes[rms_shape(d->C, d->dtype, 0)].G, rpb = (G > 256 ? G : 256) / G;
-    // a row to a workgroup: fewer, whose records of C floats are much of the traffic
-    const long long blocks = (d->rows + rpb - 1) / rpb, most = G > 64 ? kRmsMaxParts / 2 : kRmsMaxParts;
-    return (int)(blocks < most ? blocks : most);
-}
+int rms_backward_parts(const wtc_rms_desc* d) { return row_parts(d->rows, d->C, d->dtype); }
 
 int launch_rms_forward(const wtc_rms_desc* d, const void* x, const void* r, const float* w, void* y, void* h,
                        float* rstd, float* scale, void* stream) {
@@ -357,11 +253,11 @@ int launch_rms_forward(const wtc_rms_desc* d, const void* x, const void* r, cons
     a.rows = d->rows; a.x_stride = d->x_stride; a.r_stride = d->r_stride;
     a.C = d->C; a.eps = d->eps; a.inv_C = 1.f / (float)d->C;
     const ForwardLaunch f = {a, reinterpret_cast<hipStream_t>(stream)};
-    const int at = rms_shape(d->C, d->dtype, d->rows);
+    const int at = row_shape(d->C, d->dtype, d->rows);
     if (d->dtype == WTC_BF16)
-        rms_dispatch<uint16_t>(at, f);
+        row_dispatch<uint16_t>(at, f);
     else
-        rms_dispatch<float>(at, f);
+        row_dispatch<float>(at, f);
     return hipGetLastError() == hipSuccess ? WTC_OK : WTC_EHIP;
 }
 
@@ -375,13 +271,14 @@ int launch_rms_backward(const wtc_rms_desc* d, const void* dy, const void* dh, c
     const int n = rms_backward_parts(d);
     if (n > 0) {
         const BackwardLaunch f = {a, st, n};
-        const int at = rms_shape(d->C, d->dtype, 0);
+        const int at = row_shape(d->C, d->dtype, 0);
         if (d->dtype == WTC_BF16)
-            rms_dispatch<uint16_t>(at, f);
+            row_dispatch<uint16_t>(at, f);
         else
-            rms_dispatch<float>(at, f);
+            row_dispatch<float>(at, f);
     }
-    hipLaunchKernelGGL(k_rms_join, dim3((unsigned)((d->C + 31) / 32)), dim3(1024), 0, st, parts, n, d->C, dw);
+    hipLaunchKernelGGL(k_row_join, dim3((unsigned)((d->C + 31) / 32)), dim3(1024), 0, st, parts, n, d->C, dw, d->C,
+                       static_cast<float*>(nullptr));
     return hipGetLastError() == hipSuccess ? WTC_OK : WTC_EHIP;
 }
 

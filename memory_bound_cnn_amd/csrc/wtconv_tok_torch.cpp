@@ -16,6 +16,7 @@
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/autograd_not_implemented_fallback.h>
+#include <torch/csrc/autograd/VariableTypeUtils.h>
 #include <torch/extension.h>
 #include <torch/library.h>
 
@@ -648,7 +649,10 @@ TORCH_LIBRARY_IMPL(wtconv_tokens, Autograd, m) {
         m.impl(part, torch::autograd::autogradNotImplementedFallback());
 }
 
+#include "wtc_tok_torch_mixer.h"
+
 PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
+    mixer_python(m);
     using nogil = py::call_guard<py::gil_scoped_release>;
     m.def("rms_norm", [](const Tensor& x, const Tensor& weight, const OptTensor& residual, double eps) {
         return OP(rms_norm).call(x, weight, residual, eps);

@@ -7,7 +7,9 @@ their first rows in ``cu_seqlens``.
 ``rms_norm``, ``rms_norm_fp8``, ``rotary``, ``attention``, ``rotary_attention``
 and ``dropout`` run in libwtconv's kernels (include/wtconv_tokens.h) on the
 current stream and have gradients (first ones only), except ``rms_norm_fp8``.
-``TokenBlock`` runs them together.
+``TokenBlock`` runs them together.  So do ``layer_norm``, ``gated_scan`` and the
+``expert_`` functions, and ``ScanBlock``, for planes too large for attention,
+runs those together; ``gated_scan_step`` and ``expert_order`` have no gradient.
 
 They go through the extension module ``_tokens`` (csrc/wtconv_tok_torch.cpp),
 which is loaded by the first call and must have been built; ``token_binding``
@@ -21,10 +23,13 @@ the backward pass to a thread of its own: within
 pass of 8 tokens take 32 us (norm) and 31 us (attention) instead of 75 and 72.
 """
 
+from typing import NamedTuple
+
 import torch
 
-__all__ = ["rms_norm", "rms_norm_fp8", "rotary", "attention", "rotary_attention", "dropout", "image_positions",
-           "rotary_frequencies", "RMSNorm", "TokenBlock"]
+__all__ = ["rms_norm", "rms_norm_fp8", "rotary", "attention", "rotary_attention", "dropout", "layer_norm", "gated_scan",
+           "gated_scan_step", "ExpertOrder", "expert_order", "expert_gather", "expert_linear", "expert_combine",
+           "image_positions", "rotary_frequencies", "RMSNorm", "TokenBlock", "LayerNorm", "Experts", "ScanBlock"]
 
 _ops = None
 
@@ -93,6 +98,67 @@ def dropout(x, p, rng, residual=None):
     elements, so every call of a step takes another offset.  p is taken to
     multiples of 2^-16."""
     return (_ops or _load()).dropout(x, p, rng, residual)
+
+
+def layer_norm(x, weight, bias=None, residual=None, eps=1e-6):
+    """y = (h - mean(h)) / sqrt(var(h) + eps) * weight + bias over the last
+    axis, h = x + residual in x's type.  Returns y, or (y, h) with a residual.
+    x [..., C] float32 or bfloat16, C up to 16384, weight and bias [C] float32."""
+    y, *h = (_ops or _load()).layer_norm(x, weight, bias, residual, eps)
+    return (y, *h) if h else y
+
+
+def gated_scan(x, gate, cu_seqlens, state=None, reverse=False):
+    """h_t = a_t h_(t-1) + (1 - a_t) x_t along each sequence of a pack, a =
+    sigmoid(gate): (y, last).  x and gate [T, C] (views of one projection, or
+    separate), y is h in x's type; h itself is float32.  cu_seqlens [n + 1] int32
+    as for :func:`attention`; tokens of no sequence get zeros.  state [n, C]
+    float32: what each sequence starts from, zeros unless given; last [n, C]
+    float32: what it leaves.  reverse: from the last token to the first."""
+    y, last = (_ops or _load()).gated_scan(x, gate, cu_seqlens, state, reverse)
+    return y, last
+
+
+def gated_scan_step(x, gate, state, out=None):
+    """:func:`gated_scan` of one more token of each sequence: (y, new state).  x
+    and gate [n, C], state [n, C] float32.  out: where the new state goes (state
+    itself, in a loop or a captured graph); a new tensor unless given.  No gradient."""
+    out = torch.empty_like(state, memory_format=torch.contiguous_format) if out is None else out
+    return (_ops or _load()).gated_scan_step(x, gate, state, out), out
+
+
+class ExpertOrder(NamedTuple):
+    """Pairs of a token and one of its k experts (pair t k + j) in the order of
+    the experts, those of one in the order of the pairs.  int32."""
+    slot: torch.Tensor         # [T, k]: each pair's place, -1 for pairs of no expert
+    pair: torch.Tensor         # [T k]: the pair at each place, -1 past the last one
+    cu_experts: torch.Tensor   # [E + 1]: expert e's places are cu_experts[e] up to cu_experts[e + 1]
+
+
+def expert_order(experts, n_experts):
+    """The order of tokens by expert.  experts [T, k] int32; a number outside of 0
+    .. n_experts - 1 (-1, for a token that only pads a batch) is no expert's.
+    n_experts up to 512."""
+    return ExpertOrder(*(_ops or _load()).expert_order(experts, n_experts))
+
+
+def expert_gather(x, order):
+    """x [T, C] to the rows of the experts, [T k, C] in the order of ``order``
+    (:func:`expert_order`); rows of no pair are zeros."""
+    return (_ops or _load()).expert_gather(x, order.slot, order.cu_experts)
+
+
+def expert_linear(x, weight, cu_experts, bias=None):
+    """x weight[e]^T + bias[e] for the rows of each expert e, cu_experts[e] up to
+    cu_experts[e + 1]; zeros for the rows of none.  x [R, K], weight [E, N, K] and
+    bias [E, N] in x's type, K and N multiples of 8; cu_experts [E + 1] int32."""
+    return (_ops or _load()).expert_linear(x, weight, bias, cu_experts)
+
+
+def expert_combine(rows, weights, order):
+    """The rows of the experts [T k, C] back to their tokens: y[t] = sum over j of
+    weights[t, j] times the row of pair (t, j).  weights [T, k] float32."""
+    return (_ops or _load()).expert_combine(rows, weights, order.slot, order.cu_experts)
 
 
 def rotary_frequencies(sections, base=10000.0, device=None):
@@ -189,3 +255,101 @@ class TokenBlock(torch.nn.Module):
                              causal=self.causal)
         h = self._dropout(self.proj(a.reshape(T, -1)), x, rng[0])
         return self._dropout(self.down(torch.nn.functional.gelu(self.up(self.norm2(h)))), h, rng[1])
+
+
+class LayerNorm(torch.nn.Module):
+    """:func:`layer_norm` with its weight and bias, which stay float32."""
+
+    def __init__(self, channels, eps=1e-6, bias=True, device=None):
+        super().__init__()
+        self.eps = eps
+        self.weight = torch.nn.Parameter(torch.ones(channels, dtype=torch.float32, device=device))
+        self.bias = torch.nn.Parameter(torch.zeros(channels, dtype=torch.float32, device=device)) if bias else None
+
+    def _apply(self, fn, recurse=True):
+        return super()._apply(_keep_dtype(fn), recurse)
+
+    def forward(self, x, residual=None):
+        return layer_norm(x, self.weight, self.bias, residual, self.eps)
+
+
+def _autocast(x):
+    """x in the type that autocast gives a linear layer."""
+    return x.to(torch.get_autocast_dtype(x.device.type)) if torch.is_autocast_enabled(x.device.type) else x
+
+
+class Experts(torch.nn.Module):
+    """A two-layer branch in several versions, of which each token takes the k
+    that a linear layer gives it the largest logits for, weighted by their softmax:
+        sum_j w_j down_e(gelu(up_e(x))),  e = e_j(x).
+    x [T, C] -> [T, C]."""
+
+    def __init__(self, channels, hidden, experts, k=2, device=None, dtype=torch.bfloat16):
+        super().__init__()
+        if not 1 <= k <= experts:
+            raise ValueError(f"{k} of {experts} experts a token")
+        self.experts, self.k = experts, k
+        f = dict(device=device, dtype=dtype)
+        self.router = torch.nn.Linear(channels, experts, bias=False, **f)
+
+        def uniform(*shape, fan):
+            return torch.nn.Parameter(torch.empty(*shape, **f).uniform_(-fan ** -0.5, fan ** -0.5))
+
+        self.up = uniform(experts, hidden, channels, fan=channels)
+        self.up_bias = uniform(experts, hidden, fan=channels)
+        self.down = uniform(experts, channels, hidden, fan=hidden)
+        self.down_bias = uniform(experts, channels, fan=hidden)
+
+    def forward(self, x):
+        x = _autocast(x)
+        top, chosen = self.router(x).float().topk(self.k, dim=1)
+        order = expert_order(chosen.to(torch.int32), self.experts)
+        up, up_bias, down, down_bias = (p.to(x.dtype) for p in (self.up, self.up_bias, self.down, self.down_bias))
+        rows = expert_linear(expert_gather(x, order), up, order.cu_experts, up_bias)
+        rows = expert_linear(torch.nn.functional.gelu(rows), down, order.cu_experts, down_bias)
+        return expert_combine(rows, torch.softmax(top, 1), order)
+
+
+class ScanBlock(torch.nn.Module):
+    """Pre-norm gated recurrence and experts over packed tokens, for planes too
+    large for attention:
+        h = x + proj(scan(values, gates of in(norm(x))))
+        out = h + experts(norm(h))
+    x [T, C].  Half of the channels run from each sequence's first token to its
+    last and half the other way; with causal all from the first, and
+    :meth:`step` takes one more token of each sequence."""
+
+    def __init__(self, channels, hidden=None, experts=8, k=2, causal=False, device=None, dtype=torch.bfloat16):
+        super().__init__()
+        if not causal and channels % 2:
+            raise ValueError(f"{channels} channels do not divide into two directions")
+        f = dict(device=device, dtype=dtype)
+        self.causal = causal
+        self.norm1, self.norm2 = LayerNorm(channels, device=device), LayerNorm(channels, device=device)
+        self.values = torch.nn.Linear(channels, 2 * channels, **f)   # and gates
+        self.proj = torch.nn.Linear(channels, channels, bias=False, **f)
+        self.experts = Experts(channels, hidden or 2 * channels, experts, k, **f)
+
+    def _branch(self, x, mixed):
+        n, h = self.norm2(self.proj(mixed).to(x.dtype), x)   # another type under autocast
+        return h + self.experts(n).to(x.dtype)
+
+    def forward(self, x, cu_seqlens):
+        C = x.shape[1]
+        if self.causal:
+            v, g = self.values(self.norm1(x)).split(C, 1)
+            mixed, _ = gated_scan(v, g, cu_seqlens)
+        else:
+            v, v_back, g, g_back = self.values(self.norm1(x)).split(C // 2, 1)
+            mixed = torch.cat([gated_scan(v, g, cu_seqlens)[0], gated_scan(v_back, g_back, cu_seqlens, reverse=True)[0]], 1)
+        return self._branch(x, mixed)
+
+    def step(self, x, state):
+        """One more token of each of n sequences: (out, state).  x [n, C]; state [n,
+        C] float32, zeros at first, is updated in place.  No gradient."""
+        if not self.causal:
+            raise ValueError("only a causal block takes one token after another")
+        with torch.no_grad():
+            v, g = self.values(self.norm1(x)).split(x.shape[1], 1)
+            mixed, state = gated_scan_step(v, g, state, out=state)
+            return self._branch(x, mixed), state
