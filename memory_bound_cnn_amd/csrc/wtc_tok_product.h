@@ -8,12 +8,12 @@
 // 8 (r / 4) + 4 h + r % 4, h = lane / 32: four consecutive ones at a time.
 //   An operand lies in memory with its terms (what is summed over) along the
 // rows or across them:
-//   Along   a row of the tile is a row of the output's (or a column's) 128 bytes
-//           of terms; a lane reads 16 bytes of its row.
+//   Along   a row of the tile is a step's terms of a row (or column) of the
+//           output; a lane reads 16 bytes of its row.
 //   Across  a row of the tile is one term, its 16-byte chunks are rows (columns)
 //           of the output; bfloat16 is read with the transposing instruction,
 //           float32 a value at a time.
-// A step takes 128 bytes of terms.  Tiles are copied by the memory system 1024
+// A step takes 64 or 128 bytes of terms.  Tiles are copied by the memory system 1024
 // consecutive bytes of shared memory at a time, and the chunks of a row are
 // permuted on that way so that reads meet no bank twice.
 #pragma once
@@ -34,13 +34,9 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) char lds_char;
 
-template <typename T>
-constexpr int kTerms = 128 / (int)sizeof(T);   // of a step
-// A lane's terms of one read: 8 bfloat16 or 4 float32, of the two halves 16 or 8.
+// A lane's terms of one read are 16 bytes, those of the two halves of a wave 32.
 template <typename T>
 constexpr int kRead = 2 * kVec<T>;
-template <typename T>
-constexpr int kReads = kTerms<T> / kRead<T>;   // 4
 
 __device__ __forceinline__ void mma(const u32x4& a, const u32x4& b, f32x16& c, uint16_t) {
     c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -62,44 +58,51 @@ __device__ __forceinline__ void copy1024(uint32_t dst, const char* base, uint32_
                  : "m0", "memory");
 }
 
-// N rows (or columns) of an operand whose terms lie along its rows.
-template <typename T, int N, int WAVES>
+// N rows (or columns) of an operand whose terms lie along its rows, BYTES (64 or 128) of terms.
+template <typename T, int N, int WAVES, int BYTES>
 struct Along {
-    static constexpr int kBytes = N * 128, kCopies = kBytes / 1024 / WAVES;
+    static constexpr int kBytes = N * BYTES, kCopies = kBytes / 1024 / WAVES, kChunks = BYTES / 16;
     static_assert(kBytes % (1024 * WAVES) == 0, "whole copies");
+    // 16 lanes read a chunk of 16 rows: those rows' chunks that share banks, 256 bytes apart, are exchanged
+    static constexpr __host__ __device__ int turn(int row) { return (row * BYTES / 256) & (kChunks - 1); }
     // bytes from the operand's first row to the lane's part of each copy; rows past `last` repeat it
     uint32_t off[kCopies];
     int unit[kCopies];      // the chunk of the row
     __device__ __forceinline__ void place(uint32_t row_bytes, int last, int wave, int lane) {
 #pragma unroll
         for (int i = 0; i < kCopies; ++i) {
-            const int r = (wave * kCopies + i) * 8 + lane / 8;
-            unit[i] = (lane % 8) ^ ((r >> 1) & 7);
+            const int r = (wave * kCopies + i) * (64 / kChunks) + lane / kChunks;
+            unit[i] = (lane % kChunks) ^ turn(r);
             off[i] = (uint32_t)min(r, last) * row_bytes + unit[i] * 16;
         }
     }
-    // base: the step's first term of the operand's first row; chunks: of terms that are there, if fewer than 8
+    // base: the step's first term of the operand's first row; chunks: of terms that are there, if fewer than a step's
     __device__ __forceinline__ void copy(uint32_t dst, const char* base, int chunks, int wave) const {
 #pragma unroll
         for (int i = 0; i < kCopies; ++i) {
-            const uint32_t back = chunks < 8 && unit[i] >= chunks ? (uint32_t)(unit[i] - chunks + 1) * 16 : 0;
+            const uint32_t back = chunks < kChunks && unit[i] >= chunks ? (uint32_t)(unit[i] - chunks + 1) * 16 : 0;
             copy1024(dst + (wave * kCopies + i) * 1024, base, off[i] - back);
         }
     }
-    __device__ static __forceinline__ int lane_part(int lane) { return (lane & 31) * 128; }
+    // Zeros to the chunks of terms that are not there.
+    __device__ static __forceinline__ void clear(char* tile, int chunks) {
+        for (int u = threadIdx.x; u < N * kChunks; u += 64 * WAVES)
+            if (((u % kChunks) ^ turn(u / kChunks)) >= chunks) *reinterpret_cast<u32x4*>(tile + u * 16) = u32x4{0u, 0u, 0u, 0u};
+    }
+    __device__ static __forceinline__ int lane_part(int lane) { return (lane & 31) * BYTES; }
     // 16 bytes of terms of row r0 + lane % 32, r0 a multiple of 32
     __device__ static __forceinline__ u32x4 read(const char* tile, int part, int r0, int at, int lane) {
-        const int unit = (2 * at + (lane >> 5)) ^ ((lane >> 1) & 7);
-        return *reinterpret_cast<const u32x4*>(tile + part + r0 * 128 + unit * 16);
+        const int unit = (2 * at + (lane >> 5)) ^ turn(lane & 31);
+        return *reinterpret_cast<const u32x4*>(tile + part + r0 * BYTES + unit * 16);
     }
 };
 
 // The same of an operand whose terms lie across: a row of the tile is one term
 // with N of the output's rows (or columns).
-template <typename T, int N, int WAVES>
+template <typename T, int N, int WAVES, int BYTES>
 struct Across {
     static constexpr int kRow = N * (int)sizeof(T), kChunks = kRow / 16;
-    static constexpr int kBytes = kTerms<T> * kRow, kCopies = kBytes / 1024 / WAVES;
+    static constexpr int kBytes = BYTES / (int)sizeof(T) * kRow, kCopies = kBytes / 1024 / WAVES;
     static constexpr int kRowsEach = 1024 / kRow > 0 ? 1024 / kRow : 1;
     static_assert(kBytes % (1024 * WAVES) == 0 && 1024 % kRow == 0 && kRow >= 256, "whole copies, and chunks to permute");
     // the permutation of a row's chunks: bfloat16 by 64 bytes, with the four terms of one
@@ -121,6 +124,11 @@ struct Across {
 #pragma unroll
         for (int i = 0; i < kCopies; ++i)
             copy1024(dst + (wave * kCopies + i) * 1024, base, (uint32_t)min(term[i], last) * row_bytes + unit[i]);
+    }
+    // Zeros to the terms from `there` on.
+    __device__ static __forceinline__ void clear(char* tile, int there) {
+        for (int b = there * kRow + (int)threadIdx.x * 16; b < kBytes; b += 64 * WAVES * 16)
+            *reinterpret_cast<u32x4*>(tile + b) = u32x4{0u, 0u, 0u, 0u};
     }
     // The lane's part: of the terms it reads first, and its column's.
     __device__ static __forceinline__ int lane_part(int lane) {
@@ -149,24 +157,6 @@ struct Across {
         return v;
     }
 };
-
-// Zeros the terms from `there` on (counted from the step's first).
-template <typename T>
-__device__ __forceinline__ u32x4 cut(u32x4 v, int at, int there, int lane) {
-    const int first = kRead<T> * at + kVec<T> * (lane >> 5);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (sizeof(T) == 2) {
-            if (first + 2 * i >= there)
-                v[i] = 0;
-            else if (first + 2 * i + 1 >= there)
-                v[i] &= 0xFFFFu;
-        } else {
-            if (first + i >= there) v[i] = 0;
-        }
-    }
-    return v;
-}
 
 // ------------------------------------------------------------------ work
 // The rows of a tile: SIZE of one expert's, or of no expert's (before the first's, after the last's).
@@ -213,14 +203,30 @@ __device__ __forceinline__ int spread(int id, int all) {
 // Stores 32 rows by 32 NB columns of a wave from its blocks (see above) through
 // shared memory (`at`, kStoreBytes of the wave's own), so that a store has whole
 // rows of 16-byte chunks.  Rows `rows` and more, and columns `columns` and more,
-// are not there.  bias: of the wave's first column, or null.
+// are not there.
 template <typename T, int NB>
 constexpr int kStoreRow = 32 * NB * (int)sizeof(T) + 16;
 template <typename T, int NB>
 constexpr int kStoreBytes = 32 * kStoreRow<T, NB>;
 
+// Elements at .. at + 3 (a multiple of four) of an aligned row.
+__device__ __forceinline__ void load_four(const uint16_t* p, int at, float (&v)[4]) {
+    const u32x2 u = *reinterpret_cast<const u32x2*>(p + at);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t e = u[i];
+        v[2 * i] = __builtin_bit_cast(float, e << 16);
+        v[2 * i + 1] = __builtin_bit_cast(float, e & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ void load_four(const float* p, int at, float (&v)[4]) {
+    const f32x4 u = *reinterpret_cast<const f32x4*>(p + at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = u[i];
+}
+
 template <typename T, int NB>
-__device__ __forceinline__ void store_block(char* at, T* out, long long stride, int rows, int columns, const T* bias, int lane,
+__device__ __forceinline__ void store_block(char* at, T* out, long long stride, int rows, int columns, int lane,
                                             const f32x16 (&c)[NB]) {
     constexpr int ROW = kStoreRow<T, NB>, CH = 32 * NB * (int)sizeof(T) / 16;
     asm volatile("" ::: "memory");
@@ -229,12 +235,7 @@ __device__ __forceinline__ void store_block(char* at, T* out, long long stride, 
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-            f32x4 v = {c[nb][4 * g], c[nb][4 * g + 1], c[nb][4 * g + 2], c[nb][4 * g + 3]};
-            const int j = 32 * nb + 8 * g + 4 * (lane >> 5);
-            if (bias && j < columns) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] += to_f32(bias[j + i]);
-            }
+            const f32x4 v = {c[nb][4 * g], c[nb][4 * g + 1], c[nb][4 * g + 2], c[nb][4 * g + 3]};
             char* to = p + (32 * nb + 8 * g) * (int)sizeof(T);
             if constexpr (sizeof(T) == 2)
                 *reinterpret_cast<u32x2*>(to) = u32x2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};

@@ -8,6 +8,10 @@
 // copied to shared memory STAGES - 1 steps ahead of their products.
 #pragma once
 
+#include <limits.h>
+
+#include <type_traits>
+
 #include "wtc_tok_product.h"
 
 namespace wtc {
@@ -24,6 +28,18 @@ struct Args {
     int R, E, K, N, splits;
 };
 
+// The expert with the rank-th most rows, for up to 64 experts; beyond, experts in their order.
+__device__ __forceinline__ int expert_of_rank(const int* cu, int E, int R, int rank, int lane) {
+    if (E > 64) return rank;
+    const int n = lane < E ? segment_begin(cu, E, R, lane + 2) - segment_begin(cu, E, R, lane + 1) : INT_MIN;
+    int before = 0;
+    for (int e = 0; e < E; ++e) {
+        const int m = __builtin_amdgcn_readlane(n, e);
+        before += m > n || (m == n && e < lane);
+    }
+    return __builtin_ctzll(__builtin_amdgcn_ballot_w64(lane < E && before == rank) | (1ull << 63)) % E;
+}
+
 // Waits until at most N of the wave's copies are on their way.
 template <int N>
 __device__ __forceinline__ void wait_copies() {
@@ -36,39 +52,55 @@ __device__ __forceinline__ void meet() {
 }
 
 // The products of one step: NB blocks of columns by MB of rows, from the wave's first.
-template <typename T, int NB, int MB, typename Cols, typename RowsOp>
+template <typename T, int READS, int NB, int MB, typename Cols, typename RowsOp>
 __device__ __forceinline__ void step(const char* cols, const char* rows, int cpart, int rpart, int col0, int row0, int lane,
-                                     bool partial, int there, f32x16 (&acc)[MB][NB]) {
+                                     f32x16 (&acc)[MB][NB]) {
+    constexpr int GROUP = 64 / (NB + MB) / 4 < READS ? 2 : READS;   // reads at once, of up to 64 registers
 #pragma unroll
-    for (int at = 0; at < kReads<T>; ++at) {
-        u32x4 a[NB], b[MB];
+    for (int g = 0; g < READS; g += GROUP) {
+        u32x4 a[GROUP][NB], b[GROUP][MB];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) a[nb] = Cols::read(cols, cpart, col0 + 32 * nb, at, lane);
+        for (int at = 0; at < GROUP; ++at) {
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb) b[mb] = RowsOp::read(rows, rpart, row0 + 32 * mb, at, lane);
-        if (partial) {
-            if (at * kRead<T> >= there) break;
+            for (int nb = 0; nb < NB; ++nb) a[at][nb] = Cols::read(cols, cpart, col0 + 32 * nb, g + at, lane);
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) a[nb] = cut<T>(a[nb], at, there, lane);
-#pragma unroll
-            for (int mb = 0; mb < MB; ++mb) b[mb] = cut<T>(b[mb], at, there, lane);
+            for (int mb = 0; mb < MB; ++mb) b[at][mb] = RowsOp::read(rows, rpart, row0 + 32 * mb, g + at, lane);
         }
+        __builtin_amdgcn_sched_barrier(0);   // all reads are on their way before the first product
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb)
+        for (int at = 0; at < GROUP; ++at)
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) mma(a[nb], b[mb], acc[mb][nb], T{});
+            for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    mma(a[at][nb], b[at][mb], acc[mb][nb], T{});
+                    if (at == 0 && mb == 0 && nb == 0) {
+                        __builtin_amdgcn_sched_barrier(0);
+                        __builtin_amdgcn_s_setprio(1);
+                    }
+                }
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_setprio(0);
     }
 }
 
+template <typename T>
+__device__ __forceinline__ float add_terms(const u32x4& v) {
+    float x[kVec<T>];
+    unpack(Raw<T>{v}, x);
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kVec<T>; i += 4) s += (x[i] + x[i + 1]) + (x[i + 2] + x[i + 3]);
+    return s;
+}
+
 // WM x WN waves of MB x NB blocks each.
-template <typename T, bool BACK, int WM, int WN, int MB, int NB, int STAGES>
-__global__ void __launch_bounds__(64 * WM * WN) k_product_rows(Args a) {
-    constexpr int WAVES = WM * WN, BM = 32 * WM * MB, BN = 32 * WN * NB, TERMS = kTerms<T>;
-    using X = Along<T, BM, WAVES>;
-    using WF = Along<T, BN, WAVES>;
-    using WB = Across<T, BN, WAVES>;
-    constexpr int STAGE = X::kBytes + WF::kBytes, COPIES = X::kCopies + WF::kCopies;
-    static_assert(WF::kBytes == WB::kBytes && WF::kCopies == WB::kCopies, "one size");
+template <typename T, bool BACK, int WM, int WN, int MB, int NB, int BYTES, int STAGES>
+__global__ void __launch_bounds__(64 * WM * WN, 2) k_product_rows(Args a) {
+    constexpr int WAVES = WM * WN, BM = 32 * WM * MB, BN = 32 * WN * NB, TERMS = BYTES / (int)sizeof(T), READS = BYTES / 32;
+    using X = Along<T, BM, WAVES, BYTES>;
+    using W = typename std::conditional<BACK, Across<T, BN, WAVES, BYTES>, Along<T, BN, WAVES, BYTES>>::type;
+    constexpr int STAGE = X::kBytes + W::kBytes, COPIES = X::kCopies + W::kCopies;
     constexpr int STORE = WAVES * kStoreBytes<T, NB>, LDS = STAGES * STAGE > STORE ? STAGES * STAGE : STORE;
     static_assert(LDS <= 160 * 1024, "shared memory");
     __shared__ __align__(16) char lds[LDS];
@@ -80,9 +112,24 @@ __global__ void __launch_bounds__(64 * WM * WN) k_product_rows(Args a) {
     const int high = min(8, (int)a.slots - 8 * group), col0 = in / high * BN;
     const Rows r = find_rows<BM>(a.cu, a.E, a.R, 8 * group + in % high, lane);
     if (r.count == 0) return;
-    f32x16 acc[MB][NB] = {};
     const bool none = r.expert < 0;
     const size_t expert = none ? 0 : r.expert;
+    const int col = col0 + 32 * NB * wn;
+    f32x16 acc[MB][NB] = {};
+    if (!BACK && !none && a.b) {   // the sums start from the bias
+        const T* bias = static_cast<const T*>(a.b) + expert * a.N;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                float v[4];
+                load_four(bias, min(col + 32 * nb + 8 * g + 4 * (lane >> 5), columns - 4), v);
+#pragma unroll
+                for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[mb][nb][4 * g + i] = v[i];
+            }
+    }
     if (!none) {
         constexpr int SZ = (int)sizeof(T);
         const uint32_t xrow = (uint32_t)a.x_stride * SZ, wrow = (uint32_t)a.K * SZ;
@@ -91,62 +138,62 @@ __global__ void __launch_bounds__(64 * WM * WN) k_product_rows(Args a) {
                         (BACK ? (size_t)col0 * SZ : (size_t)col0 * a.K * SZ);
         const int here = min(columns - col0, BN);
         X xt;
-        WF wf;
-        WB wb;
+        W wt;
         xt.place(xrow, r.count - 1, wave, lane);
         if constexpr (BACK)
-            wb.place(here / kVec<T> - 1, wave, lane);
+            wt.place(here / kVec<T> - 1, wave, lane);
         else
-            wf.place(wrow, here - 1, wave, lane);
+            wt.place(wrow, here - 1, wave, lane);
         const uint32_t lds0 = lds_address(lds);
         const int steps = (terms + TERMS - 1) / TERMS;
         auto copy = [&](int s) {
             const uint32_t at = lds0 + (uint32_t)(s % STAGES) * STAGE;
             const int left = terms - s * TERMS;
-            xt.copy(at, x + (size_t)s * 128, left / kVec<T>, wave);
+            xt.copy(at, x + (size_t)s * BYTES, left / kVec<T>, wave);
             if constexpr (BACK)
-                wb.copy(at + X::kBytes, w + (size_t)s * TERMS * wrow, wrow, left - 1, wave);
+                wt.copy(at + X::kBytes, w + (size_t)s * TERMS * wrow, wrow, left - 1, wave);
             else
-                wf.copy(at + X::kBytes, w + (size_t)s * 128, left / kVec<T>, wave);
+                wt.copy(at + X::kBytes, w + (size_t)s * BYTES, left / kVec<T>, wave);
         };
 #pragma unroll
         for (int s = 0; s < STAGES - 1; ++s)
             if (s < steps) copy(s);
-        const int xpart = X::lane_part(lane), wpart = BACK ? WB::lane_part(lane) : WF::lane_part(lane);
+        const int xpart = X::lane_part(lane), wpart = W::lane_part(lane);
         for (int s = 0; s < steps; ++s) {
             if (s + STAGES - 1 <= steps)
                 wait_copies<(STAGES - 2) * COPIES>();
             else
                 wait_copies<0>();
             meet();   // step s is there; everyone is done with the one before it
-            if (s + STAGES - 1 < steps) copy(s + STAGES - 1);
-            const char* at = lds + s % STAGES * STAGE;
+            char* at = lds + s % STAGES * STAGE;
             const int left = terms - s * TERMS;
-            if (left >= TERMS)
-                step<T, NB, MB, typename std::conditional<BACK, WB, WF>::type, X>(at + X::kBytes, at, wpart, xpart, 32 * NB * wn,
-                                                                                  32 * MB * wm, lane, false, 0, acc);
-            else
-                step<T, NB, MB, typename std::conditional<BACK, WB, WF>::type, X>(at + X::kBytes, at, wpart, xpart, 32 * NB * wn,
-                                                                                  32 * MB * wm, lane, true, left, acc);
+            if (left < TERMS) {   // the last step
+                X::clear(at, left / kVec<T>);
+                if constexpr (BACK)
+                    W::clear(at + X::kBytes, left);
+                else
+                    W::clear(at + X::kBytes, left / kVec<T>);
+                meet();
+            }
+            if (s + STAGES - 1 < steps) copy(s + STAGES - 1);
+            step<T, READS, NB, MB, W, X>(at + X::kBytes, at, wpart, xpart, 32 * NB * wn, 32 * MB * wm, lane, acc);
         }
         meet();   // no tile is read any more
     }
-    const int col = col0 + 32 * NB * wn;
-    const T* bias = BACK || none || !a.b ? nullptr : static_cast<const T*>(a.b) + expert * a.N + col;
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
         const int row = 32 * (MB * wm + mb);
         if (row >= r.count || col >= columns) break;
         store_block<T, NB>(lds + wave * kStoreBytes<T, NB>, static_cast<T*>(a.y) + (long long)(r.start + row) * columns + col,
-                           columns, r.count - row, columns - col, bias, lane, acc[mb]);
+                           columns, r.count - row, columns - col, lane, acc[mb]);
     }
 }
 
-template <typename T, int WM, int WN, int MB, int NB, int STAGES>
-__global__ void __launch_bounds__(64 * WM * WN) k_product_weights(Args a) {
-    constexpr int WAVES = WM * WN, BM = 32 * WM * MB, BN = 32 * WN * NB, TERMS = kTerms<T>;
-    using G = Across<T, BM, WAVES>;
-    using X = Across<T, BN, WAVES>;
+template <typename T, int WM, int WN, int MB, int NB, int BYTES, int STAGES>
+__global__ void __launch_bounds__(64 * WM * WN, 2) k_product_weights(Args a) {
+    constexpr int WAVES = WM * WN, BM = 32 * WM * MB, BN = 32 * WN * NB, TERMS = BYTES / (int)sizeof(T), READS = BYTES / 32;
+    using G = Across<T, BM, WAVES, BYTES>;
+    using X = Across<T, BN, WAVES, BYTES>;
     constexpr int STAGE = G::kBytes + X::kBytes, COPIES = G::kCopies + X::kCopies;
     constexpr int STORE = WAVES * kStoreBytes<float, NB>, LDS = STAGES * STAGE > STORE ? STAGES * STAGE : STORE;
     static_assert(LDS <= 160 * 1024, "shared memory");
@@ -154,16 +201,18 @@ __global__ void __launch_bounds__(64 * WM * WN) k_product_weights(Args a) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
     const int ktiles = (a.K + BN - 1) / BN, ntiles = (a.N + BM - 1) / BM;
-    int id = spread(blockIdx.x, gridDim.x);
+    // the tiles of the expert with the most rows first; those of one are spread over the XCDs by runs
+    const int per = ktiles * ntiles * a.splits, rank = blockIdx.x / per;
+    int id = spread(blockIdx.x % per, per);
+    const int e = expert_of_rank(a.cu, a.E, a.R, rank, lane);
     const int col0 = id % ktiles * BN;
     id /= ktiles;
-    const int row0 = id % ntiles * BM;
-    id /= ntiles;
-    const int split = id % a.splits, e = id / a.splits;
+    const int row0 = id % ntiles * BM, split = id / ntiles;
     const int first = segment_begin(a.cu, a.E, a.R, e + 1), count = max(segment_begin(a.cu, a.E, a.R, e + 2) - first, 0);
     const int all = (count + TERMS - 1) / TERMS;
     const int begin = (int)((long long)all * split / a.splits), end = (int)((long long)all * (split + 1) / a.splits);
-    f32x16 acc[MB][NB] = {}, sum[MB] = {};
+    f32x16 acc[MB][NB] = {};
+    float sum[MB] = {};   // of dy's columns: the lane's half of the terms
     const bool sums = a.db && col0 == 0 && wn == 0;
     constexpr int SZ = (int)sizeof(T);
     const uint32_t grow = (uint32_t)a.g_stride * SZ, xrow = (uint32_t)a.x_stride * SZ;
@@ -184,29 +233,27 @@ __global__ void __launch_bounds__(64 * WM * WN) k_product_weights(Args a) {
     for (int s = 0; s < STAGES - 1; ++s)
         if (begin + s < end) copy(begin + s);
     const int gpart = G::lane_part(lane), xpart = X::lane_part(lane);
-    const uint32_t one = sizeof(T) == 2 ? 0x3F803F80u : 0x3F800000u;
-    const u32x4 ones = {one, one, one, one};
     for (int s = begin; s < end; ++s) {
         if (s + STAGES - 1 <= end)
             wait_copies<(STAGES - 2) * COPIES>();
         else
             wait_copies<0>();
         meet();
-        if (s + STAGES - 1 < end) copy(s + STAGES - 1);
-        const char* at = lds + (s - begin) % STAGES * STAGE;
+        char* at = lds + (s - begin) % STAGES * STAGE;
         const int left = count - s * TERMS;
-        if (left >= TERMS)
-            step<T, NB, MB, X, G>(at + G::kBytes, at, xpart, gpart, 32 * NB * wn, 32 * MB * wm, lane, false, 0, acc);
-        else
-            step<T, NB, MB, X, G>(at + G::kBytes, at, xpart, gpart, 32 * NB * wn, 32 * MB * wm, lane, true, left, acc);
+        if (left < TERMS) {   // the expert's last step
+            G::clear(at, left);
+            X::clear(at + G::kBytes, left);
+            meet();
+        }
+        if (s + STAGES - 1 < end) copy(s + STAGES - 1);
+        step<T, READS, NB, MB, X, G>(at + G::kBytes, at, xpart, gpart, 32 * NB * wn, 32 * MB * wm, lane, acc);
         if (sums) {
 #pragma unroll
-            for (int k = 0; k < kReads<T>; ++k)
+            for (int k = 0; k < READS; ++k)
 #pragma unroll
                 for (int mb = 0; mb < MB; ++mb) {
-                    u32x4 v = G::read(at, gpart, 32 * (MB * wm + mb), k, lane);
-                    if (left < TERMS) v = cut<T>(v, k, left, lane);
-                    mma(ones, v, sum[mb], T{});
+                    sum[mb] += add_terms<T>(G::read(at, gpart, 32 * (MB * wm + mb), k, lane));
                 }
         }
     }
@@ -217,20 +264,23 @@ __global__ void __launch_bounds__(64 * WM * WN) k_product_weights(Args a) {
     for (int mb = 0; mb < MB; ++mb) {
         const int row = row0 + 32 * (MB * wm + mb);
         if (row >= a.N) break;
-        if (sums && lane < 32 && row + lane < a.N) {   // every register of a lane is its row's sum
-            if (a.splits == 1)
-                static_cast<T*>(a.db)[(size_t)e * a.N + row + lane] = from_f32<T>(sum[mb][0]);
-            else
-                a.parts[a.splits * weights + ((size_t)split * a.E + e) * a.N + row + lane] = sum[mb][0];
+        if (sums) {
+            const float both = sum[mb] + __shfl_xor(sum[mb], 32);
+            if (lane < 32 && row + lane < a.N) {
+                if (a.splits == 1)
+                    static_cast<T*>(a.db)[(size_t)e * a.N + row + lane] = from_f32<T>(both);
+                else
+                    a.parts[a.splits * weights + ((size_t)split * a.E + e) * a.N + row + lane] = both;
+            }
         }
         if (col >= a.K) continue;
         const size_t to = ((size_t)e * a.N + row) * a.K + col;
         if (a.splits == 1)
             store_block<T, NB>(lds + wave * kStoreBytes<T, NB>, static_cast<T*>(a.y) + to, a.K, a.N - row, a.K - col,
-                               static_cast<const T*>(nullptr), lane, acc[mb]);
+                               lane, acc[mb]);
         else
             store_block<float, NB>(lds + wave * kStoreBytes<float, NB>, a.parts + split * weights + to, a.K, a.N - row, a.K - col,
-                                   static_cast<const float*>(nullptr), lane, acc[mb]);
+                                   lane, acc[mb]);
     }
 }
 
@@ -253,28 +303,42 @@ __global__ void __launch_bounds__(256) k_product_join(Args a, long long n, long 
 
 constexpr int kTile = 128;   // rows and columns of a workgroup's tile
 
-template <typename T>
-int run_rows(Args a, bool back, hipStream_t st) {
-    const int columns = back ? a.K : a.N;
-    a.slots = row_slots(a.R, a.E, kTile);
-    const long long groups = a.slots * ((columns + kTile - 1) / kTile);
+template <typename T, bool BACK, int WM, int WN, int MB, int NB, int BYTES, int STAGES>
+int launch_rows(Args a, hipStream_t st) {
+    constexpr int BM = 32 * WM * MB, BN = 32 * WN * NB;
+    a.slots = row_slots(a.R, a.E, BM);
+    const long long groups = a.slots * (((BACK ? a.K : a.N) + BN - 1) / BN);
     if (groups > (1 << 23)) return WTC_ESHAPE;
-    if (back)
-        hipLaunchKernelGGL((k_product_rows<T, true, 2, 2, 2, 2, 2>), dim3((unsigned)groups), dim3(256), 0, st, a);
-    else
-        hipLaunchKernelGGL((k_product_rows<T, false, 2, 2, 2, 2, 2>), dim3((unsigned)groups), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((k_product_rows<T, BACK, WM, WN, MB, NB, BYTES, STAGES>), dim3((unsigned)groups), dim3(64 * WM * WN), 0, st, a);
+    return hipGetLastError() == hipSuccess ? WTC_OK : WTC_EHIP;
+}
+template <typename T, bool BACK>
+int run_rows_way(const Args& a, hipStream_t st) {
+    const long long big = (a.R / 128) * (((BACK ? a.K : a.N) + 255) / 256);
+    if (sizeof(T) == 2 && big >= 512) return launch_rows<T, BACK, 1, 4, 4, 2, 64, 3>(a, st);
+    return launch_rows<T, BACK, 2, 2, 2, 2, 128, 2>(a, st);
+}
+template <typename T>
+int run_rows(const Args& a, bool back, hipStream_t st) {
+    return back ? run_rows_way<T, true>(a, st) : run_rows_way<T, false>(a, st);
+}
+template <typename T, int WM, int WN, int MB, int NB, int BYTES, int STAGES>
+int launch_weights(const Args& a, hipStream_t st) {
+    constexpr int BM = 32 * WM * MB, BN = 32 * WN * NB;
+    const long long groups = (long long)((a.K + BN - 1) / BN) * ((a.N + BM - 1) / BM) * a.E * a.splits;
+    if (groups > (1 << 23)) return WTC_ESHAPE;
+    hipLaunchKernelGGL((k_product_weights<T, WM, WN, MB, NB, BYTES, STAGES>), dim3((unsigned)groups), dim3(64 * WM * WN), 0, st, a);
     return hipGetLastError() == hipSuccess ? WTC_OK : WTC_EHIP;
 }
 template <typename T>
 int run_weights(const Args& a, hipStream_t st) {
-    const long long groups = (long long)((a.K + kTile - 1) / kTile) * ((a.N + kTile - 1) / kTile) * a.E * a.splits;
-    if (groups > (1 << 23)) return WTC_ESHAPE;
-    hipLaunchKernelGGL((k_product_weights<T, 2, 2, 2, 2, 2>), dim3((unsigned)groups), dim3(256), 0, st, a);
-    if (a.splits > 1) {
+    const long long big = (long long)(a.K / 256) * (a.N / 128) * a.E;
+    const int r = sizeof(T) == 2 && big >= 256 ? launch_weights<T, 1, 4, 4, 2, 64, 3>(a, st) : launch_weights<T, 2, 2, 2, 2, 128, 2>(a, st);
+    if (r == WTC_OK && a.splits > 1) {
         const long long n = (long long)a.E * a.N * a.K, m = a.db ? (long long)a.E * a.N : 0, blocks = ((n + m) / 4 + 255) / 256;
         hipLaunchKernelGGL(k_product_join<T>, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, st, a, n, m);
     }
-    return hipGetLastError() == hipSuccess ? WTC_OK : WTC_EHIP;
+    return hipGetLastError() == hipSuccess ? r : WTC_EHIP;
 }
 
 }  // namespace product
