@@ -41,8 +41,8 @@ int launch_layer_forward(const wtc_layer_desc* d, const void* x, const void* r, 
 int launch_layer_backward(const wtc_layer_desc* d, const void* dy, const void* dh, const void* h, const float* w,
                           const float* stats, void* dx, float* dw, float* db, float* parts, void* stream);
 
-// Gated recurrence: tokens of a tile, at whose start the forward pass keeps the state for the backward pass
-constexpr int kScanTile = 128;
+// Gated recurrence: the forward pass keeps the state before every kScanKept-th token for the backward pass
+constexpr int kScanKept = 16;
 size_t scan_workspace(const wtc_scan_desc* d);
 int launch_scan_forward(const wtc_scan_desc* d, const void* x, const void* f, const int* cu, const float* state, void* y,
                         float* last, float* kept, void* workspace, void* stream);

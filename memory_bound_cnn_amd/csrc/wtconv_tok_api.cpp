@@ -242,7 +242,7 @@ int wtconv_layer_norm_backward(const wtc_layer_desc* d, const void* dy, const vo
 
 size_t wtconv_gated_scan_kept(const wtc_scan_desc* d) {
     if (check_scan(d) != WTC_OK) return 0;
-    return (size_t)((d->T + kScanTile - 1) / kScanTile) * d->C * sizeof(float);
+    return (size_t)((d->T + kScanKept - 1) / kScanKept) * d->C * sizeof(float);
 }
 
 size_t wtconv_gated_scan_workspace(const wtc_scan_desc* d) {

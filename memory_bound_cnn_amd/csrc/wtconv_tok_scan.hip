@@ -4,22 +4,24 @@
 // backward pass: with G_t = a_(t+1) dh_(t+1) (the last state's gradient at the end),
 //   dh_t = dy_t + G_t,  dx = (1 - a) dh,  df = dh (h_(t-1) - x) a (1 - a).
 //
-// Both are compositions of maps h -> A h + B, which are associative: a token's
-// map, a thread's four tokens, a wave's eight such groups (by shuffles), the
-// four waves of a workgroup (through shared memory).  A workgroup walks one
-// part of the pack, 128 tokens by 128 bytes of channels at a time, with the
-// state in registers.  With several parts a first kernel composes each part's
-// map, so that a part can begin with the state that those before it leave: it
-// reads only the tokens behind the part's last sequence start, and none of the
-// part is read twice where sequences are short.  A token that starts a sequence
-// has A = 0, and a composition with A = 0 takes nothing from what came before
-// it, not even a NaN.
+// A thread walks the tokens of one part of the pack, two channels of them, with
+// the state in registers: no lane waits for another, and the loads of the next
+// tokens are on their way meanwhile.  What a part does to the state that enters
+// it is a map h -> A h + B.  With several parts a first kernel computes each
+// part's map, and a second one composes them to the state that each part begins
+// with.  A map needs only the tokens behind the part's last sequence start
+// (before its first end, in the backward pass), so that little is read twice
+// where sequences are short; a sequence that starts in the part gives A = 0, and
+// nothing is then taken from what came before, not even a NaN.
 //
 // Bound by device memory: 3 T C e bytes forward (x, f in, y out), 5 T C e
-// backward (x, f, dy in, dx, df out), which takes the state at each tile's start
-// from the forward pass (4 bytes for 128 tokens and channel) and computes the others
-// again.  All of it is float32.
+// backward (x, f, dy in, dx, df out), and the maps' reading of two tensors in
+// long sequences.  The forward pass keeps the state of every 16th token (4 bytes
+// a channel) for the backward pass, which computes the others again.  All of it
+// is float32.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "wtc_tok_device.h"
 #include "wtc_tok_internal.h"
@@ -27,12 +29,8 @@
 namespace wtc {
 namespace {
 
-constexpr int kLanes = 8;                       // lanes along the channels, 16 bytes each
-constexpr int kGroups = 256 / kLanes;           // groups along the tokens
-constexpr int kEach = kScanTile / kGroups;      // tokens of a thread, consecutive
-static_assert(kEach * kGroups == kScanTile, "whole groups");
-template <typename T>
-constexpr int kWidth = kLanes * kVec<T>;        // channels of a workgroup
+constexpr int V = 2;                  // channels of a thread
+constexpr int kAhead = 8;              // tokens whose loads are on their way together
 
 struct ScanArgs {
     const void *x, *f, *dy;
@@ -40,19 +38,57 @@ struct ScanArgs {
     const float *state, *dlast, *kept_in;
     void *y, *df;                // y: dx in the backward pass
     float *last, *kept;          // last: the gradient of state in the backward pass
-    float2* maps;                // [parts][C], of each part
+    float2* maps;                // [parts][C]
+    float* starts;               // [parts][C]: the state that a part begins with
     long long x_stride, f_stride, g_stride;
-    int T, n_seq, C, reverse, parts, part_tiles;
+    int T, n_seq, C, pairs, reverse, parts, len;   // pairs: of channels; len: tokens of a part
 };
 
-// h -> A h + B; A = 0 exactly where a sequence starts in it (or a gate is that small).
-struct Map {
-    float A, B;
+// ------------------------------------------------------------------ two channels
+// Two elements as they lie in memory.  ONE: rows of a single channel; else the
+// last thread of a row has its last two, the first of which may be another's
+// too: both then compute and store the same.
+typedef uint32_t u32_any __attribute__((aligned(2)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(4)));
+template <typename T>
+struct Two {
+    uint32_t u[sizeof(T) / 2];
 };
-__device__ __forceinline__ float apply(const Map& m, float h) { return m.A == 0.f ? m.B : fmaf(m.A, h, m.B); }
-// first one, then the other
-__device__ __forceinline__ Map after(const Map& one, const Map& other) {
-    return {other.A == 0.f ? 0.f : other.A * one.A, apply(other, one.B)};
+template <bool ONE, typename T>
+__device__ __forceinline__ Two<T> load_two(const T* p) {
+    Two<T> r;
+    if constexpr (sizeof(T) == 2) {
+        r.u[0] = ONE ? (uint32_t)p[0] : *reinterpret_cast<const u32_any*>(p);
+    } else if constexpr (ONE) {
+        r.u[0] = __builtin_bit_cast(uint32_t, p[0]);
+        r.u[1] = 0u;
+    } else {
+        const u32x2_any v = *reinterpret_cast<const u32x2_any*>(p);
+        r.u[0] = v[0];
+        r.u[1] = v[1];
+    }
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ float value(const Two<T>& r, int i) {
+    if constexpr (sizeof(T) == 2) return __builtin_bit_cast(float, i ? r.u[0] & 0xFFFF0000u : r.u[0] << 16);
+    return __builtin_bit_cast(float, r.u[i % (sizeof(T) / 2)]);
+}
+template <bool ONE, typename T>
+__device__ __forceinline__ void store_two(T* p, const float (&v)[V]) {
+    if constexpr (ONE) {
+        p[0] = from_f32<T>(v[0]);
+    } else if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<u32_any*>(p) = bf16x2_rne(v[0], v[1]);
+    } else {
+        *reinterpret_cast<u32x2_any*>(p) = u32x2_any{__builtin_bit_cast(uint32_t, v[0]), __builtin_bit_cast(uint32_t, v[1])};
+    }
+}
+template <bool ONE>
+__device__ __forceinline__ void load_state(const float* p, float (&v)[V]) {
+    const Two<float> r = load_two<ONE>(p);
+    v[0] = value(r, 0);
+    v[1] = value(r, 1);
 }
 
 // sigmoid(f) and 1 - sigmoid(f).  float32: the exponent's product is rounded at
@@ -63,9 +99,9 @@ __device__ __forceinline__ void gate(float f, float& a, float& take) {
     float e;
     if constexpr (sizeof(T) == 2) {
         const float t = f * -1.4426950408889634f;
-        e = __builtin_amdgcn_exp2f(t > 126.f ? 126.f : t);
+        e = __builtin_amdgcn_exp2f(t > 126.f ? 126.f : t);   // a NaN stays one
     } else {
-        const float v = f < -87.f ? 87.f : f > 104.f ? -104.f : -f, t = v * 1.4426950408889634f;   // a NaN stays one
+        const float v = f < -87.f ? 87.f : f > 104.f ? -104.f : -f, t = v * 1.4426950408889634f;
         const float low = fmaf(v, 1.4426950408889634f, -t) + v * 1.9259629911266175e-8f;
         e = __builtin_amdgcn_exp2f(t);
         e = fmaf(e, low * 0.6931471805599453f, e);
@@ -74,514 +110,342 @@ __device__ __forceinline__ void gate(float f, float& a, float& take) {
     take = e * a;
 }
 
+// ------------------------------------------------------------------ places
 // Places of a pack in the order they are walked: place p is token p, or with
 // `reverse` token T - 1 - p.  Sequence s = 0 .. n_seq - 1 in that order is
-// places begin(s) .. begin(s + 1) - 1; number(s) is its row of the states.
+// places begin(s) .. begin(s + 1) - 1.
 __device__ __forceinline__ int begin_of(const ScanArgs& a, int s) {
     const int v = min(max(a.cu[a.reverse ? a.n_seq - s : s], 0), a.T);
     return a.reverse ? a.T - v : v;
 }
-__device__ __forceinline__ int number_of(const ScanArgs& a, int s) { return a.reverse ? a.n_seq - 1 - s : s; }
+__device__ __forceinline__ size_t state_of(const ScanArgs& a, int s, int c) {
+    return (size_t)(a.reverse ? a.n_seq - 1 - s : s) * a.C + c;
+}
 __device__ __forceinline__ long long row_of(const ScanArgs& a, int p) { return a.reverse ? a.T - 1 - p : p; }
 
-// The last sequence that begins at place p or before, by all lanes of a wave;
-// -1 if none does.
-__device__ __forceinline__ int find_sequence(const ScanArgs& a, int p, int lane) {
-    int lo = -1, hi = a.n_seq;   // it is in lo .. hi - 1; begin(lo) <= p < begin(hi), as far as those are sequences
-    while (hi - lo > 1) {
-        const int step = (hi - lo - 1 + 63) / 64, s = lo + 1 + lane * step;
-        const int n = __builtin_popcountll(__builtin_amdgcn_ballot_w64(s < hi && begin_of(a, min(s, hi - 1)) <= p));
-        const int found = n > 0 ? lo + 1 + (n - 1) * step : lo;
-        hi = min(hi, lo + 1 + n * step);
-        lo = found;
-    }
-    return lo;
-}
-
-// Which sequence starts, and which ends, at each place of a tile (-1: none).
-struct Marks {
-    int start[kScanTile], end[kScanTile];
-};
-
-// The places of sequences, and the one that a workgroup is in.
+// The sequence of a place: its number, and the places from .. to - 1 of it.
+// Places of no sequence have number -1.
 struct Where {
-    int lo, hi;           // places outside of these belong to no sequence
-    int from, to;         // places strictly between them have no start and no end
+    int s, from, to;
 };
-__device__ __forceinline__ Where where_begin(const ScanArgs& a) {
-    Where w;
-    w.lo = a.n_seq > 0 ? begin_of(a, 0) : 0;
-    w.hi = a.n_seq > 0 ? begin_of(a, a.n_seq) : 0;
-    w.from = 0;
-    w.to = -1;
-    return w;
-}
-// Whether the tile at p0 has marks, which are then in `m` (for all threads).
-__device__ __forceinline__ bool mark(const ScanArgs& a, int p0, Where& w, Marks& m, int lane) {
-    const int end = min(p0 + kScanTile, a.T);
-    if (p0 > w.from && end < w.to) return false;
-    const int s0 = find_sequence(a, p0, lane);
-    if (s0 >= 0 && s0 < a.n_seq) {
-        w.from = begin_of(a, s0);
-        w.to = begin_of(a, s0 + 1);
-        if (p0 > w.from && end < w.to) return false;
+__device__ __forceinline__ Where find(const ScanArgs& a, int p) {
+    int lo = -1, hi = a.n_seq;   // begin(lo) <= p < begin(hi), as far as those are sequences
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (begin_of(a, mid) <= p)
+            lo = mid;
+        else
+            hi = mid;
     }
-    __syncthreads();   // the marks' last use is over
-    if (threadIdx.x < kScanTile) m.start[threadIdx.x] = m.end[threadIdx.x] = -1;
-    __syncthreads();
-    for (int s = max(s0, 0) + (int)threadIdx.x; s < a.n_seq; s += 256) {
-        const int b = begin_of(a, s), e = begin_of(a, s + 1);
-        if (b >= end) break;
-        if (e <= b) continue;
-        if (b >= p0) m.start[b - p0] = s;
-        if (e > p0 && e <= end) m.end[e - 1 - p0] = s;
+    if (lo >= 0) {
+        const Where w = {lo, begin_of(a, lo), begin_of(a, lo + 1)};
+        if (p >= w.from && p < w.to) return w;
+        if (lo == a.n_seq - 1 && p >= w.to) return {-1, w.to, a.T};
+    } else if (a.n_seq > 0) {
+        return {-1, 0, begin_of(a, 0)};
     }
-    __syncthreads();
-    return true;
+    return {-1, p, p + 1};
 }
-
-// One float per channel of a row of the states.
-template <int V>
-__device__ __forceinline__ void load_state(const float* row, int n, float (&v)[V]) {
-#pragma unroll
-    for (int i = 0; i < V; i += 4) {
-        float part[4];
-        load_part(row + i, n - i, part);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[i + j] = part[j];
-    }
-}
-template <int V>
-__device__ __forceinline__ void store_state(float* row, int n, const float (&v)[V]) {
-#pragma unroll
-    for (int i = 0; i < V; i += 4) {
-        const float part[4] = {v[i], v[i + 1], v[i + 2], v[i + 3]};
-        store_part(row + i, n - i, part);
-    }
-}
-
-// The maps of the groups of tokens composed over the workgroup, in their order
-// or (BACK) the other way.  `m` becomes the composition of all before this
-// thread's group in its wave; waves: that of each whole wave, in `sums`.
-template <int V>
-struct Sums {
-    float2 m[2][4][kLanes][V];   // two, in turn: one barrier a scan
-};
-template <bool BACK, int V>
-__device__ __forceinline__ void scan_wave(Map (&m)[V], float2 (&sums)[4][kLanes][V], int lane, int wave) {
-#pragma unroll
-    for (int o = kLanes; o < 64; o <<= 1) {
-        const bool there = BACK ? lane + o < 64 : lane >= o;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            Map p;
-            p.A = BACK ? __shfl_down(m[i].A, o) : __shfl_up(m[i].A, o);
-            p.B = BACK ? __shfl_down(m[i].B, o) : __shfl_up(m[i].B, o);
-            if (there) m[i] = after(p, m[i]);
+// That of place p, which lies in the sequence after w's (before it) or anywhere else.
+template <bool BACK>
+__device__ __forceinline__ void move_to(const ScanArgs& a, int p, Where& w) {
+    if (p >= w.from && p < w.to) return;
+    const int s = BACK ? w.s - 1 : w.s + 1;
+    if (w.s >= 0 && s >= 0 && s < a.n_seq) {
+        const Where next = BACK ? Where{s, begin_of(a, s), w.from} : Where{s, w.to, begin_of(a, s + 1)};
+        if (p >= next.from && p < next.to) {
+            w = next;
+            return;
         }
     }
-    if (BACK ? lane < kLanes : lane >= 64 - kLanes) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) sums[wave][lane % kLanes][i] = make_float2(m[i].A, m[i].B);
-    }
-    const bool first = BACK ? lane >= 64 - kLanes : lane < kLanes;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        Map p;
-        p.A = BACK ? __shfl_down(m[i].A, kLanes) : __shfl_up(m[i].A, kLanes);
-        p.B = BACK ? __shfl_down(m[i].B, kLanes) : __shfl_up(m[i].B, kLanes);
-        m[i] = first ? Map{1.f, 0.f} : p;
-    }
-}
-// After a barrier: `at` is the state before this thread's group, `carry` that
-// after the whole workgroup's.
-template <bool BACK, int V>
-__device__ __forceinline__ void scan_apply(const Map (&m)[V], const float2 (&sums)[4][kLanes][V], int lane, int wave,
-                                           float (&carry)[V], float (&at)[V]) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        float c = carry[i], mine = c;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int w = BACK ? 3 - k : k;
-            if (w == wave) mine = c;
-            const float2 s = sums[w][lane % kLanes][i];
-            c = apply(Map{s.x, s.y}, c);
-        }
-        carry[i] = c;
-        at[i] = apply(m[i], mine);
-    }
+    w = find(a, p);
 }
 
-// The state that the parts before (BACK: after) this one leave: their maps
-// composed, a run of them by each group.
-template <bool BACK, int V>
-__device__ __forceinline__ void carry_in(const ScanArgs& a, int part, int c, int n, float2 (&sums)[4][kLanes][V], int lane,
-                                         int wave, float (&carry)[V]) {
-    const int group = threadIdx.x / kLanes, many = BACK ? a.parts - 1 - part : part, run = (many + kGroups - 1) / kGroups;
-    Map m[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        m[i] = {1.f, 0.f};
-        carry[i] = 0.f;
-    }
-    if (many == 0) return;
-    const int turn = BACK ? kGroups - 1 - group : group;   // scan_wave's order of the groups
-    for (int k = turn * run; k < min((turn + 1) * run, many); ++k) {
-        const float2* p = a.maps + (size_t)(BACK ? a.parts - 1 - k : k) * a.C + c;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (i < n) {
-                const float2 v = p[i];
-                m[i] = after(m[i], Map{v.x, v.y});
-            }
-    }
-    float at[V];
-    scan_wave<BACK>(m, sums, lane, wave);
-    __syncthreads();
-    scan_apply<BACK>(m, sums, lane, wave, carry, at);
-    __syncthreads();
+// A thread's part and channels.
+struct Mine {
+    int part, c;
+};
+template <bool ONE>
+__device__ __forceinline__ Mine mine_of(const ScanArgs& a) {
+    const unsigned id = blockIdx.x * 256u + threadIdx.x;
+    const int part = (int)(id / (unsigned)a.pairs);
+    return {part, ONE ? 0 : min((int)(id % (unsigned)a.pairs) * V, a.C - V)};
 }
 
-// A thread's four tokens of a tile, as they lie in memory.
-template <typename T>
+// Rows of tokens p .. p + N - 1, as they lie in memory; those from `end` on are the last one's.
+template <typename T, bool ONE, int N>
 struct Rows {
-    Raw<T> v[kEach];
-    __device__ __forceinline__ void fetch(const void* base, long long stride, const ScanArgs& a, int p, int c, int n) {
+    Two<T> v[N];
+    __device__ __forceinline__ void fetch(const void* base, long long stride, const ScanArgs& a, int p, int end, int c) {
+        const T* q = static_cast<const T*>(base) + c;
+        const long long step = a.reverse ? -stride : stride;
+        q += row_of(a, min(p, end - 1)) * stride;
+        const int there = end - p;
+        if (there >= N) {
 #pragma unroll
-        for (int j = 0; j < kEach; ++j) {
-            const bool there = p + j < a.T;
-            v[j] = load_raw(static_cast<const T*>(base) + row_of(a, there ? p + j : 0) * stride + c, there ? n : 0);
+            for (int j = 0; j < N; ++j) v[j] = load_two<ONE>(q + j * step);
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[j] = load_two<ONE>(q + (j < there ? j : max(there - 1, 0)) * step);
         }
     }
 };
 
-// The maps of a thread's tokens (a: A, b: B) and their composition.
-template <typename T>
-struct Tokens {
-    static constexpr int V = kVec<T>;
-    float a[kEach][V], b[kEach][V];
-    int start[kEach];   // the sequence that starts there, or -1
-
-    __device__ __forceinline__ void make(const ScanArgs& s, const Rows<T>& x, const Rows<T>& f, bool marks, const Marks& m,
-                                         const Where& w, int p, int at, int c, int n) {
+// ------------------------------------------------------------------ maps of parts
+template <typename T, bool BACK, bool ONE>
+__global__ void __launch_bounds__(256) k_scan_maps(ScanArgs a) {
+    auto [part, c] = mine_of<ONE>(a);
+    if (BACK) ++part;                     // the first has none; forward, the last
+    if (part >= (BACK ? a.parts : a.parts - 1)) return;
+    const int first = part * a.len, end = min(first + a.len, a.T);
+    float A[V] = {}, B[V] = {};
+    const Where w = find(a, BACK ? first : end - 1);
+    int from = first, to = first;         // the places that count; with none the map is zero
+    if (BACK ? w.s >= 0 && w.from < first : w.s >= 0) {
+        const bool cut = BACK ? w.to <= end : w.from >= first;   // the sequence ends (starts) in the part
+        from = BACK ? first : max(w.from, first);
+        to = BACK ? min(w.to, end) : end;
+        const float* in = BACK ? a.dlast : a.state;
+        if (cut && in) load_state<ONE>(in + state_of(a, w.s, c), B);
 #pragma unroll
-        for (int j = 0; j < kEach; ++j) {
-            float xv[V], fv[V];
-            unpack(x.v[j], xv);
-            unpack(f.v[j], fv);
+        for (int i = 0; i < V; ++i) A[i] = cut ? 0.f : 1.f;
+    }
+    const void* xs = BACK ? a.dy : a.x;
+    const long long stride = BACK ? a.g_stride : a.x_stride;
+    Rows<T, ONE, kAhead> x, f;
+    // BACK: the tokens up to place q - 1, from the last one
+    auto fetch = [&](int q) {
+        const int p = BACK ? max(q - kAhead, from) : q;
+        x.fetch(xs, stride, a, p, to, c);
+        f.fetch(a.f, a.f_stride, a, p, to, c);
+    };
+    if (from < to) fetch(BACK ? to : from);
+    for (int done = 0; done < to - from; done += kAhead) {
+        const int count = min(to - from - done, kAhead);
+        const Rows<T, ONE, kAhead> xr = x, fr = f;
+        if (done + kAhead < to - from) fetch(BACK ? to - done - kAhead : from + done + kAhead);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int j = BACK ? kAhead - 1 - k : k;
+            const bool there = j < count;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                float take;
-                gate<T>(fv[i], a[j][i], take);
-                b[j][i] = take * xv[i];
-            }
-            start[j] = -1;
-            if (marks) {
-                start[j] = m.start[at + j];
-                const bool none = p + j < w.lo || p + j >= w.hi;
-                if (none || start[j] >= 0) {
-                    float h[V];
-#pragma unroll
-                    for (int i = 0; i < V; ++i) h[i] = 0.f;
-                    if (!none && s.state) load_state(s.state + (size_t)number_of(s, start[j]) * s.C + c, n, h);
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        b[j][i] = none ? 0.f : s.state ? fmaf(a[j][i], h[i], b[j][i]) : b[j][i];
-                        a[j][i] = 0.f;
-                    }
-                }
+                float keep, take;
+                gate<T>(value(fr.v[j], i), keep, take);
+                const float in = value(xr.v[j], i);
+                const float next = BACK ? keep * (in + B[i]) : fmaf(keep, B[i], take * in);
+                A[i] = there ? A[i] * keep : A[i];
+                B[i] = there ? next : B[i];
             }
         }
     }
-    __device__ __forceinline__ void compose(Map (&m)[V]) const {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            m[i] = {a[0][i], b[0][i]};
-#pragma unroll
-            for (int j = 1; j < kEach; ++j) m[i] = after(m[i], Map{a[j][i], b[j][i]});
-        }
-    }
-};
+    for (int i = 0; i < (ONE ? 1 : V); ++i) a.maps[(size_t)part * a.C + c + i] = make_float2(A[i], B[i]);
+}
 
-// The map of a part: of its tokens from the last sequence start on.
-template <typename T>
-__global__ void __launch_bounds__(256) k_scan_parts(ScanArgs a) {
-    constexpr int V = kVec<T>;
-    __shared__ Sums<V> sums;
-    __shared__ Marks marks;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, at = (int)(threadIdx.x / kLanes) * kEach;
-    const int part = blockIdx.y, c = blockIdx.x * kWidth<T> + (lane % kLanes) * V, n = a.C - c;
-    const int first = part * a.part_tiles, end = first + a.part_tiles;   // the last part has none
-    Where w = where_begin(a);
-    const int s = find_sequence(a, end * kScanTile - 1, lane);
-    int tile = s < 0 ? end - 1 : max(first, min(begin_of(a, s) / kScanTile, end - 1));
-    float A[V], B[V];
+// The state that each part begins with (BACK: G behind its last token): 128
+// threads of a channel have up to kRun parts each, in order, and take what the
+// threads before them leave.
+constexpr int kRun = 8, kMostParts = 128 * kRun, kCols = 8;
+__device__ __forceinline__ float apply(const float2& m, float h) { return m.x == 0.f ? m.y : fmaf(m.x, h, m.y); }
+// first one, then the other
+__device__ __forceinline__ float2 after(const float2& one, const float2& other) {
+    return make_float2(other.x == 0.f ? 0.f : other.x * one.x, apply(other, one.y));
+}
+
+template <bool BACK>
+__global__ void __launch_bounds__(1024) k_scan_starts(ScanArgs a) {
+    __shared__ float2 whole[16][kCols];   // of a wave's eight threads of a channel
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane % kCols, c = blockIdx.x * kCols + col;
+    const int run = (a.parts + 127) / 128, first = (int)(threadIdx.x / kCols) * run;
+    auto part_of = [&](int k) { return BACK ? a.parts - 1 - k : k; };
+    float2 m[kRun];
+    float2 all = make_float2(1.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        A[i] = 1.f;
-        B[i] = 0.f;
+    for (int k = 0; k < kRun; ++k) {   // the last part's map (BACK: the first one's) is not there, nor needed
+        const bool there = k < run && first + k + 1 < a.parts && c < a.C;
+        m[k] = there ? a.maps[(size_t)part_of(first + k) * a.C + c] : make_float2(1.f, 0.f);
     }
-    Rows<T> x, f;
-    x.fetch(a.x, a.x_stride, a, tile * kScanTile + at, c, n);
-    f.fetch(a.f, a.f_stride, a, tile * kScanTile + at, c, n);
-    for (; tile < end; ++tile) {
-        const int p0 = tile * kScanTile;
-        const bool marked = mark(a, p0, w, marks, lane);
-        Tokens<T> t;
-        t.make(a, x, f, marked, marks, w, p0 + at, at, c, n);
-        if (tile + 1 < end) {
-            x.fetch(a.x, a.x_stride, a, p0 + kScanTile + at, c, n);
-            f.fetch(a.f, a.f_stride, a, p0 + kScanTile + at, c, n);
-        }
-        Map m[V];
-        t.compose(m);
-        scan_wave<false>(m, sums.m[tile & 1], lane, wave);
-        __syncthreads();
 #pragma unroll
-        for (int i = 0; i < V; ++i)
+    for (int k = 0; k < kRun; ++k) all = after(all, m[k]);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 v = sums.m[tile & 1][k][lane % kLanes][i];
-                const Map r = after(Map{A[i], B[i]}, Map{v.x, v.y});
-                A[i] = r.A;
-                B[i] = r.B;
-            }
+    for (int o = kCols; o < 64; o <<= 1) {
+        const float2 p = make_float2(__shfl_up(all.x, o), __shfl_up(all.y, o));
+        if (lane >= o) all = after(p, all);
     }
-    if (threadIdx.x < kLanes) {
+    if (lane >= 64 - kCols) whole[wave][col] = all;
+    const float2 p = make_float2(__shfl_up(all.x, kCols), __shfl_up(all.y, kCols));
+    __syncthreads();
+    float h = 0.f;
+    for (int w = 0; w < wave; ++w) h = apply(whole[w][col], h);
+    if (lane >= kCols) h = apply(p, h);
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (i < n) a.maps[(size_t)part * a.C + c + i] = make_float2(A[i], B[i]);
+    for (int k = 0; k < kRun; ++k) {
+        if (k < run && first + k < a.parts && c < a.C) a.starts[(size_t)part_of(first + k) * a.C + c] = h;
+        h = apply(m[k], h);
     }
 }
 
 // What sequences with no token leave behind.
-template <int V>
-__device__ __forceinline__ void pass_on(const ScanArgs& a, const float* from, float* to, int part, int c, int n) {
-    for (int s = part * kGroups + (int)(threadIdx.x / kLanes); s < a.n_seq; s += a.parts * kGroups) {
+template <bool ONE>
+__device__ __forceinline__ void pass_on(const ScanArgs& a, const float* from, float* to, int part, int c) {
+    for (int s = part; s < a.n_seq; s += a.parts) {
         if (begin_of(a, s + 1) > begin_of(a, s)) continue;
-        float v[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = 0.f;
-        const size_t row = (size_t)number_of(a, s) * a.C + c;
-        if (from) load_state(from + row, n, v);
-        store_state(to + row, n, v);
+        float v[V] = {};
+        if (from) load_state<ONE>(from + state_of(a, s, c), v);
+        store_two<ONE>(to + state_of(a, s, c), v);
     }
 }
 
-template <typename T>
+// ------------------------------------------------------------------ forward
+template <typename T, bool ONE>
 __global__ void __launch_bounds__(256) k_scan_forward(ScanArgs a) {
-    constexpr int V = kVec<T>;
-    __shared__ Sums<V> sums;
-    __shared__ Marks marks;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, at = (int)(threadIdx.x / kLanes) * kEach;
-    const int part = blockIdx.y, c = blockIdx.x * kWidth<T> + (lane % kLanes) * V, n = a.C - c;
-    const int first = part * a.part_tiles, end = min(first + a.part_tiles, (a.T + kScanTile - 1) / kScanTile);
-    if (a.last) pass_on<V>(a, a.state, a.last, part, c, n);
+    const auto [part, c] = mine_of<ONE>(a);
+    if (part >= a.parts) return;
+    if (a.last) pass_on<ONE>(a, a.state, a.last, part, c);
+    const int first = part * a.len, end = min(first + a.len, a.T);
     if (first >= end) return;
-    Rows<T> x, f;
-    x.fetch(a.x, a.x_stride, a, first * kScanTile + at, c, n);
-    f.fetch(a.f, a.f_stride, a, first * kScanTile + at, c, n);
-    Where w = where_begin(a);
-    float carry[V];
-    carry_in<false>(a, part, c, n, sums.m[0], lane, wave, carry);
-    for (int tile = first; tile < end; ++tile) {
-        const int p0 = tile * kScanTile;
-        const bool marked = mark(a, p0, w, marks, lane);
-        Tokens<T> t;
-        t.make(a, x, f, marked, marks, w, p0 + at, at, c, n);
-        if (tile + 1 < end) {
-            x.fetch(a.x, a.x_stride, a, p0 + kScanTile + at, c, n);
-            f.fetch(a.f, a.f_stride, a, p0 + kScanTile + at, c, n);
+    Rows<T, ONE, kAhead> x, f;
+    x.fetch(a.x, a.x_stride, a, first, end, c);
+    f.fetch(a.f, a.f_stride, a, first, end, c);
+    float h[V] = {};
+    if (part > 0) load_state<ONE>(a.starts + (size_t)part * a.C + c, h);
+    Where w = find(a, first);
+    const long long step = a.reverse ? -a.C : a.C;
+    for (int p0 = first; p0 < end; p0 += kAhead) {
+        const Rows<T, ONE, kAhead> xr = x, fr = f;
+        if (p0 + kAhead < end) {
+            x.fetch(a.x, a.x_stride, a, p0 + kAhead, end, c);
+            f.fetch(a.f, a.f_stride, a, p0 + kAhead, end, c);
         }
-        Map m[V];
-        t.compose(m);
-        scan_wave<false>(m, sums.m[tile & 1], lane, wave);
-        if (a.kept && threadIdx.x < kLanes) store_state(a.kept + (size_t)tile * a.C + c, n, carry);
-        __syncthreads();
-        float h[V];
-        scan_apply<false>(m, sums.m[tile & 1], lane, wave, carry, h);
-#pragma unroll
-        for (int j = 0; j < kEach; ++j) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) h[i] = apply(Map{t.a[j][i], t.b[j][i]}, h[i]);
-            const int p = p0 + at + j;
-            if (p < a.T) store_part(static_cast<T*>(a.y) + row_of(a, p) * a.C + c, n, h);
-            if (marked && a.last) {
-                const int s = marks.end[at + j];
-                if (s >= 0) store_state(a.last + (size_t)number_of(a, s) * a.C + c, n, h);
-            }
-        }
-    }
-}
-
-// Backward.  What a token hands to the one before it is G = a (dy + G'), with
-// the last state's gradient added to dy at a sequence's end; a token that
-// starts a sequence hands on nothing (a = 0, as in the forward pass).
-template <typename T>
-struct Grads {
-    static constexpr int V = kVec<T>;
-    float g[kEach][V];   // dy, and the last state's gradient
-
-    __device__ __forceinline__ void make(const ScanArgs& s, const Rows<T>& dy, bool marks, const Marks& m, const Where& w,
-                                         int p, int at, int c, int n) {
-#pragma unroll
-        for (int j = 0; j < kEach; ++j) {
-            unpack(dy.v[j], g[j]);
-            if (marks) {
-                const int e = m.end[at + j];
-                if (e >= 0 && s.dlast) {
-                    float d[V];
-                    load_state(s.dlast + (size_t)number_of(s, e) * s.C + c, n, d);
-#pragma unroll
-                    for (int i = 0; i < V; ++i) g[j][i] += d[i];
-                }
-                if (p + j < w.lo || p + j >= w.hi) {
-#pragma unroll
-                    for (int i = 0; i < V; ++i) g[j][i] = 0.f;
-                }
-            }
-        }
-    }
-    __device__ __forceinline__ void compose(const float (&a)[kEach][V], Map (&m)[V]) const {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            m[i] = {1.f, 0.f};
-#pragma unroll
-            for (int j = kEach - 1; j >= 0; --j) {
-                m[i].B = a[j][i] == 0.f ? 0.f : a[j][i] * (g[j][i] + m[i].B);
-                m[i].A = a[j][i] == 0.f ? 0.f : a[j][i] * m[i].A;
-            }
-        }
-    }
-};
-
-// The map of a part for the backward pass: of its tokens up to the first sequence start.
-template <typename T>
-__global__ void __launch_bounds__(256) k_scan_parts_back(ScanArgs a) {
-    constexpr int V = kVec<T>;
-    __shared__ Sums<V> sums;
-    __shared__ Marks marks;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, at = (int)(threadIdx.x / kLanes) * kEach;
-    const int part = blockIdx.y + 1, c = blockIdx.x * kWidth<T> + (lane % kLanes) * V, n = a.C - c;   // the first has none
-    const int tiles = (a.T + kScanTile - 1) / kScanTile;
-    const int first = part * a.part_tiles, end = min(first + a.part_tiles, tiles);
-    Where w = where_begin(a);
-    const int s = find_sequence(a, first * kScanTile - 1, lane) + 1;   // the next to begin
-    int tile = s >= a.n_seq ? end - 1 : min(max(begin_of(a, s) / kScanTile, first), end - 1);
-    float A[V], B[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        A[i] = 1.f;
-        B[i] = 0.f;
-    }
-    Rows<T> dy, f;
-    dy.fetch(a.dy, a.g_stride, a, tile * kScanTile + at, c, n);
-    f.fetch(a.f, a.f_stride, a, tile * kScanTile + at, c, n);
-    for (; tile >= first; --tile) {
-        const int p0 = tile * kScanTile;
-        const bool marked = mark(a, p0, w, marks, lane);
-        Tokens<T> t;
-        Grads<T> g;
-        t.make(a, f, f, marked, marks, w, p0 + at, at, c, n);   // its B is not used
-        g.make(a, dy, marked, marks, w, p0 + at, at, c, n);
-        if (tile > first) {
-            dy.fetch(a.dy, a.g_stride, a, p0 - kScanTile + at, c, n);
-            f.fetch(a.f, a.f_stride, a, p0 - kScanTile + at, c, n);
-        }
-        Map m[V];
-        g.compose(t.a, m);
-        scan_wave<true>(m, sums.m[tile & 1], lane, wave);
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-#pragma unroll
-            for (int k = 3; k >= 0; --k) {
-                const float2 v = sums.m[tile & 1][k][lane % kLanes][i];
-                const Map r = after(Map{A[i], B[i]}, Map{v.x, v.y});
-                A[i] = r.A;
-                B[i] = r.B;
-            }
-    }
-    if (threadIdx.x < kLanes) {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (i < n) a.maps[(size_t)part * a.C + c + i] = make_float2(A[i], B[i]);
-    }
-}
-
-template <typename T>
-__global__ void __launch_bounds__(256) k_scan_backward(ScanArgs a) {
-    constexpr int V = kVec<T>;
-    __shared__ Sums<V> ahead, back;
-    __shared__ Marks marks;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, at = (int)(threadIdx.x / kLanes) * kEach;
-    const int part = blockIdx.y, c = blockIdx.x * kWidth<T> + (lane % kLanes) * V, n = a.C - c;
-    const int first = part * a.part_tiles, end = min(first + a.part_tiles, (a.T + kScanTile - 1) / kScanTile);
-    if (a.last) pass_on<V>(a, a.dlast, a.last, part, c, n);
-    if (first >= end) return;
-    Rows<T> x, f, dy;
-    auto fetch = [&](int tile) {
-        x.fetch(a.x, a.x_stride, a, tile * kScanTile + at, c, n);
-        f.fetch(a.f, a.f_stride, a, tile * kScanTile + at, c, n);
-        dy.fetch(a.dy, a.g_stride, a, tile * kScanTile + at, c, n);
-    };
-    fetch(end - 1);
-    Where w = where_begin(a);
-    float carry[V];
-    carry_in<true>(a, part, c, n, back.m[0], lane, wave, carry);
-    for (int tile = end - 1; tile >= first; --tile) {
-        const int p0 = tile * kScanTile;
-        const bool marked = mark(a, p0, w, marks, lane);
-        Tokens<T> t;
-        Grads<T> g;
-        t.make(a, x, f, marked, marks, w, p0 + at, at, c, n);
-        g.make(a, dy, marked, marks, w, p0 + at, at, c, n);
-        const Rows<T> xr = x, fr = f;
-        if (tile > first) fetch(tile - 1);
-        float kept[V];
-        load_state(a.kept_in + (size_t)tile * a.C + c, n, kept);
-        Map m[V], r[V];
-        t.compose(m);
-        g.compose(t.a, r);
-        scan_wave<false>(m, ahead.m[tile & 1], lane, wave);
-        scan_wave<true>(r, back.m[tile & 1], lane, wave);
-        __syncthreads();
-        float h[kEach + 1][V], G[V];   // the states before each token and after the last
-        scan_apply<false>(m, ahead.m[tile & 1], lane, wave, kept, h[0]);
-        scan_apply<true>(r, back.m[tile & 1], lane, wave, carry, G);
-#pragma unroll
-        for (int j = 0; j < kEach; ++j)
-#pragma unroll
-            for (int i = 0; i < V; ++i) h[j + 1][i] = apply(Map{t.a[j][i], t.b[j][i]}, h[j][i]);
-#pragma unroll
-        for (int j = kEach - 1; j >= 0; --j) {
-            float xv[V], fv[V], dx[V], df[V];
-            unpack(xr.v[j], xv);
-            unpack(fr.v[j], fv);
-            const int p = p0 + at + j;
-            const bool none = marked && (p < w.lo || p >= w.hi);
-            if (t.start[j] >= 0) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) h[j][i] = 0.f;
-                if (a.state) load_state(a.state + (size_t)number_of(a, t.start[j]) * a.C + c, n, h[j]);
-            }
-            float ds[V];
+        if (a.kept && p0 % kScanKept == 0) store_two<ONE>(a.kept + (size_t)(p0 / kScanKept) * a.C + c, h);
+        T* y = static_cast<T*>(a.y) + row_of(a, p0) * a.C + c;
+        auto token = [&](int j) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 float keep, take;
-                gate<T>(fv[i], keep, take);
-                const float dh = g.g[j][i] + G[i];
-                dx[i] = none ? 0.f : take * dh;
-                df[i] = none ? 0.f : dh * (h[j][i] - xv[i]) * (keep * take);
-                ds[i] = keep * dh;
-                G[i] = t.a[j][i] == 0.f ? 0.f : t.a[j][i] * dh;
+                gate<T>(value(fr.v[j], i), keep, take);
+                h[i] = fmaf(keep, h[i], take * value(xr.v[j], i));
             }
-            if (p < a.T) {
-                store_part(static_cast<T*>(a.y) + row_of(a, p) * a.C + c, n, dx);
-                store_part(static_cast<T*>(a.df) + row_of(a, p) * a.C + c, n, df);
+        };
+        if (w.s >= 0 && p0 > w.from && p0 + kAhead < w.to) {   // no start and no end
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                token(j);
+                store_two<ONE>(y + j * step, h);
             }
-            if (t.start[j] >= 0 && a.last && !none) store_state(a.last + (size_t)number_of(a, t.start[j]) * a.C + c, n, ds);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int p = p0 + j;
+                if (p >= end) break;
+                move_to<false>(a, p, w);
+                if (w.s < 0) {
+                    h[0] = h[1] = 0.f;
+                } else {
+                    if (p == w.from) {
+                        h[0] = h[1] = 0.f;
+                        if (a.state) load_state<ONE>(a.state + state_of(a, w.s, c), h);
+                    }
+                    token(j);
+                    if (p + 1 == w.to && a.last) store_two<ONE>(a.last + state_of(a, w.s, c), h);
+                }
+                store_two<ONE>(y + j * step, h);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ backward
+// From the last token to the first, kScanKept at a time: their states again from
+// the kept one, and then the gradients.
+template <typename T, bool ONE>
+__global__ void __launch_bounds__(256) k_scan_backward(ScanArgs a) {
+    constexpr int N = kScanKept;
+    const auto [part, c] = mine_of<ONE>(a);
+    if (part >= a.parts) return;
+    if (a.last) pass_on<ONE>(a, a.dlast, a.last, part, c);
+    const int first = part * a.len, end = min(first + a.len, a.T);
+    if (first >= end) return;
+    float G[V] = {};
+    if (part + 1 < a.parts) load_state<ONE>(a.starts + (size_t)part * a.C + c, G);
+    Where w = find(a, end - 1);
+    const long long step = a.reverse ? -a.C : a.C;
+    for (int p0 = first + (end - first - 1) / N * N; p0 >= first; p0 -= N) {
+        Rows<T, ONE, N> x, f, dy;
+        x.fetch(a.x, a.x_stride, a, p0, end, c);
+        f.fetch(a.f, a.f_stride, a, p0, end, c);
+        dy.fetch(a.dy, a.g_stride, a, p0, end, c);
+        float now[V], h[N][V], keep[N][V], take[N][V];   // h: the states before each token
+        load_state<ONE>(a.kept_in + (size_t)(p0 / N) * a.C + c, now);
+        const long long to = row_of(a, p0) * a.C + c;
+        T *dx = static_cast<T*>(a.y) + to, *df = static_cast<T*>(a.df) + to;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) gate<T>(value(f.v[j], i), keep[j][i], take[j][i]);
+        auto forward = [&](int j) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) now[i] = fmaf(keep[j][i], now[i], take[j][i] * value(x.v[j], i));
+        };
+        auto token = [&](int j) {   // G becomes what the token hands to the one before it
+            float vx[V], vf[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float dh = G[i] + value(dy.v[j], i);
+                vx[i] = take[j][i] * dh;
+                vf[i] = keep[j][i] * vx[i] * (h[j][i] - value(x.v[j], i));
+                G[i] = keep[j][i] * dh;
+            }
+            store_two<ONE>(dx + j * step, vx);
+            store_two<ONE>(df + j * step, vf);
+        };
+        if (w.s >= 0 && p0 > w.from && p0 + N < w.to) {   // no start and no end
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) h[j][i] = now[i];
+                if (j + 1 < N) forward(j);
+            }
+#pragma unroll
+            for (int j = N - 1; j >= 0; --j) token(j);
+        } else {
+            const Where last = w;
+            Where up = find(a, p0);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const int p = p0 + j;
+                if (p < end) {
+                    move_to<false>(a, p, up);
+                    if (p == up.from) {   // of a sequence, or a place of none
+                        now[0] = now[1] = 0.f;
+                        if (up.s >= 0 && a.state) load_state<ONE>(a.state + state_of(a, up.s, c), now);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < V; ++i) h[j][i] = now[i];
+                if (j + 1 < N) forward(j);
+            }
+            w = last;
+#pragma unroll
+            for (int j = N - 1; j >= 0; --j) {
+                const int p = p0 + j;
+                if (p >= end) continue;
+                move_to<true>(a, p, w);
+                if (w.s < 0) {
+                    const float zero[V] = {};
+                    store_two<ONE>(dx + j * step, zero);
+                    store_two<ONE>(df + j * step, zero);
+                    G[0] = G[1] = 0.f;
+                    continue;
+                }
+                if (p + 1 == w.to) {
+                    G[0] = G[1] = 0.f;
+                    if (a.dlast) load_state<ONE>(a.dlast + state_of(a, w.s, c), G);
+                }
+                token(j);
+                if (p == w.from && a.last) store_two<ONE>(a.last + state_of(a, w.s, c), G);
+            }
         }
     }
 }
@@ -595,6 +459,26 @@ struct StepArgs {
     int C, chunks;   // chunks: of 16 bytes of x, a row
 };
 
+// One float per channel of a row of the states.
+template <int N>
+__device__ __forceinline__ void load_states(const float* row, int n, float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        float part[4];
+        load_part(row + i, n - i, part);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[i + j] = part[j];
+    }
+}
+template <int N>
+__device__ __forceinline__ void store_states(float* row, int n, const float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        const float part[4] = {v[i], v[i + 1], v[i + 2], v[i + 3]};
+        store_part(row + i, n - i, part);
+    }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(256) k_scan_step(StepArgs a) {
     constexpr int V = kVec<T>;
@@ -605,7 +489,7 @@ __global__ void __launch_bounds__(256) k_scan_step(StepArgs a) {
         float x[V], f[V], h[V];
         unpack(load_raw(static_cast<const T*>(a.x) + row * a.x_stride + c, n), x);
         unpack(load_raw(static_cast<const T*>(a.f) + row * a.f_stride + c, n), f);
-        load_state(a.state + row * a.C + c, n, h);
+        load_states(a.state + row * a.C + c, n, h);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             float keep, take;
@@ -613,54 +497,59 @@ __global__ void __launch_bounds__(256) k_scan_step(StepArgs a) {
             h[i] = fmaf(keep, h[i], take * x[i]);
         }
         store_part(static_cast<T*>(a.y) + row * a.C + c, n, h);
-        store_state(a.out + row * a.C + c, n, h);
+        store_states(a.out + row * a.C + c, n, h);
     }
 }
 
-// Parts of the pack: enough workgroups to fill the chip four times.
+// Parts of the pack: enough for four waves a vector unit, of 64 tokens at least.
 struct Split {
-    int groups, parts, part_tiles;   // groups: of channels
+    int parts, len;
 };
 Split split_of(const wtc_scan_desc* d) {
-    const int width = d->dtype == WTC_BF16 ? kWidth<uint16_t> : kWidth<float>;
+    const long long pairs = (d->C + 1) / 2, want = (262144 + pairs - 1) / pairs, most = (d->T + 63) / 64;
+    long long parts = want < most ? want : most;
+    parts = parts < 1 ? 1 : parts > kMostParts ? kMostParts : parts;
     Split s;
-    s.groups = (d->C + width - 1) / width;
-    const long long tiles = (d->T + kScanTile - 1) / kScanTile;
-    long long parts = 1024 / s.groups;
-    parts = parts < 1 ? 1 : parts > tiles ? (tiles < 1 ? 1 : tiles) : parts;
-    s.part_tiles = (int)((tiles + parts - 1) / parts);
-    s.parts = s.part_tiles < 1 ? 1 : (int)((tiles + s.part_tiles - 1) / s.part_tiles);
+    s.len = (int)(((d->T + parts - 1) / parts + kScanKept - 1) / kScanKept * kScanKept);
+    s.parts = s.len < 1 ? 1 : (int)((d->T + s.len - 1) / s.len);
     return s;
 }
+static_assert(kScanKept % kAhead == 0, "what is kept is kept at the start of a step");
 
 ScanArgs scan_args(const wtc_scan_desc* d, const Split& s, const void* x, const void* f, const int* cu, const float* state,
-                   void* maps) {
+                   void* workspace) {
     ScanArgs a = {};
-    a.x = x; a.f = f; a.cu = cu; a.state = state; a.maps = static_cast<float2*>(maps);
+    a.x = x; a.f = f; a.cu = cu; a.state = state;
+    a.maps = static_cast<float2*>(workspace);
+    a.starts = reinterpret_cast<float*>(a.maps + (size_t)s.parts * d->C);
     a.x_stride = d->x_stride; a.f_stride = d->f_stride; a.g_stride = d->g_stride;
-    a.T = (int)d->T; a.n_seq = d->n_seq; a.C = d->C; a.reverse = d->reverse;
-    a.parts = s.parts; a.part_tiles = s.part_tiles;
+    a.T = (int)d->T; a.n_seq = d->n_seq; a.C = d->C; a.pairs = (d->C + 1) / 2; a.reverse = d->reverse;
+    a.parts = s.parts; a.len = s.len;
     return a;
 }
 
-template <typename T>
-void run_forward(const ScanArgs& a, const Split& s, hipStream_t st) {
-    if (s.parts > 1)
-        hipLaunchKernelGGL(k_scan_parts<T>, dim3((unsigned)s.groups, (unsigned)(s.parts - 1)), dim3(256), 0, st, a);
-    hipLaunchKernelGGL(k_scan_forward<T>, dim3((unsigned)s.groups, (unsigned)s.parts), dim3(256), 0, st, a);
+template <typename T, bool BACK, bool ONE>
+void run_scan(const ScanArgs& a, hipStream_t st) {
+    const dim3 grid((unsigned)(((long long)a.parts * a.pairs + 255) / 256));
+    if (a.parts > 1) {
+        hipLaunchKernelGGL((k_scan_maps<T, BACK, ONE>), grid, dim3(256), 0, st, a);
+        hipLaunchKernelGGL(k_scan_starts<BACK>, dim3((unsigned)((a.C + kCols - 1) / kCols)), dim3(1024), 0, st, a);
+    }
+    if constexpr (BACK)
+        hipLaunchKernelGGL((k_scan_backward<T, ONE>), grid, dim3(256), 0, st, a);
+    else
+        hipLaunchKernelGGL((k_scan_forward<T, ONE>), grid, dim3(256), 0, st, a);
 }
-template <typename T>
-void run_backward(const ScanArgs& a, const Split& s, hipStream_t st) {
-    if (s.parts > 1)
-        hipLaunchKernelGGL(k_scan_parts_back<T>, dim3((unsigned)s.groups, (unsigned)(s.parts - 1)), dim3(256), 0, st, a);
-    hipLaunchKernelGGL(k_scan_backward<T>, dim3((unsigned)s.groups, (unsigned)s.parts), dim3(256), 0, st, a);
+template <typename T, bool BACK>
+void run_scan(const ScanArgs& a, hipStream_t st) {
+    a.C == 1 ? run_scan<T, BACK, true>(a, st) : run_scan<T, BACK, false>(a, st);
 }
 
 }  // namespace
 
 size_t scan_workspace(const wtc_scan_desc* d) {
     const Split s = split_of(d);
-    return s.parts > 1 ? (size_t)s.parts * d->C * sizeof(float2) : 0;
+    return s.parts > 1 ? (size_t)s.parts * d->C * (sizeof(float2) + sizeof(float)) : 0;
 }
 
 int launch_scan_forward(const wtc_scan_desc* d, const void* x, const void* f, const int* cu, const float* state, void* y,
@@ -669,10 +558,7 @@ int launch_scan_forward(const wtc_scan_desc* d, const void* x, const void* f, co
     ScanArgs a = scan_args(d, s, x, f, cu, state, workspace);
     a.y = y; a.last = last; a.kept = kept;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-    if (d->dtype == WTC_BF16)
-        run_forward<uint16_t>(a, s, st);
-    else
-        run_forward<float>(a, s, st);
+    d->dtype == WTC_BF16 ? run_scan<uint16_t, false>(a, st) : run_scan<float, false>(a, st);
     return hipGetLastError() == hipSuccess ? WTC_OK : WTC_EHIP;
 }
 
@@ -683,10 +569,7 @@ int launch_scan_backward(const wtc_scan_desc* d, const void* x, const void* f, c
     ScanArgs a = scan_args(d, s, x, f, cu, state, workspace);
     a.kept_in = kept; a.dy = dy; a.dlast = dlast; a.y = dx; a.df = df; a.last = dstate;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-    if (d->dtype == WTC_BF16)
-        run_backward<uint16_t>(a, s, st);
-    else
-        run_backward<float>(a, s, st);
+    d->dtype == WTC_BF16 ? run_scan<uint16_t, true>(a, st) : run_scan<float, true>(a, st);
     return hipGetLastError() == hipSuccess ? WTC_OK : WTC_EHIP;
 }
 
