@@ -13,7 +13,7 @@
 //   Across  a row of the tile is one term, its 16-byte chunks are rows (columns)
 //           of the output; bfloat16 is read with the transposing instruction,
 //           float32 a value at a time.
-// A step takes 64 or 128 bytes of terms.  Tiles are copied by the memory system 1024
+// A step takes 128 bytes of terms.  Tiles are copied by the memory system 1024
 // consecutive bytes of shared memory at a time, and the chunks of a row are
 // permuted on that way so that reads meet no bank twice.
 #pragma once
@@ -34,17 +34,57 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) char lds_char;
 
-// A lane's terms of one read are 16 bytes, those of the two halves of a wave 32.
+// A lane's eight terms of a read; those of the two halves of a wave are a step of the matrix instruction.
+// A float32 is the sum of three bfloat16 (8 of its 24 bits each, split exactly), and its product six of theirs:
+// the three left out are below 2^-24 of it, so this is float32's own precision in 192 cycles a block, where the
+// float32 instructions take 512.
+constexpr int kRead = 16;
+constexpr int kStepBytes = 128;
 template <typename T>
-constexpr int kRead = 2 * kVec<T>;
-
-__device__ __forceinline__ void mma(const u32x4& a, const u32x4& b, f32x16& c, uint16_t) {
+struct Frag;
+template <>
+struct Frag<uint16_t> {
+    u32x4 v;
+};
+template <>
+struct Frag<float> {
+    u32x4 v[3];   // high, middle and low parts
+};
+// Eight terms as they lie in memory.
+template <typename T>
+struct Eight {
+    u32x4 u[sizeof(T) / 2];
+};
+__device__ __forceinline__ Frag<uint16_t> frag(const Eight<uint16_t>& x) { return {x.u[0]}; }
+__device__ __forceinline__ Frag<float> frag(const Eight<float>& x) {
+    Frag<float> f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t p = x.u[i / 2][2 * i % 4], q = x.u[i / 2][2 * i % 4 + 1];
+        float a = __builtin_bit_cast(float, p), b = __builtin_bit_cast(float, q);
+        const uint32_t hi = bf16x2_rne(a, b);
+        a -= __builtin_bit_cast(float, hi << 16);   // each difference is exact
+        b -= __builtin_bit_cast(float, hi & 0xFFFF0000u);
+        const uint32_t mid = bf16x2_rne(a, b);
+        a -= __builtin_bit_cast(float, mid << 16);
+        b -= __builtin_bit_cast(float, mid & 0xFFFF0000u);
+        f.v[0][i] = hi;
+        f.v[1][i] = mid;
+        f.v[2][i] = bf16x2_rne(a, b);
+    }
+    return f;
+}
+__device__ __forceinline__ void mma(const u32x4& a, const u32x4& b, f32x16& c) {
     c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
-__device__ __forceinline__ void mma(const u32x4& a, const u32x4& b, f32x16& c, float) {
-    const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(x[i], y[i], c, 0, 0, 0);
+__device__ __forceinline__ void mma(const Frag<uint16_t>& a, const Frag<uint16_t>& b, f32x16& c) { mma(a.v, b.v, c); }
+__device__ __forceinline__ void mma(const Frag<float>& a, const Frag<float>& b, f32x16& c) {
+    mma(a.v[0], b.v[2], c);   // the smallest first
+    mma(a.v[2], b.v[0], c);
+    mma(a.v[1], b.v[1], c);
+    mma(a.v[0], b.v[1], c);
+    mma(a.v[1], b.v[0], c);
+    mma(a.v[0], b.v[0], c);
 }
 
 __device__ __forceinline__ uint32_t lds_address(const void* p) { return (uint32_t)(uintptr_t)(lds_char*)p; }
@@ -58,30 +98,44 @@ __device__ __forceinline__ void copy1024(uint32_t dst, const char* base, uint32_
                  : "m0", "memory");
 }
 
-// N rows (or columns) of an operand whose terms lie along its rows, BYTES (64 or 128) of terms.
-template <typename T, int N, int WAVES, int BYTES>
+// v, but what is derived from it is not kept in registers over a loop.
+__device__ __forceinline__ int anew(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+// N rows (or columns) of an operand whose terms lie along its rows, a step's 128 bytes of terms.
+template <typename T, int N, int WAVES>
 struct Along {
-    static constexpr int kBytes = N * BYTES, kCopies = kBytes / 1024 / WAVES, kChunks = BYTES / 16;
+    static constexpr int kBytes = N * kStepBytes, kCopies = kBytes / 1024 / WAVES, kChunks = kStepBytes / 16;
     static_assert(kBytes % (1024 * WAVES) == 0, "whole copies");
     // 16 lanes read a chunk of 16 rows: those rows' chunks that share banks, 256 bytes apart, are exchanged
-    static constexpr __host__ __device__ int turn(int row) { return (row * BYTES / 256) & (kChunks - 1); }
-    // bytes from the operand's first row to the lane's part of each copy; rows past `last` repeat it
-    uint32_t off[kCopies];
-    int unit[kCopies];      // the chunk of the row
+    static constexpr __host__ __device__ int turn(int row) { return (row * kStepBytes / 256) & (kChunks - 1); }
+    uint32_t off[kCopies];   // bytes from the operand's first row to the lane's part of each copy
+    static __device__ __forceinline__ int row_at(int i, int wave, int lane) {
+        return (wave * kCopies + i) * (64 / kChunks) + lane / kChunks;
+    }
+    static __device__ __forceinline__ int unit_at(int row, int lane) { return (lane % kChunks) ^ turn(row); }   // the chunk
+    // rows past `last` repeat it
     __device__ __forceinline__ void place(uint32_t row_bytes, int last, int wave, int lane) {
 #pragma unroll
         for (int i = 0; i < kCopies; ++i) {
-            const int r = (wave * kCopies + i) * (64 / kChunks) + lane / kChunks;
-            unit[i] = (lane % kChunks) ^ turn(r);
-            off[i] = (uint32_t)min(r, last) * row_bytes + unit[i] * 16;
+            const int r = row_at(i, wave, lane);
+            off[i] = (uint32_t)min(r, last) * row_bytes + unit_at(r, lane) * 16;
         }
     }
     // base: the step's first term of the operand's first row; chunks: of terms that are there, if fewer than a step's
-    __device__ __forceinline__ void copy(uint32_t dst, const char* base, int chunks, int wave) const {
+    __device__ __forceinline__ void copy(uint32_t dst, const char* base, int chunks, int wave, int lane) const {
+        dst += wave * (kCopies * 1024);
+        if (chunks >= kChunks) {
 #pragma unroll
-        for (int i = 0; i < kCopies; ++i) {
-            const uint32_t back = chunks < kChunks && unit[i] >= chunks ? (uint32_t)(unit[i] - chunks + 1) * 16 : 0;
-            copy1024(dst + (wave * kCopies + i) * 1024, base, off[i] - back);
+            for (int i = 0; i < kCopies; ++i) copy1024(dst + i * 1024, base, off[i]);
+        } else {
+            lane = anew(lane);
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i)
+                copy1024(dst + i * 1024, base,
+                         off[i] - (uint32_t)max(unit_at(row_at(i, wave, lane), lane) - chunks + 1, 0) * 16);
         }
     }
     // Zeros to the chunks of terms that are not there.
@@ -89,41 +143,57 @@ struct Along {
         for (int u = threadIdx.x; u < N * kChunks; u += 64 * WAVES)
             if (((u % kChunks) ^ turn(u / kChunks)) >= chunks) *reinterpret_cast<u32x4*>(tile + u * 16) = u32x4{0u, 0u, 0u, 0u};
     }
-    __device__ static __forceinline__ int lane_part(int lane) { return (lane & 31) * BYTES; }
-    // 16 bytes of terms of row r0 + lane % 32, r0 a multiple of 32
-    __device__ static __forceinline__ u32x4 read(const char* tile, int part, int r0, int at, int lane) {
-        const int unit = (2 * at + (lane >> 5)) ^ turn(lane & 31);
-        return *reinterpret_cast<const u32x4*>(tile + part + r0 * BYTES + unit * 16);
+    __device__ static __forceinline__ int lane_part(int lane) { return (lane & 31) * kStepBytes; }
+    // Terms 16 at + 8 h .. of row r0 + lane % 32, r0 a multiple of 32
+    __device__ static __forceinline__ Eight<T> read(const char* tile, int part, int r0, int at, int lane) {
+        constexpr int UNITS = (int)sizeof(T) / 2;
+        Eight<T> x;
+#pragma unroll
+        for (int k = 0; k < UNITS; ++k) {
+            const int unit = (UNITS * (2 * at + (lane >> 5)) + k) ^ turn(lane & 31);
+            x.u[k] = *reinterpret_cast<const u32x4*>(tile + part + r0 * kStepBytes + unit * 16);
+        }
+        return x;
     }
 };
 
 // The same of an operand whose terms lie across: a row of the tile is one term
 // with N of the output's rows (or columns).
-template <typename T, int N, int WAVES, int BYTES>
+template <typename T, int N, int WAVES>
 struct Across {
     static constexpr int kRow = N * (int)sizeof(T), kChunks = kRow / 16;
-    static constexpr int kBytes = BYTES / (int)sizeof(T) * kRow, kCopies = kBytes / 1024 / WAVES;
+    static constexpr int kTerms = kStepBytes / (int)sizeof(T);
+    static constexpr int kBytes = kTerms * kRow, kCopies = kBytes / 1024 / WAVES;
     static constexpr int kRowsEach = 1024 / kRow > 0 ? 1024 / kRow : 1;
     static_assert(kBytes % (1024 * WAVES) == 0 && 1024 % kRow == 0 && kRow >= 256, "whole copies, and chunks to permute");
     // the permutation of a row's chunks: bfloat16 by 64 bytes, with the four terms of one
     // transposing read; float32 by 128 bytes, with the halves of the wave
     static __device__ __forceinline__ int turn(int term) {
-        return sizeof(T) == 2 ? (term & 3) << 2 : ((term >> 2) & 1) << 3;
+        return sizeof(T) == 2 ? (term & 3) << 2 : ((term >> 3) & 1) << 3;
     }
-    uint32_t unit[kCopies];   // bytes along the row
-    int term[kCopies];
-    __device__ __forceinline__ void place(int last_chunk, int wave, int lane) {
+    uint32_t off[kCopies];   // bytes from the step's first term of the operand's first row (column)
+    static __device__ __forceinline__ int term_at(int i, int wave, int lane) {
+        return (wave * kCopies + i) * kRowsEach + lane / kChunks;
+    }
+    __device__ __forceinline__ void place(uint32_t row_bytes, int last_chunk, int wave, int lane) {
 #pragma unroll
         for (int i = 0; i < kCopies; ++i) {
-            term[i] = (wave * kCopies + i) * kRowsEach + lane / kChunks;
-            unit[i] = (uint32_t)min((lane % kChunks) ^ turn(term[i]), last_chunk) * 16;
+            const int t = term_at(i, wave, lane);
+            off[i] = (uint32_t)t * row_bytes + (uint32_t)min((lane % kChunks) ^ turn(t), last_chunk) * 16;
         }
     }
     // base: the step's first term of the operand's first row (column); last: the last term that is there
-    __device__ __forceinline__ void copy(uint32_t dst, const char* base, uint32_t row_bytes, int last, int wave) const {
+    __device__ __forceinline__ void copy(uint32_t dst, const char* base, uint32_t row_bytes, int last, int wave, int lane) const {
+        dst += wave * (kCopies * 1024);
+        if (last >= kTerms - 1) {
 #pragma unroll
-        for (int i = 0; i < kCopies; ++i)
-            copy1024(dst + (wave * kCopies + i) * 1024, base, (uint32_t)min(term[i], last) * row_bytes + unit[i]);
+            for (int i = 0; i < kCopies; ++i) copy1024(dst + i * 1024, base, off[i]);
+        } else {
+            lane = anew(lane);
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i)
+                copy1024(dst + i * 1024, base, off[i] - (uint32_t)max(term_at(i, wave, lane) - last, 0) * row_bytes);
+        }
     }
     // Zeros to the terms from `there` on.
     __device__ static __forceinline__ void clear(char* tile, int there) {
@@ -133,11 +203,11 @@ struct Across {
     // The lane's part: of the terms it reads first, and its column's.
     __device__ static __forceinline__ int lane_part(int lane) {
         if constexpr (sizeof(T) == 2) return (8 * (lane >> 5) + ((lane & 15) >> 2)) * kRow + (lane & 3) * 8;
-        return 4 * (lane >> 5) * kRow + (lane & 3) * 4;
+        return 8 * (lane >> 5) * kRow + (lane & 3) * 4;
     }
-    // The terms of row (column) r0 + lane % 32
-    __device__ static __forceinline__ u32x4 read(const char* tile, int part, int r0, int at, int lane) {
-        u32x4 v;
+    // Terms 16 at + 8 h .. of row (column) r0 + lane % 32
+    __device__ static __forceinline__ Eight<T> read(const char* tile, int part, int r0, int at, int lane) {
+        Eight<T> x;
         if constexpr (sizeof(T) == 2) {
             const int c = (r0 / 8 + ((lane >> 4) & 1) * 2) ^ turn((lane & 15) >> 2);   // the last bit is in `part`
 #pragma unroll
@@ -145,16 +215,16 @@ struct Across {
                 const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                     (__attribute__((address_space(3))) s16x4*)(lds_char*)(tile + part + (16 * at + 4 * k) * kRow + c * 16));
                 const u32x2 u = __builtin_bit_cast(u32x2, t);
-                v[2 * k] = u[0];
-                v[2 * k + 1] = u[1];
+                x.u[0][2 * k] = u[0];
+                x.u[0][2 * k + 1] = u[1];
             }
         } else {
-            const int c = (r0 / 4 + ((lane & 31) >> 2)) ^ turn(4 * (lane >> 5));
+            const int c = (r0 / 4 + ((lane & 31) >> 2)) ^ turn(8 * (lane >> 5));
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v[i] = *reinterpret_cast<const uint32_t*>(tile + part + (8 * at + i) * kRow + c * 16);
+            for (int i = 0; i < 8; ++i)
+                x.u[i / 4][i % 4] = *reinterpret_cast<const uint32_t*>(tile + part + (16 * at + i) * kRow + c * 16);
         }
-        return v;
+        return x;
     }
 };
 
@@ -171,19 +241,23 @@ __device__ __forceinline__ int segment_begin(const int* cu, int E, int R, int s)
     return min(max(cu[s - 1], 0), R);
 }
 // Segment s may use the tiles from floor(begin / SIZE) + s on, which leaves it
-// ceil(rows / SIZE) at least; whose a tile is, is found by searching cu, 64
+// ceil(rows / SIZE) at least; whose a tile is, is found by searching cu, 63
 // segments at a time.  count = 0: a tile of none.
 template <int SIZE>
 __device__ __forceinline__ Rows find_rows(const int* cu, int E, int R, int slot, int lane) {
-    int lo = 0, hi = E + 2;   // the segment is in lo .. hi - 1
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 63) / 64, s = lo + lane * step;
-        const bool at = s < hi && segment_begin(cu, E, R, s < hi ? s : hi) / SIZE + s <= slot;
-        const int n = __builtin_popcountll(__builtin_amdgcn_ballot_w64(at)), k = n > 0 ? n - 1 : 0;
+    int lo = 0, hi = E + 2, b, e;   // the segment is in lo .. hi - 1
+    for (;;) {
+        const int step = (hi - lo + 62) / 63, s = lo + lane * step, begin = segment_begin(cu, E, R, min(s, hi));
+        const int n = __builtin_popcountll(__builtin_amdgcn_ballot_w64(s < hi && begin / SIZE + s <= slot)), k = n > 0 ? n - 1 : 0;
         lo += k * step;
         hi = min(hi, lo + step);
+        if (step == 1) {   // the segment's bounds are two lanes' own
+            b = __builtin_amdgcn_readlane(begin, k);
+            e = __builtin_amdgcn_readlane(begin, k + 1);
+            break;
+        }
     }
-    const int b = segment_begin(cu, E, R, lo), e = segment_begin(cu, E, R, lo + 1), tile = slot - (b / SIZE + lo);
+    const int tile = slot - (b / SIZE + lo);
     Rows r;
     r.expert = lo == 0 || lo == E + 1 ? -1 : lo - 1;
     r.start = b + tile * SIZE;

@@ -5,7 +5,7 @@
 //   k_product_weights         dW[e] = sum_r dy[r] x[r]^T,  db[e] = sum_r dy[r]
 //
 // Bound by the matrix units.  A workgroup's tiles of the two operands are
-// copied to shared memory STAGES - 1 steps ahead of their products.
+// copied to shared memory a step ahead, and read from there half a step ahead, of their products.
 #pragma once
 
 #include <limits.h>
@@ -51,58 +51,112 @@ __device__ __forceinline__ void meet() {
     asm volatile("" ::: "memory");
 }
 
-// The products of one step: NB blocks of columns by MB of rows, from the wave's first.
-template <typename T, int READS, int NB, int MB, typename Cols, typename RowsOp>
-__device__ __forceinline__ void step(const char* cols, const char* rows, int cpart, int rpart, int col0, int row0, int lane,
-                                     f32x16 (&acc)[MB][NB]) {
-    constexpr int GROUP = 64 / (NB + MB) / 4 < READS ? 2 : READS;   // reads at once, of up to 64 registers
+// Half a step's terms of a wave's blocks, as they lie in shared memory, and their products.
+template <typename T, int NB, int MB, bool INTERLEAVE>
+struct Half {
+    static constexpr int READS = 64 / (int)sizeof(T) / kRead;
+    Eight<T> a[READS][NB], b[READS][MB];
+    template <typename Cols, typename RowsOp>
+    __device__ __forceinline__ void read(const char* cols, const char* rows, int cpart, int rpart, int col0, int row0, int lane,
+                                         int half) {
 #pragma unroll
-    for (int g = 0; g < READS; g += GROUP) {
-        u32x4 a[GROUP][NB], b[GROUP][MB];
+        for (int at = 0; at < READS; ++at) {
 #pragma unroll
-        for (int at = 0; at < GROUP; ++at) {
+            for (int nb = 0; nb < NB; ++nb) a[at][nb] = Cols::read(cols, cpart, col0 + 32 * nb, READS * half + at, lane);
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) a[at][nb] = Cols::read(cols, cpart, col0 + 32 * nb, g + at, lane);
-#pragma unroll
-            for (int mb = 0; mb < MB; ++mb) b[at][mb] = RowsOp::read(rows, rpart, row0 + 32 * mb, g + at, lane);
+            for (int mb = 0; mb < MB; ++mb) b[at][mb] = RowsOp::read(rows, rpart, row0 + 32 * mb, READS * half + at, lane);
         }
-        __builtin_amdgcn_sched_barrier(0);   // all reads are on their way before the first product
+    }
+    __device__ __forceinline__ void products(f32x16 (&acc)[MB][NB]) const {
+        // reads and products in turn, or what was to be read is on its way before the first product
+        if (!INTERLEAVE) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int at = 0; at < GROUP; ++at)
+        for (int at = 0; at < READS; ++at) {
+            Frag<T> fa[NB];
 #pragma unroll
-            for (int mb = 0; mb < MB; ++mb)
+            for (int nb = 0; nb < NB; ++nb) fa[nb] = frag(a[at][nb]);
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    mma(a[at][nb], b[at][mb], acc[mb][nb], T{});
-                    if (at == 0 && mb == 0 && nb == 0) {
-                        __builtin_amdgcn_sched_barrier(0);
-                        __builtin_amdgcn_s_setprio(1);
-                    }
-                }
+            for (int mb = 0; mb < MB; ++mb) {
+                const Frag<T> fb = frag(b[at][mb]);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) mma(fa[nb], fb, acc[mb][nb]);
+            }
+        }
+        if (INTERLEAVE) {
+            constexpr int PRODUCTS = READS * NB * MB, LOADS = READS * (NB + MB);
+#pragma unroll
+            for (int i = 0; i < PRODUCTS; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);     // a matrix instruction
+                if ((i + 1) * LOADS / PRODUCTS > i * LOADS / PRODUCTS) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // a read
+            }
+        }
         __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_setprio(0);
+    }
+};
+
+// Steps begin .. end - 1 with STAGES buffers: copy(s, buffer) sends a step's tiles on their way (COPIES of a wave),
+// read(half, set, buffer) reads half a step, last(buffer) clears what the final step lacks.  A half is read while the
+// one before it is multiplied.
+template <typename Set, int STAGES, int COPIES, typename Copy, typename Read, typename Last, typename Products>
+__device__ __forceinline__ void run_steps(int begin, int end, bool partial, const Copy& copy, const Read& read, const Last& last,
+                                          const Products& products) {
+    if (begin >= end) return;
+#pragma unroll
+    for (int s = 0; s < STAGES; ++s)
+        if (begin + s < end) copy(begin + s, s);
+    if (begin + STAGES <= end)
+        wait_copies<(STAGES - 1) * COPIES>();
+    else
+        wait_copies<0>();
+    meet();
+    if (partial && begin + 1 == end) {
+        last(0);
+        meet();
+    }
+    Set p, q;
+    read(0, p, 0);
+    for (int s = begin; s < end; ++s) {
+        const int here = (s - begin) % STAGES, next = (s + 1 - begin) % STAGES;
+        read(1, q, here);
+        products(p);
+        if (STAGES > 2 && s + STAGES <= end)
+            wait_copies<(STAGES - 2) * COPIES>();
+        else
+            wait_copies<0>();
+        meet();   // step s + 1 has come, and all of step s is in registers
+        if (partial && s + 2 == end) {
+            last(next);
+            meet();
+        }
+        if (s + STAGES < end) copy(s + STAGES, here);
+        if (s + 1 < end) read(0, p, next);
+        products(q);
     }
 }
 
 template <typename T>
-__device__ __forceinline__ float add_terms(const u32x4& v) {
-    float x[kVec<T>];
-    unpack(Raw<T>{v}, x);
+__device__ __forceinline__ float add_terms(const Eight<T>& v) {
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < kVec<T>; i += 4) s += (x[i] + x[i + 1]) + (x[i + 2] + x[i + 3]);
+    for (int k = 0; k < (int)sizeof(T) / 2; ++k) {
+        float x[kVec<T>];
+        unpack(Raw<T>{v.u[k]}, x);
+#pragma unroll
+        for (int i = 0; i < kVec<T>; i += 4) s += (x[i] + x[i + 1]) + (x[i + 2] + x[i + 3]);
+    }
     return s;
 }
 
 // WM x WN waves of MB x NB blocks each.
-template <typename T, bool BACK, int WM, int WN, int MB, int NB, int BYTES, int STAGES>
+template <typename T, bool BACK, int WM, int WN, int MB, int NB, int STAGES>
 __global__ void __launch_bounds__(64 * WM * WN, 2) k_product_rows(Args a) {
-    constexpr int WAVES = WM * WN, BM = 32 * WM * MB, BN = 32 * WN * NB, TERMS = BYTES / (int)sizeof(T), READS = BYTES / 32;
-    using X = Along<T, BM, WAVES, BYTES>;
-    using W = typename std::conditional<BACK, Across<T, BN, WAVES, BYTES>, Along<T, BN, WAVES, BYTES>>::type;
+    constexpr int WAVES = WM * WN, BM = 32 * WM * MB, BN = 32 * WN * NB, TERMS = kStepBytes / (int)sizeof(T);
+    using X = Along<T, BM, WAVES>;
+    using W = typename std::conditional<BACK, Across<T, BN, WAVES>, Along<T, BN, WAVES>>::type;
     constexpr int STAGE = X::kBytes + W::kBytes, COPIES = X::kCopies + W::kCopies;
     constexpr int STORE = WAVES * kStoreBytes<T, NB>, LDS = STAGES * STAGE > STORE ? STAGES * STAGE : STORE;
     static_assert(LDS <= 160 * 1024, "shared memory");
+    using Set = Half<T, NB, MB, sizeof(T) == 2>;
     __shared__ __align__(16) char lds[LDS];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
@@ -141,43 +195,33 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) k_product_rows(Args a) {
         W wt;
         xt.place(xrow, r.count - 1, wave, lane);
         if constexpr (BACK)
-            wt.place(here / kVec<T> - 1, wave, lane);
+            wt.place(wrow, here / kVec<T> - 1, wave, lane);
         else
             wt.place(wrow, here - 1, wave, lane);
         const uint32_t lds0 = lds_address(lds);
         const int steps = (terms + TERMS - 1) / TERMS;
-        auto copy = [&](int s) {
-            const uint32_t at = lds0 + (uint32_t)(s % STAGES) * STAGE;
-            const int left = terms - s * TERMS;
-            xt.copy(at, x + (size_t)s * BYTES, left / kVec<T>, wave);
-            if constexpr (BACK)
-                wt.copy(at + X::kBytes, w + (size_t)s * TERMS * wrow, wrow, left - 1, wave);
-            else
-                wt.copy(at + X::kBytes, w + (size_t)s * BYTES, left / kVec<T>, wave);
-        };
-#pragma unroll
-        for (int s = 0; s < STAGES - 1; ++s)
-            if (s < steps) copy(s);
         const int xpart = X::lane_part(lane), wpart = W::lane_part(lane);
-        for (int s = 0; s < steps; ++s) {
-            if (s + STAGES - 1 <= steps)
-                wait_copies<(STAGES - 2) * COPIES>();
-            else
-                wait_copies<0>();
-            meet();   // step s is there; everyone is done with the one before it
-            char* at = lds + s % STAGES * STAGE;
-            const int left = terms - s * TERMS;
-            if (left < TERMS) {   // the last step
-                X::clear(at, left / kVec<T>);
+        run_steps<Set, STAGES, COPIES>(
+            0, steps, terms % TERMS != 0,
+            [&](int s, int buffer) {
+                const uint32_t at = lds0 + (uint32_t)buffer * STAGE;
+                const int left = terms - s * TERMS;
+                xt.copy(at, x + (size_t)s * kStepBytes, left / kVec<T>, wave, lane);
                 if constexpr (BACK)
-                    W::clear(at + X::kBytes, left);
+                    wt.copy(at + X::kBytes, w + (size_t)s * TERMS * wrow, wrow, left - 1, wave, lane);
                 else
-                    W::clear(at + X::kBytes, left / kVec<T>);
-                meet();
-            }
-            if (s + STAGES - 1 < steps) copy(s + STAGES - 1);
-            step<T, READS, NB, MB, W, X>(at + X::kBytes, at, wpart, xpart, 32 * NB * wn, 32 * MB * wm, lane, acc);
-        }
+                    wt.copy(at + X::kBytes, w + (size_t)s * kStepBytes, left / kVec<T>, wave, lane);
+            },
+            [&](int half, Set& set, int buffer) {
+                const char* at = lds + buffer * STAGE;
+                set.template read<W, X>(at + X::kBytes, at, wpart, xpart, 32 * NB * wn, 32 * MB * wm, lane, half);
+            },
+            [&](int buffer) {
+                char* at = lds + buffer * STAGE;
+                X::clear(at, terms % TERMS / kVec<T>);
+                W::clear(at + X::kBytes, BACK ? terms % TERMS : terms % TERMS / kVec<T>);
+            },
+            [&](const Set& set) { set.products(acc); });
         meet();   // no tile is read any more
     }
 #pragma unroll
@@ -189,14 +233,15 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) k_product_rows(Args a) {
     }
 }
 
-template <typename T, int WM, int WN, int MB, int NB, int BYTES, int STAGES>
+template <typename T, int WM, int WN, int MB, int NB, int STAGES>
 __global__ void __launch_bounds__(64 * WM * WN, 2) k_product_weights(Args a) {
-    constexpr int WAVES = WM * WN, BM = 32 * WM * MB, BN = 32 * WN * NB, TERMS = BYTES / (int)sizeof(T), READS = BYTES / 32;
-    using G = Across<T, BM, WAVES, BYTES>;
-    using X = Across<T, BN, WAVES, BYTES>;
+    constexpr int WAVES = WM * WN, BM = 32 * WM * MB, BN = 32 * WN * NB, TERMS = kStepBytes / (int)sizeof(T);
+    using G = Across<T, BM, WAVES>;
+    using X = Across<T, BN, WAVES>;
     constexpr int STAGE = G::kBytes + X::kBytes, COPIES = G::kCopies + X::kCopies;
     constexpr int STORE = WAVES * kStoreBytes<float, NB>, LDS = STAGES * STAGE > STORE ? STAGES * STAGE : STORE;
     static_assert(LDS <= 160 * 1024, "shared memory");
+    using Set = Half<T, NB, MB, sizeof(T) == 2>;
     __shared__ __align__(16) char lds[LDS];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
@@ -220,43 +265,36 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) k_product_weights(Args a) {
     const char* x = static_cast<const char*>(a.x) + ((long long)first * a.x_stride + col0) * SZ;
     G gt;
     X xt;
-    gt.place(min(a.N - row0, BM) / kVec<T> - 1, wave, lane);
-    xt.place(min(a.K - col0, BN) / kVec<T> - 1, wave, lane);
+    gt.place(grow, min(a.N - row0, BM) / kVec<T> - 1, wave, lane);
+    xt.place(xrow, min(a.K - col0, BN) / kVec<T> - 1, wave, lane);
     const uint32_t lds0 = lds_address(lds);
-    auto copy = [&](int s) {
-        const uint32_t at = lds0 + (uint32_t)((s - begin) % STAGES) * STAGE;
-        const int last = count - 1 - s * TERMS;
-        gt.copy(at, g + (size_t)s * TERMS * grow, grow, last, wave);
-        xt.copy(at + G::kBytes, x + (size_t)s * TERMS * xrow, xrow, last, wave);
-    };
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s)
-        if (begin + s < end) copy(begin + s);
     const int gpart = G::lane_part(lane), xpart = X::lane_part(lane);
-    for (int s = begin; s < end; ++s) {
-        if (s + STAGES - 1 <= end)
-            wait_copies<(STAGES - 2) * COPIES>();
-        else
-            wait_copies<0>();
-        meet();
-        char* at = lds + (s - begin) % STAGES * STAGE;
-        const int left = count - s * TERMS;
-        if (left < TERMS) {   // the expert's last step
-            G::clear(at, left);
-            X::clear(at + G::kBytes, left);
-            meet();
-        }
-        if (s + STAGES - 1 < end) copy(s + STAGES - 1);
-        step<T, READS, NB, MB, X, G>(at + G::kBytes, at, xpart, gpart, 32 * NB * wn, 32 * MB * wm, lane, acc);
-        if (sums) {
+    run_steps<Set, STAGES, COPIES>(
+        begin, end, end == all && count % TERMS != 0,
+        [&](int s, int buffer) {
+            const uint32_t at = lds0 + (uint32_t)buffer * STAGE;
+            const int last = count - 1 - s * TERMS;
+            gt.copy(at, g + (size_t)s * TERMS * grow, grow, last, wave, lane);
+            xt.copy(at + G::kBytes, x + (size_t)s * TERMS * xrow, xrow, last, wave, lane);
+        },
+        [&](int half, Set& set, int buffer) {
+            const char* at = lds + buffer * STAGE;
+            set.template read<X, G>(at + G::kBytes, at, xpart, gpart, 32 * NB * wn, 32 * MB * wm, lane, half);
+        },
+        [&](int buffer) {
+            char* at = lds + buffer * STAGE;
+            G::clear(at, count % TERMS);
+            X::clear(at + G::kBytes, count % TERMS);
+        },
+        [&](const Set& set) {
+            set.products(acc);
+            if (sums) {
 #pragma unroll
-            for (int k = 0; k < READS; ++k)
+                for (int k = 0; k < Set::READS; ++k)
 #pragma unroll
-                for (int mb = 0; mb < MB; ++mb) {
-                    sum[mb] += add_terms<T>(G::read(at, gpart, 32 * (MB * wm + mb), k, lane));
-                }
-        }
-    }
+                    for (int mb = 0; mb < MB; ++mb) sum[mb] += add_terms<T>(set.b[k][mb]);
+            }
+        });
     meet();
     const int col = col0 + 32 * NB * wn;
     const size_t weights = (size_t)a.E * a.N * a.K;
@@ -303,37 +341,43 @@ __global__ void __launch_bounds__(256) k_product_join(Args a, long long n, long 
 
 constexpr int kTile = 128;   // rows and columns of a workgroup's tile
 
-template <typename T, bool BACK, int WM, int WN, int MB, int NB, int BYTES, int STAGES>
+template <typename T, bool BACK, int WM, int WN, int MB, int NB, int STAGES>
 int launch_rows(Args a, hipStream_t st) {
     constexpr int BM = 32 * WM * MB, BN = 32 * WN * NB;
     a.slots = row_slots(a.R, a.E, BM);
     const long long groups = a.slots * (((BACK ? a.K : a.N) + BN - 1) / BN);
     if (groups > (1 << 23)) return WTC_ESHAPE;
-    hipLaunchKernelGGL((k_product_rows<T, BACK, WM, WN, MB, NB, BYTES, STAGES>), dim3((unsigned)groups), dim3(64 * WM * WN), 0, st, a);
+    hipLaunchKernelGGL((k_product_rows<T, BACK, WM, WN, MB, NB, STAGES>), dim3((unsigned)groups), dim3(64 * WM * WN), 0, st, a);
     return hipGetLastError() == hipSuccess ? WTC_OK : WTC_EHIP;
 }
 template <typename T, bool BACK>
 int run_rows_way(const Args& a, hipStream_t st) {
-    const long long big = (a.R / 128) * (((BACK ? a.K : a.N) + 255) / 256);
-    if (sizeof(T) == 2 && big >= 512) return launch_rows<T, BACK, 1, 4, 4, 2, 64, 3>(a, st);
-    return launch_rows<T, BACK, 2, 2, 2, 2, 128, 2>(a, st);
+    const int columns = BACK ? a.K : a.N;
+    auto tiles = [&](int rows, int cols) {   // about: an expert's last tile is half full in the mean
+        return (a.R / rows + (a.R / rows < a.E ? a.R / rows : a.E)) * ((columns + cols - 1) / cols);
+    };
+    const int big = tiles(256, 256), middle = tiles(128, 128);
+    if constexpr (sizeof(T) == 2 && !BACK)   // back, the larger tile would spill a register
+        if (big >= 256 && 5 * ((big + 255) / 256) <= 3 * ((middle + 511) / 512)) return launch_rows<T, BACK, 2, 4, 4, 2, 2>(a, st);
+    if (middle >= 384) return launch_rows<T, BACK, 2, 2, 2, 2, 2>(a, st);
+    if (tiles(64, 128) >= 256) return launch_rows<T, BACK, 2, 2, 1, 2, 2>(a, st);
+    return launch_rows<T, BACK, 1, 4, 1, 1, 4>(a, st);
 }
 template <typename T>
 int run_rows(const Args& a, bool back, hipStream_t st) {
     return back ? run_rows_way<T, true>(a, st) : run_rows_way<T, false>(a, st);
 }
-template <typename T, int WM, int WN, int MB, int NB, int BYTES, int STAGES>
+template <typename T, int WM, int WN, int MB, int NB, int STAGES>
 int launch_weights(const Args& a, hipStream_t st) {
     constexpr int BM = 32 * WM * MB, BN = 32 * WN * NB;
     const long long groups = (long long)((a.K + BN - 1) / BN) * ((a.N + BM - 1) / BM) * a.E * a.splits;
     if (groups > (1 << 23)) return WTC_ESHAPE;
-    hipLaunchKernelGGL((k_product_weights<T, WM, WN, MB, NB, BYTES, STAGES>), dim3((unsigned)groups), dim3(64 * WM * WN), 0, st, a);
+    hipLaunchKernelGGL((k_product_weights<T, WM, WN, MB, NB, STAGES>), dim3((unsigned)groups), dim3(64 * WM * WN), 0, st, a);
     return hipGetLastError() == hipSuccess ? WTC_OK : WTC_EHIP;
 }
 template <typename T>
 int run_weights(const Args& a, hipStream_t st) {
-    const long long big = (long long)(a.K / 256) * (a.N / 128) * a.E;
-    const int r = sizeof(T) == 2 && big >= 256 ? launch_weights<T, 1, 4, 4, 2, 64, 3>(a, st) : launch_weights<T, 2, 2, 2, 2, 128, 2>(a, st);
+    const int r = launch_weights<T, 2, 2, 2, 2, 2>(a, st);
     if (r == WTC_OK && a.splits > 1) {
         const long long n = (long long)a.E * a.N * a.K, m = a.db ? (long long)a.E * a.N : 0, blocks = ((n + m) / 4 + 255) / 256;
         hipLaunchKernelGGL(k_product_join<T>, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, st, a, n, m);
