@@ -294,7 +294,7 @@ int wtconv_expert_order(long long n, int E, const int* experts, int* slot, int* 
     if (!cu_experts || (n > 0 && (!experts || !slot || !pair))) return WTC_EINVAL;
     const size_t need = order_workspace(n, E);
     if (need > 0 && (!workspace || workspace_bytes < need)) return WTC_EWORKSPACE;
-    if (!aligned(workspace, 4)) return WTC_EINVAL;
+    if (!aligned(workspace, 16)) return WTC_EINVAL;
     return launch_expert_order(n, E, experts, slot, pair, cu_experts, workspace, stream);
 }
 

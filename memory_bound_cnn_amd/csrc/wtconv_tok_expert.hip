@@ -23,7 +23,7 @@ namespace wtc {
 namespace {
 
 // ------------------------------------------------------------------ order
-constexpr int kOneGroup = 8192;
+constexpr int kOneGroup = 8192, kMostUnits = 1024;
 
 struct OrderArgs {
     const int* experts;
@@ -137,28 +137,27 @@ __global__ void __launch_bounds__(1024) k_order_sum(OrderArgs a) {
     __shared__ int totals[WTC_EXPERTS_MAX], sums[16];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int e = wave; e < a.E; e += 16) {
-        int before = 0;
-        for (int u0 = 0; u0 < a.units; u0 += 256) {   // four units a lane
-            int v[4], s = 0;
+        int* row = a.counts + (size_t)e * a.units;
+        int4 v[kMostUnits / 256];   // of four units a lane, all on their way at once
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int u = u0 + 4 * lane + i;
-                v[i] = u < a.units ? a.counts[(size_t)e * a.units + u] : 0;
-                s += v[i];
-            }
+        for (int i = 0; i < kMostUnits / 256; ++i) {
+            const int u = 256 * i + 4 * lane;
+            v[i] = u < a.units ? *reinterpret_cast<const int4*>(row + u) : make_int4(0, 0, 0, 0);
+        }
+        int before = 0;
+#pragma unroll
+        for (int i = 0; i < kMostUnits / 256; ++i) {
+            const int u = 256 * i + 4 * lane, s = v[i].x + v[i].y + v[i].z + v[i].w;
+            if (256 * i >= a.units) break;
             int up = s;
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) {
                 const int t = __shfl_up(up, o);
                 if (lane >= o) up += t;
             }
-            int at = before + up - s;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int u = u0 + 4 * lane + i;
-                if (u < a.units) a.counts[(size_t)e * a.units + u] = at;
-                at += v[i];
-            }
+            const int at = before + up - s;
+            if (u < a.units)
+                *reinterpret_cast<int4*>(row + u) = make_int4(at, at + v[i].x, at + v[i].x + v[i].y, at + v[i].x + v[i].y + v[i].z);
             before += __shfl(up, 63);
         }
         if (lane == 0) totals[e] = before;
@@ -333,8 +332,8 @@ OrderPlan order_plan(long long n, int E) {
     if (n <= kOneGroup) {
         p.units = 16;
     } else {   // counts of at most 2^15 numbers, for one workgroup to sum
-        const long long most = 32768 / E, runs = (n + 63) / 64, least = most < 32 ? 32 : most > 1024 ? 1024 : most;
-        p.units = (int)(least < runs ? least : runs);
+        const long long most = 32768 / E, runs = (n + 63) / 64, least = most < 32 ? 32 : most > kMostUnits ? kMostUnits : most;
+        p.units = (int)(((least < runs ? least : runs) + 3) / 4 * 4);   // counts are summed four at a time
     }
     p.run = (int)(((n + p.units - 1) / p.units + 63) / 64 * 64);
     return p;
