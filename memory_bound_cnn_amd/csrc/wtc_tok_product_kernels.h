@@ -354,9 +354,10 @@ template <typename T, bool BACK>
 int run_rows_way(const Args& a, hipStream_t st) {
     const int columns = BACK ? a.K : a.N;
     auto tiles = [&](int rows, int cols) {   // about: an expert's last tile is half full in the mean
-        return (a.R / rows + (a.R / rows < a.E ? a.R / rows : a.E)) * ((columns + cols - 1) / cols);
+        const long long full = a.R / rows;
+        return (full + (full < a.E ? full : a.E)) * ((columns + cols - 1) / cols);
     };
-    const int big = tiles(256, 256), middle = tiles(128, 128);
+    const long long big = tiles(256, 256), middle = tiles(128, 128);
     if constexpr (sizeof(T) == 2 && !BACK)   // back, the larger tile would spill a register
         if (big >= 256 && 5 * ((big + 255) / 256) <= 3 * ((middle + 511) / 512)) return launch_rows<T, BACK, 2, 4, 4, 2, 2>(a, st);
     if (middle >= 384) return launch_rows<T, BACK, 2, 2, 2, 2, 2>(a, st);

@@ -89,19 +89,21 @@ wtc_scan_desc scan_desc(const Tensor& x, const Tensor& gate, const Tensor& cu, b
     cu_check(cu, x);
     return {x.size(0), x.stride(0), gate.stride(0), 0, sequences(cu), narrow(x.size(1), "channels of x"), dtype, reverse};
 }
-void state_check(const OptTensor& t, const char* name, const Tensor& x, const Tensor& cu) {
-    if (t) check(*t, name, at::kFloat, x, {cu.size(0) - 1, x.size(1)});
+// a state [n, C], or its gradient, as the kernels read it; undefined if there is none
+Tensor state_of(const OptTensor& t, const char* name, const Tensor& x, const Tensor& cu) {
+    if (!t) return Tensor();
+    check(*t, name, at::kFloat, x, {cu.size(0) - 1, x.size(1)}, false);
+    return t->contiguous();
 }
-Tensors scan_forward(const Tensor& x0, const Tensor& gate0, const Tensor& cu, const OptTensor& state, bool reverse, bool keep) {
+Tensors scan_forward(const Tensor& x0, const Tensor& gate0, const Tensor& cu, const OptTensor& state0, bool reverse, bool keep) {
     scan_desc(x0, gate0, cu, reverse);
-    state_check(state, "state", x0, cu);
-    const Tensor x = dense_rows(x0), gate = dense_rows(gate0);
+    const Tensor x = dense_rows(x0), gate = dense_rows(gate0), state = state_of(state0, "state", x0, cu);
     const wtc_scan_desc d = scan_desc(x, gate, cu, reverse);
     const size_t bytes = wtconv_gated_scan_workspace(&d), kept = keep ? wtconv_gated_scan_kept(&d) : 0;
     const Tensor y = empty(x.sizes(), x), last = empty({d.n_seq, d.C}, x, at::kFloat),
                  k = keep ? empty({(int64_t)(kept / sizeof(float))}, x, at::kFloat) : Tensor(), ws = workspace(bytes, x);
     const On on(x);
-    raise_on(wtconv_gated_scan_forward(&d, in(x), in(gate), in_as<int>(cu), state ? in_as<float>(*state) : nullptr, out(y),
+    raise_on(wtconv_gated_scan_forward(&d, in(x), in(gate), in_as<int>(cu), in_as<float>(state), out(y),
                                        floats(last), floats(k), out(ws), bytes, on.stream),
              "wtconv_gated_scan_forward");
     return keep ? Tensors{y, last, k} : Tensors{y, last};
@@ -115,25 +117,24 @@ Tensors _gated_scan_forward(const Tensor& x, const Tensor& gate, const Tensor& c
     return scan_forward(x, gate, cu, state, reverse, true);
 }
 // [dx, dgate], or [dx, dgate, dstate] with a state
-Tensors _gated_scan_backward(const Tensor& dy0, const OptTensor& dlast, const Tensor& x0, const Tensor& gate0, const Tensor& cu,
-                             const OptTensor& state, const Tensor& kept, bool reverse) {
+Tensors _gated_scan_backward(const Tensor& dy0, const OptTensor& dlast0, const Tensor& x0, const Tensor& gate0, const Tensor& cu,
+                             const OptTensor& state0, const Tensor& kept, bool reverse) {
     scan_desc(x0, gate0, cu, reverse);
     check_like(dy0, "dy", x0);
-    state_check(state, "state", x0, cu);
-    state_check(dlast, "dlast", x0, cu);
+    const Tensor state = state_of(state0, "state", x0, cu), dlast = state_of(dlast0, "dlast", x0, cu);
     const Tensor x = dense_rows(x0), gate = dense_rows(gate0), dy = dense_rows(dy0);
     wtc_scan_desc d = scan_desc(x, gate, cu, reverse);
     d.g_stride = dy.stride(0);
     check(kept, "kept", at::kFloat, x, {(int64_t)(wtconv_gated_scan_kept(&d) / sizeof(float))});
     const size_t bytes = wtconv_gated_scan_workspace(&d);
     const Tensor dx = empty(x.sizes(), x), dgate = empty(x.sizes(), x), ws = workspace(bytes, x),
-                 dstate = state ? empty({d.n_seq, d.C}, x, at::kFloat) : Tensor();
+                 dstate = state0 ? empty({d.n_seq, d.C}, x, at::kFloat) : Tensor();
     const On on(x);
-    raise_on(wtconv_gated_scan_backward(&d, in(x), in(gate), in_as<int>(cu), state ? in_as<float>(*state) : nullptr,
-                                        in_as<float>(kept), in(dy), dlast ? in_as<float>(*dlast) : nullptr, out(dx), out(dgate),
+    raise_on(wtconv_gated_scan_backward(&d, in(x), in(gate), in_as<int>(cu), in_as<float>(state), in_as<float>(kept), in(dy),
+                                        in_as<float>(dlast), out(dx), out(dgate),
                                         floats(dstate), out(ws), bytes, on.stream),
              "wtconv_gated_scan_backward");
-    return state ? Tensors{dx, dgate, dstate} : Tensors{dx, dgate};
+    return state0 ? Tensors{dx, dgate, dstate} : Tensors{dx, dgate};
 }
 // y; the new state goes to `to`, which may be state
 Tensor gated_scan_step(const Tensor& x0, const Tensor& gate0, const Tensor& state, Tensor to) {
@@ -141,6 +142,7 @@ Tensor gated_scan_step(const Tensor& x0, const Tensor& gate0, const Tensor& stat
     check_like(gate0, "gate", x0);
     check(state, "state", at::kFloat, x0, x0.sizes());
     check(to, "out", at::kFloat, x0, x0.sizes());
+    at::assert_no_partial_overlap(to, state);   // it may be state itself
     const Tensor x = dense_rows(x0), gate = dense_rows(gate0), y = empty(x.sizes(), x);
     const wtc_scan_desc d = {x.size(0), x.stride(0), gate.stride(0), 0, 0, narrow(x.size(1), "channels of x"), dtype, 0};
     const On on(x);
@@ -189,11 +191,11 @@ Tensor expert_gather(const Tensor& x0, const Tensor& slot, const Tensor& cu) {
 Tensor _expert_sum(const Tensor& rows0, const OptTensor& weights, const Tensor& slot) {
     wtc_rows_desc d = rows_desc(rows0, slot, 1, "rows");
     TORCH_CHECK_VALUE(rows0.size(0) == slot.numel(), "rows has ", rows0.size(0), " rows, slot ", slot.numel(), " places");
-    if (weights) check(*weights, "weights", at::kFloat, rows0, slot.sizes());
-    const Tensor r = dense_rows(rows0), y = empty({slot.size(0), r.size(1)}, r);
+    if (weights) check(*weights, "weights", at::kFloat, rows0, slot.sizes(), false);
+    const Tensor r = dense_rows(rows0), w = weights ? weights->contiguous() : Tensor(), y = empty({slot.size(0), r.size(1)}, r);
     d.r_stride = r.stride(0);
     const On on(r);
-    raise_on(wtconv_expert_combine(&d, in(r), weights ? in_as<float>(*weights) : nullptr, in_as<int>(slot), out(y), on.stream),
+    raise_on(wtconv_expert_combine(&d, in(r), in_as<float>(w), in_as<int>(slot), out(y), on.stream),
              "wtconv_expert_combine");
     return y;
 }
@@ -201,13 +203,13 @@ Tensor expert_combine(const Tensor& rows, const Tensor& weights, const Tensor& s
     experts_of(cu, rows);
     return _expert_sum(rows, weights, slot);
 }
-std::tuple<Tensor, Tensor> _expert_combine_backward(const Tensor& dy0, const Tensor& rows0, const Tensor& weights,
+std::tuple<Tensor, Tensor> _expert_combine_backward(const Tensor& dy0, const Tensor& rows0, const Tensor& weights0,
                                                     const Tensor& slot, const Tensor& cu) {
     wtc_rows_desc d = rows_desc(rows0, slot, experts_of(cu, rows0), "rows");
     TORCH_CHECK_VALUE(rows0.size(0) == slot.numel(), "rows has ", rows0.size(0), " rows, slot ", slot.numel(), " places");
-    check(weights, "weights", at::kFloat, rows0, slot.sizes());
+    check(weights0, "weights", at::kFloat, rows0, slot.sizes(), false);
     check(dy0, "dy", rows0.scalar_type(), rows0, {slot.size(0), rows0.size(1)}, false);
-    const Tensor r = dense_rows(rows0), dy = dense_rows(dy0), dr = empty(r.sizes(), r), dw = empty(slot.sizes(), r, at::kFloat);
+    const Tensor r = dense_rows(rows0), dy = dense_rows(dy0), weights = weights0.contiguous(), dr = empty(r.sizes(), r), dw = empty(slot.sizes(), r, at::kFloat);
     d.r_stride = r.stride(0);
     d.x_stride = dy.stride(0);
     const On on(r);

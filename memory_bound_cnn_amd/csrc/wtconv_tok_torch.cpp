@@ -12,6 +12,7 @@
 // The gradients are C++ nodes because a backward pass runs on a thread of
 // PyTorch's own: with Python nodes a step of a small norm spent 128 us on the
 // host, two thirds of it there.
+#include <ATen/MemoryOverlap.h>
 #include <c10/core/AutogradState.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>

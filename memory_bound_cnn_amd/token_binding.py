@@ -17,9 +17,14 @@ __all__ = [
     "wtc_rms_desc", "wtc_rotary_desc", "wtc_attn_strides", "wtc_attn_desc",
     "wtconv_rms_norm_forward", "wtconv_rms_norm_backward", "wtconv_rotary", "wtconv_dropout",
     "wtconv_attention_forward", "wtconv_attention_backward", "RMS_MAX_C", "ATTN_MAX_D",
+    "wtc_layer_desc", "wtc_scan_desc", "wtc_rows_desc", "wtc_expert_desc",
+    "wtconv_layer_norm_forward", "wtconv_layer_norm_backward", "wtconv_gated_scan_forward", "wtconv_gated_scan_backward",
+    "wtconv_gated_scan_step", "wtconv_expert_order", "wtconv_expert_gather", "wtconv_expert_combine",
+    "wtconv_expert_combine_backward", "wtconv_expert_linear_forward", "wtconv_expert_linear_input_grad",
+    "wtconv_expert_linear_weight_grad", "EXPERTS_MAX",
 ]
 
-RMS_MAX_C, ROTARY_MAX_AXES, ATTN_MAX_D = 16384, 4, 128   # limits in include/wtconv_tokens.h
+RMS_MAX_C, ROTARY_MAX_AXES, ATTN_MAX_D, EXPERTS_MAX = 16384, 4, 128, 512   # limits in include/wtconv_tokens.h
 _DTYPE = {torch.float32: WTC_FP32, torch.bfloat16: WTC_BF16}
 _I, _LL, _P, _SZ = ctypes.c_int, ctypes.c_longlong, ctypes.c_void_p, ctypes.c_size_t
 
@@ -45,6 +50,24 @@ class wtc_attn_desc(ctypes.Structure):
                 + [(name, wtc_attn_strides) for name in ("q", "k", "v", "o", "g", "dq", "dk", "dv")])
 
 
+class wtc_layer_desc(ctypes.Structure):
+    _fields_ = [("rows", _LL), ("x_stride", _LL), ("r_stride", _LL), ("g_stride", _LL), ("C", _I), ("dtype", _I),
+                ("eps", ctypes.c_float)]
+
+
+class wtc_scan_desc(ctypes.Structure):
+    _fields_ = [("T", _LL), ("x_stride", _LL), ("f_stride", _LL), ("g_stride", _LL), ("n_seq", _I), ("C", _I),
+                ("dtype", _I), ("reverse", _I)]
+
+
+class wtc_rows_desc(ctypes.Structure):
+    _fields_ = [("T", _LL), ("x_stride", _LL), ("r_stride", _LL), ("k", _I), ("E", _I), ("C", _I), ("dtype", _I)]
+
+
+class wtc_expert_desc(ctypes.Structure):
+    _fields_ = [("R", _LL), ("x_stride", _LL), ("g_stride", _LL), ("E", _I), ("K", _I), ("N", _I), ("dtype", _I)]
+
+
 _lib = None
 
 
@@ -59,13 +82,27 @@ def _load():
                 ("wtconv_rotary", [_P] * 6),
                 ("wtconv_dropout", [_LL, _I, ctypes.c_double] + [_P] * 5),
                 ("wtconv_attention_forward", [_P] * 9 + [_SZ, _P]),
-                ("wtconv_attention_backward", [_P] * 13 + [_SZ, _P])):
+                ("wtconv_attention_backward", [_P] * 13 + [_SZ, _P]),
+                ("wtconv_layer_norm_forward", [_P] * 9),
+                ("wtconv_layer_norm_backward", [_P] * 10 + [_SZ, _P]),
+                ("wtconv_gated_scan_forward", [_P] * 9 + [_SZ, _P]),
+                ("wtconv_gated_scan_backward", [_P] * 12 + [_SZ, _P]),
+                ("wtconv_gated_scan_step", [_P] * 7),
+                ("wtconv_expert_order", [_LL, _I] + [_P] * 5 + [_SZ, _P]),
+                ("wtconv_expert_gather", [_P] * 6),
+                ("wtconv_expert_combine", [_P] * 6),
+                ("wtconv_expert_combine_backward", [_P] * 9),
+                ("wtconv_expert_linear_forward", [_P] * 7),
+                ("wtconv_expert_linear_input_grad", [_P] * 6),
+                ("wtconv_expert_linear_weight_grad", [_P] * 7 + [_SZ, _P])):
             f = getattr(lib, name)
             f.restype, f.argtypes = _I, args
         for name in ("wtconv_rms_norm_backward_workspace", "wtconv_attention_forward_workspace",
-                     "wtconv_attention_backward_workspace"):
+                     "wtconv_attention_backward_workspace", "wtconv_layer_norm_backward_workspace",
+                     "wtconv_gated_scan_kept", "wtconv_gated_scan_workspace", "wtconv_expert_linear_weight_grad_workspace"):
             f = getattr(lib, name)
             f.restype, f.argtypes = _SZ, [_P]
+        lib.wtconv_expert_order_workspace.restype, lib.wtconv_expert_order_workspace.argtypes = _SZ, [_LL, _I]
         _lib = lib
     return _lib
 
@@ -270,3 +307,239 @@ def wtconv_attention_backward(q, k, v, out, lse, dout, cu_seqlens, causal=False,
           out.data_ptr(), lse.data_ptr(), _ptr(out_low), dout.data_ptr(), cu_seqlens.data_ptr(), dq.data_ptr(), dk.data_ptr(),
           dv.data_ptr(), _ptr(ws), size)
     return dq, dk, dv
+
+
+def wtconv_layer_norm_forward(x, weight, bias=None, residual=None, eps=1e-6, want_stats=False):
+    """(y, h, stats) for x [rows, C]: h is None without a residual, stats [rows,
+    2] (mean and reciprocal deviation) unless wanted."""
+    dtype = _activation(x, "x", 2)
+    rows, C = x.shape
+    dev = x.device
+    _check(weight, "weight", torch.float32, dev, (C,), True)
+    if bias is not None:
+        _check(bias, "bias", torch.float32, dev, (C,), True)
+    if residual is not None:
+        _check(residual, "residual", x.dtype, dev, x.shape)
+    y = torch.empty((rows, C), dtype=x.dtype, device=dev)
+    h = None if residual is None else torch.empty((rows, C), dtype=x.dtype, device=dev)
+    stats = torch.empty((rows, 2), dtype=torch.float32, device=dev) if want_stats else None
+    d = wtc_layer_desc(rows, x.stride(0), 0 if residual is None else residual.stride(0), 0, C, dtype, eps)
+    _call("wtconv_layer_norm_forward", dev, ctypes.addressof(d), x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(bias),
+          y.data_ptr(), _ptr(h), _ptr(stats))
+    return y, h, stats
+
+
+def wtconv_layer_norm_backward(dy, dh, h, weight, stats, want_db=True, workspace=None):
+    """(dx, dw, db): dx is the gradient of x and of the residual.  h: the norm's
+    input; dh: the gradient reaching h by its other use, or None."""
+    dtype = _activation(h, "h", 2)
+    rows, C = h.shape
+    dev = h.device
+    _check(dy, "dy", h.dtype, dev, h.shape)
+    if dh is not None:
+        _check(dh, "dh", h.dtype, dev, h.shape, True)
+    _check(weight, "weight", torch.float32, dev, (C,), True)
+    _check(stats, "stats", torch.float32, dev, (rows, 2), True)
+    dx = torch.empty((rows, C), dtype=h.dtype, device=dev)
+    dw = torch.empty(C, dtype=torch.float32, device=dev)
+    db = torch.empty(C, dtype=torch.float32, device=dev) if want_db else None
+    d = wtc_layer_desc(rows, h.stride(0), 0, dy.stride(0), C, dtype, 0.0)
+    ws, size = _workspace(_load().wtconv_layer_norm_backward_workspace(ctypes.addressof(d)), dev, workspace)
+    _call("wtconv_layer_norm_backward", dev, ctypes.addressof(d), dy.data_ptr(), _ptr(dh), h.data_ptr(), weight.data_ptr(),
+          stats.data_ptr(), dx.data_ptr(), dw.data_ptr(), _ptr(db), _ptr(ws), size)
+    return dx, dw, db
+
+
+def _scan_desc(x, gate, cu_seqlens, state, reverse):
+    dtype = _activation(x, "x", 2)
+    dev = x.device
+    _check(gate, "gate", x.dtype, dev, x.shape)
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must be [n + 1]")
+    _narrow("cu_seqlens", *cu_seqlens.shape)
+    _check(cu_seqlens, "cu_seqlens", torch.int32, dev, cu_seqlens.shape, True)
+    n = cu_seqlens.shape[0] - 1
+    if state is not None:
+        _check(state, "state", torch.float32, dev, (n, x.shape[1]), True)
+    return wtc_scan_desc(x.shape[0], x.stride(0), gate.stride(0), 0, n, x.shape[1], dtype, reverse)
+
+
+def wtconv_gated_scan_forward(x, gate, cu_seqlens, state=None, reverse=False, want_kept=False, workspace=None):
+    """(y, last, kept) for x and gate [T, C]: last [n, C] float32; kept, what the
+    backward pass needs, unless wanted None."""
+    d = _scan_desc(x, gate, cu_seqlens, state, reverse)
+    dev = x.device
+    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    last = torch.empty((d.n_seq, x.shape[1]), dtype=torch.float32, device=dev)
+    lib = _load()
+    kept = torch.empty(lib.wtconv_gated_scan_kept(ctypes.addressof(d)) // 4, dtype=torch.float32, device=dev) if want_kept else None
+    ws, size = _workspace(lib.wtconv_gated_scan_workspace(ctypes.addressof(d)), dev, workspace)
+    _call("wtconv_gated_scan_forward", dev, ctypes.addressof(d), x.data_ptr(), gate.data_ptr(), cu_seqlens.data_ptr(),
+          _ptr(state), y.data_ptr(), last.data_ptr(), _ptr(kept), _ptr(ws), size)
+    return y, last, kept
+
+
+def wtconv_gated_scan_backward(dy, dlast, x, gate, cu_seqlens, state, kept, reverse=False, workspace=None):
+    """(dx, dgate, dstate): dlast or None (zeros); dstate None without a state."""
+    d = _scan_desc(x, gate, cu_seqlens, state, reverse)
+    dev = x.device
+    _check(dy, "dy", x.dtype, dev, x.shape)
+    if dlast is not None:
+        _check(dlast, "dlast", torch.float32, dev, (d.n_seq, x.shape[1]), True)
+    d.g_stride = dy.stride(0)
+    lib = _load()
+    _check(kept, "kept", torch.float32, dev, (lib.wtconv_gated_scan_kept(ctypes.addressof(d)) // 4,), True)
+    dx, dgate = (torch.empty(x.shape, dtype=x.dtype, device=dev) for _ in range(2))
+    dstate = None if state is None else torch.empty_like(state)
+    ws, size = _workspace(lib.wtconv_gated_scan_workspace(ctypes.addressof(d)), dev, workspace)
+    _call("wtconv_gated_scan_backward", dev, ctypes.addressof(d), x.data_ptr(), gate.data_ptr(), cu_seqlens.data_ptr(),
+          _ptr(state), kept.data_ptr(), dy.data_ptr(), _ptr(dlast), dx.data_ptr(), dgate.data_ptr(), _ptr(dstate), _ptr(ws), size)
+    return dx, dgate, dstate
+
+
+def wtconv_gated_scan_step(x, gate, state, out=None):
+    """(y, new state) of one more token of each of n sequences.  out may be state."""
+    dtype = _activation(x, "x", 2)
+    dev = x.device
+    _check(gate, "gate", x.dtype, dev, x.shape)
+    _check(state, "state", torch.float32, dev, x.shape, True)
+    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    if out is None:
+        out = torch.empty(x.shape, dtype=torch.float32, device=dev)
+    else:
+        _check(out, "out", torch.float32, dev, x.shape, True)
+    d = wtc_scan_desc(x.shape[0], x.stride(0), gate.stride(0), 0, 0, x.shape[1], dtype, 0)
+    _call("wtconv_gated_scan_step", dev, ctypes.addressof(d), x.data_ptr(), gate.data_ptr(), state.data_ptr(), y.data_ptr(),
+          out.data_ptr())
+    return y, out
+
+
+def wtconv_expert_order(experts, E, workspace=None):
+    """(slot, pair, cu_experts) of experts [T, k] int32."""
+    if not experts.is_cuda:
+        raise ValueError("experts must be a CUDA tensor")
+    dev = experts.device
+    if experts.dim() != 2:
+        raise ValueError(f"experts has shape {tuple(experts.shape)}, expected [T, k]")
+    _check(experts, "experts", torch.int32, dev, experts.shape, True)
+    _narrow("experts", E)
+    n = experts.numel()
+    slot = torch.empty_like(experts)
+    pair = torch.empty(n, dtype=torch.int32, device=dev)
+    cu = torch.empty(max(E, 0) + 1, dtype=torch.int32, device=dev)
+    ws, size = _workspace(_load().wtconv_expert_order_workspace(n, E), dev, workspace)
+    _call("wtconv_expert_order", dev, n, E, experts.data_ptr(), slot.data_ptr(), pair.data_ptr(), cu.data_ptr(), _ptr(ws), size)
+    return slot, pair, cu
+
+
+def _rows_desc(t, name, slot, cu_experts):
+    dtype = _activation(t, name, 2)
+    if slot.dim() != 2 or slot.shape[1] < 1:
+        raise ValueError(f"slot has shape {tuple(slot.shape)}, expected [T, k]")
+    _check(slot, "slot", torch.int32, t.device, slot.shape, True)
+    E = 1
+    if cu_experts is not None:
+        if cu_experts.dim() != 1 or cu_experts.shape[0] < 2:
+            raise ValueError("cu_experts must be [E + 1]")
+        _check(cu_experts, "cu_experts", torch.int32, t.device, cu_experts.shape, True)
+        E = cu_experts.shape[0] - 1
+    _narrow("slot", slot.shape[1], E)
+    return wtc_rows_desc(slot.shape[0], 0, 0, slot.shape[1], E, t.shape[1], dtype)
+
+
+def wtconv_expert_gather(x, slot, cu_experts):
+    """x [T, C] to the rows [T k, C] of slot [T, k]."""
+    d = _rows_desc(x, "x", slot, cu_experts)
+    if x.shape[0] != slot.shape[0]:
+        raise ValueError(f"x has {x.shape[0]} rows, slot {slot.shape[0]}")
+    d.x_stride = x.stride(0)
+    rows = torch.empty((slot.numel(), x.shape[1]), dtype=x.dtype, device=x.device)
+    _call("wtconv_expert_gather", x.device, ctypes.addressof(d), x.data_ptr(), slot.data_ptr(), cu_experts.data_ptr(),
+          rows.data_ptr())
+    return rows
+
+
+def wtconv_expert_combine(rows, weights, slot):
+    """The sum of each token's rows, with weights [T, k] float32 or None (ones)."""
+    d = _rows_desc(rows, "rows", slot, None)
+    if rows.shape[0] != slot.numel():
+        raise ValueError(f"rows has {rows.shape[0]} rows, slot {slot.numel()} places")
+    if weights is not None:
+        _check(weights, "weights", torch.float32, rows.device, slot.shape, True)
+    d.r_stride = rows.stride(0)
+    y = torch.empty((slot.shape[0], rows.shape[1]), dtype=rows.dtype, device=rows.device)
+    _call("wtconv_expert_combine", rows.device, ctypes.addressof(d), rows.data_ptr(), _ptr(weights), slot.data_ptr(), y.data_ptr())
+    return y
+
+
+def wtconv_expert_combine_backward(dy, rows, weights, slot, cu_experts):
+    """(drows, dweights)"""
+    d = _rows_desc(rows, "rows", slot, cu_experts)
+    dev = rows.device
+    if rows.shape[0] != slot.numel():
+        raise ValueError(f"rows has {rows.shape[0]} rows, slot {slot.numel()} places")
+    _check(weights, "weights", torch.float32, dev, slot.shape, True)
+    _check(dy, "dy", rows.dtype, dev, (slot.shape[0], rows.shape[1]))
+    d.x_stride, d.r_stride = dy.stride(0), rows.stride(0)
+    drows = torch.empty(rows.shape, dtype=rows.dtype, device=dev)
+    dweights = torch.empty(slot.shape, dtype=torch.float32, device=dev)
+    _call("wtconv_expert_combine_backward", dev, ctypes.addressof(d), dy.data_ptr(), rows.data_ptr(), weights.data_ptr(),
+          slot.data_ptr(), cu_experts.data_ptr(), drows.data_ptr(), dweights.data_ptr())
+    return drows, dweights
+
+
+def _expert_desc(t, name, K, N, E, cu_experts):
+    dtype = _activation(t, name, 2)
+    _check(cu_experts, "cu_experts", torch.int32, t.device, (E + 1,), True)
+    _narrow("weight", K, N, E)
+    return wtc_expert_desc(t.shape[0], 0, 0, E, K, N, dtype)
+
+
+def wtconv_expert_linear_forward(x, weight, cu_experts, bias=None):
+    """x [R, K] weight[e]^T + bias[e], weight [E, N, K]."""
+    if weight.dim() != 3:
+        raise ValueError(f"weight has shape {tuple(weight.shape)}, expected [E, N, K]")
+    E, N, K = weight.shape
+    d = _expert_desc(x, "x", K, N, E, cu_experts)
+    dev = x.device
+    _check(x, "x", x.dtype, dev, (x.shape[0], K))
+    _check(weight, "weight", x.dtype, dev, weight.shape, True)
+    if bias is not None:
+        _check(bias, "bias", x.dtype, dev, (E, N), True)
+    d.x_stride = x.stride(0)
+    y = torch.empty((x.shape[0], N), dtype=x.dtype, device=dev)
+    _call("wtconv_expert_linear_forward", dev, ctypes.addressof(d), x.data_ptr(), weight.data_ptr(), _ptr(bias),
+          cu_experts.data_ptr(), y.data_ptr())
+    return y
+
+
+def wtconv_expert_linear_input_grad(dy, weight, cu_experts):
+    """dy [R, N] weight[e], weight [E, N, K]."""
+    if weight.dim() != 3:
+        raise ValueError(f"weight has shape {tuple(weight.shape)}, expected [E, N, K]")
+    E, N, K = weight.shape
+    d = _expert_desc(dy, "dy", K, N, E, cu_experts)
+    dev = dy.device
+    _check(dy, "dy", dy.dtype, dev, (dy.shape[0], N))
+    _check(weight, "weight", dy.dtype, dev, weight.shape, True)
+    d.g_stride = dy.stride(0)
+    dx = torch.empty((dy.shape[0], K), dtype=dy.dtype, device=dev)
+    _call("wtconv_expert_linear_input_grad", dev, ctypes.addressof(d), dy.data_ptr(), weight.data_ptr(), cu_experts.data_ptr(),
+          dx.data_ptr())
+    return dx
+
+
+def wtconv_expert_linear_weight_grad(dy, x, cu_experts, want_db=True, workspace=None):
+    """(dweight [E, N, K], dbias [E, N] or None) for dy [R, N] and x [R, K]."""
+    _activation(dy, "dy", 2)
+    E = cu_experts.shape[0] - 1
+    d = _expert_desc(x, "x", x.shape[1], dy.shape[1], E, cu_experts)
+    dev = x.device
+    _check(dy, "dy", x.dtype, dev, (x.shape[0], dy.shape[1]))
+    d.x_stride, d.g_stride = x.stride(0), dy.stride(0)
+    dw = torch.empty((E, dy.shape[1], x.shape[1]), dtype=x.dtype, device=dev)
+    db = torch.empty((E, dy.shape[1]), dtype=x.dtype, device=dev) if want_db else None
+    ws, size = _workspace(_load().wtconv_expert_linear_weight_grad_workspace(ctypes.addressof(d)), dev, workspace)
+    _call("wtconv_expert_linear_weight_grad", dev, ctypes.addressof(d), dy.data_ptr(), x.data_ptr(), cu_experts.data_ptr(),
+          dw.data_ptr(), _ptr(db), _ptr(ws), size)
+    return dw, db
