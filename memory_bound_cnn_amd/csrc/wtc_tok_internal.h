@@ -42,7 +42,7 @@ int launch_layer_backward(const wtc_layer_desc* d, const void* dy, const void* d
                           const float* stats, void* dx, float* dw, float* db, float* parts, void* stream);
 
 // Gated recurrence: the forward pass keeps the state before every kScanKept-th token for the backward pass
-constexpr int kScanKept = 16;
+constexpr int kScanKept = 8;
 size_t scan_workspace(const wtc_scan_desc* d);
 int launch_scan_forward(const wtc_scan_desc* d, const void* x, const void* f, const int* cu, const float* state, void* y,
                         float* last, float* kept, void* workspace, void* stream);

@@ -300,7 +300,7 @@ struct LayerNorm : torch::autograd::Function<LayerNorm> {
 };
 
 struct GatedScan : torch::autograd::Function<GatedScan> {
-    // Saves its inputs and the state at every 128th token.
+    // Saves its inputs and the state before every 8th token.
     static variable_list forward(AutogradContext* ctx, const Tensor& x, const Tensor& gate, const Tensor& cu,
                                  const OptTensor& state, bool reverse) {
         const NoGraph guard;

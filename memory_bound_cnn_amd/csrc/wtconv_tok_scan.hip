@@ -16,7 +16,7 @@
 //
 // Bound by device memory: 3 T C e bytes forward (x, f in, y out), 5 T C e
 // backward (x, f, dy in, dx, df out), and the maps' reading of two tensors in
-// long sequences.  The forward pass keeps the state of every 16th token (4 bytes
+// long sequences.  The forward pass keeps the state of every 8th token (4 bytes
 // a channel) for the backward pass, which computes the others again.  All of it
 // is float32.
 #include <hip/hip_runtime.h>
@@ -91,24 +91,40 @@ __device__ __forceinline__ void load_state(const float* p, float (&v)[V]) {
     v[1] = value(r, 1);
 }
 
-// sigmoid(f) and 1 - sigmoid(f).  float32: the exponent's product is rounded at
-// its own size, so exp is of float32's accuracy only with its lower part; what
-// bfloat16 holds of f is coarser than that.
+// A token's gate: with e = exp(-|f|) the smaller of a and 1 - a is e / (1 + e),
+// the larger 1 less that.  The state then moves from the nearer of itself and
+// the input by the smaller one's share of their difference: the same as a h +
+// (1 - a) x, but where a is close to 1 an error of a's last bit, made again in
+// each step, does not add up over 1 / (1 - a) of them.
+//   float32: the exponent's product is rounded at its own size, so exp is of
+// float32's accuracy only with its lower part, and the reciprocal with a Newton
+// step; what bfloat16 holds of f is coarser than either.
+struct Gate {
+    float m;   // the smaller one, negative if that is a
+    __device__ __forceinline__ bool slow() const { return __builtin_bit_cast(int, m) >= 0; }   // a is the larger
+};
 template <typename T>
-__device__ __forceinline__ void gate(float f, float& a, float& take) {
-    float e;
-    if constexpr (sizeof(T) == 2) {
-        const float t = f * -1.4426950408889634f;
-        e = __builtin_amdgcn_exp2f(t > 126.f ? 126.f : t);   // a NaN stays one
-    } else {
-        const float v = f < -87.f ? 87.f : f > 104.f ? -104.f : -f, t = v * 1.4426950408889634f;
-        const float low = fmaf(v, 1.4426950408889634f, -t) + v * 1.9259629911266175e-8f;
-        e = __builtin_amdgcn_exp2f(t);
+__device__ __forceinline__ Gate gate(float f) {
+    constexpr float L = 1.4426950408889634f;
+    const float t = -fabsf(f) * L;
+    float e = __builtin_amdgcn_exp2f(t);
+    if constexpr (sizeof(T) == 4) {
+        const float v = fabsf(f) < 200.f ? f : 0.f;   // beyond, e is 0 (an infinity's lower part would be a NaN)
+        const float low = fmaf(-fabsf(v), L, fabsf(v) * L) - fabsf(v) * 1.9259629911266175e-8f;
         e = fmaf(e, low * 0.6931471805599453f, e);
     }
-    a = __builtin_amdgcn_rcpf(1.f + e);
-    take = e * a;
+    const float d = 1.f + e;
+    float r = __builtin_amdgcn_rcpf(d);
+    if constexpr (sizeof(T) == 4) r = fmaf(fmaf(-d, r, 1.f), r, r);
+    const float m = e * r;
+    return {f >= 0.f ? m : -m};
 }
+// a h + (1 - a) x
+__device__ __forceinline__ float move(const Gate& g, float h, float x) { return fmaf(g.m, x - h, g.slow() ? h : x); }
+// a v, (1 - a) v, and a (1 - a) v
+__device__ __forceinline__ float keep(const Gate& g, float v) { return fmaf(g.m, -v, g.slow() ? v : 0.f); }
+__device__ __forceinline__ float take(const Gate& g, float v) { return (g.slow() ? g.m : 1.f + g.m) * v; }
+__device__ __forceinline__ float both(const Gate& g, float v) { return fabsf(g.m) * (1.f - fabsf(g.m)) * v; }
 
 // ------------------------------------------------------------------ places
 // Places of a pack in the order they are walked: place p is token p, or with
@@ -230,11 +246,10 @@ __global__ void __launch_bounds__(256) k_scan_maps(ScanArgs a) {
             const bool there = j < count;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                float keep, take;
-                gate<T>(value(fr.v[j], i), keep, take);
+                const Gate g = gate<T>(value(fr.v[j], i));
                 const float in = value(xr.v[j], i);
-                const float next = BACK ? keep * (in + B[i]) : fmaf(keep, B[i], take * in);
-                A[i] = there ? A[i] * keep : A[i];
+                const float next = BACK ? keep(g, in + B[i]) : move(g, B[i], in);
+                A[i] = there ? keep(g, A[i]) : A[i];
                 B[i] = there ? next : B[i];
             }
         }
@@ -322,11 +337,7 @@ __global__ void __launch_bounds__(256) k_scan_forward(ScanArgs a) {
         T* y = static_cast<T*>(a.y) + row_of(a, p0) * a.C + c;
         auto token = [&](int j) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                float keep, take;
-                gate<T>(value(fr.v[j], i), keep, take);
-                h[i] = fmaf(keep, h[i], take * value(xr.v[j], i));
-            }
+            for (int i = 0; i < V; ++i) h[i] = move(gate<T>(value(fr.v[j], i)), h[i], value(xr.v[j], i));
         };
         if (w.s >= 0 && p0 > w.from && p0 + kAhead < w.to) {   // no start and no end
 #pragma unroll
@@ -376,26 +387,27 @@ __global__ void __launch_bounds__(256) k_scan_backward(ScanArgs a) {
         x.fetch(a.x, a.x_stride, a, p0, end, c);
         f.fetch(a.f, a.f_stride, a, p0, end, c);
         dy.fetch(a.dy, a.g_stride, a, p0, end, c);
-        float now[V], h[N][V], keep[N][V], take[N][V];   // h: the states before each token
+        float now[V], h[N][V];   // h: the states before each token
+        Gate g[N][V];
         load_state<ONE>(a.kept_in + (size_t)(p0 / N) * a.C + c, now);
         const long long to = row_of(a, p0) * a.C + c;
         T *dx = static_cast<T*>(a.y) + to, *df = static_cast<T*>(a.df) + to;
 #pragma unroll
         for (int j = 0; j < N; ++j)
 #pragma unroll
-            for (int i = 0; i < V; ++i) gate<T>(value(f.v[j], i), keep[j][i], take[j][i]);
+            for (int i = 0; i < V; ++i) g[j][i] = gate<T>(value(f.v[j], i));
         auto forward = [&](int j) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) now[i] = fmaf(keep[j][i], now[i], take[j][i] * value(x.v[j], i));
+            for (int i = 0; i < V; ++i) now[i] = move(g[j][i], now[i], value(x.v[j], i));
         };
         auto token = [&](int j) {   // G becomes what the token hands to the one before it
             float vx[V], vf[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const float dh = G[i] + value(dy.v[j], i);
-                vx[i] = take[j][i] * dh;
-                vf[i] = keep[j][i] * vx[i] * (h[j][i] - value(x.v[j], i));
-                G[i] = keep[j][i] * dh;
+                vx[i] = take(g[j][i], dh);
+                vf[i] = both(g[j][i], dh) * (h[j][i] - value(x.v[j], i));
+                G[i] = keep(g[j][i], dh);
             }
             store_two<ONE>(dx + j * step, vx);
             store_two<ONE>(df + j * step, vf);
@@ -491,11 +503,7 @@ __global__ void __launch_bounds__(256) k_scan_step(StepArgs a) {
         unpack(load_raw(static_cast<const T*>(a.f) + row * a.f_stride + c, n), f);
         load_states(a.state + row * a.C + c, n, h);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float keep, take;
-            gate<T>(f[i], keep, take);
-            h[i] = fmaf(keep, h[i], take * x[i]);
-        }
+        for (int i = 0; i < V; ++i) h[i] = move(gate<T>(f[i]), h[i], x[i]);
         store_part(static_cast<T*>(a.y) + row * a.C + c, n, h);
         store_states(a.out + row * a.C + c, n, h);
     }

@@ -81,7 +81,7 @@ def test_gated_scan_rejects_pointers_and_workspaces():
     lib, d = tb._load(), scan()
     f, b, s = lib.wtconv_gated_scan_forward, lib.wtconv_gated_scan_backward, lib.wtconv_gated_scan_step
     need = lib.wtconv_gated_scan_workspace(ref(d))
-    assert need > 0 and lib.wtconv_gated_scan_kept(ref(d)) == 13 * 8 * 4        # the state of every 16th token
+    assert need > 0 and lib.wtconv_gated_scan_kept(ref(d)) == 25 * 8 * 4        # the state of every 8th token
     assert lib.wtconv_gated_scan_workspace(ref(scan(T=64))) == 0
     assert f(None, *[P] * 8, need, None) == EINVAL
     for at in (0, 1, 2, 4):
