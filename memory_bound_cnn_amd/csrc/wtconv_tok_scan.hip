@@ -11,8 +11,10 @@
 // part's map, and a second one composes them to the state that each part begins
 // with.  A map needs only the tokens behind the part's last sequence start
 // (before its first end, in the backward pass), so that little is read twice
-// where sequences are short; a sequence that starts in the part gives A = 0, and
-// nothing is then taken from what came before, not even a NaN.
+// where sequences are short.  A sequence that starts in the part is marked by A <
+// 0: nothing is then taken from what came before, not even a NaN.  An A of 0 is
+// one that became too small for float32; a NaN passes it, as it would pass every
+// one of the part's steps.
 //
 // Bound by device memory: 3 T C e bytes forward (x, f in, y out), 5 T C e
 // backward (x, f, dy in, dx, df out), and the maps' reading of two tensors in
@@ -208,6 +210,7 @@ struct Rows {
 };
 
 // ------------------------------------------------------------------ maps of parts
+constexpr float kCut = -1.f;   // in A's place: what comes before does not count
 template <typename T, bool BACK, bool ONE>
 __global__ void __launch_bounds__(256) k_scan_maps(ScanArgs a) {
     auto [part, c] = mine_of<ONE>(a);
@@ -216,15 +219,16 @@ __global__ void __launch_bounds__(256) k_scan_maps(ScanArgs a) {
     const int first = part * a.len, end = min(first + a.len, a.T);
     float A[V] = {}, B[V] = {};
     const Where w = find(a, BACK ? first : end - 1);
-    int from = first, to = first;         // the places that count; with none the map is zero
+    int from = first, to = first;         // the places that count; with none the state is zero
+    bool cut = true;
     if (BACK ? w.s >= 0 && w.from < first : w.s >= 0) {
-        const bool cut = BACK ? w.to <= end : w.from >= first;   // the sequence ends (starts) in the part
+        cut = BACK ? w.to <= end : w.from >= first;   // the sequence ends (starts) in the part
         from = BACK ? first : max(w.from, first);
         to = BACK ? min(w.to, end) : end;
         const float* in = BACK ? a.dlast : a.state;
         if (cut && in) load_state<ONE>(in + state_of(a, w.s, c), B);
 #pragma unroll
-        for (int i = 0; i < V; ++i) A[i] = cut ? 0.f : 1.f;
+        for (int i = 0; i < V; ++i) A[i] = 1.f;
     }
     const void* xs = BACK ? a.dy : a.x;
     const long long stride = BACK ? a.g_stride : a.x_stride;
@@ -255,17 +259,17 @@ __global__ void __launch_bounds__(256) k_scan_maps(ScanArgs a) {
         }
     }
 #pragma unroll
-    for (int i = 0; i < (ONE ? 1 : V); ++i) a.maps[(size_t)part * a.C + c + i] = make_float2(A[i], B[i]);
+    for (int i = 0; i < (ONE ? 1 : V); ++i) a.maps[(size_t)part * a.C + c + i] = make_float2(cut ? kCut : A[i], B[i]);
 }
 
 // The state that each part begins with (BACK: G behind its last token): 128
 // threads of a channel have up to kRun parts each, in order, and take what the
 // threads before them leave.
 constexpr int kRun = 8, kMostParts = 128 * kRun, kCols = 8;
-__device__ __forceinline__ float apply(const float2& m, float h) { return m.x == 0.f ? m.y : fmaf(m.x, h, m.y); }
+__device__ __forceinline__ float apply(const float2& m, float h) { return m.x < 0.f ? m.y : fmaf(m.x, h, m.y); }
 // first one, then the other
 __device__ __forceinline__ float2 after(const float2& one, const float2& other) {
-    return make_float2(other.x == 0.f ? 0.f : other.x * one.x, apply(other, one.y));
+    return make_float2(one.x < 0.f || other.x < 0.f ? kCut : other.x * one.x, apply(other, one.y));
 }
 
 template <bool BACK>

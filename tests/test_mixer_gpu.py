@@ -281,6 +281,34 @@ def test_gated_scan_keeps_sequences_apart(reverse, dtype):
 
 
 @BOTH
+@pytest.mark.parametrize("reverse", [False, True])
+def test_gated_scan_not_finite_is_not_forgotten(reverse, dtype):
+    """Gates that forget all but 1e-4 of the state in a step, whose product over a part is 0 in float32: what is not finite
+    stays in the states of its channel up to the sequence's end, and a gradient's up to its start, and reach no other."""
+    T, n, C = 9000, 5000, 8
+    x, gate = scan_inputs(T, C, dtype, seed=21)
+    gate = gate * 0 - 9
+    x[100, 3], x[4800, 5], x[6000, 2] = float("nan"), float("inf"), float("nan")
+    dy = torch.ones_like(x)
+    dy[4100, 1], dy[8000, 7] = float("nan"), float("-inf")
+    cu = torch.tensor([0, n, T], dtype=torch.int32, device=DEV)
+    leaves = [t.clone().requires_grad_() for t in (x, gate)]
+    y, last = tokens.gated_scan(*leaves, cu, reverse=reverse)
+    dx, = torch.autograd.grad(y, leaves[:1], dy)
+    bad = torch.zeros(T, C, dtype=torch.bool)
+    bad_dx = bad.clone()
+    for t, c, to in ((100, 3, bad), (4800, 5, bad), (6000, 2, bad), (4100, 1, bad_dx), (8000, 7, bad_dx)):
+        a, b = (0, n) if t < n else (n, T)
+        to[t:b, c] = True
+        if reverse == (to is bad):   # from t towards the start
+            to[t:b, c], to[a:t + 1, c] = False, True
+    assert torch.equal(~y.isfinite().cpu(), bad)
+    assert torch.equal(~dx.isfinite().cpu(), bad_dx)
+    ends = [0, n] if reverse else [n - 1, T - 1]
+    assert torch.equal(~last.isfinite().cpu(), bad[ends])
+
+
+@BOTH
 def test_gated_scan_gates_at_their_ends(dtype):
     """Gates of +-infinity and beyond what exp holds: all of the state, or none of it."""
     C, T = 6, 40
