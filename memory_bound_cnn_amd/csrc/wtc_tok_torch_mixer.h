@@ -275,6 +275,23 @@ Tensors _expert_linear_weight_grad(const Tensor& dy0, const Tensor& x0, const Te
 }  // namespace op
 
 // ================================================================== gradients
+// A leaf's gradient belongs to the stream on which the leaf was first used, for as long as a pass that used it lives.  Of
+// an eager pass that is the default stream, which PyTorch would make wait for a capture: that ends the process.  Refused.
+void check_capture() {
+    const auto node = torch::autograd::get_current_node();
+    if (!node) return;
+    hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
+    if (hipStreamIsCapturing(c10::hip::getCurrentHIPStream().stream(), &status) != hipSuccess || status == hipStreamCaptureStatusNone)
+        return;
+    for (size_t i = 0; i < node->num_outputs(); ++i) {
+        const auto& to = node->next_edge(i).function;
+        if (!to || !node->task_should_compute_output(i) || !dynamic_cast<torch::autograd::AccumulateGrad*>(to.get())) continue;
+        const auto stream = to->stream();
+        TORCH_CHECK(!stream || stream->id() != 0, "a backward pass cannot be captured while an eager pass of the same leaves lives; "
+                    "delete its outputs, or detach the leaves anew");
+    }
+}
+
 struct LayerNorm : torch::autograd::Function<LayerNorm> {
     // Saves the norm's input (h, or x without a residual) and two floats per row.
     static variable_list forward(AutogradContext* ctx, const Tensor& x, const Tensor& weight, const OptTensor& bias,
@@ -289,6 +306,7 @@ struct LayerNorm : torch::autograd::Function<LayerNorm> {
     }
     static variable_list backward(AutogradContext* ctx, const variable_list& g) {
         once(g, false);
+        check_capture();
         const variable_list s = ctx->get_saved_variables();
         const Tensor dh = g.size() > 1 ? g[1] : Tensor();
         if (!g[0].defined()) return {dh, Tensor(), Tensor(), dh, Tensor()};
@@ -313,6 +331,7 @@ struct GatedScan : torch::autograd::Function<GatedScan> {
     }
     static variable_list backward(AutogradContext* ctx, const variable_list& g) {
         once(g, false);
+        check_capture();
         if (!g[0].defined() && !g[1].defined()) return variable_list(5);
         const variable_list s = ctx->get_saved_variables();
         const NoGraph guard;
@@ -330,6 +349,7 @@ struct ExpertGather : torch::autograd::Function<ExpertGather> {
     }
     static variable_list backward(AutogradContext* ctx, const variable_list& g) {
         once(g, true);
+        check_capture();
         const Tensor slot = ctx->get_saved_variables()[0];
         const NoGraph guard;
         return {OP(_expert_sum).call(g[0], std::nullopt, slot), Tensor(), Tensor()};
@@ -344,6 +364,7 @@ struct ExpertCombine : torch::autograd::Function<ExpertCombine> {
     }
     static variable_list backward(AutogradContext* ctx, const variable_list& g) {
         once(g, false);
+        check_capture();
         const variable_list s = ctx->get_saved_variables();
         const NoGraph guard;
         const auto [dr, dw] = OP(_expert_combine_backward).call(g[0], s[0], s[1], s[2], s[3]);
@@ -360,6 +381,7 @@ struct ExpertLinear : torch::autograd::Function<ExpertLinear> {
     }
     static variable_list backward(AutogradContext* ctx, const variable_list& g) {
         once(g, false);
+        check_capture();
         const variable_list s = ctx->get_saved_variables();
         const bool has_bias = ctx->saved_data["bias"].toBool(), bias = has_bias && ctx->needs_input_grad(2);
         variable_list r(4);

@@ -93,6 +93,27 @@ def test_operators_replay_in_a_graph(name):
         compare(got, step())
 
 
+@pytest.mark.parametrize("name", ["layer_norm", "gated_scan", "expert_linear"])
+def test_a_backward_pass_is_not_captured_beside_an_eager_one(name):
+    """Its leaves' gradients would belong to the default stream: refused, and captured once the eager pass is gone."""
+    call, args = operator_calls()[name]
+    leaves = [t.detach().requires_grad_() for t in args]
+
+    def step():
+        return torch.autograd.grad(sum(t.float().square().sum() for t in flat(call(*leaves))), leaves)
+    want = [t.clone() for t in step()]
+    eager = call(*leaves)
+    with pytest.raises(RuntimeError, match="cannot be captured while an eager pass"):
+        captured(step)
+    torch.cuda.synchronize()
+    del eager
+    graph, out = captured(step)
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        compare(out, want)
+
+
 def test_larger_packs_replay_in_a_graph():
     """What has workspaces: scans of several parts, orders of several workgroups, weights' gradients of several splits;
     two graphs of the same work replayed in turn."""
