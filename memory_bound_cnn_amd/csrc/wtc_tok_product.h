@@ -138,6 +138,10 @@ struct Along {
                          off[i] - (uint32_t)max(unit_at(row_at(i, wave, lane), lane) - chunks + 1, 0) * 16);
         }
     }
+    // The wave's i-th copy of a step that has all its terms.
+    __device__ __forceinline__ void copy_one(int i, uint32_t dst, const char* base, int wave) const {
+        copy1024(dst + (wave * kCopies + i) * 1024, base, off[i]);
+    }
     // Zeros to the chunks of terms that are not there.
     __device__ static __forceinline__ void clear(char* tile, int chunks) {
         for (int u = threadIdx.x; u < N * kChunks; u += 64 * WAVES)
@@ -194,6 +198,9 @@ struct Across {
             for (int i = 0; i < kCopies; ++i)
                 copy1024(dst + i * 1024, base, off[i] - (uint32_t)max(term_at(i, wave, lane) - last, 0) * row_bytes);
         }
+    }
+    __device__ __forceinline__ void copy_one(int i, uint32_t dst, const char* base, int wave) const {
+        copy1024(dst + (wave * kCopies + i) * 1024, base, off[i]);
     }
     // Zeros to the terms from `there` on.
     __device__ static __forceinline__ void clear(char* tile, int there) {

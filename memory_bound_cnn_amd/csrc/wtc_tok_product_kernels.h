@@ -56,15 +56,33 @@ template <typename T, int NB, int MB, bool INTERLEAVE>
 struct Half {
     static constexpr int READS = 64 / (int)sizeof(T) / kRead;
     Eight<T> a[READS][NB], b[READS][MB];
+    static constexpr int LOADS = READS * (NB + MB), PRODUCTS = READS * NB * MB;
+    template <typename Cols, typename RowsOp>
+    __device__ __forceinline__ void read_one(int i, const char* cols, const char* rows, int cpart, int rpart, int col0, int row0,
+                                             int lane, int half) {
+        const int at = i / (NB + MB), block = i % (NB + MB);
+        if (block < NB)
+            a[at][block] = Cols::read(cols, cpart, col0 + 32 * block, READS * half + at, lane);
+        else
+            b[at][block - NB] = RowsOp::read(rows, rpart, row0 + 32 * (block - NB), READS * half + at, lane);
+    }
     template <typename Cols, typename RowsOp>
     __device__ __forceinline__ void read(const char* cols, const char* rows, int cpart, int rpart, int col0, int row0, int lane,
                                          int half) {
 #pragma unroll
-        for (int at = 0; at < READS; ++at) {
+        for (int i = 0; i < LOADS; ++i) read_one<Cols, RowsOp>(i, cols, rows, cpart, rpart, col0, row0, lane, half);
+    }
+    // f(n) behind the n-th product, where its instructions stay.
+    template <typename F>
+    __device__ __forceinline__ void products(f32x16 (&acc)[MB][NB], const F& f) const {
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) a[at][nb] = Cols::read(cols, cpart, col0 + 32 * nb, READS * half + at, lane);
-#pragma unroll
-            for (int mb = 0; mb < MB; ++mb) b[at][mb] = RowsOp::read(rows, rpart, row0 + 32 * mb, READS * half + at, lane);
+        for (int n = 0; n < PRODUCTS; ++n) {
+            const int at = n / (MB * NB), mb = n / NB % MB, nb = n % NB;
+            mma(frag(a[at][nb]), frag(b[at][mb]), acc[mb][nb]);
+            __builtin_amdgcn_sched_barrier(0);
+            f(n);
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
     __device__ __forceinline__ void products(f32x16 (&acc)[MB][NB]) const {
@@ -83,7 +101,6 @@ struct Half {
             }
         }
         if (INTERLEAVE) {
-            constexpr int PRODUCTS = READS * NB * MB, LOADS = READS * (NB + MB);
 #pragma unroll
             for (int i = 0; i < PRODUCTS; ++i) {
                 __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);     // a matrix instruction
@@ -97,7 +114,11 @@ struct Half {
 // Steps begin .. end - 1 with STAGES buffers: copy(s, buffer) sends a step's tiles on their way (COPIES of a wave),
 // read(half, set, buffer) reads half a step, last(buffer) clears what the final step lacks.  A half is read while the
 // one before it is multiplied.
-template <typename Set, int STAGES, int COPIES, typename Copy, typename Read, typename Last, typename Products>
+//   SPREAD: a step's second half has the copies and reads one by one between its products (copy's and read's last
+// argument is which one) instead of all before the first: for one workgroup a unit, whose waves are all at this point at
+// once.  256 x 256, 50176 rows x 1024 -> 4096: 426 -> 401 us forward, 428 -> 416 back.  With two workgroups the other's
+// products fill the time, and the products between the copies come late: 128 x 128, 449 -> 479, 459 -> 501.
+template <typename Set, int STAGES, int COPIES, bool SPREAD, typename Copy, typename Read, typename Last, typename Products>
 __device__ __forceinline__ void run_steps(int begin, int end, bool partial, const Copy& copy, const Read& read, const Last& last,
                                           const Products& products) {
     if (begin >= end) return;
@@ -128,9 +149,21 @@ __device__ __forceinline__ void run_steps(int begin, int end, bool partial, cons
             last(next);
             meet();
         }
-        if (s + STAGES < end) copy(s + STAGES, here);
-        if (s + 1 < end) read(0, p, next);
-        products(q);
+        if constexpr (SPREAD) {
+            const bool more = s + STAGES < end, whole = more && !(partial && s + STAGES + 1 == end);
+            if (more && !whole) copy(s + STAGES, here);
+            products(q, [&](int n) {   // behind the last step, reads of a buffer that nothing is made of
+#pragma unroll
+                for (int i = n * Set::LOADS / Set::PRODUCTS; i < (n + 1) * Set::LOADS / Set::PRODUCTS; ++i) read(0, p, next, i);
+#pragma unroll
+                for (int i = n * COPIES / Set::PRODUCTS; i < (n + 1) * COPIES / Set::PRODUCTS; ++i)
+                    if (whole) copy(s + STAGES, here, i);
+            });
+        } else {
+            if (s + STAGES < end) copy(s + STAGES, here);
+            if (s + 1 < end) read(0, p, next);
+            products(q);
+        }
     }
 }
 
@@ -148,7 +181,7 @@ __device__ __forceinline__ float add_terms(const Eight<T>& v) {
 }
 
 // WM x WN waves of MB x NB blocks each.
-template <typename T, bool BACK, int WM, int WN, int MB, int NB, int STAGES>
+template <typename T, bool BACK, int WM, int WN, int MB, int NB, int STAGES, bool SPREAD>
 __global__ void __launch_bounds__(64 * WM * WN, 2) k_product_rows(Args a) {
     constexpr int WAVES = WM * WN, BM = 32 * WM * MB, BN = 32 * WN * NB, TERMS = kStepBytes / (int)sizeof(T);
     using X = Along<T, BM, WAVES>;
@@ -201,27 +234,38 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) k_product_rows(Args a) {
         const uint32_t lds0 = lds_address(lds);
         const int steps = (terms + TERMS - 1) / TERMS;
         const int xpart = X::lane_part(lane), wpart = W::lane_part(lane);
-        run_steps<Set, STAGES, COPIES>(
+        run_steps<Set, STAGES, COPIES, SPREAD>(
             0, steps, terms % TERMS != 0,
-            [&](int s, int buffer) {
+            [&](int s, int buffer, int one = -1) {
                 const uint32_t at = lds0 + (uint32_t)buffer * STAGE;
                 const int left = terms - s * TERMS;
-                xt.copy(at, x + (size_t)s * kStepBytes, left / kVec<T>, wave, lane);
-                if constexpr (BACK)
-                    wt.copy(at + X::kBytes, w + (size_t)s * TERMS * wrow, wrow, left - 1, wave, lane);
-                else
-                    wt.copy(at + X::kBytes, w + (size_t)s * kStepBytes, left / kVec<T>, wave, lane);
+                const char* xs = x + (size_t)s * kStepBytes;
+                const char* ws = w + (BACK ? (size_t)s * TERMS * wrow : (size_t)s * kStepBytes);
+                if (one >= X::kCopies) {
+                    wt.copy_one(one - X::kCopies, at + X::kBytes, ws, wave);
+                } else if (one >= 0) {
+                    xt.copy_one(one, at, xs, wave);
+                } else {
+                    xt.copy(at, xs, left / kVec<T>, wave, lane);
+                    if constexpr (BACK)
+                        wt.copy(at + X::kBytes, ws, wrow, left - 1, wave, lane);
+                    else
+                        wt.copy(at + X::kBytes, ws, left / kVec<T>, wave, lane);
+                }
             },
-            [&](int half, Set& set, int buffer) {
+            [&](int half, Set& set, int buffer, int one = -1) {
                 const char* at = lds + buffer * STAGE;
-                set.template read<W, X>(at + X::kBytes, at, wpart, xpart, 32 * NB * wn, 32 * MB * wm, lane, half);
+                if (one >= 0)
+                    set.template read_one<W, X>(one, at + X::kBytes, at, wpart, xpart, 32 * NB * wn, 32 * MB * wm, lane, half);
+                else
+                    set.template read<W, X>(at + X::kBytes, at, wpart, xpart, 32 * NB * wn, 32 * MB * wm, lane, half);
             },
             [&](int buffer) {
                 char* at = lds + buffer * STAGE;
                 X::clear(at, terms % TERMS / kVec<T>);
                 W::clear(at + X::kBytes, BACK ? terms % TERMS : terms % TERMS / kVec<T>);
             },
-            [&](const Set& set) { set.products(acc); });
+            [&](const Set& set, const auto&... between) { set.products(acc, between...); });
         meet();   // no tile is read any more
     }
 #pragma unroll
@@ -269,7 +313,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) k_product_weights(Args a) {
     xt.place(xrow, min(a.K - col0, BN) / kVec<T> - 1, wave, lane);
     const uint32_t lds0 = lds_address(lds);
     const int gpart = G::lane_part(lane), xpart = X::lane_part(lane);
-    run_steps<Set, STAGES, COPIES>(
+    run_steps<Set, STAGES, COPIES, false>(
         begin, end, end == all && count % TERMS != 0,
         [&](int s, int buffer) {
             const uint32_t at = lds0 + (uint32_t)buffer * STAGE;
@@ -341,25 +385,40 @@ __global__ void __launch_bounds__(256) k_product_join(Args a, long long n, long 
 
 constexpr int kTile = 128;   // rows and columns of a workgroup's tile
 
-template <typename T, bool BACK, int WM, int WN, int MB, int NB, int STAGES>
+template <typename T, bool BACK, int WM, int WN, int MB, int NB, int STAGES, bool SPREAD = false>
 int launch_rows(Args a, hipStream_t st) {
     constexpr int BM = 32 * WM * MB, BN = 32 * WN * NB;
     a.slots = row_slots(a.R, a.E, BM);
     const long long groups = a.slots * (((BACK ? a.K : a.N) + BN - 1) / BN);
     if (groups > (1 << 23)) return WTC_ESHAPE;
-    hipLaunchKernelGGL((k_product_rows<T, BACK, WM, WN, MB, NB, STAGES>), dim3((unsigned)groups), dim3(64 * WM * WN), 0, st, a);
+    hipLaunchKernelGGL((k_product_rows<T, BACK, WM, WN, MB, NB, STAGES, SPREAD>), dim3((unsigned)groups), dim3(64 * WM * WN), 0,
+                       st, a);
     return hipGetLastError() == hipSuccess ? WTC_OK : WTC_EHIP;
 }
+// The tile, by what the rounds of workgroups take.  Measured (us, 8 experts, bfloat16; rows x terms -> columns):
+//   256 x 256 against 128 x 128 where the estimates are near each other: 12544 x 1024 -> 1024 29.0 and 33.6, 16384 49.4 and
+// 44.4, 24000 52.4 and 61.1, 32768 77.2 and 74.9, 50176 106.6 and 107.2; 12544 x 512 -> 2048 33.6 and 35.7; 25088 x 2048 ->
+// 512 49.3 and 59.0, 40000 91.6 and 87.5; far from there, 50176 x 1024 -> 4096 401 and 451, 4096 x 1024 -> 1024 25.4 and
+// 18.4.  The worst found is 8192 x 1024 -> 1024: 29.6 taken, 26.5.
+//   128 x 128 against 64 x 128 around 384 tiles: 216 of them 25.1 and 23.8, 320 17.5 and 18.1, 384 11.3 and 11.1, 424 31.4
+// and 45.5; float32 200 84.6 and 80.3, 432 45.6 and 52.0.
+//   64 x 128 against 32 x 128 around 256 tiles: 160 of them 20.5 and 16.9, 192 11.7 and 11.2, 320 14.0 and 17.8; float32
+// 128 19.1 and 15.3, 160 37.4 and 38.5, 320 30.8 and 32.6.  Few tiles wait for their weights: four stages of the smallest
+// 6.9 us for 98 rows x 512 -> 2048, two 8.9, eight 7.8.
 template <typename T, bool BACK>
 int run_rows_way(const Args& a, hipStream_t st) {
-    const int columns = BACK ? a.K : a.N;
+    const int columns = BACK ? a.K : a.N, steps = ((BACK ? a.N : a.K) + 63) / 64;
     auto tiles = [&](int rows, int cols) {   // about: an expert's last tile is half full in the mean
         const long long full = a.R / rows;
         return (full + (full < a.E ? full : a.E)) * ((columns + cols - 1) / cols);
     };
-    const long long big = tiles(256, 256), middle = tiles(128, 128);
-    if constexpr (sizeof(T) == 2 && !BACK)   // back, the larger tile would spill a register
-        if (big >= 256 && 5 * ((big + 255) / 256) <= 3 * ((middle + 511) / 512)) return launch_rows<T, BACK, 2, 4, 4, 2, 2>(a, st);
+    const long long middle = tiles(128, 128);
+    if constexpr (sizeof(T) == 2) {
+        // microseconds: a round of one large tile a unit takes 1.55 a step and 3.5 for its beginning and end, and the last
+        // round is paid whole; 512 of the smaller, two a unit, take 1.06 and 1.2, and a quarter of that where they run out
+        const double large = (double)((tiles(256, 256) + 255) / 256) * (1.55 * steps + 3.5);
+        if (middle > 512 && large <= (middle / 512.0 + 0.25) * (1.06 * steps + 1.2)) return launch_rows<T, BACK, 2, 4, 4, 2, 2, true>(a, st);
+    }
     if (middle >= 384) return launch_rows<T, BACK, 2, 2, 2, 2, 2>(a, st);
     if (tiles(64, 128) >= 256) return launch_rows<T, BACK, 2, 2, 1, 2, 2>(a, st);
     return launch_rows<T, BACK, 1, 4, 1, 1, 4>(a, st);

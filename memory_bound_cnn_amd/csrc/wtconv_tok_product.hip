@@ -7,12 +7,15 @@
 namespace wtc {
 namespace {
 
-// Workgroups that share the rows of one tile of dW: where there are fewer tiles
-// than places for them on the chip, and the experts' rows are long.
+// Workgroups that share the rows of one tile of dW: to about 768 of them, which also evens out experts of unequal size,
+// if each has 1024 rows (float32: 171, of six products) to pay for the partial sums' way through memory.  Measured (us, 8
+// experts, whole / in 2 / in 3 / in 4): 512 tiles bfloat16, 12544 rows 49.5 / 53.0, 16384 63.1 / 60.3 / 68, 32768 121 / 93.7 /
+// 99.6 / 126, 50176 186 / 147 / 158 / 165; 768 tiles, 25000 rows of 4 experts 159 / 205; 1024 tiles, 100000 rows 488 / 485 /
+// 507; 256 tiles float32, 2048 rows 39.1 / 34.0 / 37.4, 6007 94.9 / 62.5 / 55.3 / 58.5, 12544 188 / 112 / 92.4 / 94.4.
 int splits_of(const wtc_expert_desc* d) {
     const long long tiles = (long long)d->E * ((d->K + 127) / 128) * ((d->N + 127) / 128);
-    const long long most = d->R / d->E / 512, want = (512 + tiles - 1) / tiles;
-    return (int)(want < most ? want : most < 1 ? 1 : most);
+    const long long most = d->R / d->E * (d->dtype == WTC_BF16 ? 1 : 6) / 1024, want = (768 + tiles / 2) / tiles;
+    return (int)(want < most ? (want < 1 ? 1 : want) : most < 1 ? 1 : most);
 }
 
 product::Args args_of(const wtc_expert_desc* d, const int* cu) {

@@ -583,6 +583,13 @@ def test_expert_linear(counts, K, N, dtype):
 
 
 @BOTH
+def test_expert_linear_of_the_largest_tiles(dtype):
+    """Enough tiles for those of 256 x 256 in both directions (bfloat16), with a part of a step, of a tile's rows and of its
+    columns left over, experts of one row and of none; in float32 the weights' gradient of three parts."""
+    check_product(*product_case([1, 3000, 0, 2543, 128, 4000, 257, 2615], 1000, 1016, dtype, bias=True, seed=77), dtype)
+
+
+@BOTH
 @pytest.mark.parametrize("counts,K,N", [([30000, 2769], 64, 256), ([5000, 0, 9000, 2400], 264, 1032), ([700, 900, 2000], 1096, 512),
                                         ([3000], 64, 64), ([9000], 72, 40)])
 def test_expert_linear_large(counts, K, N, dtype):
