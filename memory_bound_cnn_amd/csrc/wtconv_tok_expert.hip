@@ -6,14 +6,20 @@
 // sum:     y[t] = sum_j w[t, j] rows[slot[t, j]]   (gather's gradient with w = 1)
 // and sum's gradient: drows[slot[t, j]] = w[t, j] dy[t], dw[t, j] = dy[t] . rows[slot[t, j]].
 //
-// The sort ranks 64 pairs at a time: the lanes with a lane's expert are found
-// by one ballot a bit of the expert's number, and a wave walks a run of pairs of
-// its own with its experts' next places in shared memory, so that it meets no
-// other wave.  Up to kOneGroup pairs one workgroup does it all; beyond, a first
-// kernel counts each run, a second sums the counts and a third places.
+// The sort counts each run of pairs in shared memory (whole numbers, whose order
+// does not show), sums the counts, and ranks 64 pairs at a time: the lanes with a
+// lane's expert are found by one ballot a bit of the expert's number, and a wave
+// walks a run of its own with its experts' next places in shared memory, so that
+// it meets no other wave.  Up to kOneGroup pairs one workgroup does it all;
+// beyond, a first kernel counts, a second sums the counts of each expert and a
+// third places.  Bound by latency: 50176 pairs of 8 experts 2.9 + 2.4 + 3.9 us,
+// 265638 of 118 3.9 + 3.5 + 6.2, one workgroup 3.7 (64 pairs) to 7.9 (6000).
 //   The others are copies bound by device memory, by token: a token's row is
 // read (or written) once for its k.  Rows of no pair, which follow those of the
-// last expert, get zeros.
+// last expert, get zeros.  25088 x 384 bf16, two rows a token: gather 14.7 us
+// (58 MB, 3.9 TB/s), sum 14.6, its gradient 18.6 (96 MB, 5.2 TB/s); 20011 x 771
+// float32, three rows: 43, 62 and 98 us (247, 247 and 432 MB: 5.7, 4.0 and 4.4
+// TB/s; rows of 3084 bytes begin inside a cache line, and sum's are anywhere).
 #include <hip/hip_runtime.h>
 
 #include "wtc_tok_device.h"
@@ -23,13 +29,15 @@ namespace wtc {
 namespace {
 
 // ------------------------------------------------------------------ order
-constexpr int kOneGroup = 8192, kMostUnits = 1024;
+// One workgroup or three kernels (us, 8 / 64 / 512 experts): 4096 pairs 6.2 / 6.4 / 7.5 and 7.6 / 7.8 / 8.9, 6000 7.5 / 8.3 /
+// 9.9 and 7.6 / 8.1 / 9.1, 8192 9.1 / 9.6 / 11.7 and 8.0 / 8.2 / 9.2, 32768 27.5 / 29 / 35 and 7.9 / 8.4 / 10.1.
+constexpr int kOneGroup = 6144, kMostUnits = 1024;
 
 struct OrderArgs {
     const int* experts;
     int *slot, *pair, *cu;
-    int* counts;               // [E][units]: a run's pairs of an expert, then where they begin
-    int n, E, bits, units, run;   // run: pairs of a unit, a multiple of 64
+    int *counts, *totals;      // [E][units]: a unit's pairs of an expert, then where they begin; [E]
+    int n, E, bits, units, run;   // run: pairs of a wave, a multiple of 64
 };
 
 // Lanes with this lane's expert, of those that have one.
@@ -56,10 +64,13 @@ __device__ __forceinline__ void walk(const OrderArgs& a, int first, int last, in
         f(p, e, there, same, lanes_below(same));
     }
 }
+// Pairs of each expert in a run, added to counts in shared memory: whole numbers, in any order.
 __device__ __forceinline__ void count_run(const OrderArgs& a, int first, int last, int lane, int* mine) {
-    walk(a, first, last, lane, [&](int, int e, bool there, uint64_t same, int rank) {
-        if (there && rank == 0) mine[e] += __builtin_popcountll(same);
-    });
+#pragma unroll 4
+    for (int p = first + lane; p < last; p += 64) {
+        const int e = a.experts[p];
+        if (e >= 0 && e < a.E) atomicAdd(mine + e, 1);
+    }
 }
 __device__ __forceinline__ void place_run(const OrderArgs& a, int first, int last, int lane, int* mine) {
     walk(a, first, last, lane, [&](int p, int e, bool there, uint64_t same, int rank) {
@@ -72,8 +83,8 @@ __device__ __forceinline__ void place_run(const OrderArgs& a, int first, int las
         if (there) a.pair[at] = p;
     });
 }
-// Exclusive sums over the experts by a workgroup of 1024: thread e has expert
-// e's total; all get the sum of all.
+// Exclusive sums over the threads of a workgroup of WAVES waves; all get the sum of all.
+template <int WAVES>
 __device__ __forceinline__ int expert_starts(int total, int* sums, int& all) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     int v = total;
@@ -86,7 +97,7 @@ __device__ __forceinline__ int expert_starts(int total, int* sums, int& all) {
     __syncthreads();
     int before = 0;
     all = 0;
-    for (int w = 0; w < 16; ++w) {
+    for (int w = 0; w < WAVES; ++w) {
         if (w < wave) before += sums[w];
         all += sums[w];
     }
@@ -111,7 +122,7 @@ __global__ void __launch_bounds__(1024) k_order_one(OrderArgs a) {
             count[w * a.E + e] = total;
             total += v;
         }
-    const int start = expert_starts(total, sums, all);
+    const int start = expert_starts<16>(total, sums, all);
     if (e < a.E) {
         a.cu[e] = start;
         for (int w = 0; w < 16; ++w) count[w * a.E + e] += start;
@@ -122,62 +133,86 @@ __global__ void __launch_bounds__(1024) k_order_one(OrderArgs a) {
     for (int r = all + threadIdx.x; r < a.n; r += 1024) a.pair[r] = -1;
 }
 
-__global__ void __launch_bounds__(64) k_order_count(OrderArgs a) {
-    extern __shared__ int count[];
-    const int lane = threadIdx.x, unit = blockIdx.x;
-    for (int e = lane; e < a.E; e += 64) count[e] = 0;
-    __syncthreads();
-    const int first = (int)min((long long)unit * a.run, (long long)a.n), last = (int)min((long long)first + a.run, (long long)a.n);
-    count_run(a, first, last, lane, count);
-    __syncthreads();
-    for (int e = lane; e < a.E; e += 64) a.counts[(size_t)e * a.units + unit] = count[e];
+// The run of one of a unit's four waves.
+struct Run {
+    int first, last;
+};
+__device__ __forceinline__ Run run_of(const OrderArgs& a, int wave) {
+    const long long first = min(((long long)blockIdx.x * 4 + wave) * a.run, (long long)a.n);
+    return {(int)first, (int)min(first + a.run, (long long)a.n)};
 }
-// Counts to the places where the runs' pairs of an expert begin, from the expert's own first; cu.
-__global__ void __launch_bounds__(1024) k_order_sum(OrderArgs a) {
-    __shared__ int totals[WTC_EXPERTS_MAX], sums[16];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int e = wave; e < a.E; e += 16) {
-        int* row = a.counts + (size_t)e * a.units;
-        int4 v[kMostUnits / 256];   // of four units a lane, all on their way at once
+__global__ void __launch_bounds__(256) k_order_count(OrderArgs a) {
+    extern __shared__ int count[];   // [E]
+    const int lane = threadIdx.x & 63;
+    for (int e = threadIdx.x; e < a.E; e += 256) count[e] = 0;
+    __syncthreads();
+    const Run r = run_of(a, threadIdx.x >> 6);
+    count_run(a, r.first, r.last, lane, count);
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += 256) a.counts[(size_t)e * a.units + blockIdx.x] = count[e];
+}
+// Counts of an expert to the places, among the expert's own, where each unit's pairs of it begin; its total.
+__global__ void __launch_bounds__(64) k_order_sum(OrderArgs a) {
+    const int lane = threadIdx.x, e = blockIdx.x;
+    int* row = a.counts + (size_t)e * a.units;
+    int4 v[kMostUnits / 256];   // of four units a lane, all on their way at once
 #pragma unroll
-        for (int i = 0; i < kMostUnits / 256; ++i) {
-            const int u = 256 * i + 4 * lane;
-            v[i] = u < a.units ? *reinterpret_cast<const int4*>(row + u) : make_int4(0, 0, 0, 0);
-        }
-        int before = 0;
-#pragma unroll
-        for (int i = 0; i < kMostUnits / 256; ++i) {
-            const int u = 256 * i + 4 * lane, s = v[i].x + v[i].y + v[i].z + v[i].w;
-            if (256 * i >= a.units) break;
-            int up = s;
-#pragma unroll
-            for (int o = 1; o < 64; o <<= 1) {
-                const int t = __shfl_up(up, o);
-                if (lane >= o) up += t;
-            }
-            const int at = before + up - s;
-            if (u < a.units)
-                *reinterpret_cast<int4*>(row + u) = make_int4(at, at + v[i].x, at + v[i].x + v[i].y, at + v[i].x + v[i].y + v[i].z);
-            before += __shfl(up, 63);
-        }
-        if (lane == 0) totals[e] = before;
+    for (int i = 0; i < kMostUnits / 256; ++i) {
+        const int u = 256 * i + 4 * lane;
+        v[i] = u < a.units ? *reinterpret_cast<const int4*>(row + u) : make_int4(0, 0, 0, 0);
     }
-    __syncthreads();
-    const int e = threadIdx.x;
-    int all;
-    const int start = expert_starts(e < a.E ? totals[e] : 0, sums, all);
-    if (e < a.E) a.cu[e] = start;
-    if (e == 0) a.cu[a.E] = all;
+    int before = 0;
+#pragma unroll
+    for (int i = 0; i < kMostUnits / 256; ++i) {
+        const int u = 256 * i + 4 * lane, s = v[i].x + v[i].y + v[i].z + v[i].w;
+        if (256 * i >= a.units) break;
+        int up = s;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int t = __shfl_up(up, o);
+            if (lane >= o) up += t;
+        }
+        const int at = before + up - s;
+        if (u < a.units)
+            *reinterpret_cast<int4*>(row + u) = make_int4(at, at + v[i].x, at + v[i].x + v[i].y, at + v[i].x + v[i].y + v[i].z);
+        before += __shfl(up, 63);
+    }
+    if (lane == 0) a.totals[e] = before;
 }
-__global__ void __launch_bounds__(64) k_order_place(OrderArgs a) {
-    extern __shared__ int next[];
-    const int lane = threadIdx.x, unit = blockIdx.x;
-    for (int e = lane; e < a.E; e += 64) next[e] = a.cu[e] + a.counts[(size_t)e * a.units + unit];
+__global__ void __launch_bounds__(256) k_order_place(OrderArgs a) {
+    extern __shared__ int next[];   // [4][E]
+    __shared__ int sums[4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int e = threadIdx.x; e < 4 * a.E; e += 256) next[e] = 0;
+    const Run r = run_of(a, wave);
     __syncthreads();
-    const int first = (int)min((long long)unit * a.run, (long long)a.n), last = (int)min((long long)first + a.run, (long long)a.n);
-    place_run(a, first, last, lane, next);
-    for (long long r = (long long)a.cu[a.E] + unit * 64 + lane; r < a.n; r += (long long)a.units * 64) a.pair[r] = -1;
+    count_run(a, r.first, r.last, lane, next + wave * a.E);
+    // every unit finds the experts' first places for itself, two experts a thread
+    int total[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) total[i] = 2 * (int)threadIdx.x + i < a.E ? a.totals[2 * threadIdx.x + i] : 0;
+    int all, start = expert_starts<4>(total[0] + total[1], sums, all);   // the counts are whole behind its barrier
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int e = 2 * (int)threadIdx.x + i;
+        if (e < a.E) {
+            if (blockIdx.x == 0) a.cu[e] = start;
+            int at = start + a.counts[(size_t)e * a.units + blockIdx.x];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const int v = next[w * a.E + e];
+                next[w * a.E + e] = at;
+                at += v;
+            }
+        }
+        start += total[i];
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.cu[a.E] = all;
+    __syncthreads();
+    place_run(a, r.first, r.last, lane, next + wave * a.E);
+    for (long long p = (long long)all + blockIdx.x * 256 + threadIdx.x; p < a.n; p += (long long)a.units * 256) a.pair[p] = -1;
 }
+static_assert(WTC_EXPERTS_MAX <= 512, "two experts a thread");
 
 // ------------------------------------------------------------------ rows
 struct RowsArgs {
@@ -192,16 +227,13 @@ struct RowsArgs {
     FastDiv div;      // by chunks
 };
 
-constexpr int kUnits = 4;   // 16-byte chunks of a thread
-
-// f(token, channel) for the chunks of a workgroup, in the order of memory.
+// f(token, channel) for 16-byte chunks in the order of memory: one a thread, so that as many as possible are on their way
+// (four one after another: 25088 x 384 bf16 gather 16.5 us and 14.5 so, 2213 x 2005 sum 18.8 and 10.3).
 template <typename T, typename F>
 __device__ __forceinline__ void each_chunk(const RowsArgs& a, const F& f) {
-    const long long u0 = (long long)blockIdx.x * (256 * kUnits), t0 = u0 / a.chunks;
-    const int rest = (int)(u0 - t0 * a.chunks);
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-        const int v = rest + i * 256 + (int)threadIdx.x, q = fdiv(v, a.div);
+    for (long long u0 = (long long)blockIdx.x * 256; u0 < a.T * a.chunks; u0 += (long long)gridDim.x * 256) {
+        const long long t0 = u0 / a.chunks;
+        const int v = (int)(u0 - t0 * a.chunks) + (int)threadIdx.x, q = fdiv(v, a.div);
         if (t0 + q < a.T) f(t0 + q, (v - q * a.chunks) * kVec<T>);
     }
 }
@@ -322,7 +354,10 @@ RowsArgs rows_args(const wtc_rows_desc* d, const int* slot, const int* cu) {
     a.div = make_div(a.chunks);
     return a;
 }
-dim3 chunk_grid(const RowsArgs& a) { return dim3((unsigned)((a.T * a.chunks + 256 * kUnits - 1) / (256 * kUnits))); }
+dim3 chunk_grid(const RowsArgs& a) {
+    const long long blocks = (a.T * a.chunks + 255) / 256;
+    return dim3((unsigned)(blocks < (1 << 23) ? blocks : 1 << 23));
+}
 
 struct OrderPlan {
     int units, run;
@@ -330,19 +365,21 @@ struct OrderPlan {
 OrderPlan order_plan(long long n, int E) {
     OrderPlan p;
     if (n <= kOneGroup) {
-        p.units = 16;
-    } else {   // counts of at most 2^15 numbers, for one workgroup to sum
-        const long long most = 32768 / E, runs = (n + 63) / 64, least = most < 32 ? 32 : most > kMostUnits ? kMostUnits : most;
-        p.units = (int)(((least < runs ? least : runs) + 3) / 4 * 4);   // counts are summed four at a time
+        p.units = 16;   // waves of the one workgroup
+        p.run = (int)(((n + 15) / 16 + 63) / 64 * 64);
+    } else {   // a unit has four waves; counts are summed four at a time
+        const long long most = (n + 255) / 256;
+        p.units = (int)(((most < kMostUnits ? most : kMostUnits) + 3) / 4 * 4);
+        const long long waves = 4LL * p.units;
+        p.run = (int)(((n + waves - 1) / waves + 63) / 64 * 64);
     }
-    p.run = (int)(((n + p.units - 1) / p.units + 63) / 64 * 64);
     return p;
 }
 
 }  // namespace
 
 size_t order_workspace(long long n, int E) {
-    return n <= kOneGroup ? 0 : (size_t)E * order_plan(n, E).units * sizeof(int);
+    return n <= kOneGroup ? 0 : (size_t)E * (order_plan(n, E).units + 1) * sizeof(int);
 }
 
 int launch_expert_order(long long n, int E, const int* experts, int* slot, int* pair, int* cu, void* workspace, void* stream) {
@@ -355,9 +392,10 @@ int launch_expert_order(long long n, int E, const int* experts, int* slot, int* 
     if (n <= kOneGroup) {
         hipLaunchKernelGGL(k_order_one, dim3(1), dim3(1024), 16 * E * sizeof(int), st, a);
     } else {
-        hipLaunchKernelGGL(k_order_count, dim3((unsigned)p.units), dim3(64), E * sizeof(int), st, a);
-        hipLaunchKernelGGL(k_order_sum, dim3(1), dim3(1024), 0, st, a);
-        hipLaunchKernelGGL(k_order_place, dim3((unsigned)p.units), dim3(64), E * sizeof(int), st, a);
+        a.totals = a.counts + (size_t)E * a.units;
+        hipLaunchKernelGGL(k_order_count, dim3((unsigned)p.units), dim3(256), E * sizeof(int), st, a);
+        hipLaunchKernelGGL(k_order_sum, dim3((unsigned)E), dim3(64), 0, st, a);
+        hipLaunchKernelGGL(k_order_place, dim3((unsigned)p.units), dim3(256), 4 * E * sizeof(int), st, a);
     }
     return hipGetLastError() == hipSuccess ? WTC_OK : WTC_EHIP;
 }
@@ -387,8 +425,9 @@ int launch_rows_sum(const wtc_rows_desc* d, const void* rows, const float* weigh
 namespace {
 template <typename T>
 void run_sum_back(const RowsArgs& a, hipStream_t st) {
-    // as few lanes as leave no more than four steps each
-    const int G = a.chunks <= 16 ? 4 : a.chunks <= 64 ? 16 : 64;
+    // as few lanes as leave no more than four steps each, 4, 16 or 64 of them (us): 48 chunks (25088 x 384 bf16) by 16 lanes
+    // 18.6, by 64 22.2; 9 chunks (44273 x 35 float32, six rows a token) by 4 30.9, by 16 27.9
+    const int G = a.chunks <= 4 ? 4 : a.chunks <= 64 ? 16 : 64;
     const long long blocks = (a.T * G + 255) / 256;
     const dim3 grid((unsigned)(blocks < (1 << 20) ? blocks : 1 << 20));
     if (G == 4)
