@@ -77,8 +77,15 @@ __device__ __forceinline__ Frag<float> frag(const Eight<float>& x) {
 __device__ __forceinline__ void mma(const u32x4& a, const u32x4& b, f32x16& c) {
     c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
-__device__ __forceinline__ void mma(const Frag<uint16_t>& a, const Frag<uint16_t>& b, f32x16& c) { mma(a.v, b.v, c); }
-__device__ __forceinline__ void mma(const Frag<float>& a, const Frag<float>& b, f32x16& c) {
+__device__ __forceinline__ void mma(const u32x4& a, const u32x4& b, f32x4& c) {
+    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+template <typename C>
+__device__ __forceinline__ void mma(const Frag<uint16_t>& a, const Frag<uint16_t>& b, C& c) {
+    mma(a.v, b.v, c);
+}
+template <typename C>
+__device__ __forceinline__ void mma(const Frag<float>& a, const Frag<float>& b, C& c) {
     mma(a.v[0], b.v[2], c);   // the smallest first
     mma(a.v[2], b.v[0], c);
     mma(a.v[1], b.v[1], c);
@@ -248,14 +255,15 @@ __device__ __forceinline__ int segment_begin(const int* cu, int E, int R, int s)
     return min(max(cu[s - 1], 0), R);
 }
 // Segment s may use the tiles from floor(begin / SIZE) + s on, which leaves it
-// ceil(rows / SIZE) at least; whose a tile is, is found by searching cu, 63
-// segments at a time.  count = 0: a tile of none.
-template <int SIZE>
+// ceil(rows / SIZE) at least; or, where there are fewer rows than that, a tile is
+// numbered by its first row (BY_ROW).  Whose a tile is, is found by searching cu,
+// 63 segments at a time.  count = 0: a tile of none.
+template <int SIZE, bool BY_ROW = false>
 __device__ __forceinline__ Rows find_rows(const int* cu, int E, int R, int slot, int lane) {
     int lo = 0, hi = E + 2, b, e;   // the segment is in lo .. hi - 1
     for (;;) {
         const int step = (hi - lo + 62) / 63, s = lo + lane * step, begin = segment_begin(cu, E, R, min(s, hi));
-        const int n = __builtin_popcountll(__builtin_amdgcn_ballot_w64(s < hi && begin / SIZE + s <= slot)), k = n > 0 ? n - 1 : 0;
+        const int n = __builtin_popcountll(__builtin_amdgcn_ballot_w64(s < hi && (BY_ROW ? begin : begin / SIZE + s) <= slot)), k = n > 0 ? n - 1 : 0;
         lo += k * step;
         hi = min(hi, lo + step);
         if (step == 1) {   // the segment's bounds are two lanes' own
@@ -264,7 +272,7 @@ __device__ __forceinline__ Rows find_rows(const int* cu, int E, int R, int slot,
             break;
         }
     }
-    const int tile = slot - (b / SIZE + lo);
+    const int tile = BY_ROW ? ((slot - b) % SIZE == 0 ? (slot - b) / SIZE : -1) : slot - (b / SIZE + lo);
     Rows r;
     r.expert = lo == 0 || lo == E + 1 ? -1 : lo - 1;
     r.start = b + tile * SIZE;

@@ -277,6 +277,74 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) k_product_rows(Args a) {
     }
 }
 
+// Forward, of few rows: 16 of them by 16 columns, whose terms WAVES waves share.  Nothing is read twice in a tile, so the
+// operands come straight into registers, AHEAD reads of 32 terms on their way while those before are multiplied; the waves'
+// sums are added in their order.  A lane has row (column) lane % 16 and terms 8 (lane / 16) .. of a read.
+template <typename T, int WAVES, bool BY_ROW>
+__global__ void __launch_bounds__(64 * WAVES) k_product_few(Args a) {
+    constexpr int AHEAD = 16 / (int)sizeof(T), SIDE = 16, READ = 32;
+    __shared__ __align__(16) f32x4 sums[WAVES][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), part = 8 * (lane / SIDE);
+    const int tiles = (a.N + SIDE - 1) / SIDE, col0 = (int)(blockIdx.x % tiles) * SIDE;
+    const Rows r = find_rows<SIDE, BY_ROW>(a.cu, a.E, a.R, (int)(blockIdx.x / tiles), lane);
+    if (r.count == 0) return;
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    if (r.expert >= 0) {
+        const T* x = static_cast<const T*>(a.x) + (r.start + min(lane % SIDE, r.count - 1)) * a.x_stride;
+        const T* w = static_cast<const T*>(a.w) + ((size_t)r.expert * a.N + min(col0 + lane % SIDE, a.N - 1)) * a.K;
+        const int reads = (a.K + READ - 1) / READ, begin = reads * wave / WAVES, end = reads * (wave + 1) / WAVES;
+        Eight<T> xn[AHEAD], wn[AHEAD];
+        auto fetch = [&](int s0) {
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                const int at = min(READ * (s0 + k) + part, a.K - 8);   // past the end: the last terms that are there
+#pragma unroll
+                for (int u = 0; u < (int)sizeof(T) / 2; ++u) {
+                    wn[k].u[u] = *reinterpret_cast<const u32x4*>(w + at + u * kVec<T>);
+                    xn[k].u[u] = *reinterpret_cast<const u32x4*>(x + at + u * kVec<T>);
+                }
+            }
+        };
+        if (begin < end) fetch(begin);
+        for (int s0 = begin; s0 < end; s0 += AHEAD) {
+            Eight<T> xs[AHEAD], ws[AHEAD];
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                const bool there = s0 + k < end && READ * (s0 + k) + part < a.K;
+#pragma unroll
+                for (int u = 0; u < (int)sizeof(T) / 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        ws[k].u[u][i] = there ? wn[k].u[u][i] : 0u;
+                        xs[k].u[u][i] = there ? xn[k].u[u][i] : 0u;
+                    }
+            }
+            if (s0 + AHEAD < end) fetch(s0 + AHEAD);
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) mma(frag(ws[k]), frag(xs[k]), acc);
+        }
+        sums[wave][lane] = acc;
+    }
+    __syncthreads();
+    const int row = lane % SIDE, col = col0 + part / 2;
+    if (wave > 0 || row >= r.count || col >= a.N) return;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    if (r.expert >= 0) {
+        if (a.b) {
+            float b[4];
+            load_four(static_cast<const T*>(a.b) + (size_t)r.expert * a.N, col, b);
+            v = f32x4{b[0], b[1], b[2], b[3]};
+        }
+#pragma unroll
+        for (int k = 0; k < WAVES; ++k) v += sums[k][lane];
+    }
+    T* to = static_cast<T*>(a.y) + (long long)(r.start + row) * a.N + col;
+    if constexpr (sizeof(T) == 2)
+        *reinterpret_cast<u32x2*>(to) = u32x2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
+    else
+        *reinterpret_cast<f32x4*>(to) = v;
+}
+
 template <typename T, int WM, int WN, int MB, int NB, int STAGES>
 __global__ void __launch_bounds__(64 * WM * WN, 2) k_product_weights(Args a) {
     constexpr int WAVES = WM * WN, BM = 32 * WM * MB, BN = 32 * WN * NB, TERMS = kStepBytes / (int)sizeof(T);
@@ -395,6 +463,17 @@ int launch_rows(Args a, hipStream_t st) {
                        st, a);
     return hipGetLastError() == hipSuccess ? WTC_OK : WTC_EHIP;
 }
+template <typename T>
+int launch_few(const Args& a, long long slots, hipStream_t st) {
+    constexpr int WAVES = 4;
+    const dim3 grid((unsigned)(slots * ((a.N + 15) / 16)));
+    if (slots == a.R)
+        hipLaunchKernelGGL((k_product_few<T, WAVES, true>), grid, dim3(64 * WAVES), 0, st, a);
+    else
+        hipLaunchKernelGGL((k_product_few<T, WAVES, false>), grid, dim3(64 * WAVES), 0, st, a);
+    return hipGetLastError() == hipSuccess ? WTC_OK : WTC_EHIP;
+}
+
 // The tile, by what the rounds of workgroups take.  Measured (us, 8 experts, bfloat16; rows x terms -> columns):
 //   256 x 256 against 128 x 128 where the estimates are near each other: 12544 x 1024 -> 1024 29.0 and 33.6, 16384 49.4 and
 // 44.4, 24000 52.4 and 61.1, 32768 77.2 and 74.9, 50176 106.6 and 107.2; 12544 x 512 -> 2048 33.6 and 35.7; 25088 x 2048 ->
@@ -405,6 +484,11 @@ int launch_rows(Args a, hipStream_t st) {
 //   64 x 128 against 32 x 128 around 256 tiles: 160 of them 20.5 and 16.9, 192 11.7 and 11.2, 320 14.0 and 17.8; float32
 // 128 19.1 and 15.3, 160 37.4 and 38.5, 320 30.8 and 32.6.  Few tiles wait for their weights: four stages of the smallest
 // 6.9 us for 98 rows x 512 -> 2048, two 8.9, eight 7.8.
+//   Forward, tiles of 16 x 16 with the terms shared by four waves, against 32 x 128, by the number of those tiles.  bfloat16:
+// 128 of them (one row x 512 -> 2048) 4.1 and 5.4, 448 (98 x 2048 -> 512) 9.8 and 14.1, 512 (8 x 8192 -> 1024) 22.5 and 47.5,
+// 640 (196 x 2048 -> 512) 13.6 and 14.1, 1024 (392) 17.7 and 14.4; with few terms 64 (4 x 256 -> 256) 4.2 and 5.3, 160 (98)
+// 4.7 and 4.1.  float32: 226 (2 x 88 -> 1808) 4.0 and 5.6, 256 (2 x 512 -> 2048) 4.6 and 14.7, 1017 (98 x 88 -> 1808) 7.4 and
+// 5.9, 1056 (400 x 2048 -> 512) 33.8 and 52.3, 1792 (98 x 512 -> 2048) 14.4 and 16.3, 2240 (1000 x 2048 -> 512) 68 and 52.
 template <typename T, bool BACK>
 int run_rows_way(const Args& a, hipStream_t st) {
     const int columns = BACK ? a.K : a.N, steps = ((BACK ? a.N : a.K) + 63) / 64;
@@ -412,6 +496,11 @@ int run_rows_way(const Args& a, hipStream_t st) {
         const long long full = a.R / rows;
         return (full + (full < a.E ? full : a.E)) * ((columns + cols - 1) / cols);
     };
+    if constexpr (!BACK) {
+        const bool wide = sizeof(T) == 4;
+        const long long slots = row_slots(a.R, a.E, 16), rows = slots < a.R ? slots : a.R, few = rows * ((columns + 15) / 16);
+        if (few <= (a.K >= (wide ? 256 : 512) ? (wide ? 1536 : 640) : (wide ? 256 : 128))) return launch_few<T>(a, rows, st);
+    }
     const long long middle = tiles(128, 128);
     if constexpr (sizeof(T) == 2) {
         // microseconds: a round of one large tile a unit takes 1.55 a step and 3.5 for its beginning and end, and the last

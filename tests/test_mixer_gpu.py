@@ -583,6 +583,17 @@ def test_expert_linear(counts, K, N, dtype):
 
 
 @BOTH
+@pytest.mark.parametrize("counts,K,N", [([1], 2048, 64), ([0, 2, 0, 1], 1000, 72), ([0] * 100 + [1] + [0] * 50 + [2, 0, 1] + [0] * 300, 520, 40),
+                                        ([16, 17, 0, 15], 264, 136), ([33, 1], 72, 24), ([1] * 3, 8, 8), ([3, 2, 4], 4104, 16)])
+def test_expert_linear_of_few_rows(counts, K, N, dtype):
+    """A step of a few sequences: fewer rows than experts or not, rows of no expert on both sides, terms that end inside a
+    read, waves with none."""
+    x, w, b, cu, dy = product_case(counts, K, N, dtype, True, seed=K + N, before=2, after=3)
+    x[:2], x[-3:] = math.nan, math.inf
+    check_product(x, w, b, cu, dy, dtype)
+
+
+@BOTH
 def test_expert_linear_of_the_largest_tiles(dtype):
     """Enough tiles for those of 256 x 256 in both directions (bfloat16), with a part of a step, of a tile's rows and of its
     columns left over, experts of one row and of none; in float32 the weights' gradient of three parts."""
