@@ -80,18 +80,30 @@ __device__ __forceinline__ void mma(const u32x4& a, const u32x4& b, f32x16& c) {
 __device__ __forceinline__ void mma(const u32x4& a, const u32x4& b, f32x4& c) {
     c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
-template <typename C>
-__device__ __forceinline__ void mma(const Frag<uint16_t>& a, const Frag<uint16_t>& b, C& c) {
-    mma(a.v, b.v, c);
+// Sums of products.  Those of float32's lower parts are apart: they are 2^-8 of the others and less, so that their six-fold
+// number of additions does not round the whole.
+template <typename T, typename V>
+struct Sum {
+    V v = {};
+    __device__ __forceinline__ V all() const { return v; }
+};
+template <typename V>
+struct Sum<float, V> {
+    V v = {}, low = {};
+    __device__ __forceinline__ V all() const { return v + low; }
+};
+template <typename V>
+__device__ __forceinline__ void mma(const Frag<uint16_t>& a, const Frag<uint16_t>& b, Sum<uint16_t, V>& c) {
+    mma(a.v, b.v, c.v);
 }
-template <typename C>
-__device__ __forceinline__ void mma(const Frag<float>& a, const Frag<float>& b, C& c) {
-    mma(a.v[0], b.v[2], c);   // the smallest first
-    mma(a.v[2], b.v[0], c);
-    mma(a.v[1], b.v[1], c);
-    mma(a.v[0], b.v[1], c);
-    mma(a.v[1], b.v[0], c);
-    mma(a.v[0], b.v[0], c);
+template <typename V>
+__device__ __forceinline__ void mma(const Frag<float>& a, const Frag<float>& b, Sum<float, V>& c) {
+    mma(a.v[0], b.v[2], c.low);   // the smallest first
+    mma(a.v[2], b.v[0], c.low);
+    mma(a.v[1], b.v[1], c.low);
+    mma(a.v[0], b.v[0], c.v);
+    mma(a.v[0], b.v[1], c.low);
+    mma(a.v[1], b.v[0], c.low);
 }
 
 __device__ __forceinline__ uint32_t lds_address(const void* p) { return (uint32_t)(uintptr_t)(lds_char*)p; }
@@ -314,23 +326,25 @@ __device__ __forceinline__ void load_four(const float* p, int at, float (&v)[4])
     for (int i = 0; i < 4; ++i) v[i] = u[i];
 }
 
-template <typename T, int NB>
+template <typename T, int NB, typename S>
 __device__ __forceinline__ void store_block(char* at, T* out, long long stride, int rows, int columns, int lane,
-                                            const f32x16 (&c)[NB]) {
+                                            const S (&sums)[NB]) {
     constexpr int ROW = kStoreRow<T, NB>, CH = 32 * NB * (int)sizeof(T) / 16;
     asm volatile("" ::: "memory");
     char* p = at + (lane & 31) * ROW + (lane >> 5) * 4 * (int)sizeof(T);
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
+    for (int nb = 0; nb < NB; ++nb) {
+        const f32x16 c = sums[nb].all();
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-            const f32x4 v = {c[nb][4 * g], c[nb][4 * g + 1], c[nb][4 * g + 2], c[nb][4 * g + 3]};
+            const f32x4 v = {c[4 * g], c[4 * g + 1], c[4 * g + 2], c[4 * g + 3]};
             char* to = p + (32 * nb + 8 * g) * (int)sizeof(T);
             if constexpr (sizeof(T) == 2)
                 *reinterpret_cast<u32x2*>(to) = u32x2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
             else
                 *reinterpret_cast<f32x4*>(to) = v;
         }
+    }
     asm volatile("" ::: "memory");   // a wave's own accesses to shared memory stay in order
 #pragma unroll
     for (int i = 0; i < 32 * CH / 64; ++i) {

@@ -74,7 +74,7 @@ struct Half {
     }
     // f(n) behind the n-th product, where its instructions stay.
     template <typename F>
-    __device__ __forceinline__ void products(f32x16 (&acc)[MB][NB], const F& f) const {
+    __device__ __forceinline__ void products(Sum<T, f32x16> (&acc)[MB][NB], const F& f) const {
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int n = 0; n < PRODUCTS; ++n) {
@@ -85,7 +85,7 @@ struct Half {
             __builtin_amdgcn_sched_barrier(0);
         }
     }
-    __device__ __forceinline__ void products(f32x16 (&acc)[MB][NB]) const {
+    __device__ __forceinline__ void products(Sum<T, f32x16> (&acc)[MB][NB]) const {
         // reads and products in turn, or what was to be read is on its way before the first product
         if (!INTERLEAVE) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) k_product_rows(Args a) {
     const bool none = r.expert < 0;
     const size_t expert = none ? 0 : r.expert;
     const int col = col0 + 32 * NB * wn;
-    f32x16 acc[MB][NB] = {};
+    Sum<T, f32x16> acc[MB][NB];
     if (!BACK && !none && a.b) {   // the sums start from the bias
         const T* bias = static_cast<const T*>(a.b) + expert * a.N;
 #pragma unroll
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) k_product_rows(Args a) {
 #pragma unroll
                 for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[mb][nb][4 * g + i] = v[i];
+                    for (int i = 0; i < 4; ++i) acc[mb][nb].v[4 * g + i] = v[i];
             }
     }
     if (!none) {
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(64 * WAVES) k_product_few(Args a) {
     const int tiles = (a.N + SIDE - 1) / SIDE, col0 = (int)(blockIdx.x % tiles) * SIDE;
     const Rows r = find_rows<SIDE, BY_ROW>(a.cu, a.E, a.R, (int)(blockIdx.x / tiles), lane);
     if (r.count == 0) return;
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    Sum<T, f32x4> acc;
     if (r.expert >= 0) {
         const T* x = static_cast<const T*>(a.x) + (r.start + min(lane % SIDE, r.count - 1)) * a.x_stride;
         const T* w = static_cast<const T*>(a.w) + ((size_t)r.expert * a.N + min(col0 + lane % SIDE, a.N - 1)) * a.K;
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(64 * WAVES) k_product_few(Args a) {
 #pragma unroll
             for (int k = 0; k < AHEAD; ++k) mma(frag(ws[k]), frag(xs[k]), acc);
         }
-        sums[wave][lane] = acc;
+        sums[wave][lane] = acc.all();
     }
     __syncthreads();
     const int row = lane % SIDE, col = col0 + part / 2;
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) k_product_weights(Args a) {
     const int first = segment_begin(a.cu, a.E, a.R, e + 1), count = max(segment_begin(a.cu, a.E, a.R, e + 2) - first, 0);
     const int all = (count + TERMS - 1) / TERMS;
     const int begin = (int)((long long)all * split / a.splits), end = (int)((long long)all * (split + 1) / a.splits);
-    f32x16 acc[MB][NB] = {};
+    Sum<T, f32x16> acc[MB][NB];
     float sum[MB] = {};   // of dy's columns: the lane's half of the terms
     const bool sums = a.db && col0 == 0 && wn == 0;
     constexpr int SZ = (int)sizeof(T);
