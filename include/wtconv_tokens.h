@@ -228,10 +228,11 @@ typedef struct {
  * float32 or NULL: h after the sequence's final token (the first token with
  * reverse); a sequence with no token has state[s] there.  cu_seqlens as for
  * attention; tokens of no sequence get zeros.  y [T, C] contiguous.  kept or
- * NULL: what the backward pass needs, wtconv_gated_scan_kept() float32.  h is
- * float32 throughout.  A value that is not finite never reaches another sequence.
- * state and last must not overlap. */
-size_t wtconv_gated_scan_kept(const wtc_scan_desc* d);
+ * NULL: what the backward pass needs, wtconv_gated_scan_kept() bytes.  h is
+ * float32 throughout.  A value that is not finite stays to its sequence's end and
+ * never reaches another.  States and x are to stay below 2^127, as differences of two
+ * are taken.  state and last must not overlap. */
+size_t wtconv_gated_scan_kept(const wtc_scan_desc* d);        /* bytes: 4 for each channel of every 8th token */
 size_t wtconv_gated_scan_workspace(const wtc_scan_desc* d);   /* of both passes; 0 bytes, and NULL is taken, for short packs */
 int wtconv_gated_scan_forward(const wtc_scan_desc* d, const void* x, const void* gate, const int* cu_seqlens,
                               const float* state, void* y, float* last, float* kept, void* workspace, size_t workspace_bytes,
@@ -309,7 +310,10 @@ typedef struct {
 /* y[r] = weight[e] x[r] + bias[e] for the rows cu_experts[e] <= r < cu_experts[e + 1]
  * of each expert, zeros for the rows of none.  weight [E, N, K], bias [E, N] or NULL,
  * y [R, N]: contiguous.  cu_experts [E + 1] int32, non-decreasing; entries are clamped
- * to 0 .. R on the device.  Sums are float32.  All tensors are 16-byte aligned. */
+ * to 0 .. R on the device.  Sums are float32.  All tensors are 16-byte aligned.
+ * float32 factors are taken as three bfloat16 parts: above 3.3895e38 (bfloat16's largest)
+ * they count as infinite, results that an infinity would leave infinite may be NaN, and
+ * below about 2^-110 they keep fewer than 24 bits. */
 int wtconv_expert_linear_forward(const wtc_expert_desc* d, const void* x, const void* weight, const void* bias,
                                  const int* cu_experts, void* y, void* stream);
 /* dx[r] = dy[r] weight[e]; zeros for the rows of no expert.  dx [R, K] contiguous. */

@@ -4,8 +4,15 @@
 //   k_product_rows, back      dx[r] = dy[r] W[e]                 terms N, columns K
 //   k_product_weights         dW[e] = sum_r dy[r] x[r]^T,  db[e] = sum_r dy[r]
 //
-// Bound by the matrix units.  A workgroup's tiles of the two operands are
-// copied to shared memory a step ahead, and read from there half a step ahead, of their products.
+// Bound by the matrix units where there are many rows, and by the weights' way from memory where there are few.  A
+// workgroup's tiles of the two operands are copied to shared memory a step ahead, and read from there half a step ahead,
+// of their products.  Measured: 50176 rows of 8 uneven experts, 1024 -> 4096, bfloat16: 401 to 452 us forward (1050 to 930
+// TFLOP/s), 416 to 469 for the input's gradient, 450 to 525 for the weights', from card to card and with how warm it is (a
+// library product of the same size and one expert: 383, 429 and 594); matrix units busy 60, 68 and 49 % of the time. The
+// copies' way is what holds the large tiles back: without them (timed alone, on tiles that do not change) the loop runs at
+// 1200 to 1300 TFLOP/s, at the clocks that power allows. float32, 6007 rows of 5 experts, 392 -> 1544: 78, 96 and 88 + 8 us
+// (101, 82 and 83 TFLOP/s; the float32 matrix instructions reach 153 at best), where splitting the factors in three takes
+// the vector units 54 to 59 % of the time and the products the matrix units 37 to 46, side by side for little of it.
 #pragma once
 
 #include <limits.h>
@@ -180,9 +187,9 @@ __device__ __forceinline__ float add_terms(const Eight<T>& v) {
     return s;
 }
 
-// WM x WN waves of MB x NB blocks each.
+// WM x WN waves of MB x NB blocks each; three workgroups a unit of the tiles of 64 x 128, as many as shared memory holds.
 template <typename T, bool BACK, int WM, int WN, int MB, int NB, int STAGES, bool SPREAD>
-__global__ void __launch_bounds__(64 * WM * WN, 2) k_product_rows(Args a) {
+__global__ void __launch_bounds__(64 * WM * WN, WM * WN * MB * NB == 8 ? 3 : 2) k_product_rows(Args a) {
     constexpr int WAVES = WM * WN, BM = 32 * WM * MB, BN = 32 * WN * NB, TERMS = kStepBytes / (int)sizeof(T);
     using X = Along<T, BM, WAVES>;
     using W = typename std::conditional<BACK, Across<T, BN, WAVES>, Along<T, BN, WAVES>>::type;

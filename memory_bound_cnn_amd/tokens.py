@@ -21,6 +21,11 @@ Steps of small packs wait for the host, and most of that for PyTorch's handing
 the backward pass to a thread of its own: within
 ``torch.autograd.set_multithreading_enabled(False)`` a forward and a backward
 pass of 8 tokens take 32 us (norm) and 31 us (attention) instead of 75 and 72.
+
+Forward and backward passes can be captured into graphs.  A backward pass is not,
+while an eager pass of the same leaves lives: PyTorch ties a leaf's gradient to
+the stream on which the leaf was used first.  ``layer_norm``, ``gated_scan`` and
+the ``expert_`` functions refuse it.
 """
 
 from typing import NamedTuple
@@ -114,7 +119,8 @@ def gated_scan(x, gate, cu_seqlens, state=None, reverse=False):
     separate), y is h in x's type; h itself is float32.  cu_seqlens [n + 1] int32
     as for :func:`attention`; tokens of no sequence get zeros.  state [n, C]
     float32: what each sequence starts from, zeros unless given; last [n, C]
-    float32: what it leaves.  reverse: from the last token to the first."""
+    float32: what it leaves.  reverse: from the last token to the first.  With
+    gradients, half a byte a channel and token is kept beside the inputs."""
     y, last = (_ops or _load()).gated_scan(x, gate, cu_seqlens, state, reverse)
     return y, last
 
@@ -151,7 +157,9 @@ def expert_gather(x, order):
 def expert_linear(x, weight, cu_experts, bias=None):
     """x weight[e]^T + bias[e] for the rows of each expert e, cu_experts[e] up to
     cu_experts[e + 1]; zeros for the rows of none.  x [R, K], weight [E, N, K] and
-    bias [E, N] in x's type, K and N multiples of 8; cu_experts [E + 1] int32."""
+    bias [E, N] in x's type, K and N multiples of 8; cu_experts [E + 1] int32.
+    float32 is computed to float32's precision, but from bfloat16 parts: finite
+    values above 3.3895e38 count as infinite, and an infinity may give a NaN."""
     return (_ops or _load()).expert_linear(x, weight, bias, cu_experts)
 
 
