@@ -142,7 +142,7 @@ Tensor gated_scan_step(const Tensor& x0, const Tensor& gate0, const Tensor& stat
     check_like(gate0, "gate", x0);
     check(state, "state", at::kFloat, x0, x0.sizes());
     check(to, "out", at::kFloat, x0, x0.sizes());
-    at::assert_no_partial_overlap(to, state);   // it may be state itself
+    for (const Tensor& t : {state, x0, gate0}) at::assert_no_partial_overlap(to, t);   // it may be one of them itself
     const Tensor x = dense_rows(x0), gate = dense_rows(gate0), y = empty(x.sizes(), x);
     const wtc_scan_desc d = {x.size(0), x.stride(0), gate.stride(0), 0, 0, narrow(x.size(1), "channels of x"), dtype, 0};
     const On on(x);

@@ -208,6 +208,20 @@ def test_step_refuses_gradients_and_overlaps():
         tokens.gated_scan_step(x, x, long[:32].view(4, 8), out=long[8:].view(4, 8))
 
 
+def test_step_into_its_inputs():
+    """The new state may replace an input of its type as a whole, not a part of one."""
+    x, gate, state = normal(gen(), 4, 8), normal(gen(1), 4, 8), normal(gen(2), 4, 8)
+    y, new = tokens.gated_scan_step(x, gate, state)
+    for i in range(3):
+        args = [x.clone(), gate.clone(), state.clone()]
+        again, out = tokens.gated_scan_step(*args, out=args[i])
+        assert torch.equal(again, y) and torch.equal(out, new) and out.data_ptr() == args[i].data_ptr()
+    long = torch.zeros(40, device=DEV)
+    for args in ((long[:32].view(4, 8), gate), (x, long[:32].view(4, 8))):
+        with pytest.raises(RuntimeError, match="memory"):
+            tokens.gated_scan_step(*args, state, out=long[8:].view(4, 8))
+
+
 def test_step_in_place_is_seen_by_autograd():
     """A state that is saved for a gradient and then overwritten is an error, not a wrong gradient."""
     s = normal(gen(), 4, 8)
