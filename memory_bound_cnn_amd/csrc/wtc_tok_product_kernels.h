@@ -7,8 +7,9 @@
 // Bound by the matrix units where there are many rows, and by the weights' way from memory where there are few.  A
 // workgroup's tiles of the two operands are copied to shared memory a step ahead, and read from there half a step ahead,
 // of their products.  Measured: 50176 rows of 8 uneven experts, 1024 -> 4096, bfloat16: 401 to 452 us forward (1050 to 930
-// TFLOP/s), 416 to 469 for the input's gradient, 450 to 525 for the weights', from card to card and with how warm it is (a
-// library product of the same size and one expert: 383, 429 and 594); matrix units busy 60, 68 and 49 % of the time. The
+// TFLOP/s), 416 to 469 for the input's gradient, 372 to 511 for the weights' (one kernel over and over, and all in turn as a
+// training step has them, when the card's power holds the clocks down; a library product of the same size and one expert:
+// 383, 429 and 594); matrix units busy 60 to 68 % of the time. The
 // copies' way is what holds the large tiles back: without them (timed alone, on tiles that do not change) the loop runs at
 // 1200 to 1300 TFLOP/s, at the clocks that power allows. float32, 6007 rows of 5 experts, 392 -> 1544: 78, 96 and 88 + 8 us
 // (101, 82 and 83 TFLOP/s; the float32 matrix instructions reach 153 at best), where splitting the factors in three takes
@@ -30,22 +31,51 @@ struct Args {
     const int* cu;
     void* y;                    // dx, dW
     void* db;
-    float* parts;               // k_product_weights, split: [splits][E][N][K], then [splits][E][N]
+    float* parts;               // k_product_weights: sums of experts' parts, [slots][N][K], then [slots][N]
     long long x_stride, g_stride, slots;
-    int R, E, K, N, splits;
+    int R, E, K, N, rows;       // rows: of a part of an expert, about
 };
 
-// The expert with the rank-th most rows, for up to 64 experts; beyond, experts in their order.
-__device__ __forceinline__ int expert_of_rank(const int* cu, int E, int R, int rank, int lane) {
-    if (E > 64) return rank;
-    const int n = lane < E ? segment_begin(cu, E, R, lane + 2) - segment_begin(cu, E, R, lane + 1) : INT_MIN;
-    int before = 0;
-    for (int e = 0; e < E; ++e) {
-        const int m = __builtin_amdgcn_readlane(n, e);
-        before += m > n || (m == n && e < lane);
-    }
-    return __builtin_ctzll(__builtin_amdgcn_ballot_w64(lane < E && before == rank) | (1ull << 63)) % E;
+// For the weights' gradients an expert's rows are taken in `parts` equal parts, of 5/8 to 5/4 of `rows` each, or in one if
+// it has less.  Parts of experts with several have a place for their sums, in the experts' order.
+struct Part {
+    int expert, part, parts, place;   // place: of the expert's first part
+};
+__host__ __device__ __forceinline__ int parts_of(int count, int rows) {
+    const int n = (int)((count + 3LL * rows / 4) / rows);
+    return n < 1 ? 1 : n;
 }
+inline long long most_parts(long long R, int E, int rows) { return E + R / rows; }
+inline long long most_places(long long R, int rows) {   // parts of an expert with several: at most 8/5 of its rows / `rows`
+    return 4 * R < 5LL * rows ? 0 : (8 * R + 5LL * rows - 1) / (5LL * rows);
+}
+// The number-th part: of up to 64 experts those with the longest parts first, beyond in the experts' order.  expert -1: none.
+__device__ __forceinline__ Part find_part(const int* cu, int E, int R, int rows, int number, int lane) {
+    int before = 0, place = 0;   // parts and places of the experts before the 64 at e0
+    for (int e0 = 0; e0 < E; e0 += 64) {
+        const int e = e0 + lane, there = min(E - e0, 64);
+        const int count = e < E ? max(segment_begin(cu, E, R, e + 2) - segment_begin(cu, E, R, e + 1), 0) : 0;
+        const int parts = e < E ? parts_of(count, rows) : 0, length = parts > 0 ? count / parts : 0;
+        int first = before, mine = place;
+        for (int i = 0; i < there; ++i) {
+            const int p = __builtin_amdgcn_readlane(parts, i), l = __builtin_amdgcn_readlane(length, i);
+            if (E <= 64 ? l > length || (l == length && i < lane) : i < lane) first += p;
+            if (i < lane && p > 1) mine += p;
+            before += p;
+            if (p > 1) place += p;
+        }
+        const uint64_t found = __builtin_amdgcn_ballot_w64(e < E && number >= first && number < first + parts);
+        if (found) {
+            const int at = __builtin_ctzll(found);
+            return {e0 + at, number - __builtin_amdgcn_readlane(first, at), __builtin_amdgcn_readlane(parts, at),
+                    __builtin_amdgcn_readlane(mine, at)};
+        }
+    }
+    return {-1, 0, 0, 0};
+}
+
+// With rows in no order experts can have more of them together than there are: those without a place remain whole.
+__device__ __forceinline__ bool no_place(const Args& a, int place, int parts) { return parts > 1 && place + parts > a.slots; }
 
 // Waits until at most N of the wave's copies are on their way.
 template <int N>
@@ -352,7 +382,7 @@ __global__ void __launch_bounds__(64 * WAVES) k_product_few(Args a) {
         *reinterpret_cast<f32x4*>(to) = v;
 }
 
-template <typename T, int WM, int WN, int MB, int NB, int STAGES>
+template <typename T, int WM, int WN, int MB, int NB, int STAGES, bool SPREAD>
 __global__ void __launch_bounds__(64 * WM * WN, 2) k_product_weights(Args a) {
     constexpr int WAVES = WM * WN, BM = 32 * WM * MB, BN = 32 * WN * NB, TERMS = kStepBytes / (int)sizeof(T);
     using G = Across<T, BM, WAVES>;
@@ -365,16 +395,18 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) k_product_weights(Args a) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
     const int ktiles = (a.K + BN - 1) / BN, ntiles = (a.N + BM - 1) / BM;
-    // the tiles of the expert with the most rows first; those of one are spread over the XCDs by runs
-    const int per = ktiles * ntiles * a.splits, rank = blockIdx.x / per;
-    int id = spread(blockIdx.x % per, per);
-    const int e = expert_of_rank(a.cu, a.E, a.R, rank, lane);
-    const int col0 = id % ktiles * BN;
-    id /= ktiles;
-    const int row0 = id % ntiles * BM, split = id / ntiles;
+    // the longest parts first; the tiles of one are spread over the XCDs by runs
+    const int per = ktiles * ntiles, id = spread(blockIdx.x % per, per);
+    Part part = find_part(a.cu, a.E, a.R, a.rows, blockIdx.x / per, lane);
+    if (part.expert < 0) return;
+    if (no_place(a, part.place, part.parts)) {
+        if (part.part > 0) return;
+        part.parts = 1;
+    }
+    const int e = part.expert, col0 = id % ktiles * BN, row0 = id / ktiles * BM;
     const int first = segment_begin(a.cu, a.E, a.R, e + 1), count = max(segment_begin(a.cu, a.E, a.R, e + 2) - first, 0);
     const int all = (count + TERMS - 1) / TERMS;
-    const int begin = (int)((long long)all * split / a.splits), end = (int)((long long)all * (split + 1) / a.splits);
+    const int begin = (int)((long long)all * part.part / part.parts), end = (int)((long long)all * (part.part + 1) / part.parts);
     Sum<T, f32x16> acc[MB][NB];
     float sum[MB] = {};   // of dy's columns: the lane's half of the terms
     const bool sums = a.db && col0 == 0 && wn == 0;
@@ -388,25 +420,35 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) k_product_weights(Args a) {
     xt.place(xrow, min(a.K - col0, BN) / kVec<T> - 1, wave, lane);
     const uint32_t lds0 = lds_address(lds);
     const int gpart = G::lane_part(lane), xpart = X::lane_part(lane);
-    run_steps<Set, STAGES, COPIES, false>(
+    run_steps<Set, STAGES, COPIES, SPREAD>(
         begin, end, end == all && count % TERMS != 0,
-        [&](int s, int buffer) {
+        [&](int s, int buffer, int one = -1) {
             const uint32_t at = lds0 + (uint32_t)buffer * STAGE;
             const int last = count - 1 - s * TERMS;
-            gt.copy(at, g + (size_t)s * TERMS * grow, grow, last, wave, lane);
-            xt.copy(at + G::kBytes, x + (size_t)s * TERMS * xrow, xrow, last, wave, lane);
+            const char *gs = g + (size_t)s * TERMS * grow, *xs = x + (size_t)s * TERMS * xrow;
+            if (one >= G::kCopies) {
+                xt.copy_one(one - G::kCopies, at + G::kBytes, xs, wave);
+            } else if (one >= 0) {
+                gt.copy_one(one, at, gs, wave);
+            } else {
+                gt.copy(at, gs, grow, last, wave, lane);
+                xt.copy(at + G::kBytes, xs, xrow, last, wave, lane);
+            }
         },
-        [&](int half, Set& set, int buffer) {
+        [&](int half, Set& set, int buffer, int one = -1) {
             const char* at = lds + buffer * STAGE;
-            set.template read<X, G>(at + G::kBytes, at, xpart, gpart, 32 * NB * wn, 32 * MB * wm, lane, half);
+            if (one >= 0)
+                set.template read_one<X, G>(one, at + G::kBytes, at, xpart, gpart, 32 * NB * wn, 32 * MB * wm, lane, half);
+            else
+                set.template read<X, G>(at + G::kBytes, at, xpart, gpart, 32 * NB * wn, 32 * MB * wm, lane, half);
         },
         [&](int buffer) {
             char* at = lds + buffer * STAGE;
             G::clear(at, count % TERMS);
             X::clear(at + G::kBytes, count % TERMS);
         },
-        [&](const Set& set) {
-            set.products(acc);
+        [&](const Set& set, const auto&... between) {
+            set.products(acc, between...);
             if (sums) {
 #pragma unroll
                 for (int k = 0; k < Set::READS; ++k)
@@ -416,7 +458,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) k_product_weights(Args a) {
         });
     meet();
     const int col = col0 + 32 * NB * wn;
-    const size_t weights = (size_t)a.E * a.N * a.K;
+    const size_t weights = (size_t)a.N * a.K, place = part.place + part.part;
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
         const int row = row0 + 32 * (MB * wm + mb);
@@ -424,41 +466,55 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) k_product_weights(Args a) {
         if (sums) {
             const float both = sum[mb] + __shfl_xor(sum[mb], 32);
             if (lane < 32 && row + lane < a.N) {
-                if (a.splits == 1)
+                if (part.parts == 1)
                     static_cast<T*>(a.db)[(size_t)e * a.N + row + lane] = from_f32<T>(both);
                 else
-                    a.parts[a.splits * weights + ((size_t)split * a.E + e) * a.N + row + lane] = both;
+                    a.parts[a.slots * weights + place * a.N + row + lane] = both;
             }
         }
         if (col >= a.K) continue;
-        const size_t to = ((size_t)e * a.N + row) * a.K + col;
-        if (a.splits == 1)
-            store_block<T, NB>(lds + wave * kStoreBytes<T, NB>, static_cast<T*>(a.y) + to, a.K, a.N - row, a.K - col,
-                               lane, acc[mb]);
+        const size_t to = (size_t)row * a.K + col;
+        if (part.parts == 1)
+            store_block<T, NB>(lds + wave * kStoreBytes<T, NB>, static_cast<T*>(a.y) + e * weights + to, a.K, a.N - row,
+                               a.K - col, lane, acc[mb]);
         else
-            store_block<float, NB>(lds + wave * kStoreBytes<float, NB>, a.parts + split * weights + to, a.K, a.N - row, a.K - col,
-                                   lane, acc[mb]);
+            store_block<float, NB>(lds + wave * kStoreBytes<float, NB>, a.parts + place * weights + to, a.K, a.N - row,
+                                   a.K - col, lane, acc[mb]);
     }
 }
 
-// The splits' sums in their order: n weights of dW, then m of db.
+// The sums of the experts' parts in their order: N K weights of an expert, then N of db.  Every gridDim.y-th such
+// expert is one row of workgroups'.
 template <typename T>
-__global__ void __launch_bounds__(256) k_product_join(Args a, long long n, long long m) {
-    for (long long u = (long long)blockIdx.x * 256 + threadIdx.x; 4 * u < n + m; u += (long long)gridDim.x * 256) {
-        const bool bias = 4 * u >= n;   // n and m are multiples of 8
-        const float* p = a.parts + (bias ? a.splits * n + 4 * u - n : 4 * u);
-        const long long far = bias ? m : n;
-        f32x4 v = {0.f, 0.f, 0.f, 0.f};
-        for (int s = 0; s < a.splits; ++s) v += *reinterpret_cast<const f32x4*>(p + s * far);
-        T* to = bias ? static_cast<T*>(a.db) + (4 * u - n) : static_cast<T*>(a.y) + 4 * u;
-        if constexpr (sizeof(T) == 2)
-            *reinterpret_cast<u32x2*>(to) = u32x2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
-        else
-            *reinterpret_cast<f32x4*>(to) = v;
+__global__ void __launch_bounds__(256) k_product_join(Args a) {
+    const int lane = threadIdx.x & 63;
+    const long long n = (long long)a.N * a.K, m = a.db ? a.N : 0;
+    int place = 0, p0 = 0;
+    unsigned nth = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 64) {
+        const int mine = e0 + lane;
+        const int count = mine < a.E ? segment_begin(a.cu, a.E, a.R, mine + 2) - segment_begin(a.cu, a.E, a.R, mine + 1) : 0;
+        const int p = parts_of(max(count, 0), a.rows);
+        for (uint64_t split = __builtin_amdgcn_ballot_w64(p > 1); split; split &= split - 1, place += p0) {
+            const int at = __builtin_ctzll(split), parts = __builtin_amdgcn_readlane(p, at);
+            p0 = parts;
+            const long long e = e0 + at;
+            if (nth++ % gridDim.y != blockIdx.y || no_place(a, place, parts)) continue;
+            for (long long u = (long long)blockIdx.x * 256 + threadIdx.x; 4 * u < n + m; u += (long long)gridDim.x * 256) {
+                const bool bias = 4 * u >= n;   // n and m are multiples of 8
+                const float* sums = a.parts + (bias ? a.slots * n + place * m + 4 * u - n : place * n + 4 * u);
+                const long long far = bias ? m : n;
+                f32x4 v = {0.f, 0.f, 0.f, 0.f};
+                for (int s = 0; s < parts; ++s) v += *reinterpret_cast<const f32x4*>(sums + s * far);
+                T* to = bias ? static_cast<T*>(a.db) + e * m + (4 * u - n) : static_cast<T*>(a.y) + e * n + 4 * u;
+                if constexpr (sizeof(T) == 2)
+                    *reinterpret_cast<u32x2*>(to) = u32x2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
+                else
+                    *reinterpret_cast<f32x4*>(to) = v;
+            }
+        }
     }
 }
-
-constexpr int kTile = 128;   // rows and columns of a workgroup's tile
 
 template <typename T, bool BACK, int WM, int WN, int MB, int NB, int STAGES, bool SPREAD = false>
 int launch_rows(Args a, hipStream_t st) {
@@ -523,20 +579,25 @@ template <typename T>
 int run_rows(const Args& a, bool back, hipStream_t st) {
     return back ? run_rows_way<T, true>(a, st) : run_rows_way<T, false>(a, st);
 }
-template <typename T, int WM, int WN, int MB, int NB, int STAGES>
+template <typename T, int WM, int WN, int MB, int NB, int STAGES, bool SPREAD = false>
 int launch_weights(const Args& a, hipStream_t st) {
     constexpr int BM = 32 * WM * MB, BN = 32 * WN * NB;
-    const long long groups = (long long)((a.K + BN - 1) / BN) * ((a.N + BM - 1) / BM) * a.E * a.splits;
+    const long long groups = (long long)((a.K + BN - 1) / BN) * ((a.N + BM - 1) / BM) * most_parts(a.R, a.E, a.rows);
     if (groups > (1 << 23)) return WTC_ESHAPE;
-    hipLaunchKernelGGL((k_product_weights<T, WM, WN, MB, NB, STAGES>), dim3((unsigned)groups), dim3(64 * WM * WN), 0, st, a);
+    hipLaunchKernelGGL((k_product_weights<T, WM, WN, MB, NB, STAGES, SPREAD>), dim3((unsigned)groups), dim3(64 * WM * WN), 0, st,
+                       a);
     return hipGetLastError() == hipSuccess ? WTC_OK : WTC_EHIP;
 }
 template <typename T>
-int run_weights(const Args& a, hipStream_t st) {
-    const int r = launch_weights<T, 2, 2, 2, 2, 2>(a, st);
-    if (r == WTC_OK && a.splits > 1) {
-        const long long n = (long long)a.E * a.N * a.K, m = a.db ? (long long)a.E * a.N : 0, blocks = ((n + m) / 4 + 255) / 256;
-        hipLaunchKernelGGL(k_product_join<T>, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, st, a, n, m);
+int run_weights(const Args& a, bool large, hipStream_t st) {
+    int r;
+    if constexpr (sizeof(T) == 2)
+        r = large ? launch_weights<T, 2, 4, 4, 2, 2, true>(a, st) : launch_weights<T, 2, 2, 2, 2, 2>(a, st);
+    else
+        r = launch_weights<T, 2, 2, 2, 2, 2>(a, st);
+    if (r == WTC_OK && a.slots > 0) {
+        const long long blocks = (((long long)a.K + 1) * a.N / 4 + 255) / 256;
+        hipLaunchKernelGGL(k_product_join<T>, dim3((unsigned)(blocks < 512 ? blocks : 512), a.E < 4 ? a.E : 4), dim3(256), 0, st, a);
     }
     return hipGetLastError() == hipSuccess ? r : WTC_EHIP;
 }

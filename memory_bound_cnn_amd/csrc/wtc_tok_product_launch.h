@@ -8,8 +8,8 @@ namespace product {
 
 int rows_bf16(const Args& a, bool back, hipStream_t st);
 int rows_fp32(const Args& a, bool back, hipStream_t st);
-int weights_bf16(const Args& a, hipStream_t st);
-int weights_fp32(const Args& a, hipStream_t st);
+int weights_bf16(const Args& a, bool large, hipStream_t st);
+int weights_fp32(const Args& a, bool large, hipStream_t st);
 
 }  // namespace product
 }  // namespace wtc

@@ -1,27 +1,44 @@
 // The experts' products: launches.  The kernels are wtc_tok_product_kernels.h,
 // compiled for each type by wtconv_tok_product_bf16.hip and _fp32.hip.
 #include <hip/hip_runtime.h>
+#include <limits.h>
 
 #include "wtc_tok_product_launch.h"
 
 namespace wtc {
 namespace {
 
-// Workgroups that share the rows of one tile of dW: to about 768 of them, which also evens out experts of unequal size,
-// if each has 1024 rows (float32: 171, of six products) to pay for the partial sums' way through memory.  Measured (us, 8
-// experts, whole / in 2 / in 3 / in 4): 512 tiles bfloat16, 12544 rows 49.5 / 53.0, 16384 63.1 / 60.3 / 68, 32768 121 / 93.7 /
-// 99.6 / 126, 50176 186 / 147 / 158 / 165; 768 tiles, 25000 rows of 4 experts 159 / 205; 1024 tiles, 100000 rows 488 / 485 /
-// 507; 256 tiles float32, 2048 rows 39.1 / 34.0 / 37.4, 6007 94.9 / 62.5 / 55.3 / 58.5, 12544 188 / 112 / 92.4 / 94.4.
-int splits_of(const wtc_expert_desc* d) {
-    const long long tiles = (long long)d->E * ((d->K + 127) / 128) * ((d->N + 127) / 128);
-    const long long most = d->R / d->E * (d->dtype == WTC_BF16 ? 1 : 6) / 1024, want = (768 + tiles / 2) / tiles;
-    return (int)(want < most ? (want < 1 ? 1 : want) : most < 1 ? 1 : most);
+// How the weights' gradients are shared out: tiles of 256 x 256 or of 128 x 128, and the rows of a part of an expert (see
+// find_part): as many as leave a part to every place on the chip, and enough to pay for the partial sums' way through memory.
+// Measured (us; 8 experts of bfloat16 unless said): experts whole, and in parts of 1/2, 1 and 3/2 of those rows; first experts
+// of equal size, then one with two thirds of all rows.
+//   128 x 128: 12544 rows x 512 -> 2048 35.5, 61, 37, 39 and 87, 51, 44, 44; float32 12544 x 512 -> 1024 95, 100, 92, 91 and
+// 439, 108, 96, 102; 4 experts 30000 x 256 -> 256 401, 56, 47, 50 and 1398, 77, 62, 61.
+//   256 x 256: 50176 x 1024 -> 4096 359, 359, 362, 361 and 729, 403, 393, 432; x 1024 -> 1024 147, 161, 118, 118 and 689, 168,
+// 146, 139; 4 experts 25088 x 1024 -> 2048 141, 138, 113, 114 and 465, 152, 126, 130.
+//   256 x 256 against 128 x 128, in parts of those rows: 50176 x 1024 -> 4096 362 and 458, 1024 -> 1024 118 and 147, 4 experts
+// 100000 x 512 -> 512 (1562 rows a place) 84 and 106, 64 experts 8192 x 512 -> 1024 55 and 68; but 12544 x 512 -> 2048 (784
+// rows a place, 128 tiles) 54 and 37.
+struct Share {
+    bool large;
+    int rows;
+    long long places;   // for sums of parts
+};
+Share share_of(const wtc_expert_desc* d) {
+    auto tiles = [&](int side) { return (long long)((d->K + side - 1) / side) * ((d->N + side - 1) / side); };
+    const bool wide = d->dtype != WTC_BF16;
+    Share s;
+    s.large = !wide && 3 * tiles(256) < tiles(128) && (d->R * tiles(256) >= 256 * 1280 || d->E * tiles(256) >= 512);
+    const long long each = s.large ? d->R * tiles(256) / 256 : d->R * tiles(128) / 512, least = wide ? 192 : 1024;
+    s.rows = (int)(each < least ? least : each > INT_MAX / 2 ? INT_MAX / 2 : (each + 63) / 64 * 64);
+    s.places = product::most_places(d->R, s.rows);
+    return s;
 }
 
 product::Args args_of(const wtc_expert_desc* d, const int* cu) {
     product::Args a = {};
     a.cu = cu;
-    a.R = (int)d->R; a.E = d->E; a.K = d->K; a.N = d->N; a.splits = 1;
+    a.R = (int)d->R; a.E = d->E; a.K = d->K; a.N = d->N;
     a.x_stride = d->x_stride; a.g_stride = d->g_stride;
     return a;
 }
@@ -29,8 +46,7 @@ product::Args args_of(const wtc_expert_desc* d, const int* cu) {
 }  // namespace
 
 size_t expert_weights_workspace(const wtc_expert_desc* d) {
-    const int s = splits_of(d);
-    return s > 1 ? (size_t)s * d->E * ((size_t)d->N * d->K + d->N) * sizeof(float) : 0;
+    return (size_t)share_of(d).places * ((size_t)d->N * d->K + d->N) * sizeof(float);
 }
 
 int launch_expert_forward(const wtc_expert_desc* d, const void* x, const void* w, const void* b, const int* cu, void* y,
@@ -49,9 +65,11 @@ int launch_expert_input_grad(const wtc_expert_desc* d, const void* dy, const voi
 int launch_expert_weight_grad(const wtc_expert_desc* d, const void* dy, const void* x, const int* cu, void* dw, void* db,
                               void* workspace, void* stream) {
     product::Args a = args_of(d, cu);
-    a.x = x; a.g = dy; a.y = dw; a.db = db; a.splits = splits_of(d); a.parts = static_cast<float*>(workspace);
+    a.x = x; a.g = dy; a.y = dw; a.db = db; a.parts = static_cast<float*>(workspace);
+    const Share s = share_of(d);
+    a.rows = s.rows; a.slots = s.places;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-    return d->dtype == WTC_BF16 ? product::weights_bf16(a, st) : product::weights_fp32(a, st);
+    return d->dtype == WTC_BF16 ? product::weights_bf16(a, s.large, st) : product::weights_fp32(a, false, st);
 }
 
 }  // namespace wtc

@@ -7,7 +7,7 @@ namespace wtc {
 namespace product {
 
 int rows_bf16(const Args& a, bool back, hipStream_t st) { return run_rows<uint16_t>(a, back, st); }
-int weights_bf16(const Args& a, hipStream_t st) { return run_weights<uint16_t>(a, st); }
+int weights_bf16(const Args& a, bool large, hipStream_t st) { return run_weights<uint16_t>(a, large, st); }
 
 }  // namespace product
 }  // namespace wtc

@@ -7,7 +7,7 @@ namespace wtc {
 namespace product {
 
 int rows_fp32(const Args& a, bool back, hipStream_t st) { return run_rows<float>(a, back, st); }
-int weights_fp32(const Args& a, hipStream_t st) { return run_weights<float>(a, st); }
+int weights_fp32(const Args& a, bool large, hipStream_t st) { return run_weights<float>(a, large, st); }
 
 }  // namespace product
 }  // namespace wtc

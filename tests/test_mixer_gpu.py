@@ -583,6 +583,26 @@ def test_expert_linear(counts, K, N, dtype):
 
 
 @BOTH
+@pytest.mark.parametrize("counts,K,N", [([9000, 100, 0, 300], 520, 264), ([40] * 20 + [3000, 0, 1500] + [17] * 25, 520, 1000),
+                                        ([8] * 70 + [2500, 0, 1300] + [5] * 30, 64, 40), ([1200, 1300], 72, 80)])
+def test_expert_linear_of_uneven_experts(counts, K, N, dtype):
+    """Gradients of weights in parts of an expert's rows: some experts whole, some in parts, up to 64 of them and more."""
+    check_product(*product_case(counts, K, N, dtype, bias=True, seed=len(counts)), dtype)
+
+
+def test_expert_linear_with_bounds_in_no_order():
+    """Experts whose rows overlap have more together than there are: their gradients are anything, but stay where they belong."""
+    x, w, b, cu, dy = product_case([3000, 0, 0, 0], 64, 48, "fp32", True, seed=8)
+    guard = torch.full((4 * 48 * 64,), 7.0, device=DEV)
+    bad = torch.tensor([0, 3000, 0, 3000, -5], dtype=torch.int32, device=DEV)
+    leaves = [t.clone().requires_grad_() for t in (x, w, b)]
+    torch.autograd.grad(tokens.expert_linear(leaves[0], leaves[1], bad, leaves[2]), leaves, dy)
+    torch.cuda.synchronize()
+    assert torch.equal(guard, torch.full_like(guard, 7.0))
+    check_product(x, w, b, cu, dy, "fp32")
+
+
+@BOTH
 @pytest.mark.parametrize("counts,K,N", [([1], 2048, 64), ([0, 2, 0, 1], 1000, 72), ([0] * 100 + [1] + [0] * 50 + [2, 0, 1] + [0] * 300, 520, 40),
                                         ([16, 17, 0, 15], 264, 136), ([33, 1], 72, 24), ([1] * 3, 8, 8), ([3, 2, 4], 4104, 16)])
 def test_expert_linear_of_few_rows(counts, K, N, dtype):
