@@ -49,27 +49,40 @@ inline long long most_parts(long long R, int E, int rows) { return E + R / rows;
 inline long long most_places(long long R, int rows) {   // parts of an expert with several: at most 8/5 of its rows / `rows`
     return 4 * R < 5LL * rows ? 0 : (8 * R + 5LL * rows - 1) / (5LL * rows);
 }
-// The number-th part: of up to 64 experts those with the longest parts first, beyond in the experts' order.  expert -1: none.
+// The number-th part: of up to 16 experts those with the longest parts first, beyond in the experts' order (parts are then
+// many to a place, and finding the order takes longer than it gives).  expert -1: none.
 __device__ __forceinline__ Part find_part(const int* cu, int E, int R, int rows, int number, int lane) {
+    constexpr int RANKED = 16;
     int before = 0, place = 0;   // parts and places of the experts before the 64 at e0
     for (int e0 = 0; e0 < E; e0 += 64) {
-        const int e = e0 + lane, there = min(E - e0, 64);
+        const int e = e0 + lane;
         const int count = e < E ? max(segment_begin(cu, E, R, e + 2) - segment_begin(cu, E, R, e + 1), 0) : 0;
         const int parts = e < E ? parts_of(count, rows) : 0, length = parts > 0 ? count / parts : 0;
-        int first = before, mine = place;
-        for (int i = 0; i < there; ++i) {
-            const int p = __builtin_amdgcn_readlane(parts, i), l = __builtin_amdgcn_readlane(length, i);
-            if (E <= 64 ? l > length || (l == length && i < lane) : i < lane) first += p;
-            if (i < lane && p > 1) mine += p;
-            before += p;
-            if (p > 1) place += p;
+        int first = parts, mine = parts > 1 ? parts : 0;   // parts and places up to this expert
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int p = __shfl_up(first, o), m = __shfl_up(mine, o);
+            if (lane >= o) first += p, mine += m;
         }
+        const int all = __builtin_amdgcn_readlane(first, 63), places = __builtin_amdgcn_readlane(mine, 63);
+        first -= parts;
+        mine -= parts > 1 ? parts : 0;
+        if (E <= RANKED) {
+            first = 0;
+            for (int i = 0; i < E; ++i) {
+                const int l = __builtin_amdgcn_readlane(length, i);
+                if (l > length || (l == length && i < lane)) first += __builtin_amdgcn_readlane(parts, i);
+            }
+        }
+        first += before;
         const uint64_t found = __builtin_amdgcn_ballot_w64(e < E && number >= first && number < first + parts);
         if (found) {
             const int at = __builtin_ctzll(found);
             return {e0 + at, number - __builtin_amdgcn_readlane(first, at), __builtin_amdgcn_readlane(parts, at),
-                    __builtin_amdgcn_readlane(mine, at)};
+                    place + __builtin_amdgcn_readlane(mine, at)};
         }
+        before += all;
+        place += places;
     }
     return {-1, 0, 0, 0};
 }
@@ -397,7 +410,9 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) k_product_weights(Args a) {
     const int ktiles = (a.K + BN - 1) / BN, ntiles = (a.N + BM - 1) / BM;
     // the longest parts first; the tiles of one are spread over the XCDs by runs
     const int per = ktiles * ntiles, id = spread(blockIdx.x % per, per);
-    Part part = find_part(a.cu, a.E, a.R, a.rows, blockIdx.x / per, lane);
+    // no places: no expert has several parts, and few rows
+    Part part = {(int)(blockIdx.x / per), 0, 1, 0};
+    if (a.slots > 0) part = find_part(a.cu, a.E, a.R, a.rows, blockIdx.x / per, lane);
     if (part.expert < 0) return;
     if (no_place(a, part.place, part.parts)) {
         if (part.part > 0) return;
@@ -582,7 +597,7 @@ int run_rows(const Args& a, bool back, hipStream_t st) {
 template <typename T, int WM, int WN, int MB, int NB, int STAGES, bool SPREAD = false>
 int launch_weights(const Args& a, hipStream_t st) {
     constexpr int BM = 32 * WM * MB, BN = 32 * WN * NB;
-    const long long groups = (long long)((a.K + BN - 1) / BN) * ((a.N + BM - 1) / BM) * most_parts(a.R, a.E, a.rows);
+    const long long groups = (long long)((a.K + BN - 1) / BN) * ((a.N + BM - 1) / BM) * (a.slots > 0 ? most_parts(a.R, a.E, a.rows) : a.E);
     if (groups > (1 << 23)) return WTC_ESHAPE;
     hipLaunchKernelGGL((k_product_weights<T, WM, WN, MB, NB, STAGES, SPREAD>), dim3((unsigned)groups), dim3(64 * WM * WN), 0, st,
                        a);

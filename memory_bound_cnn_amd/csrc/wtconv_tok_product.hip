@@ -17,8 +17,8 @@ namespace {
 //   256 x 256: 50176 x 1024 -> 4096 359, 359, 362, 361 and 729, 403, 393, 432; x 1024 -> 1024 147, 161, 118, 118 and 689, 168,
 // 146, 139; 4 experts 25088 x 1024 -> 2048 141, 138, 113, 114 and 465, 152, 126, 130.
 //   256 x 256 against 128 x 128, in parts of those rows: 50176 x 1024 -> 4096 362 and 458, 1024 -> 1024 118 and 147, 4 experts
-// 100000 x 512 -> 512 (1562 rows a place) 84 and 106, 64 experts 8192 x 512 -> 1024 55 and 68; but 12544 x 512 -> 2048 (784
-// rows a place, 128 tiles) 54 and 37.
+// 100000 x 512 -> 512 (1562 rows a place) 84 and 106; 12544 x 512 -> 2048 (784) 54 and 37, 64 experts 8192 x 512 -> 1024 (256)
+// 33 and 33.
 struct Share {
     bool large;
     int rows;
@@ -28,7 +28,7 @@ Share share_of(const wtc_expert_desc* d) {
     auto tiles = [&](int side) { return (long long)((d->K + side - 1) / side) * ((d->N + side - 1) / side); };
     const bool wide = d->dtype != WTC_BF16;
     Share s;
-    s.large = !wide && 3 * tiles(256) < tiles(128) && (d->R * tiles(256) >= 256 * 1280 || d->E * tiles(256) >= 512);
+    s.large = !wide && 3 * tiles(256) < tiles(128) && d->R * tiles(256) >= 256 * 1280;
     const long long each = s.large ? d->R * tiles(256) / 256 : d->R * tiles(128) / 512, least = wide ? 192 : 1024;
     s.rows = (int)(each < least ? least : each > INT_MAX / 2 ? INT_MAX / 2 : (each + 63) / 64 * 64);
     s.places = product::most_places(d->R, s.rows);

@@ -584,7 +584,8 @@ def test_expert_linear(counts, K, N, dtype):
 
 @BOTH
 @pytest.mark.parametrize("counts,K,N", [([9000, 100, 0, 300], 520, 264), ([40] * 20 + [3000, 0, 1500] + [17] * 25, 520, 1000),
-                                        ([8] * 70 + [2500, 0, 1300] + [5] * 30, 64, 40), ([1200, 1300], 72, 80)])
+                                        ([8] * 70 + [2500, 0, 1300] + [5] * 30, 64, 40), ([1200, 1300], 72, 80),
+                                        ([14000, 0, 3001, 70, 4000], 1000, 1016), ([30] * 20 + [9000] + [500] * 30, 1000, 1016)])
 def test_expert_linear_of_uneven_experts(counts, K, N, dtype):
     """Gradients of weights in parts of an expert's rows: some experts whole, some in parts, up to 64 of them and more."""
     check_product(*product_case(counts, K, N, dtype, bias=True, seed=len(counts)), dtype)
