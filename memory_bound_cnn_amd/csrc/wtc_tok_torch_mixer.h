@@ -505,8 +505,10 @@ void mixer_python(py::module_& m) {
     m.def("gated_scan", [](const Tensor& x, const Tensor& gate, const Tensor& cu, const OptTensor& state, bool reverse) {
         return OP(gated_scan).call(x, gate, cu, state, reverse);
     }, nogil());
-    m.def("gated_scan_step", [](const Tensor& x, const Tensor& gate, const Tensor& state, const Tensor& to) {
-        return OP(gated_scan_step).call(x, gate, state, to);
+    m.def("gated_scan_step", [](const Tensor& x, const Tensor& gate, const Tensor& state, const OptTensor& out) {
+        Tensor to = out ? *out : at::empty_like(state, state.options(), at::MemoryFormat::Contiguous);
+        Tensor y = OP(gated_scan_step).call(x, gate, state, to);
+        return std::make_tuple(std::move(y), std::move(to));
     }, nogil());
     m.def("expert_order", [](const Tensor& experts, int64_t n_experts) { return OP(expert_order).call(experts, n_experts); },
           nogil());

@@ -129,8 +129,7 @@ def gated_scan_step(x, gate, state, out=None):
     """:func:`gated_scan` of one more token of each sequence: (y, new state).  x
     and gate [n, C], state [n, C] float32.  out: where the new state goes (state
     itself, in a loop or a captured graph); a new tensor unless given.  No gradient."""
-    out = torch.empty_like(state, memory_format=torch.contiguous_format) if out is None else out
-    return (_ops or _load()).gated_scan_step(x, gate, state, out), out
+    return (_ops or _load()).gated_scan_step(x, gate, state, out)
 
 
 class ExpertOrder(NamedTuple):
