@@ -2,6 +2,7 @@
 // cu[e + 1] - 1) with its weights W[e] [N, K]:
 //   k_product_rows, forward   y[r]  = W[e] x[r] + b[e]          terms K, columns N
 //   k_product_rows, back      dx[r] = dy[r] W[e]                 terms N, columns K
+//   k_product_few             the forward one, of a few rows
 //   k_product_weights         dW[e] = sum_r dy[r] x[r]^T,  db[e] = sum_r dy[r]
 //
 // Bound by the matrix units where there are many rows, and by the weights' way from memory where there are few.  A
@@ -9,11 +10,12 @@
 // of their products.  Measured: 50176 rows of 8 uneven experts, 1024 -> 4096, bfloat16: 401 to 452 us forward (1050 to 930
 // TFLOP/s), 416 to 469 for the input's gradient, 372 to 511 for the weights' (one kernel over and over, and all in turn as a
 // training step has them, when the card's power holds the clocks down; a library product of the same size and one expert:
-// 383, 429 and 594); matrix units busy 60 to 68 % of the time. The
-// copies' way is what holds the large tiles back: without them (timed alone, on tiles that do not change) the loop runs at
-// 1200 to 1300 TFLOP/s, at the clocks that power allows. float32, 6007 rows of 5 experts, 392 -> 1544: 78, 96 and 88 + 8 us
-// (101, 82 and 83 TFLOP/s; the float32 matrix instructions reach 153 at best), where splitting the factors in three takes
-// the vector units 54 to 59 % of the time and the products the matrix units 37 to 46, side by side for little of it.
+// 383, 429 and 594); matrix units busy 60 to 68 % of the time.  The copies' way is what holds the large tiles back: without
+// them (timed alone, on tiles that do not change) the loop runs at 1200 to 1300 TFLOP/s, at the clocks that power allows.
+// float32, 6007 rows of 5 experts, 392 -> 1544: 74 to 79 us forward, 90 to 99 for the input's gradient, 82 to 91 and 8 for
+// the weights' (98, 81 and 84 TFLOP/s at best; the float32 matrix instructions reach 153), where splitting the factors in
+// three takes the vector units 54 to 59 % of the time and the products the matrix units 37 to 46, side by side for little
+// of it.
 #pragma once
 
 #include <limits.h>

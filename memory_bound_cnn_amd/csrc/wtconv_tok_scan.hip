@@ -523,11 +523,10 @@ __global__ void __launch_bounds__(256) k_scan_step(StepArgs a) {
 // Parts of the pack: enough for four waves a vector unit, of 8 tokens at least; one where that is sooner done than three
 // kernels.  Measured (us forward / backward, bfloat16): 768 channels, one part against parts of 8 tokens, 24 tokens 7.9 /
 // 11.5 and 11.2 / 13.2, 32 8.8 / 13.0 and 11.6 / 13.2, 64 12.5 / 18.8 and 11.6 / 13.4 (one launch instead of three is the
-// host's gain), 100 16.4 / 25 and 11.6 / 13.3, 400 52 / 80 and 11.6 / 13.3.  Parts of
-// 64, 32, 16 and 8 tokens at least: 400 x 768 25 / 31, 17.6 / 21, 13.8 / 16, 11.6 / 13.3; 12544 x 384 30 / 42, 25 / 35, 23.4 /
-// 31.3, 23.4 / 31.2 (784 parts are enough there).  For two waves a unit and for four: 130219 x 384 107 / 164 and 99.7 / 154,
-// 2 x 65536 x 512 147 / 219 and 149 / 216, 12544 x 1024 36.3 / 49.5 and 37.1 / 47.8; for eight the two large ones do not
-// change (kMostParts).
+// host's gain), 100 16.4 / 25 and 11.6 / 13.3, 400 52 / 80 and 11.6 / 13.3.  Parts of 64, 32, 16 and 8 tokens at least: 400 x
+// 768 25 / 31, 17.6 / 21, 13.8 / 16, 11.6 / 13.3; 12544 x 384 30 / 42, 25 / 35, 23.4 / 31.3, 23.4 / 31.2 (784 parts are enough
+// there).  For two waves a unit and for four: 130219 x 384 107 / 164 and 99.7 / 154, 2 x 65536 x 512 147 / 219 and 149 / 216,
+// 12544 x 1024 36.3 / 49.5 and 37.1 / 47.8; for eight the two large ones do not change (kMostParts).
 struct Split {
     int parts, len;
 };
