@@ -72,7 +72,7 @@ int check_layer(const wtc_layer_desc* d) {
     return WTC_OK;
 }
 
-// place and row indices of a tile past the end stay below 2^31
+// indices past the end by a step of the recurrence, or by a tile of rows, stay below 2^31
 constexpr long long kMaxScan = kMaxTokens - (1 << 10), kMaxRows = kMaxTokens - (1 << 16);
 
 int check_scan(const wtc_scan_desc* d) {

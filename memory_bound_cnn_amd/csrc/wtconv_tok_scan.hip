@@ -34,12 +34,14 @@
 
 #include "wtc_tok_device.h"
 #include "wtc_tok_internal.h"
+#include "wtc_tok_scan.h"
 
 namespace wtc {
 namespace {
 
 constexpr int V = 2;                  // channels of a thread
 constexpr int kAhead = 8;              // tokens whose loads are on their way together
+static_assert(kScanKept % kAhead == 0, "what is kept is kept at the start of a step");
 
 struct ScanArgs {
     const void *x, *f, *dy;
@@ -223,7 +225,7 @@ __global__ void __launch_bounds__(256) k_scan_maps(ScanArgs a) {
     auto [part, c] = mine_of<ONE>(a);
     if (BACK) ++part;                     // the first has none; forward, the last
     if (part >= (BACK ? a.parts : a.parts - 1)) return;
-    const int first = part * a.len, end = min(first + a.len, a.T);
+    const int first = part * a.len, end = part_end(first, a.len, a.T);
     float A[V] = {}, B[V] = {};
     const Where w = find(a, BACK ? first : end - 1);
     int from = first, to = first;         // the places that count; with none the state is zero
@@ -272,7 +274,7 @@ __global__ void __launch_bounds__(256) k_scan_maps(ScanArgs a) {
 // The state that each part begins with (BACK: G behind its last token): 128
 // threads of a channel have up to kRun parts each, in order, and take what the
 // threads before them leave.
-constexpr int kRun = 8, kMostParts = 128 * kRun, kCols = 8;
+constexpr int kRun = kMostParts / 128, kCols = 8;
 __device__ __forceinline__ float apply(const float2& m, float h) { return m.x < 0.f ? m.y : fmaf(m.x, h, m.y); }
 // first one, then the other
 __device__ __forceinline__ float2 after(const float2& one, const float2& other) {
@@ -329,7 +331,7 @@ __global__ void __launch_bounds__(256) k_scan_forward(ScanArgs a) {
     const auto [part, c] = mine_of<ONE>(a);
     if (part >= a.parts) return;
     if (a.last) pass_on<ONE>(a, a.state, a.last, part, c);
-    const int first = part * a.len, end = min(first + a.len, a.T);
+    const int first = part * a.len, end = part_end(first, a.len, a.T);
     if (first >= end) return;
     Rows<T, ONE, kAhead> x, f;
     x.fetch(a.x, a.x_stride, a, first, end, c);
@@ -387,7 +389,7 @@ __global__ void __launch_bounds__(256) k_scan_backward(ScanArgs a) {
     const auto [part, c] = mine_of<ONE>(a);
     if (part >= a.parts) return;
     if (a.last) pass_on<ONE>(a, a.dlast, a.last, part, c);
-    const int first = part * a.len, end = min(first + a.len, a.T);
+    const int first = part * a.len, end = part_end(first, a.len, a.T);
     if (first >= end) return;
     float G[V] = {};
     if (part + 1 < a.parts) load_state<ONE>(a.starts + (size_t)part * a.C + c, G);
@@ -520,28 +522,7 @@ __global__ void __launch_bounds__(256) k_scan_step(StepArgs a) {
     }
 }
 
-// Parts of the pack: enough for four waves a vector unit, of 8 tokens at least; one where that is sooner done than three
-// kernels.  Measured (us forward / backward, bfloat16): 768 channels, one part against parts of 8 tokens, 24 tokens 7.9 /
-// 11.5 and 11.2 / 13.2, 32 8.8 / 13.0 and 11.6 / 13.2, 64 12.5 / 18.8 and 11.6 / 13.4 (one launch instead of three is the
-// host's gain), 100 16.4 / 25 and 11.6 / 13.3, 400 52 / 80 and 11.6 / 13.3.  Parts of 64, 32, 16 and 8 tokens at least: 400 x
-// 768 25 / 31, 17.6 / 21, 13.8 / 16, 11.6 / 13.3; 12544 x 384 30 / 42, 25 / 35, 23.4 / 31.3, 23.4 / 31.2 (784 parts are enough
-// there).  For two waves a unit and for four: 130219 x 384 107 / 164 and 99.7 / 154, 2 x 65536 x 512 147 / 219 and 149 / 216,
-// 12544 x 1024 36.3 / 49.5 and 37.1 / 47.8; for eight the two large ones do not change (kMostParts).
-struct Split {
-    int parts, len;
-};
-Split split_of(const wtc_scan_desc* d) {
-    const long long pairs = (d->C + 1) / 2, want = (262144 + pairs - 1) / pairs, most = d->T <= 64 ? 1 : (d->T + 7) / 8;
-    long long parts = want < most ? want : most;
-    parts = parts < 1 ? 1 : parts > kMostParts ? kMostParts : parts;
-    Split s;
-    s.len = (int)(((d->T + parts - 1) / parts + kScanKept - 1) / kScanKept * kScanKept);
-    s.parts = s.len < 1 ? 1 : (int)((d->T + s.len - 1) / s.len);
-    return s;
-}
-static_assert(kScanKept % kAhead == 0, "what is kept is kept at the start of a step");
-
-ScanArgs scan_args(const wtc_scan_desc* d, const Split& s, const void* x, const void* f, const int* cu, const float* state,
+ScanArgs scan_args(const wtc_scan_desc* d, const ScanSplit& s, const void* x, const void* f, const int* cu, const float* state,
                    void* workspace) {
     ScanArgs a = {};
     a.x = x; a.f = f; a.cu = cu; a.state = state;
@@ -573,13 +554,13 @@ void run_scan(const ScanArgs& a, hipStream_t st) {
 }  // namespace
 
 size_t scan_workspace(const wtc_scan_desc* d) {
-    const Split s = split_of(d);
+    const ScanSplit s = scan_split(d->T, d->C);
     return s.parts > 1 ? (size_t)s.parts * d->C * (sizeof(float2) + sizeof(float)) : 0;
 }
 
 int launch_scan_forward(const wtc_scan_desc* d, const void* x, const void* f, const int* cu, const float* state, void* y,
                         float* last, float* kept, void* workspace, void* stream) {
-    const Split s = split_of(d);
+    const ScanSplit s = scan_split(d->T, d->C);
     ScanArgs a = scan_args(d, s, x, f, cu, state, workspace);
     a.y = y; a.last = last; a.kept = kept;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
@@ -590,7 +571,7 @@ int launch_scan_forward(const wtc_scan_desc* d, const void* x, const void* f, co
 int launch_scan_backward(const wtc_scan_desc* d, const void* x, const void* f, const int* cu, const float* state,
                          const float* kept, const void* dy, const float* dlast, void* dx, void* df, float* dstate,
                          void* workspace, void* stream) {
-    const Split s = split_of(d);
+    const ScanSplit s = scan_split(d->T, d->C);
     ScanArgs a = scan_args(d, s, x, f, cu, state, workspace);
     a.kept_in = kept; a.dy = dy; a.dlast = dlast; a.y = dx; a.df = df; a.last = dstate;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);

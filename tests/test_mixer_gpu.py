@@ -395,6 +395,27 @@ def test_gated_scan_many_sequences():
     check_scan(x, gate, cu, normal(gen(6), 700, 4), False, "fp32")
 
 
+def test_gated_scan_of_the_largest_pack():
+    """2^31 - 1025 tokens of one channel, whose last part ends 2^31 tokens after the first one's begin if it is taken whole:
+    every 2^20th token sets the state, the others keep it, and the last one's gradient goes back to the last that set it."""
+    T, each = (1 << 31) - (1 << 10) - 1, 1 << 20
+    n = (T + each - 1) // each
+    value = (torch.arange(n, device=DEV) % 128 + 1).bfloat16()                  # exact
+    x, gate = (torch.full((T, 1), v, dtype=torch.bfloat16, device=DEV) for v in (0.0, 200.0))
+    x[::each, 0], gate[::each] = value, -200.0
+    cu = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    y, last, kept = tb.wtconv_gated_scan_forward(x, gate, cu, want_kept=True)
+    for i in range(n):
+        assert (y[i * each:(i + 1) * each] == value[i]).all(), i
+    assert last.item() == value[-1].item()
+    dy = torch.zeros_like(y)
+    dy[-1] = 3.0
+    dx, dgate, _ = tb.wtconv_gated_scan_backward(dy, torch.full_like(last, 2.0), x, gate, cu, None, kept)
+    assert dx[(n - 1) * each].item() == 5.0 and not dgate.any()
+    dx[(n - 1) * each] = 0
+    assert not dx.any()
+
+
 def test_gated_scan_is_the_same_again():
     cu = torch.tensor([0, 5000, 9000], dtype=torch.int32, device=DEV)
     x, gate = (t.requires_grad_() for t in scan_inputs(9000, 33, "bf16", seed=7))
