@@ -395,6 +395,39 @@ def test_gated_scan_many_sequences():
     check_scan(x, gate, cu, normal(gen(6), 700, 4), False, "fp32")
 
 
+@pytest.mark.parametrize("reverse", [False, True])
+def test_gated_scan_of_mostly_empty_sequences(reverse):
+    """A short pack beside many sequences with no token: their states are passed on by many threads (one that walks all of
+    them takes 0.2 us each, 0.2 s), and so are their gradients."""
+    n, T, C = 1 << 20, 37, 3
+    cu = torch.full((n + 1,), T, dtype=torch.int32, device=DEV)
+    cu[:500], cu[500:n // 2] = 0, 21
+    x, gate = scan_inputs(T, C, "fp32", seed=2)
+    state, dlast, dy = normal(gen(3), n, C), normal(gen(4), n, C), normal(gen(5), T, C)
+
+    def timed(f):
+        f()
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        got = f()
+        b.record()
+        torch.cuda.synchronize()
+        assert a.elapsed_time(b) < 20
+        return got
+    y, last, kept = timed(lambda: tb.wtconv_gated_scan_forward(x, gate, cu, state, reverse, want_kept=True))
+    dx, dgate, dstate = timed(lambda: tb.wtconv_gated_scan_backward(dy, dlast, x, gate, cu, state, kept, reverse))
+    full = [499, n // 2 - 1]
+    few = lambda t: t[full].contiguous()
+    cuf = torch.tensor([0, 21, T], dtype=torch.int32, device=DEV)
+    yf, lastf, keptf = tb.wtconv_gated_scan_forward(x, gate, cuf, few(state), reverse, want_kept=True)
+    dxf, dgatef, dstatef = tb.wtconv_gated_scan_backward(dy, few(dlast), x, gate, cuf, few(state), keptf, reverse)
+    for a, b in ((y, yf), (last[full], lastf), (dx, dxf), (dgate, dgatef), (dstate[full], dstatef)):
+        assert torch.equal(a, b)
+    empty = torch.ones(n, dtype=torch.bool, device=DEV)
+    empty[full] = False
+    assert torch.equal(last[empty], state[empty]) and torch.equal(dstate[empty], dlast[empty])
+
+
 def test_gated_scan_of_the_largest_pack():
     """2^31 - 1025 tokens of one channel, whose last part ends 2^31 tokens after the first one's begin if it is taken whole:
     every 2^20th token sets the state, the others keep it, and the last one's gradient goes back to the last that set it."""
