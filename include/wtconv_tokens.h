@@ -230,8 +230,11 @@ typedef struct {
  * attention; tokens of no sequence get zeros.  y [T, C] contiguous.  kept or
  * NULL: what the backward pass needs, wtconv_gated_scan_kept() bytes.  h is
  * float32 throughout.  A value that is not finite stays to its sequence's end and
- * never reaches another.  States and x are to stay below 2^127, as differences of two
- * are taken.  state and last must not overlap. */
+ * never reaches another: an infinity keeps its sign whatever the gates leave of it
+ * (one of +-infinity counts as a very large one) and becomes a NaN with an infinity
+ * of the other sign or a NaN alone; so does the state's gradient in the backward
+ * pass.  Finite states and x are to stay below 2^127: a difference of two that
+ * float32 does not hold counts as infinite.  state and last must not overlap. */
 size_t wtconv_gated_scan_kept(const wtc_scan_desc* d);        /* bytes: 4 for each channel of every 8th token */
 size_t wtconv_gated_scan_workspace(const wtc_scan_desc* d);   /* of both passes; 0 bytes, and NULL is taken, for short packs */
 int wtconv_gated_scan_forward(const wtc_scan_desc* d, const void* x, const void* gate, const int* cu_seqlens,

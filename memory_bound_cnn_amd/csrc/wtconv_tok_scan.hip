@@ -131,12 +131,27 @@ __device__ __forceinline__ Gate gate(float f) {
     const float m = e * r;
     return {f >= 0.f ? m : -m};
 }
-// a h + (1 - a) x
-__device__ __forceinline__ float move(const Gate& g, float h, float x) { return fmaf(g.m, x - h, g.slow() ? h : x); }
-// a v, (1 - a) v, and a (1 - a) v
-__device__ __forceinline__ float keep(const Gate& g, float v) { return fmaf(g.m, -v, g.slow() ? v : 0.f); }
+// a h + (1 - a) x, a v, (1 - a) v, and a (1 - a) v.  Differences make a NaN of an infinity that should stay one (and so
+// does a gate that became 0): ANY looks for infinities, whose step is their sum, and is for what turned into a NaN.
+template <bool ANY = false>
+__device__ __forceinline__ float move(const Gate& g, float h, float x) {
+    const float v = fmaf(g.m, x - h, g.slow() ? h : x);
+    return ANY && (isinf(h) || isinf(x)) ? (h + x) + (g.m - g.m) : v;
+}
+template <bool ANY = false>
+__device__ __forceinline__ float keep(const Gate& g, float v) {
+    const float w = fmaf(g.m, -v, g.slow() ? v : 0.f);
+    return ANY && isinf(v) ? v + (g.m - g.m) : w;
+}
 __device__ __forceinline__ float take(const Gate& g, float v) { return (g.slow() ? g.m : 1.f + g.m) * v; }
 __device__ __forceinline__ float both(const Gate& g, float v) { return fabsf(g.m) * (1.f - fabsf(g.m)) * v; }
+
+// A value of the two became a NaN (first, their sum: one comparison where there is none).
+__device__ __forceinline__ bool turned(const float (&before)[V], const float (&now)[V]) {
+    return __builtin_expect(isnan(now[0] + now[1]), 0) && ((isnan(now[0]) && !isnan(before[0])) || (isnan(now[1]) && !isnan(before[1])));
+}
+typedef std::false_type Finite;   // how a step is taken, see move
+typedef std::true_type Any;
 
 // ------------------------------------------------------------------ places
 // Places of a pack in the order they are walked: place p is token p, or with
@@ -254,18 +269,28 @@ __global__ void __launch_bounds__(256) k_scan_maps(ScanArgs a) {
         const int count = min(to - from - done, kAhead);
         const Rows<T, ONE, kAhead> xr = x, fr = f;
         if (done + kAhead < to - from) fetch(BACK ? to - done - kAhead : from + done + kAhead);
+        const float before[V] = {B[0], B[1]};
+        auto tokens = [&](auto any) {
+            constexpr bool ANY = decltype(any)::value;
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int j = BACK ? kAhead - 1 - k : k;
-            const bool there = j < count;
+            for (int k = 0; k < kAhead; ++k) {
+                const int j = BACK ? kAhead - 1 - k : k;
+                const bool there = j < count;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const Gate g = gate<T>(value(fr.v[j], i));
-                const float in = value(xr.v[j], i);
-                const float next = BACK ? keep(g, in + B[i]) : move(g, B[i], in);
-                A[i] = there ? keep(g, A[i]) : A[i];
-                B[i] = there ? next : B[i];
+                for (int i = 0; i < V; ++i) {
+                    const Gate g = gate<T>(value(fr.v[j], i));
+                    const float in = value(xr.v[j], i);
+                    const float next = BACK ? keep<ANY>(g, in + B[i]) : move<ANY>(g, B[i], in);
+                    if (!ANY) A[i] = there ? keep(g, A[i]) : A[i];
+                    B[i] = there ? next : B[i];
+                }
             }
+        };
+        tokens(Finite());
+        if (turned(before, B)) {
+            B[0] = before[0];
+            B[1] = before[1];
+            tokens(Any());
         }
     }
 #pragma unroll
@@ -276,42 +301,78 @@ __global__ void __launch_bounds__(256) k_scan_maps(ScanArgs a) {
 // threads of a channel have up to kRun parts each, in order, and take what the
 // threads before them leave.
 constexpr int kRun = kMostParts / 128, kCols = 8;
-__device__ __forceinline__ float apply(const float2& m, float h) { return m.x < 0.f ? m.y : fmaf(m.x, h, m.y); }
+template <bool ANY>   // see move; an A of 0 keeps an infinity too
+__device__ __forceinline__ float apply(const float2& m, float h) {
+    const float v = ANY && isinf(h) ? (h + m.y) + (m.x - m.x) : fmaf(m.x, h, m.y);
+    return m.x < 0.f ? m.y : v;
+}
 // first one, then the other
+template <bool ANY>
 __device__ __forceinline__ float2 after(const float2& one, const float2& other) {
-    return make_float2(one.x < 0.f || other.x < 0.f ? kCut : other.x * one.x, apply(other, one.y));
+    return make_float2(one.x < 0.f || other.x < 0.f ? kCut : other.x * one.x, apply<ANY>(other, one.y));
 }
 
 template <bool BACK>
 __global__ void __launch_bounds__(1024) k_scan_starts(ScanArgs a) {
     __shared__ float2 whole[16][kCols];   // of a wave's eight threads of a channel
+    __shared__ bool some[16];             // a wave has met an infinity
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane % kCols, c = blockIdx.x * kCols + col;
     const int run = (a.parts + 127) / 128, first = (int)(threadIdx.x / kCols) * run;
     auto part_of = [&](int k) { return BACK ? a.parts - 1 - k : k; };
+    auto map_of = [&](int k) {   // the last part's map (BACK: the first one's) is not there, nor needed
+        const bool there = k < run && first + k + 1 < a.parts && c < a.C;
+        return there ? a.maps[(size_t)part_of(first + k) * a.C + c] : make_float2(1.f, 0.f);
+    };
+    auto start = [&](int k, float h) {
+        if (k < run && first + k < a.parts && c < a.C) a.starts[(size_t)part_of(first + k) * a.C + c] = h;
+    };
+    auto join = [&](float2 all, auto any) {   // with the threads before it in the wave
+#pragma unroll
+        for (int o = kCols; o < 64; o <<= 1) {
+            const float2 p = make_float2(__shfl_up(all.x, o), __shfl_up(all.y, o));
+            if (lane >= o) all = after<decltype(any)::value>(p, all);
+        }
+        return all;
+    };
     float2 m[kRun];
     float2 all = make_float2(1.f, 0.f);
+    bool infinite = false;
 #pragma unroll
-    for (int k = 0; k < kRun; ++k) {   // the last part's map (BACK: the first one's) is not there, nor needed
-        const bool there = k < run && first + k + 1 < a.parts && c < a.C;
-        m[k] = there ? a.maps[(size_t)part_of(first + k) * a.C + c] : make_float2(1.f, 0.f);
+    for (int k = 0; k < kRun; ++k) m[k] = map_of(k);
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) {
+        infinite |= isinf(m[k].y);
+        all = after<false>(all, m[k]);
     }
-#pragma unroll
-    for (int k = 0; k < kRun; ++k) all = after(all, m[k]);
-#pragma unroll
-    for (int o = kCols; o < 64; o <<= 1) {
-        const float2 p = make_float2(__shfl_up(all.x, o), __shfl_up(all.y, o));
-        if (lane >= o) all = after(p, all);
+    all = join(all, Finite());
+    const bool rare = __builtin_amdgcn_ballot_w64(infinite) != 0;
+    if (__builtin_expect(rare, 0)) {
+        all = make_float2(1.f, 0.f);
+#pragma unroll 1
+        for (int k = 0; k < run; ++k) all = after<true>(all, map_of(k));
+        all = join(all, Any());
     }
     if (lane >= 64 - kCols) whole[wave][col] = all;
+    if (lane == 0) some[wave] = rare;
     const float2 p = make_float2(__shfl_up(all.x, kCols), __shfl_up(all.y, kCols));
     __syncthreads();
     float h = 0.f;
-    for (int w = 0; w < wave; ++w) h = apply(whole[w][col], h);
-    if (lane >= kCols) h = apply(p, h);
+    if (__builtin_expect(__builtin_amdgcn_ballot_w64(some[lane & 15]) == 0, 1)) {
+        for (int w = 0; w < wave; ++w) h = apply<false>(whole[w][col], h);
+        if (lane >= kCols) h = apply<false>(p, h);
 #pragma unroll
-    for (int k = 0; k < kRun; ++k) {
-        if (k < run && first + k < a.parts && c < a.C) a.starts[(size_t)part_of(first + k) * a.C + c] = h;
-        h = apply(m[k], h);
+        for (int k = 0; k < kRun; ++k) {
+            start(k, h);
+            h = apply<false>(m[k], h);
+        }
+    } else {
+        for (int w = 0; w < wave; ++w) h = apply<true>(whole[w][col], h);
+        if (lane >= kCols) h = apply<true>(p, h);
+#pragma unroll 1
+        for (int k = 0; k < run; ++k) {
+            start(k, h);
+            h = apply<true>(map_of(k), h);
+        }
     }
 }
 
@@ -351,17 +412,25 @@ __global__ void __launch_bounds__(256) k_scan_forward(ScanArgs a) {
         }
         if (a.kept && p0 % kScanKept == 0) store_two<ONE>(a.kept + (size_t)(p0 / kScanKept) * a.C + c, h);
         T* y = static_cast<T*>(a.y) + row_of(a, p0) * a.C + c;
-        auto token = [&](int j) {
+        auto token = [&](int j, auto any) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) h[i] = move(gate<T>(value(fr.v[j], i)), h[i], value(xr.v[j], i));
+            for (int i = 0; i < V; ++i) h[i] = move<decltype(any)::value>(gate<T>(value(fr.v[j], i)), h[i], value(xr.v[j], i));
         };
-        if (w.s >= 0 && p0 > w.from && p0 + kAhead < w.to) {   // no start and no end
+        bool plain = w.s >= 0 && p0 > w.from && p0 + kAhead < w.to;   // no start and no end
+        if (plain) {
+            const float before[V] = {h[0], h[1]};
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
-                token(j);
+                token(j, Finite());
                 store_two<ONE>(y + j * step, h);
             }
-        } else {
+            if (turned(before, h)) {
+                plain = false;
+                h[0] = before[0];
+                h[1] = before[1];
+            }
+        }
+        if (!plain) {
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
                 const int p = p0 + j;
@@ -374,7 +443,7 @@ __global__ void __launch_bounds__(256) k_scan_forward(ScanArgs a) {
                         h[0] = h[1] = 0.f;
                         if (a.state) load_state<ONE>(a.state + state_of(a, w.s, c), h);
                     }
-                    token(j);
+                    token(j, Any());
                     if (p + 1 == w.to && a.last) store_two<ONE>(a.last + state_of(a, w.s, c), h);
                 }
                 store_two<ONE>(y + j * step, h);
@@ -398,7 +467,8 @@ __global__ void __launch_bounds__(256) k_scan_backward(ScanArgs a) {
     if (part + 1 < a.parts) load_state<ONE>(a.starts + (size_t)part * a.C + c, G);
     Where w = find(a, end - 1);
     const long long step = a.reverse ? -a.C : a.C;
-    for (int p0 = first + (end - first - 1) / N * N; p0 >= first; p0 -= N) {
+    bool again = false;   // the same tokens, as the ones with a start or an end among them are taken
+    for (int p0 = first + (end - first - 1) / N * N; p0 >= first; p0 -= again ? 0 : N) {
         Rows<T, ONE, N> x, f, dy;
         x.fetch(a.x, a.x_stride, a, p0, end, c);
         f.fetch(a.f, a.f_stride, a, p0, end, c);
@@ -412,32 +482,40 @@ __global__ void __launch_bounds__(256) k_scan_backward(ScanArgs a) {
         for (int j = 0; j < N; ++j)
 #pragma unroll
             for (int i = 0; i < V; ++i) g[j][i] = gate<T>(value(f.v[j], i));
-        auto forward = [&](int j) {
+        auto forward = [&](int j, auto any) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) now[i] = move(g[j][i], now[i], value(x.v[j], i));
+            for (int i = 0; i < V; ++i) now[i] = move<decltype(any)::value>(g[j][i], now[i], value(x.v[j], i));
         };
-        auto token = [&](int j) {   // G becomes what the token hands to the one before it
+        auto token = [&](int j, auto any) {   // G becomes what the token hands to the one before it
             float vx[V], vf[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const float dh = G[i] + value(dy.v[j], i);
                 vx[i] = take(g[j][i], dh);
                 vf[i] = both(g[j][i], dh) * (h[j][i] - value(x.v[j], i));
-                G[i] = keep(g[j][i], dh);
+                G[i] = keep<decltype(any)::value>(g[j][i], dh);
             }
             store_two<ONE>(dx + j * step, vx);
             store_two<ONE>(df + j * step, vf);
         };
-        if (w.s >= 0 && p0 > w.from && p0 + N < w.to) {   // no start and no end
+        if (w.s >= 0 && p0 > w.from && p0 + N < w.to && !again) {   // no start and no end
+            const float behind[V] = {G[0], G[1]};
 #pragma unroll
             for (int j = 0; j < N; ++j) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) h[j][i] = now[i];
-                if (j + 1 < N) forward(j);
+                if (j + 1 < N) forward(j, Finite());
             }
+            again = turned(h[0], now);
 #pragma unroll
-            for (int j = N - 1; j >= 0; --j) token(j);
+            for (int j = N - 1; j >= 0; --j) token(j, Finite());
+            again |= turned(behind, G);
+            if (again) {
+                G[0] = behind[0];
+                G[1] = behind[1];
+            }
         } else {
+            again = false;
             const Where last = w;
             Where up = find(a, p0);
 #pragma unroll
@@ -452,7 +530,7 @@ __global__ void __launch_bounds__(256) k_scan_backward(ScanArgs a) {
                 }
 #pragma unroll
                 for (int i = 0; i < V; ++i) h[j][i] = now[i];
-                if (j + 1 < N) forward(j);
+                if (j + 1 < N) forward(j, Any());
             }
             w = last;
 #pragma unroll
@@ -471,7 +549,7 @@ __global__ void __launch_bounds__(256) k_scan_backward(ScanArgs a) {
                     G[0] = G[1] = 0.f;
                     if (a.dlast) load_state<ONE>(a.dlast + state_of(a, w.s, c), G);
                 }
-                token(j);
+                token(j, Any());
                 if (p == w.from && a.last) store_two<ONE>(a.last + state_of(a, w.s, c), G);
             }
         }
@@ -519,7 +597,7 @@ __global__ void __launch_bounds__(256) k_scan_step(StepArgs a) {
         unpack(load_raw(static_cast<const T*>(a.f) + row * a.f_stride + c, n), f);
         load_states(a.state + row * a.C + c, n, h);
 #pragma unroll
-        for (int i = 0; i < V; ++i) h[i] = move(gate<T>(f[i]), h[i], x[i]);
+        for (int i = 0; i < V; ++i) h[i] = move<true>(gate<T>(f[i]), h[i], x[i]);
         store_part(static_cast<T*>(a.y) + row * a.C + c, n, h);
         store_states(a.out + row * a.C + c, n, h);
     }

@@ -120,7 +120,10 @@ def gated_scan(x, gate, cu_seqlens, state=None, reverse=False):
     as for :func:`attention`; tokens of no sequence get zeros.  state [n, C]
     float32: what each sequence starts from, zeros unless given; last [n, C]
     float32: what it leaves.  reverse: from the last token to the first.  With
-    gradients, half a byte a channel and token is kept beside the inputs."""
+    gradients, half a byte a channel and token is kept beside the inputs.
+    An infinity in a state, or in its gradient, stays one to the sequence's end (a
+    NaN with one of the other sign); finite states and x are to stay below 2^127, as
+    differences of two are taken."""
     y, last = (_ops or _load()).gated_scan(x, gate, cu_seqlens, state, reverse)
     return y, last
 

@@ -309,6 +309,47 @@ def test_gated_scan_not_finite_is_not_forgotten(reverse, dtype):
 
 
 @BOTH
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("cu", [[0, 1900, 3000], [0, 45], [0, 3, 20, 20, 61]])
+def test_gated_scan_infinities_stay(cu, reverse, dtype):
+    """An infinity that enters a state, or a gradient, stays one of its sign where the gates keep most of it, where they keep
+    little (over a part 0 in float32), and where some do; it becomes a NaN with one of the other sign or a NaN gate alone.
+    What is finite is as without it."""
+    T, C, n, inf = cu[-1], 8, len(cu) - 1, math.inf
+    cut = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    x0, some = scan_inputs(T, C, dtype, seed=T)
+    at, later = (T // 3, T // 2) if not reverse else (T // 2, T // 3)
+    for gate0 in (some - 3, some * 0 + 9, some * 0 - 9):
+        x, gate = x0.clone(), gate0.clone()
+        state, dlast, dy = normal(gen(1), n, C), normal(gen(2), n, C), normal(gen(3), T, C, dtype=TYPES[dtype])
+        clean = [t.clone() for t in (x, gate, state, dy, dlast)]
+        state[:, 0] = inf
+        x[at, 1], x[at, 2] = inf, -inf
+        x[at, 3], x[later, 3] = inf, -inf
+        dlast[:, 4], dy[later, 5] = -inf, inf
+        state[:, 6], gate[later, 6] = -inf, math.nan
+
+        def run(x, gate, state, dy, dlast):
+            leaves = [t.detach().clone().requires_grad_() for t in (x, gate, state)]
+            y, last = tokens.gated_scan(leaves[0], leaves[1], cut, leaves[2], reverse)
+            return [t.detach() for t in (y, last) + torch.autograd.grad((y, last), leaves, (dy, dlast))]
+        got, want = run(x, gate, state, dy, dlast), run(*clean)
+        r = scan_ref(x, gate, cu, state, reverse, dy, dlast)
+        for name, a, b in zip(("y", "last", "dx", "df", "dstate"), got, want):
+            ref, a, b = r[name], a.cpu(), b.cpu()
+            assert torch.equal(a.isnan(), ref.isnan()), name
+            there = ref.isinf()
+            assert torch.equal(a.isinf(), there) and torch.equal(a[there].double(), ref[there]), name
+            assert torch.equal(a[ref.isfinite()], b[ref.isfinite()]), name
+        # a token at a time
+        y, new = tokens.gated_scan_step(x[at:at + 1].expand(n, C), gate[later:later + 1].expand(n, C), state)
+        a = torch.sigmoid(gate[later].double())
+        ref = a * state.double() + torch.sigmoid(-gate[later].double()) * x[at].double()
+        assert torch.equal(new.isnan(), ref.isnan()) and torch.equal(new.isinf(), ref.isinf())
+        assert torch.equal(new[ref.isinf()].double(), ref[ref.isinf()])
+
+
+@BOTH
 def test_gated_scan_gates_at_their_ends(dtype):
     """Gates of +-infinity and beyond what exp holds: all of the state, or none of it."""
     C, T = 6, 40
