@@ -136,13 +136,24 @@ Tensors _gated_scan_backward(const Tensor& dy0, const OptTensor& dlast0, const T
              "wtconv_gated_scan_backward");
     return state0 ? Tensors{dx, dgate, dstate} : Tensors{dx, dgate};
 }
+// `to`, contiguous, may be t itself, but no part of one of t's rows.  PyTorch does not say so of rows that are apart.
+void check_apart(const Tensor& to, const Tensor& t) {
+    at::assert_no_partial_overlap(to, t);
+    if (t.numel() == 0 || !dense(t) || (t.is_contiguous() && t.const_data_ptr() == to.const_data_ptr())) return;
+    // rows number `from` up to `end` have a byte in to's
+    const int64_t step = t.stride(0) * t.element_size(), length = t.size(1) * t.element_size(), bytes = to.numel() * to.element_size(),
+                  at = reinterpret_cast<intptr_t>(to.const_data_ptr()) - reinterpret_cast<intptr_t>(t.const_data_ptr());
+    const int64_t rows = step > 0 ? t.size(0) : 1, from = at < length ? 0 : step > 0 ? (at - length) / step + 1 : 1,
+                  end = at + bytes <= 0 ? 0 : step > 0 ? std::min(rows, (at + bytes - 1) / step + 1) : 1;
+    TORCH_CHECK(from >= end, "out and an input share a part of their memory");
+}
 // y; the new state goes to `to`, which may be state
 Tensor gated_scan_step(const Tensor& x0, const Tensor& gate0, const Tensor& state, Tensor to) {
     const int dtype = activation(x0, "x", 2);
     check_like(gate0, "gate", x0);
     check(state, "state", at::kFloat, x0, x0.sizes());
     check(to, "out", at::kFloat, x0, x0.sizes());
-    for (const Tensor& t : {state, x0, gate0}) at::assert_no_partial_overlap(to, t);   // it may be one of them itself
+    for (const Tensor& t : {state, x0, gate0}) check_apart(to, t);
     const Tensor x = dense_rows(x0), gate = dense_rows(gate0), y = empty(x.sizes(), x);
     const wtc_scan_desc d = {x.size(0), x.stride(0), gate.stride(0), 0, 0, narrow(x.size(1), "channels of x"), dtype, 0};
     const On on(x);

@@ -222,6 +222,28 @@ def test_step_into_its_inputs():
             tokens.gated_scan_step(*args, state, out=long[8:].view(4, 8))
 
 
+def test_step_into_memory_between_rows():
+    """The new state may lie before, behind or between the rows of an input, which are apart, but not in one of them."""
+    n, C, apart = 4, 8, 40                                     # a state is 32 long, as are the gaps between rows
+    want = tokens.gated_scan_step(normal(gen(), n, C), normal(gen(1), n, C), normal(gen(2), n, C))
+    for at in range(0, 32 + 4 * apart):
+        long = torch.zeros(32 + 4 * apart + 32, device=DEV)
+        x = long[32:32 + 4 * apart].view(n, apart)[:, :C]      # rows at 32, 72, 112, 152
+        x.copy_(normal(gen(), n, C))
+        out = long[at:at + 32].view(n, C)
+        meets = any(at < r + C and r < at + 32 for r in (32, 72, 112, 152))
+        for args in ((x, normal(gen(1), n, C)), (normal(gen(), n, C), x)):
+            if meets:
+                with pytest.raises(RuntimeError, match="memory"):
+                    tokens.gated_scan_step(*args, normal(gen(2), n, C), out=out)
+        if not meets:
+            y, new = tokens.gated_scan_step(x, normal(gen(1), n, C), normal(gen(2), n, C), out=out)
+            assert torch.equal(y, want[0]) and torch.equal(out, want[1]) and torch.equal(x, normal(gen(), n, C))
+    row = torch.zeros(64, device=DEV)
+    with pytest.raises(RuntimeError, match="memory"):          # one row for all
+        tokens.gated_scan_step(row[20:28].expand(n, C), row[:8].expand(n, C), normal(gen(2), n, C), out=row[:32].view(n, C))
+
+
 def test_step_in_place_is_seen_by_autograd():
     """A state that is saved for a gradient and then overwritten is an error, not a wrong gradient."""
     s = normal(gen(), 4, 8)
