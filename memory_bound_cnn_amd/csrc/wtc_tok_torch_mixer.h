@@ -286,21 +286,35 @@ Tensors _expert_linear_weight_grad(const Tensor& dy0, const Tensor& x0, const Te
 }  // namespace op
 
 // ================================================================== gradients
-// A leaf's gradient belongs to the stream on which the leaf was first used, for as long as a pass that used it lives.  Of
-// an eager pass that is the default stream, which PyTorch would make wait for a capture: that ends the process.  Refused.
+// Whether the backward pass from `node` on, as far as it is wanted, runs through a node of the default stream: a node
+// belongs to the stream of the forward pass that made it, and a leaf's gradient to that on which the leaf was first used,
+// for as long as a pass that used it lives.
+bool meets_default_stream(torch::autograd::Node* node) {
+    std::vector<torch::autograd::Node*> open = {node};
+    std::unordered_set<torch::autograd::Node*> seen;
+    while (!open.empty()) {
+        torch::autograd::Node* at = open.back();
+        open.pop_back();
+        for (size_t i = 0; i < at->num_outputs(); ++i) {
+            torch::autograd::Node* to = at->next_edge(i).function.get();
+            if (!to || !at->task_should_compute_output(i) || !seen.insert(to).second) continue;
+            const auto stream = to->stream();
+            if (stream && stream->id() == 0) return true;
+            open.push_back(to);
+        }
+    }
+    return false;
+}
+// PyTorch would make the default stream wait for the capture, which ends the process.  Refused; what the pass meets before
+// its first node of these operators is not seen.
 void check_capture() {
     const auto node = torch::autograd::get_current_node();
     if (!node) return;
     hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
     if (hipStreamIsCapturing(c10::hip::getCurrentHIPStream().stream(), &status) != hipSuccess || status == hipStreamCaptureStatusNone)
         return;
-    for (size_t i = 0; i < node->num_outputs(); ++i) {
-        const auto& to = node->next_edge(i).function;
-        if (!to || !node->task_should_compute_output(i) || !dynamic_cast<torch::autograd::AccumulateGrad*>(to.get())) continue;
-        const auto stream = to->stream();
-        TORCH_CHECK(!stream || stream->id() != 0, "a backward pass cannot be captured while an eager pass of the same leaves lives; "
-                    "delete its outputs, or detach the leaves anew");
-    }
+    TORCH_CHECK(!meets_default_stream(node.get()), "a backward pass cannot be captured while an eager pass of the same leaves lives; "
+                "delete its outputs, or detach the leaves anew");
 }
 
 struct LayerNorm : torch::autograd::Function<LayerNorm> {
@@ -510,6 +524,8 @@ namespace {
 
 void mixer_python(py::module_& m) {
     using nogil = py::call_guard<py::gil_scoped_release>;
+    // of the pass behind a tensor; what a captured backward pass is refused by
+    m.def("_meets_default_stream", [](const Tensor& t) { return t.grad_fn() && meets_default_stream(t.grad_fn().get()); });
     m.def("layer_norm", [](const Tensor& x, const Tensor& weight, const OptTensor& bias, const OptTensor& residual, double eps) {
         return OP(layer_norm).call(x, weight, bias, residual, eps);
     }, nogil());

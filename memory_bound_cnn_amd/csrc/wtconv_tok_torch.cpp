@@ -18,7 +18,6 @@
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/autograd_not_implemented_fallback.h>
 #include <torch/csrc/autograd/VariableTypeUtils.h>
-#include <torch/csrc/autograd/functions/accumulate_grad.h>
 #include <torch/extension.h>
 #include <torch/library.h>
 
@@ -27,6 +26,7 @@
 #include <limits>
 #include <optional>
 #include <tuple>
+#include <unordered_set>
 #include <vector>
 
 #include "../../include/wtconv_tokens.h"

@@ -25,7 +25,9 @@ pass of 8 tokens take 32 us (norm) and 31 us (attention) instead of 75 and 72.
 Forward and backward passes can be captured into graphs.  A backward pass is not,
 while an eager pass of the same leaves lives: PyTorch ties a leaf's gradient to
 the stream on which the leaf was used first.  ``layer_norm``, ``gated_scan`` and
-the ``expert_`` functions refuse it.
+the ``expert_`` functions refuse it for all leaves behind them, through whatever
+other operators; leaves that a pass reaches before the first of these functions
+(a linear layer's behind the last of them) are not looked at.
 """
 
 from typing import NamedTuple

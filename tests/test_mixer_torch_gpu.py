@@ -114,6 +114,85 @@ def test_a_backward_pass_is_not_captured_beside_an_eager_one(name):
         compare(out, want)
 
 
+def behind_other_operators(name):
+    """(module, call): leaves that reach the operators through others: a linear layer, casts, splits of a projection."""
+    torch.manual_seed(0)
+    x, cu = normal(gen(), 71, 64), torch.tensor([0, 35, 71], dtype=torch.int32, device=DEV)
+    if name == "linear":
+        m = torch.nn.Linear(64, 32, device=DEV)
+        w = torch.ones(32, device=DEV)
+        return m, lambda: tokens.layer_norm(m(x), w)
+    m = tokens.ScanBlock(64, experts=4, device=DEV, dtype=torch.float32)
+
+    def call():
+        with torch.autocast("cuda", torch.bfloat16, enabled=name == "autocast block", cache_enabled=False):
+            return m(x, cu)
+    return m, call
+
+
+BEHIND = pytest.mark.parametrize("name", ["linear", "block", "autocast block"])
+
+
+@BEHIND
+def test_leaves_of_the_default_stream_are_found(name):
+    m, call = behind_other_operators(name)
+    meets, s = tokens._load()._meets_default_stream, torch.cuda.Stream()
+
+    def aside():
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            y = call()
+        torch.cuda.current_stream().wait_stream(s)
+        return y
+    assert not meets(aside())
+    eager = call()
+    assert meets(eager) and meets(aside())      # the leaves are the eager pass's as long as that lives
+    del eager
+    assert not meets(aside())
+    with torch.no_grad():
+        assert not meets(call())
+
+
+@BEHIND
+def test_a_backward_pass_behind_others_is_not_captured_beside_an_eager_one(name):
+    m, call = behind_other_operators(name)
+    leaves = list(m.parameters())
+
+    def step():
+        return torch.autograd.grad(call().float().square().sum(), leaves)
+    want = [t.clone() for t in step()]
+    eager = call()
+    assert tokens._load()._meets_default_stream(eager)
+    with pytest.raises(RuntimeError, match="cannot be captured while an eager pass"):
+        captured(step)
+    torch.cuda.synchronize()
+    del eager
+    graph, out = captured(step)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        compare(out, want)
+
+
+def test_a_captured_pass_is_refused_for_what_it_runs_through_alone():
+    """An eager pass of leaves whose gradients are not asked for does not matter."""
+    m, call = behind_other_operators("linear")
+    b = torch.zeros(32, device=DEV)
+
+    def step():
+        mine = b.detach().requires_grad_()
+        y = tokens.layer_norm(call(), torch.ones(32, device=DEV), mine)
+        return torch.autograd.grad(y.square().sum(), (mine,))
+    want = [t.clone() for t in step()]
+    eager = call()
+    graph, out = captured(step)
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        compare(out, want)
+    assert eager.isfinite().all()
+
+
 def test_larger_packs_replay_in_a_graph():
     """What has workspaces: scans of several parts, orders of several workgroups, weights' gradients of several splits;
     two graphs of the same work replayed in turn."""
