@@ -35,6 +35,7 @@ struct Args {
     void* db;
     float* parts;               // k_product_weights: sums of experts' parts, [slots][N][K], then [slots][N]
     long long x_stride, g_stride, slots;
+    long long first;            // k_product_rows: of the launch's slots
     int R, E, K, N, rows;       // rows: of a part of an expert, about
 };
 
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(64 * WM * WN, WM * WN * MB * NB == 8 ? 3 : 2) 
     // workgroups next to each other: 8 tiles of rows, then the next columns of those
     const int id = spread(blockIdx.x, gridDim.x), group = id / (8 * tiles), in = id % (8 * tiles);
     const int high = min(8, (int)a.slots - 8 * group), col0 = in / high * BN;
-    const Rows r = find_rows<BM>(a.cu, a.E, a.R, 8 * group + in % high, lane);
+    const Rows r = find_rows<BM>(a.cu, a.E, a.R, (int)a.first + 8 * group + in % high, lane);
     if (r.count == 0) return;
     const bool none = r.expert < 0;
     const size_t expert = none ? 0 : r.expert;
@@ -536,11 +537,13 @@ __global__ void __launch_bounds__(256) k_product_join(Args a) {
 template <typename T, bool BACK, int WM, int WN, int MB, int NB, int STAGES, bool SPREAD = false>
 int launch_rows(Args a, hipStream_t st) {
     constexpr int BM = 32 * WM * MB, BN = 32 * WN * NB;
-    a.slots = row_slots(a.R, a.E, BM);
-    const long long groups = a.slots * (((BACK ? a.K : a.N) + BN - 1) / BN);
-    if (groups > (1 << 23)) return WTC_ESHAPE;
-    hipLaunchKernelGGL((k_product_rows<T, BACK, WM, WN, MB, NB, STAGES, SPREAD>), dim3((unsigned)groups), dim3(64 * WM * WN), 0,
-                       st, a);
+    const long long all = row_slots(a.R, a.E, BM), tiles = ((BACK ? a.K : a.N) + BN - 1) / BN;
+    const long long most = ((1 << 22) / tiles) & ~7LL;   // a launch has less than 2^32 threads
+    for (; a.first < all; a.first += most) {
+        a.slots = most < all - a.first ? most : all - a.first;
+        hipLaunchKernelGGL((k_product_rows<T, BACK, WM, WN, MB, NB, STAGES, SPREAD>), dim3((unsigned)(a.slots * tiles)),
+                           dim3(64 * WM * WN), 0, st, a);
+    }
     return hipGetLastError() == hipSuccess ? WTC_OK : WTC_EHIP;
 }
 template <typename T>

@@ -724,6 +724,35 @@ def test_expert_linear_large(counts, K, N, dtype):
     check_product(*product_case(counts, K, N, dtype, bias=False, seed=K + N), dtype)
 
 
+def test_expert_linear_of_more_tiles_than_a_launch_has():
+    """1.2 billion rows of 8 channels: tiles of rows in three launches.  Whole numbers that come again every 2^20 + 7 rows, so
+    that every sum is exact: products up to 48; the gradients' 10^6 (random walks of 10^6 steps of at most 2, 400 times)."""
+    R, E, P = (1 << 30) + (1 << 27), 3, (1 << 20) + 7
+    at = [77, R // 3, R // 3, R - 1000]
+    g = gen(5)
+    px, pdy = (torch.randint(-n, n + 1, (P, 8), generator=g, device=DEV).bfloat16() for n in (2, 1))
+    x, dy = (t.repeat(R // P + 1, 1)[:R] for t in (px, pdy))
+    w = torch.randint(-3, 4, (E, 8, 8), generator=g, device=DEV).bfloat16()
+    cu = torch.tensor(at, dtype=torch.int32, device=DEV)
+    # an expert's runs of rows from one multiple of P to the next
+    runs = [(e, max(r, at[e]), min(r + P, at[e + 1])) for e in range(E) for r in range(at[e] // P * P, at[e + 1], P)]
+    for out, of, turned in ((tokens.expert_linear(x, w, cu), px, w.transpose(1, 2)),
+                            (tb.wtconv_expert_linear_input_grad(dy, w, cu), pdy, w)):
+        assert not out[:at[0]].any() and not out[at[-1]:].any()
+        want = [(of.float() @ turned[e].float().contiguous()).bfloat16() for e in range(E)]
+        for e, a, b in runs:
+            assert torch.equal(out[a:b], want[e][a % P:a % P + b - a]), (e, a)
+    del out
+    dw, db = tb.wtconv_expert_linear_weight_grad(dy, x, cu)
+    # products and dy of rows 0 .. r - 1 of the first P summed: 64 and 8 columns
+    both = torch.cat([(pdy[:, :, None] * px[:, None]).view(P, 64), pdy], 1).double().cumsum(0)
+    both = torch.cat([torch.zeros_like(both[:1]), both])
+    want = torch.zeros(E, 72, dtype=torch.float64, device=DEV)
+    for e, a, b in runs:
+        want[e] += both[a % P + b - a] - both[a % P]
+    assert torch.equal(dw, want[:, :64].view(E, 8, 8).bfloat16()) and torch.equal(db, want[:, 64:].bfloat16())
+
+
 @BOTH
 def test_expert_linear_rows_of_no_expert(dtype):
     """Before the first expert's rows and after the last's: zeros, and nothing of them reaches a gradient."""
