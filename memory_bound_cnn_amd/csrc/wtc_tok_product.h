@@ -22,6 +22,7 @@
 
 #include "wtc_tok_device.h"
 #include "wtc_tok_internal.h"
+#include "wtc_tok_segment.h"
 
 namespace wtc {
 namespace product {
@@ -255,11 +256,6 @@ struct Across {
 };
 
 // ------------------------------------------------------------------ work
-// The rows of a tile: SIZE of one expert's, or of no expert's (before the first's, after the last's).
-struct Rows {
-    int expert;   // -1: rows of none
-    int start, count;
-};
 // Segment s = 0 .. E + 1 of the rows: those before the first expert's, the experts', those after the last's.
 __device__ __forceinline__ int segment_begin(const int* cu, int E, int R, int s) {
     if (s <= 0) return 0;
@@ -285,11 +281,7 @@ __device__ __forceinline__ Rows find_rows(const int* cu, int E, int R, int slot,
         }
     }
     const int tile = BY_ROW ? ((slot - b) % SIZE == 0 ? (slot - b) / SIZE : -1) : slot - (b / SIZE + lo);
-    Rows r;
-    r.expert = lo == 0 || lo == E + 1 ? -1 : lo - 1;
-    r.start = b + tile * SIZE;
-    r.count = tile < 0 ? 0 : min(max(e - b - tile * SIZE, 0), SIZE);
-    return r;
+    return rows_of<SIZE>(lo == 0 || lo == E + 1 ? -1 : lo - 1, b, e, tile);
 }
 inline long long row_slots(long long R, int E, int size) { return R / size + E + 2; }
 

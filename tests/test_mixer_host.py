@@ -57,3 +57,39 @@ int main() {
 }
 """)
     assert out.startswith("0 of ")
+
+
+def test_tiles_of_rows_stay_inside_of_them(tmp_path):
+    """Each row of a segment is in one tile, and no tile, of whatever number, reaches past its end, up to the most rows."""
+    out = run(tmp_path, r"""
+#include <climits>
+#include <cstdio>
+#include "wtc_tok_segment.h"
+
+template <int SIZE>
+static long check(int b, int e) {
+    long bad = 0;
+    const int tiles = e > b ? (int)(((long long)e - b + SIZE - 1) / SIZE) : 0;
+    const int near[] = {-1, 0, 1, 2, tiles - 2, tiles - 1, tiles, tiles + 1, tiles + 512, INT_MAX / SIZE - 1, INT_MAX / SIZE + 1,
+                        INT_MAX / SIZE + 514, INT_MAX / 2, INT_MAX};
+    for (int t : near) {
+        const wtc::product::Rows r = wtc::product::rows_of<SIZE>(7, b, e, t);
+        const long long from = (long long)b + (long long)t * SIZE, to = from + SIZE < e ? from + SIZE : e;
+        const int want = t >= 0 && from < to ? (int)(to - from) : 0;
+        bad += r.expert != 7 || r.count != want || (want && r.start != from);
+    }
+    return bad;
+}
+
+int main() {
+    const int most = INT_MAX - (1 << 16);   // as many rows as a call may have
+    const int at[] = {0, 1, 15, 16, 17, 31, 32, 33, 127, 128, 129, 255, 256, 257, 1000, 1 << 20, (1 << 30) - 1, 1 << 30,
+                      most - 513 * 256, most - 257, most - 256, most - 1, most};
+    long bad = 0, n = 0;
+    for (int b : at)
+        for (int e : at) bad += check<16>(b, e) + check<32>(b, e) + check<64>(b, e) + check<128>(b, e) + check<256>(b, e), ++n;
+    printf("%ld of %ld bad\n", bad, n);
+    return bad != 0;
+}
+""")
+    assert out.startswith("0 of ")
