@@ -294,12 +294,16 @@ class Experts(torch.nn.Module):
     """A two-layer branch in several versions, of which each token takes the k
     that a linear layer gives it the largest logits for, weighted by their softmax:
         sum_j w_j down_e(gelu(up_e(x))),  e = e_j(x).
-    x [T, C] -> [T, C]."""
+    x [T, C] -> [T, C].  channels and hidden: multiples of 8."""
 
     def __init__(self, channels, hidden, experts, k=2, device=None, dtype=torch.bfloat16):
         super().__init__()
         if not 1 <= k <= experts:
             raise ValueError(f"{k} of {experts} experts a token")
+        if experts > 512:
+            raise ValueError(f"{experts} experts: up to 512 are supported")
+        if channels % 8 or hidden % 8:
+            raise ValueError(f"{channels} channels, {hidden} hidden: expert_linear takes multiples of 8")
         self.experts, self.k = experts, k
         f = dict(device=device, dtype=dtype)
         self.router = torch.nn.Linear(channels, experts, bias=False, **f)
@@ -327,9 +331,9 @@ class ScanBlock(torch.nn.Module):
     large for attention:
         h = x + proj(scan(values, gates of in(norm(x))))
         out = h + experts(norm(h))
-    x [T, C].  Half of the channels run from each sequence's first token to its
-    last and half the other way; with causal all from the first, and
-    :meth:`step` takes one more token of each sequence."""
+    x [T, C], C a multiple of 8.  Half of the channels run from each sequence's
+    first token to its last and half the other way; with causal all from the first,
+    and :meth:`step` takes one more token of each sequence."""
 
     def __init__(self, channels, hidden=None, experts=8, k=2, causal=False, device=None, dtype=torch.bfloat16):
         super().__init__()

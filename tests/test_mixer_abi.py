@@ -223,6 +223,15 @@ def test_modules_refuse_and_keep_their_norms():
     assert tokens.LayerNorm(8, bias=False).bias is None
 
 
+@pytest.mark.parametrize("make", [lambda: tokens.Experts(100, 64, 2), lambda: tokens.Experts(64, 100, 2), lambda: tokens.ScanBlock(100),
+                                  lambda: tokens.ScanBlock(9, causal=True), lambda: tokens.ScanBlock(64, hidden=36)])
+def test_modules_refuse_sizes_that_their_products_do_not_take(make):
+    with pytest.raises(ValueError, match="multiples of 8"):
+        make()
+    with pytest.raises(ValueError, match="up to 512"):
+        tokens.Experts(8, 8, tb.EXPERTS_MAX + 1)
+
+
 @pytest.fixture
 def plain(monkeypatch):
     """The operators that the modules call, in plain PyTorch."""
