@@ -5,6 +5,7 @@ Tolerances follow from where bits are dropped.  U is the unit roundoff of the
 storage type (2^-24 float32, 2^-8 bfloat16), relative to the value; float32 work
 on n terms is given n 2^-23 relative to the sum of the terms' magnitudes."""
 
+import ctypes
 import math
 
 import numpy as np
@@ -696,6 +697,112 @@ def test_expert_linear_with_bounds_in_no_order():
     torch.cuda.synchronize()
     assert torch.equal(guard, torch.full_like(guard, 7.0))
     check_product(x, w, b, cu, dy, "fp32")
+
+
+class Guarded:
+    """Outputs and workspaces of C calls one after another in one allocation, 4 KB of a known byte around each."""
+    PAD, BYTE = 4096, 0xA5
+
+    def __init__(self, *sizes):
+        self.at, end = [], self.PAD
+        for n in sizes:
+            self.at.append((end, n))
+            end += (n + 255) // 256 * 256 + self.PAD
+        self.memory = torch.full((end,), self.BYTE, dtype=torch.uint8, device=DEV)
+
+    def __getitem__(self, i):
+        return self.memory.data_ptr() + self.at[i][0]
+
+    def tensor(self, i, dtype):
+        a, n = self.at[i]
+        return self.memory[a:a + n].view(dtype)
+
+    def check(self):
+        torch.cuda.synchronize()
+        outside = torch.ones_like(self.memory, dtype=torch.bool)
+        for a, n in self.at:
+            outside[a:a + n] = False
+        assert (self.memory[outside] == self.BYTE).all()
+
+
+@BOTH
+@pytest.mark.parametrize("R,K,N,E,bounds", [
+    (3000, 64, 48, 4, [0, 3000, 0, 3000, -5]), (3000, 64, 48, 4, [0, 3000, 3000, 3000, 3000]), (12000, 8, 8, 3, [0, 12000, 0, 12000]),
+    (20000, 264, 136, 4, [9000, 20000, -7, 20000, 0]), (9, 520, 24, 5, [9, 0, 9, 3, 5, 1 << 30]), (400, 64, 264, 3, [400, 0, 399, 1]),
+    (6000, 1000, 1016, 6, [0, 6000, 0, 6000, 0, 6000, 0])])
+def test_expert_linear_writes_its_outputs_alone(R, K, N, E, bounds, dtype):
+    """Bounds of experts in any order: outputs and sums of parts are anything, but what lies around them in memory stays."""
+    g, dt = gen(R), TYPES[dtype]
+    size = dt.itemsize
+    x, dy, w, b = (normal(g, *s, dtype=dt) for s in ((R, K), (R, N), (E, N, K), (E, N)))
+    cu = torch.tensor(bounds, dtype=torch.int32, device=DEV)
+    d = tb.wtc_expert_desc(R, K, N, E, K, N, 0 if dtype == "fp32" else 1)
+    ref, lib = ctypes.addressof(d), tb._load()
+    need = lib.wtconv_expert_linear_weight_grad_workspace(ref)
+    out = Guarded(R * N * size, R * K * size, E * N * K * size, E * N * size, need)
+    dev = x.device
+    tb._call("wtconv_expert_linear_forward", dev, ref, x.data_ptr(), w.data_ptr(), b.data_ptr(), cu.data_ptr(), out[0])
+    out.check()
+    tb._call("wtconv_expert_linear_input_grad", dev, ref, dy.data_ptr(), w.data_ptr(), cu.data_ptr(), out[1])
+    out.check()
+    tb._call("wtconv_expert_linear_weight_grad", dev, ref, dy.data_ptr(), x.data_ptr(), cu.data_ptr(), out[2], out[3], out[4], need)
+    out.check()
+    if bounds == sorted(bounds):
+        y = tokens.expert_linear(x, w, cu, b)
+        dw, db = tb.wtconv_expert_linear_weight_grad(dy, x, cu)
+        dx = tb.wtconv_expert_linear_input_grad(dy, w, cu)
+        for i, t in enumerate((y, dx, dw, db)):
+            assert torch.equal(out.tensor(i, dt), t.reshape(-1))
+
+
+@BOTH
+@pytest.mark.parametrize("reverse", [0, 1])
+@pytest.mark.parametrize("T,C,bounds", [(300, 7, [0, 100, 300]), (300, 7, [250, 20, 280, 10, 300, -3, 400]), (41, 1, [40, 0, 41]),
+                                        (2000, 34, [1999, 0, 2000, 5]), (64, 3, [0, 0, 64, 64, 2])])
+def test_gated_scan_writes_its_outputs_alone(T, C, bounds, reverse, dtype):
+    x, gate = scan_inputs(T, C, dtype, seed=T)
+    n, dt = len(bounds) - 1, TYPES[dtype]
+    dy, state, dlast = normal(gen(1), T, C, dtype=dt), normal(gen(2), n, C), normal(gen(3), n, C)
+    cu = torch.tensor(bounds, dtype=torch.int32, device=DEV)
+    d = tb.wtc_scan_desc(T, C, C, C, n, C, 0 if dtype == "fp32" else 1, reverse)
+    ref, lib = ctypes.addressof(d), tb._load()
+    kept, need = lib.wtconv_gated_scan_kept(ref), lib.wtconv_gated_scan_workspace(ref)
+    row, states = T * C * dt.itemsize, n * C * 4
+    out = Guarded(row, states, kept, need, row, row, states)
+    tb._call("wtconv_gated_scan_forward", x.device, ref, x.data_ptr(), gate.data_ptr(), cu.data_ptr(), state.data_ptr(), out[0],
+             out[1], out[2], out[3], need)
+    out.check()
+    tb._call("wtconv_gated_scan_backward", x.device, ref, x.data_ptr(), gate.data_ptr(), cu.data_ptr(), state.data_ptr(), out[2],
+             dy.data_ptr(), dlast.data_ptr(), out[4], out[5], out[6], out[3], need)
+    out.check()
+    if bounds == sorted(bounds):
+        y, last, k = tb.wtconv_gated_scan_forward(x, gate, cu, state, reverse, want_kept=True)
+        grads = tb.wtconv_gated_scan_backward(dy, dlast, x, gate, cu, state, k, reverse)
+        for i, t in zip((0, 1, 4, 5, 6), (y, last) + grads):
+            assert torch.equal(out.tensor(i, t.dtype), t.reshape(-1))
+
+
+@BOTH
+@pytest.mark.parametrize("T,k,E,C", [(1, 1, 1, 1), (63, 3, 5, 33), (700, 2, 9, 130), (5000, 2, 70, 9)])
+def test_expert_rows_write_their_outputs_alone(T, k, E, C, dtype):
+    g, dt, dev = gen(T), TYPES[dtype], torch.device(DEV, 0)
+    experts = torch.randint(-1, E, (T, k), generator=g, device=DEV).int()
+    x, rows, dy, weights = normal(g, T, C, dtype=dt), normal(g, T * k, C, dtype=dt), normal(g, T, C, dtype=dt), normal(g, T, k)
+    lib, n = tb._load(), T * k
+    need = lib.wtconv_expert_order_workspace(n, E)
+    d = tb.wtc_rows_desc(T, C, C, k, E, C, 0 if dtype == "fp32" else 1)
+    ref, one, all_rows = ctypes.addressof(d), T * C * dt.itemsize, n * C * dt.itemsize
+    out = Guarded(4 * n, 4 * n, 4 * (E + 1), need, all_rows, one, all_rows, 4 * n)
+    tb._call("wtconv_expert_order", dev, n, E, experts.data_ptr(), out[0], out[1], out[2], out[3], need)
+    out.check()
+    tb._call("wtconv_expert_gather", dev, ref, x.data_ptr(), out[0], out[2], out[4])
+    tb._call("wtconv_expert_combine", dev, ref, rows.data_ptr(), weights.data_ptr(), out[0], out[5])
+    tb._call("wtconv_expert_combine_backward", dev, ref, dy.data_ptr(), rows.data_ptr(), weights.data_ptr(), out[0], out[2], out[6], out[7])
+    out.check()
+    order = tokens.expert_order(experts, E)
+    want = tuple(order) + (tokens.expert_gather(x, order), tokens.expert_combine(rows, weights, order))
+    for i, t in zip((0, 1, 2, 4, 5, 6, 7), want + tb.wtconv_expert_combine_backward(dy, rows, weights, order.slot, order.cu_experts)):
+        assert torch.equal(out.tensor(i, t.dtype), t.reshape(-1))
 
 
 @BOTH
