@@ -278,7 +278,8 @@ typedef struct {
     long long x_stride, r_stride; /* row strides of what is by token, and of the rows read */
     int k;                        /* choices of a token, >= 1; T k < 2^31 - 2^16         */
     int E;                        /* experts, 1 .. WTC_EXPERTS_MAX                       */
-    int C;                        /* channels, 1 .. WTC_ROWS_MAX_C                       */
+    int C;                        /* channels, 1 .. WTC_ROWS_MAX_C; T rows of them, each to
+                                     16 bytes, at most 2^37 bytes                        */
     int dtype;                    /* wtc_dtype of the activations                        */
 } wtc_rows_desc;
 

@@ -97,7 +97,7 @@ int check_rows(const wtc_rows_desc* d) {
     const int st = check_order(d->T * d->k, d->E);
     if (st != WTC_OK) return st;
     const long long chunks = ((long long)d->C * elem_bytes(d->dtype) + 15) / 16;
-    return d->T * chunks > (1LL << 33) ? WTC_ESHAPE : WTC_OK;   // 2^23 workgroups
+    return d->T * chunks > (1LL << 33) ? WTC_ESHAPE : WTC_OK;   // 128 GiB
 }
 
 int check_expert(const wtc_expert_desc* d) {

@@ -425,8 +425,9 @@ int launch_rows_sum(const wtc_rows_desc* d, const void* rows, const float* weigh
 namespace {
 template <typename T>
 void run_sum_back(const RowsArgs& a, hipStream_t st) {
-    // as few lanes as leave no more than four steps each, 4, 16 or 64 of them (us): 48 chunks (25088 x 384 bf16) by 16 lanes
-    // 18.6, by 64 22.2; 9 chunks (44273 x 35 float32, six rows a token) by 4 30.9, by 16 27.9
+    // Lanes of a token: 4 up to 4 chunks, 16 up to 64, and a wave beyond, which has four steps in rows of 256 chunks and more in
+    // longer ones.  Measured (us): 48 chunks (25088 x 384 bf16) by 16 lanes 18.6, by 64 22.2; 9 chunks (44273 x 35 float32, six
+    // rows a token) by 4 30.9, by 16 27.9
     const int G = a.chunks <= 4 ? 4 : a.chunks <= 64 ? 16 : 64;
     const long long blocks = (a.T * G + 255) / 256;
     const dim3 grid((unsigned)(blocks < (1 << 20) ? blocks : 1 << 20));
